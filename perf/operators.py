@@ -149,7 +149,8 @@ def prepare(case, seed):
             s[name] = (2.0 * normal(n, h, dim)).to(TYPES[c["x"]])
         s["wq"], s["wk"] = 1.0 + 0.2 * normal(dim), 1.0 + 0.2 * normal(dim)
         s["positions"] = torch.randint(0, c["far"], (n,), generator=gen, device="cuda", dtype=torch.int32)
-        s["freqs"] = [10000.0 ** (-2.0 * i / c["rot"]) for i in range(c["rot"] // 2)]  # a model keeps this host table
+        # a model keeps this table on the host
+        s["freqs"] = torch.tensor([10000.0 ** (-2.0 * i / c["rot"]) for i in range(c["rot"] // 2)], dtype=torch.float64)
         s["slots"] = torch.randperm(slots, generator=host)[:n].to(torch.int32).cuda()
         s["qo"] = torch.zeros(n, hq, dim, dtype=out, device="cuda")
         s["kc"] = torch.zeros(slots, hkv, dim, dtype=out, device="cuda")
