@@ -399,3 +399,6 @@ def qmm_matmul_batch_ws(items, workspace, stream=None):
     if st != QMM_OK:
         raise QmmError(st, "qmm_matmul_batch_ws")
     return [it[4] for it in items]
+
+
+from .attn import *  # noqa: E402,F401,F403 - the operators of include/qmm_attn.h

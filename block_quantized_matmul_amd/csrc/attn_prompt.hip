@@ -1,0 +1,153 @@
+// Causal attention over packed prompts (qmm_attn_prompt).
+//
+//   O[t][h] = sum_{u <= t} softmax_u(scale Q[t][h] . K[u][g]) V[u][g],
+//
+// u over the tokens of t's own sequence, g = h / group. A KV head's queries
+// are flattened: row x of a sequence is token x / group, head g group + x %
+// group, so one tile of 128 rows reads its keys once for all the heads that
+// share them, whatever the group, and a short prompt fills tiles with heads
+// instead of leaving them half empty.
+//
+// One workgroup of four wavefronts takes a tile of 128 rows of one sequence
+// and KV head, each wavefront 32 rows, over blocks of 64 keys up to the
+// tile's last token; K and V of the next block are copied into LDS while the
+// present one is computed (two buffers, one barrier per block). Only the
+// blocks that cross the diagonal are masked. 64 KiB of LDS and at most 256
+// registers let two workgroups share a CU, so that one's exponentials run
+// beside the other's matrix products.
+//
+// The grid covers an upper bound of the tiles (the starts are device data);
+// each wavefront finds its tile by a scan over the starts, 64 sequences at a
+// time. KV heads are the fastest index, so that with 8 of them (or a
+// multiple) each XCD's L2 holds the keys of its own heads only; the tiles of
+// a sequence go from its last (the longest) to its first.
+#include "attn.h"
+#include "attn_core.h"
+#include "launch.h"
+
+namespace qmm {
+
+namespace {
+
+constexpr int kRows = 128;   // query rows per workgroup
+constexpr int kKeys = 64;    // keys per block
+constexpr int kThreads = 256;
+
+struct PromptArgs {
+  const void *q, *k, *v;
+  void *o;
+  int64_t qt, qh, kt, kh, vt, vh, ot, oh;
+  const int32_t *starts;
+  int n_seqs, n_tokens, group, n_kv;
+  float c;  // scale * log2(e)
+};
+
+// The tile with number `index` over all sequences: its sequence's first token
+// and length, and its own number in it. False past the last one.
+__device__ __forceinline__ bool find_tile(const PromptArgs &a, int index, int lane, int &first, int &len, int &tile) {
+  for (int s0 = 0; s0 < a.n_seqs; s0 += 64) {
+    const int s = s0 + lane;
+    int begin = 0, n = 0, tiles = 0;
+    if (s < a.n_seqs) {
+      begin = a.starts[s];
+      const int end = a.starts[s + 1];
+      if (begin >= 0 && end >= begin && end <= a.n_tokens) n = end - begin;
+      tiles = (n * a.group + kRows - 1) / kRows;
+    }
+    int sum = tiles;  // inclusive scan over the lanes
+#pragma unroll
+    for (int d = 1; d < 64; d *= 2) {
+      const int up = __shfl_up(sum, d);
+      if (lane >= d) sum += up;
+    }
+    const int all = __shfl(sum, 63);
+    if (index < all) {
+      const int at = __builtin_ctzll(__ballot(sum > index));
+      first = __builtin_amdgcn_readfirstlane(__shfl(begin, at));
+      len = __builtin_amdgcn_readfirstlane(__shfl(n, at));
+      const int left = __builtin_amdgcn_readfirstlane(__shfl(sum, at)) - 1 - index;
+      tile = left;  // the sequence's last tile comes first
+      return true;
+    }
+    index -= all;
+  }
+  return false;
+}
+
+template <class E, int D>
+__global__ __launch_bounds__(kThreads, 2) void attn_prompt_kernel(PromptArgs a) {
+  typedef typename E::one one;
+  constexpr int kTile = kKeys * D * 2;  // bytes of a K or V block
+  __shared__ __align__(1024) uint8_t lds[4 * kTile];
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int g = blockIdx.x % a.n_kv;
+  int first, len, tile;
+  if (!find_tile(a, blockIdx.x / a.n_kv, lane, first, len, tile)) return;
+
+  // this lane's row; rows past the sequence's last repeat it and are not stored
+  const int rows = len * a.group;
+  const int row = tile * kRows + wave * 32 + (lane & 31);
+  const int row_in = row < rows ? row : rows - 1;
+  const int token = row_in / a.group, head = g * a.group + row_in % a.group;
+  typename E::v8 q[D / 16];
+  load_rows<E, D>(static_cast<const one *>(a.q) + (first + token) * a.qt + head * a.qh, lane, q);
+
+  const one *kb = static_cast<const one *>(a.k) + first * a.kt + g * a.kh;
+  const one *vb = static_cast<const one *>(a.v) + first * a.vt + g * a.vh;
+  const int tile_last = tile * kRows + kRows - 1 < rows ? tile * kRows + kRows - 1 : rows - 1;
+  const int n_keys = tile_last / a.group + 1;                // keys the tile's last token sees
+  const int wave_first = __builtin_amdgcn_readfirstlane(token);  // the wavefront's first and last token
+  const int wave_last = __builtin_amdgcn_readlane(token, 31);
+  const int blocks = (n_keys + kKeys - 1) / kKeys;
+
+  const uint32_t lds0 = lds_addr(lds);
+  auto copy = [&](int b) {
+    const int n = n_keys - b * kKeys < kKeys ? n_keys - b * kKeys : kKeys;
+    const uint32_t at = lds0 + (b & 1) * 2 * kTile;
+    copy_tile<D, TileK<D>>(kb, a.kt, static_cast<int64_t>(b) * kKeys, n, kKeys, at, wave, 4, lane);
+    copy_tile<D, TileV<D>>(vb, a.vt, static_cast<int64_t>(b) * kKeys, n, kKeys, at + kTile, wave, 4, lane);
+  };
+  AttnState<D> st;
+  st.clear();
+  copy(0);
+  for (int b = 0; b < blocks; ++b) {
+    wait_loads<0>();
+    __syncthreads();  // block b has landed, and block b - 1's buffer is free
+    if (b + 1 < blocks) copy(b + 1);
+    const uint8_t *kt = lds + (b & 1) * 2 * kTile;
+    const int key0 = b * kKeys;
+    if (key0 + kKeys - 1 <= wave_first)
+      attend<E, D, 2, false>(kt, kt + kTile, q, st, a.c, kKeys, lane);
+    else if (key0 <= wave_last)
+      attend<E, D, 2, true>(kt, kt + kTile, q, st, a.c, token + 1 - key0, lane);
+  }
+  const float l = row_sum(st);
+  if (row < rows) {
+    one *o = static_cast<one *>(a.o) + (first + token) * a.ot + head * a.oh;
+    store_row<E, D>(o, st, 1.f / l, lane);
+  }
+}
+
+}  // namespace
+
+hipError_t launch_attn_prompt(int type, const qmm_heads &Q, const qmm_heads &K, const qmm_heads &V, const qmm_heads &O,
+                              int64_t n_tokens, int64_t n_q_heads, int64_t n_kv_heads, int64_t head_dim,
+                              const int32_t *seq_starts, int64_t n_seqs, float scale, hipStream_t stream) {
+  const int64_t group = n_q_heads / n_kv_heads;
+  PromptArgs a{Q.data, K.data, V.data, O.data, Q.token_stride, Q.head_stride, K.token_stride, K.head_stride,
+               V.token_stride, V.head_stride, O.token_stride, O.head_stride, seq_starts, static_cast<int>(n_seqs),
+               static_cast<int>(n_tokens), static_cast<int>(group), static_cast<int>(n_kv_heads),
+               scale * 1.4426950408889634f};
+  // sum of ceil(rows_i / kRows) <= total / kRows + the sequences that have rows
+  const int64_t with_rows = n_seqs < n_tokens ? n_seqs : n_tokens;
+  const int64_t tiles = n_tokens * group / kRows + with_rows;
+  const dim3 grid(static_cast<unsigned>(tiles * n_kv_heads));
+  if (type == QMM_T_F16)
+    return head_dim == 128 ? launch(attn_prompt_kernel<ElemF16, 128>, grid, dim3(kThreads), 0, stream, a)
+                           : launch(attn_prompt_kernel<ElemF16, 64>, grid, dim3(kThreads), 0, stream, a);
+  return head_dim == 128 ? launch(attn_prompt_kernel<ElemBF16, 128>, grid, dim3(kThreads), 0, stream, a)
+                         : launch(attn_prompt_kernel<ElemBF16, 64>, grid, dim3(kThreads), 0, stream, a);
+}
+
+}  // namespace qmm

@@ -1,0 +1,287 @@
+// Attention of a decode batch over a shared prefix and each sequence's own
+// cache (qmm_attn_shared).
+//
+// One softmax over both key ranges; it is computed in pieces of keys. A piece
+// leaves, for every row (sequence, query head), its normalised output O_i and
+// the base-2 logarithm L_i of its sum of weights, and the join is
+//   O = sum_i 2^(L_i - L) O_i,  L = log2 sum_i 2^L_i.
+//
+// The prefix is read once for all sequences: the rows of all sequences and of
+// the heads that share a KV head are flattened (row x: sequence x / group,
+// head g group + x % group) into tiles of 128, four wavefronts of 32 rows on
+// blocks of 64 keys, as the prompt kernel runs without its mask. A sequence's
+// own cache serves only `group` rows, so there a workgroup's four wavefronts
+// share one tile of 32 rows and split the piece's keys, each with blocks of
+// 32 keys of its own (copied into its own part of LDS, no barrier), and join
+// at the end through LDS.
+//
+// Both kinds of pieces are workgroups of one launch: the prefix's are bound
+// by the matrix cores, the caches' by memory. A second launch joins the
+// pieces.
+#include "attn.h"
+#include "attn_core.h"
+#include "launch.h"
+
+#include <algorithm>
+
+namespace qmm {
+
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kKeys = 64;        // keys per block, prefix
+constexpr int kOwnKeys = 32;     // keys per block of one wavefront, own cache
+constexpr int kMinPiece = 256;   // keys
+constexpr int kWantGroups = 512; // workgroups: two per CU on 256 CUs
+
+struct SharedArgs {
+  const void *q, *pk, *pv, *k, *v;
+  void *o;
+  int64_t qt, qh, pkt, pkh, pvt, pvh, ks, kt, kh, vs, vt, vh, ot, oh;
+  const int32_t *lengths;
+  float *part_o;  // [pieces][n_seqs * n_q_heads][D]
+  float *part_l;  // [pieces][n_seqs * n_q_heads]
+  int n_seqs, n_heads, group, n_kv, prefix_len, own_cap;
+  int row_tiles, prefix_pieces, prefix_step, own_tiles, own_pieces, own_step;
+  float c;  // scale * log2(e)
+};
+
+// A row's partial result; an empty piece (no keys) has L = -infinity and
+// zeros for its output.
+template <int D>
+__device__ __forceinline__ void store_partial(const SharedArgs &a, int piece, int seq, int head,
+                                              const AttnState<D> &st, float l, int lane) {
+  const int64_t at = (static_cast<int64_t>(piece) * a.n_seqs + seq) * a.n_heads + head;
+  const float f = l > 0.f || l != l ? 1.f / l : 0.f;
+  float *o = a.part_o + at * D;
+#pragma unroll
+  for (int dt = 0; dt < D / 32; ++dt)
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      *reinterpret_cast<float4_t *>(o + 32 * dt + 8 * i + 4 * (lane >> 5)) =
+          float4_t{st.o[dt][4 * i] * f, st.o[dt][4 * i + 1] * f, st.o[dt][4 * i + 2] * f, st.o[dt][4 * i + 3] * f};
+  if (lane < 32) a.part_l[at] = l == 0.f ? -__builtin_inff() : st.m + __builtin_amdgcn_logf(l);
+}
+
+template <class E, int D>
+__device__ __forceinline__ void prefix_piece(const SharedArgs &a, int item, uint8_t *lds, int wave, int lane) {
+  typedef typename E::one one;
+  constexpr int kTile = kKeys * D * 2;
+  const int g = item % a.n_kv;
+  const int rt = item / a.n_kv % a.row_tiles;
+  const int piece = item / a.n_kv / a.row_tiles;
+  const int rows = a.n_seqs * a.group;
+  const int row = rt * kSharedRows + wave * 32 + (lane & 31);
+  const int row_in = row < rows ? row : rows - 1;
+  const int seq = row_in / a.group, head = g * a.group + row_in % a.group;
+  typename E::v8 q[D / 16];
+  load_rows<E, D>(static_cast<const one *>(a.q) + seq * a.qt + head * a.qh, lane, q);
+
+  const int first = piece * a.prefix_step;
+  const int n_keys = min(a.prefix_step, a.prefix_len - first);
+  const one *kb = static_cast<const one *>(a.pk) + first * a.pkt + g * a.pkh;
+  const one *vb = static_cast<const one *>(a.pv) + first * a.pvt + g * a.pvh;
+  const bool busy = rt * kSharedRows + wave * 32 < rows;  // the wavefront has rows
+  const uint32_t lds0 = lds_addr(lds);
+  const int blocks = (n_keys + kKeys - 1) / kKeys;
+  auto copy = [&](int b) {
+    const int n = min(n_keys - b * kKeys, kKeys);
+    const uint32_t at = lds0 + (b & 1) * 2 * kTile;
+    copy_tile<D, TileK<D>>(kb, a.pkt, static_cast<int64_t>(b) * kKeys, n, kKeys, at, wave, 4, lane);
+    copy_tile<D, TileV<D>>(vb, a.pvt, static_cast<int64_t>(b) * kKeys, n, kKeys, at + kTile, wave, 4, lane);
+  };
+  AttnState<D> st;
+  st.clear();
+  copy(0);
+  for (int b = 0; b < blocks; ++b) {
+    wait_loads<0>();
+    __syncthreads();  // block b has landed, and block b - 1's buffer is free
+    if (b + 1 < blocks) copy(b + 1);
+    if (!busy) continue;
+    const uint8_t *kt = lds + (b & 1) * 2 * kTile;
+    const int left = n_keys - b * kKeys;
+    if (left >= kKeys)
+      attend<E, D, 2, false>(kt, kt + kTile, q, st, a.c, kKeys, lane);
+    else
+      attend<E, D, 2, true>(kt, kt + kTile, q, st, a.c, left, lane);
+  }
+  const float l = row_sum(st);
+  if (row < rows) store_partial<D>(a, piece, seq, head, st, l, lane);
+}
+
+template <class E, int D>
+__device__ __forceinline__ void own_piece(const SharedArgs &a, int item, uint8_t *lds, int wave, int lane) {
+  typedef typename E::one one;
+  constexpr int kTile = kOwnKeys * D * 2;
+  const int g = item % a.n_kv;
+  const int rt = item / a.n_kv % a.own_tiles;
+  const int seq = item / a.n_kv / a.own_tiles % a.n_seqs;
+  const int piece = item / a.n_kv / a.own_tiles / a.n_seqs;
+  const int row = rt * kOwnRows + (lane & 31);  // of the group
+  const int head = g * a.group + min(row, a.group - 1);
+  const int len = a.lengths[seq];
+  const int first = piece * a.own_step;
+  // a length outside [0, own_cap] is answered by the join
+  const int n_keys = len < 0 || len > a.own_cap ? 0 : min(max(len - first, 0), a.own_step);
+
+  AttnState<D> st;
+  st.clear();
+  if (n_keys > 0) {
+    typename E::v8 q[D / 16];
+    load_rows<E, D>(static_cast<const one *>(a.q) + seq * a.qt + head * a.qh, lane, q);
+    const one *kb = static_cast<const one *>(a.k) + seq * a.ks + first * a.kt + g * a.kh;
+    const one *vb = static_cast<const one *>(a.v) + seq * a.vs + first * a.vt + g * a.vh;
+    // wavefront w takes blocks w, w + 4, ...; two buffers of its own
+    const uint8_t *mine = lds + wave * 2 * kTile;
+    const uint32_t at = lds_addr(mine);
+    const int blocks = (n_keys + kOwnKeys - 1) / kOwnKeys;
+    auto copy = [&](int b) {
+      const int n = min(n_keys - b * kOwnKeys, kOwnKeys);
+      copy_tile<D, TileK<D>>(kb, a.kt, static_cast<int64_t>(b) * kOwnKeys, n, kOwnKeys, at, 0, 1, lane);
+      copy_tile<D, TileV<D>>(vb, a.vt, static_cast<int64_t>(b) * kOwnKeys, n, kOwnKeys, at + kTile, 0, 1, lane);
+    };
+    for (int b = wave; b < blocks; b += 4) {
+      copy(b);
+      wait_loads<0>();
+      __builtin_amdgcn_wave_barrier();
+      const int left = n_keys - b * kOwnKeys;
+      if (left >= kOwnKeys)
+        attend<E, D, 1, false>(mine, mine + kTile, q, st, a.c, kOwnKeys, lane);
+      else
+        attend<E, D, 1, true>(mine, mine + kTile, q, st, a.c, left, lane);
+      __builtin_amdgcn_s_waitcnt(0xc07f);  // lgkmcnt(0): the reads are done before the next copy
+      __builtin_amdgcn_wave_barrier();
+    }
+  }
+  // join the four wavefronts: the largest m, then the sums, in wavefront order
+  float l = row_sum(st);
+  __syncthreads();
+  float *ml = reinterpret_cast<float *>(lds);           // [4][32][2]
+  float *os = reinterpret_cast<float *>(lds) + 256;     // [32][D + 1], added to in turn
+  if (lane < 32) {
+    ml[(wave * 32 + lane) * 2] = st.m;
+    ml[(wave * 32 + lane) * 2 + 1] = l;
+  }
+  __syncthreads();
+  const int col = lane & 31;
+  float top = -__builtin_inff();
+#pragma unroll
+  for (int w = 0; w < 4; ++w) top = fmaxf(top, ml[(w * 32 + col) * 2]);
+  const float base = top == -__builtin_inff() ? 0.f : top;
+  l = 0.f;
+#pragma unroll
+  for (int w = 0; w < 4; ++w)
+    l += ml[(w * 32 + col) * 2 + 1] * __builtin_amdgcn_exp2f(ml[(w * 32 + col) * 2] - base);
+  const float f = __builtin_amdgcn_exp2f(st.m - base);
+#pragma unroll
+  for (int w = 0; w < 4; ++w) {
+    if (wave == w) {
+#pragma unroll
+      for (int dt = 0; dt < D / 32; ++dt)
+#pragma unroll
+        for (int r = 0; r < 16; ++r) {
+          float *x = os + col * (D + 1) + 32 * dt + 8 * (r >> 2) + 4 * (lane >> 5) + (r & 3);
+          st.o[dt][r] = st.o[dt][r] * f + (w > 0 ? *x : 0.f);
+          *x = st.o[dt][r];
+        }
+    }
+    __syncthreads();
+  }
+  if (wave == 3 && row < a.group) {
+    st.m = top;
+    store_partial<D>(a, a.prefix_pieces + piece, seq, head, st, l, lane);
+  }
+}
+
+template <class E, int D>
+__global__ __launch_bounds__(kThreads, 2) void attn_shared_kernel(SharedArgs a) {
+  __shared__ __align__(1024) uint8_t lds[4 * kKeys * D * 2];
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int prefix_items = a.prefix_pieces * a.row_tiles * a.n_kv;
+  const int item = blockIdx.x;
+  if (item < prefix_items)
+    prefix_piece<E, D>(a, item, lds, wave, lane);
+  else
+    own_piece<E, D>(a, item - prefix_items, lds, wave, lane);
+}
+
+// One workgroup of D threads per (sequence, query head): the weighted sum of
+// its pieces, in order.
+template <class E, int D> __global__ __launch_bounds__(D) void attn_join_kernel(SharedArgs a) {
+  typedef typename E::one one;
+  const int seq = blockIdx.x / a.n_heads, head = blockIdx.x % a.n_heads;
+  const int64_t rows = static_cast<int64_t>(a.n_seqs) * a.n_heads;
+  const int pieces = a.prefix_pieces + a.own_pieces;
+  const int len = a.own_cap > 0 ? a.lengths[seq] : 0;
+  float top = -__builtin_inff();
+  for (int i = 0; i < pieces; ++i) top = fmaxf(top, a.part_l[i * rows + blockIdx.x]);
+  const float base = top == -__builtin_inff() ? 0.f : top;
+  float sum = 0.f, o = 0.f;
+  for (int i = 0; i < pieces; ++i) {
+    const float w = __builtin_amdgcn_exp2f(a.part_l[i * rows + blockIdx.x] - base);
+    sum += w;
+    o += w * a.part_o[(i * rows + blockIdx.x) * D + threadIdx.x];
+  }
+  o = sum == 0.f ? 0.f : o / sum;
+  if (len < 0 || len > a.own_cap) o = __builtin_bit_cast(float, 0x7FC00000u);
+  static_cast<one *>(a.o)[seq * a.ot + head * a.oh + threadIdx.x] = static_cast<one>(o);
+}
+
+template <class E, int D> hipError_t run(const SharedArgs &a, int64_t items, hipStream_t stream) {
+  if (items > 0) {
+    const hipError_t e =
+        launch(attn_shared_kernel<E, D>, dim3(static_cast<unsigned>(items)), dim3(kThreads), 0, stream, a);
+    if (e != hipSuccess) return e;
+  }
+  return launch(attn_join_kernel<E, D>, dim3(static_cast<unsigned>(a.n_seqs * a.n_heads)), dim3(D), 0, stream, a);
+}
+
+}  // namespace
+
+// Pieces: enough workgroups to fill the GPU, but at least kMinPiece keys in
+// each, since every piece costs its rows' partial result.
+SharedPlan shared_plan(int64_t n_seqs, int64_t prefix_len, int64_t own_cap, int64_t n_q_heads, int64_t n_kv_heads) {
+  const int64_t group = n_q_heads / n_kv_heads;
+  SharedPlan p{};
+  p.row_tiles = (n_seqs * group + kSharedRows - 1) / kSharedRows;
+  p.own_tiles = (group + kOwnRows - 1) / kOwnRows;
+  auto cut = [](int64_t keys, int64_t items, int64_t block, int64_t &pieces, int64_t &step) {
+    if (keys == 0) return;
+    const int64_t want = std::max<int64_t>(1, std::min((kWantGroups + items - 1) / items, keys / kMinPiece));
+    step = ((keys + want - 1) / want + block - 1) / block * block;
+    pieces = (keys + step - 1) / step;
+  };
+  cut(prefix_len, p.row_tiles * n_kv_heads, kKeys, p.prefix_pieces, p.prefix_step);
+  cut(own_cap, n_seqs * n_kv_heads * p.own_tiles, kOwnKeys, p.own_pieces, p.own_step);
+  return p;
+}
+
+hipError_t launch_attn_shared(int type, const qmm_heads &Q, const qmm_heads &PK, const qmm_heads &PV,
+                              int64_t prefix_len, const qmm_heads &K, const qmm_heads &V, int64_t own_cap,
+                              const int32_t *lengths, const qmm_heads &O, int64_t n_seqs, int64_t n_q_heads,
+                              int64_t n_kv_heads, int64_t head_dim, float scale, void *workspace, hipStream_t stream) {
+  const SharedPlan p = shared_plan(n_seqs, prefix_len, own_cap, n_q_heads, n_kv_heads);
+  SharedArgs a{};
+  a.q = Q.data, a.pk = PK.data, a.pv = PV.data, a.k = K.data, a.v = V.data, a.o = O.data;
+  a.qt = Q.token_stride, a.qh = Q.head_stride;
+  a.pkt = PK.token_stride, a.pkh = PK.head_stride, a.pvt = PV.token_stride, a.pvh = PV.head_stride;
+  a.ks = K.seq_stride, a.kt = K.token_stride, a.kh = K.head_stride;
+  a.vs = V.seq_stride, a.vt = V.token_stride, a.vh = V.head_stride;
+  a.ot = O.token_stride, a.oh = O.head_stride;
+  a.lengths = lengths;
+  a.part_o = static_cast<float *>(workspace);
+  a.part_l = a.part_o + p.pieces() * n_seqs * n_q_heads * head_dim;
+  a.n_seqs = static_cast<int>(n_seqs), a.n_heads = static_cast<int>(n_q_heads);
+  a.group = static_cast<int>(n_q_heads / n_kv_heads), a.n_kv = static_cast<int>(n_kv_heads);
+  a.prefix_len = static_cast<int>(prefix_len), a.own_cap = static_cast<int>(own_cap);
+  a.row_tiles = static_cast<int>(p.row_tiles), a.prefix_pieces = static_cast<int>(p.prefix_pieces);
+  a.prefix_step = static_cast<int>(p.prefix_step), a.own_tiles = static_cast<int>(p.own_tiles);
+  a.own_pieces = static_cast<int>(p.own_pieces), a.own_step = static_cast<int>(p.own_step);
+  a.c = scale * 1.4426950408889634f;
+  const int64_t items = p.prefix_pieces * p.row_tiles * n_kv_heads + p.own_pieces * n_seqs * p.own_tiles * n_kv_heads;
+  if (type == QMM_T_F16) return head_dim == 128 ? run<ElemF16, 128>(a, items, stream) : run<ElemF16, 64>(a, items, stream);
+  return head_dim == 128 ? run<ElemBF16, 128>(a, items, stream) : run<ElemBF16, 64>(a, items, stream);
+}
+
+}  // namespace qmm

@@ -144,10 +144,14 @@ const char *qmm_status_string(int status) {
     case QMM_ERR_NULL: return "QMM_ERR_NULL: a required pointer is NULL";
     case QMM_ERR_TYPE: return "QMM_ERR_TYPE: unsupported weight or activation type";
     case QMM_ERR_SHAPE:
-      return "QMM_ERR_SHAPE: k must be a positive multiple of 32 (of 256 for Q4_K); sizes must be in [0, 2^31)";
+      return "QMM_ERR_SHAPE: k must be a positive multiple of 32 (of 256 for Q4_K); sizes must be in [0, 2^31) and "
+             "within the entry point's limits";
     case QMM_ERR_STRIDE:
-      return "QMM_ERR_STRIDE: row stride must be even (a multiple of 16 for Q4_K) and cover the row's blocks";
-    case QMM_ERR_ALIGN: return "QMM_ERR_ALIGN: W needs 2-byte (Q4_K: 16-byte), X, Y and out 4-byte alignment";
+      return "QMM_ERR_STRIDE: row stride must be even (a multiple of 16 for Q4_K) and cover the row's blocks; strides "
+             "of heads must be as qmm_attn.h states and keep an output's heads apart";
+    case QMM_ERR_ALIGN:
+      return "QMM_ERR_ALIGN: W needs 2-byte (Q4_K: 16-byte), X, Y and out 4-byte alignment; tensors of heads as "
+             "qmm_attn.h states";
     case QMM_ERR_HIP: return "QMM_ERR_HIP: the HIP runtime rejected the kernel launch";
     case QMM_ERR_PATH: return "QMM_ERR_PATH: unknown path, or GEMV forced with more than 8 tokens";
     case QMM_ERR_WORKSPACE: return "QMM_ERR_WORKSPACE: workspace missing or smaller than the call's *_workspace_bytes";
