@@ -55,11 +55,12 @@ struct ElemBF16 {
 __device__ __forceinline__ uint32_t lds_addr(const void *p) {
   return static_cast<uint32_t>(reinterpret_cast<uintptr_t>((const __attribute__((address_space(3))) void *)p));
 }
-// 16 bytes per lane from p into LDS at byte address lds + 16 lane (lds the
-// same in all lanes). M0 is written by a scalar move, and an LDS-DMA load
-// must not follow it directly.
-__device__ __forceinline__ void dma_to_lds(const void *p, uint32_t lds) {
-  asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, off" ::"v"(p), "s"(lds) : "memory", "m0");
+// 16 bytes per lane from base + off into LDS at byte address lds + 16 lane
+// (base and lds the same in all lanes). M0 is written by a scalar move, and
+// an LDS-DMA load must not follow it directly.
+__device__ __forceinline__ void dma_to_lds(uint32_t off, const void *base, uint32_t lds) {
+  asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, %1" ::"v"(off), "s"(base), "s"(lds)
+               : "memory", "m0");
 }
 template <int N> __device__ __forceinline__ void wait_loads() {
   asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory");
@@ -79,23 +80,48 @@ template <int D> struct TileV {
   }
 };
 
-// Copies `count` (1 .. rows) rows of a K or V tile of `rows` rows into LDS,
-// row r from base + row0 + min(r, count - 1): rows past the last valid one
-// repeat it, so nothing behind it is read and whatever the masked places
-// hold, they hold values that the row attends to anyway. `part` of `parts`
-// wavefronts; the copies are awaited with wait_loads.
-template <int D, class Tile, class E>
-__device__ __forceinline__ void copy_tile(const E *base, int64_t token_stride, int64_t row0, int count, int rows,
-                                          uint32_t lds, int part, int parts, int lane) {
-  constexpr int kChunks = D / 8;            // 16-byte chunks per row
-  constexpr int kRowsPer = 64 / kChunks;    // rows one instruction copies
-  for (int g = part; g < rows / kRowsPer; g += parts) {
-    const int r = g * kRowsPer + lane / kChunks;
-    const int c = Tile::perm(r, lane % kChunks);
-    const E *p = base + (row0 + (r < count ? r : count - 1)) * token_stride + c * 8;
-    dma_to_lds(p, __builtin_amdgcn_readfirstlane(lds + g * 1024));
+// Copies blocks of ROWS rows of a K or V into LDS, for one of PARTS wavefronts
+// that copy a block together. A copy instruction moves kPer rows; the chunk a
+// lane takes does not depend on which of the wavefront's rows it is for, so
+// one 32-bit offset per lane serves all of them and the rest of the address
+// is scalar (63 rows of 2^25 elements still fit).
+template <int D, class Tile, class E, int ROWS, int PARTS> struct Copier {
+  static constexpr int kChunks = D / 8;           // 16-byte chunks per row
+  static constexpr int kPer = 64 / kChunks;       // rows per instruction
+  static constexpr int kCount = ROWS / kPer / PARTS;
+  static_assert(kPer * PARTS % 16 == 0 || kCount == 1 || PARTS == 1, "the permutation repeats every 16 rows");
+  const uint8_t *base;  // row 0
+  int64_t row_bytes;
+  uint32_t off;  // this lane's, in its wavefront's first row group
+  int part;
+
+  __device__ __forceinline__ Copier(const typename E::one *p, int64_t token_stride, int wave, int lane)
+      : base(reinterpret_cast<const uint8_t *>(p)), row_bytes(token_stride * 2), part(wave) {
+    const int r = part * kPer + lane / kChunks;
+    off = static_cast<uint32_t>(r * row_bytes) + 16 * Tile::perm(r, lane % kChunks);
   }
-}
+  // Rows row0 .. row0 + count - 1 (1 <= count <= ROWS). Rows past the last
+  // valid one repeat it, so nothing behind it is read and whatever the
+  // masked places hold, they hold values that the row attends to anyway.
+  __device__ __forceinline__ void operator()(int64_t row0, int count, uint32_t lds, int lane) const {
+    const uint8_t *b = base + row0 * row_bytes;
+    if (count >= ROWS && PARTS > 1) {
+#pragma unroll
+      for (int j = 0; j < kCount; ++j) {
+        const uint8_t *bj = b + j * (kPer * PARTS) * row_bytes;
+        dma_to_lds(off, bj, lds + (part + j * PARTS) * 1024);
+      }
+    } else {
+#pragma unroll
+      for (int j = 0; j < kCount; ++j) {
+        const int r = (part + j * PARTS) * kPer + lane / kChunks;
+        const uint32_t o =
+            static_cast<uint32_t>((r < count ? r : count - 1) * row_bytes) + 16 * Tile::perm(r, lane % kChunks);
+        dma_to_lds(o, b, lds + (part + j * PARTS) * 1024);
+      }
+    }
+  }
+};
 
 // The state of a wavefront's 32 rows (a lane's column lane % 32).
 template <int D> struct AttnState {
@@ -141,30 +167,60 @@ template <class E> __device__ __forceinline__ typename E::v8 finite_or_zero(type
   return __builtin_bit_cast(typename E::v8, u);
 }
 
-// 32 * NT keys of LDS tiles kt and vt. With MASK, a lane's row takes the
-// block's first `lim` keys only (lim may be <= 0 or past the block); without
-// it, all. `c` is scale * log2(e) > 0.
+// Weights are kept relative to a reference m that follows the maximum only
+// when it is exceeded by more than kSlack (in base-2 units): any reference
+// gives the same quotient, and weights up to 2^kSlack neither overflow fp16
+// nor cost precision, while rescaling the outputs (64 multiplies at D = 128)
+// for every new maximum would cost as much as a quarter of a block's products.
+constexpr float kSlack = 8.f;
+
+__device__ __forceinline__ void lds_read(half8_t &v, uint32_t a) {
+  v = *reinterpret_cast<const __attribute__((address_space(3))) half8_t *>(a);
+}
+__device__ __forceinline__ void lds_read(bf16x8_t &v, uint32_t a) {
+  v = *reinterpret_cast<const __attribute__((address_space(3))) bf16x8_t *>(a);
+}
+
+__device__ __forceinline__ short4_t lds_read_transposed(uint32_t a) {
+  return __builtin_amdgcn_ds_read_tr16_b64_v4i16(reinterpret_cast<__attribute__((address_space(3))) short4_t *>(a));
+}
+
+// 32 * NT keys of the LDS tiles at byte addresses kt and vt. With MASK, a
+// lane's row takes the block's first `lim` keys only (lim may be <= 0 or past
+// the block); without it, all. `c` is scale * log2(e) > 0.
 //
 // A masked key's weight is zero, but zero times a non-finite value is a NaN:
 // with MASK, non-finite values enter the product as zeros, and where there
 // are any (no ordinary call) their contributions to the rows that do take
 // the key are added one key at a time.
 template <class E, int D, int NT, bool MASK>
-__device__ __forceinline__ void attend(const uint8_t *kt, const uint8_t *vt, const typename E::v8 q[D / 16],
-                                       AttnState<D> &st, float c, int lim, int lane) {
+__device__ __forceinline__ void attend(uint32_t kt, uint32_t vt, const typename E::v8 q[D / 16], AttnState<D> &st,
+                                       float c, int lim, int lane) {
+  typedef typename E::v8 v8;
+  constexpr int kRow = 2 * D;  // bytes of a row
   const int h = lane >> 5, col = lane & 31;
+  // K: row 32 t + col, chunk 2 ks + h: permuting is an exclusive or, so a
+  // step's address is the first one's with 32 ks flipped in
+  const uint32_t ka = kt + col * kRow + 16 * TileK<D>::perm(col, h);
+  v8 kf[D / 16 * NT];
   float16_t s[NT];
 #pragma unroll
   for (int t = 0; t < NT; ++t) s[t] = float16_t{};
 #pragma unroll
-  for (int ks = 0; ks < D / 16; ++ks) {
+  for (int i = 0; i < D / 16 * NT; ++i) lds_read(kf[i], (ka ^ (32 * (i / NT))) + (i % NT) * 32 * kRow);
 #pragma unroll
-    for (int t = 0; t < NT; ++t) {
-      const int r = 32 * t + col;
-      const auto a = *reinterpret_cast<const typename E::v8 *>(kt + r * (2 * D) + 16 * TileK<D>::perm(r, 2 * ks + h));
-      s[t] = E::mfma(a, q[ks], s[t]);
-    }
+  for (int i = 0; i < D / 16 * NT; ++i) s[i % NT] = E::mfma(kf[i], q[i / NT], s[i % NT]);
+  // reads run kAhead operands ahead of the products
+  constexpr int kAhead = 4;
+  __builtin_amdgcn_sched_group_barrier(0x100, kAhead, 0);
+#pragma unroll
+  for (int i = 0; i < D / 16 * NT - kAhead; ++i) {
+    __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+    __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
   }
+  __builtin_amdgcn_sched_group_barrier(0x008, kAhead, 0);
+  __builtin_amdgcn_sched_barrier(0);
+
   if constexpr (MASK) {
 #pragma unroll
     for (int t = 0; t < NT; ++t)
@@ -178,54 +234,66 @@ __device__ __forceinline__ void attend(const uint8_t *kt, const uint8_t *vt, con
 #pragma unroll
     for (int r = 0; r < 16; ++r) mx = fmaxf(mx, s[t][r]);
   mx = fmaxf(mx, other_half(mx)) * c;
-  const float m = fmaxf(st.m, mx);
-  const float mu = m == -__builtin_inff() ? 0.f : m;  // no key yet: weights of zero, not NaN
-  const float alpha = __builtin_amdgcn_exp2f(st.m - mu);
-  st.m = m;
-  if (__any(alpha != 1.f)) {
+  if (__any(mx > st.m + kSlack)) {  // also the first keys of a row: m is -infinity
+    const float m = fmaxf(st.m, mx);
+    const float alpha = m == -__builtin_inff() ? 1.f : __builtin_amdgcn_exp2f(st.m - m);
+    st.m = m;
     st.l *= alpha;
 #pragma unroll
     for (int i = 0; i < D / 32; ++i)
 #pragma unroll
       for (int r = 0; r < 16; ++r) st.o[i][r] *= alpha;
   }
-  typename E::v8 p[2 * NT];
+  const float mu = st.m == -__builtin_inff() ? 0.f : st.m;  // no key yet: weights of zero, not NaN
+  v8 p[2 * NT];
+  float sum[2] = {0.f, 0.f};
 #pragma unroll
   for (int t = 0; t < NT; ++t)
 #pragma unroll
     for (int r = 0; r < 16; ++r) {
       const float w = __builtin_amdgcn_exp2f(__builtin_fmaf(s[t][r], c, -mu));
-      st.l += w;
+      sum[r & 1] += w;
       p[2 * t + (r >> 3)][r & 7] = static_cast<typename E::one>(w);
     }
-  // V^T: lane column d = 32 dt + col; the 16 lanes of a read take rows
-  // key .. key + 3, columns 32 dt + 16 ((lane / 16) % 2) .. + 15
+  st.l += sum[0] + sum[1];
+
+  // V^T: lane column d = 32 dt + col; the 16 lanes of a read take rows key ..
+  // key + 3, columns 32 dt + 16 ((lane / 16) % 2) .. + 15. Again exclusive
+  // ors: 64 for dt, 32 for the second four keys (8 rows on)
   const int i16 = lane & 15;
-  const int vcol = 16 * ((lane >> 4) & 1) + 4 * (i16 & 3);
-  bool bad = false;
+  const int vrow = 4 * h + (i16 >> 2), vcol = 16 * ((lane >> 4) & 1) + 4 * (i16 & 3);
+  const uint32_t va = vt + vrow * kRow + 16 * TileV<D>::perm(vrow, vcol >> 3) + 2 * (vcol & 7);
+  auto read_v = [&](int k, int dt) {
+    const uint32_t a = (va ^ (64 * dt)) + k * 16 * kRow;
+    struct { short4_t a, b; } both;
+    both.a = lds_read_transposed(a);
+    both.b = lds_read_transposed((va ^ (64 * dt) ^ 32) + k * 16 * kRow + 8 * kRow);
+    return __builtin_bit_cast(v8, both);
+  };
+  constexpr int kSteps = 2 * NT * (D / 32);
+  v8 vf[kSteps];
+  __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-  for (int k = 0; k < 2 * NT; ++k) {
+  for (int i = 0; i < kSteps; ++i) vf[i] = read_v(i / (D / 32), i % (D / 32));
+  if constexpr (!MASK) {
 #pragma unroll
-    for (int dt = 0; dt < D / 32; ++dt) {
-      short4_t half[2];
+    for (int i = 0; i < kSteps; ++i) st.o[i % (D / 32)] = E::mfma(vf[i], p[i / (D / 32)], st.o[i % (D / 32)]);
+    constexpr int kAheadV = 3;
+    __builtin_amdgcn_sched_group_barrier(0x100, 2 * kAheadV, 0);
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const int r = 16 * k + 8 * i + 4 * h + (i16 >> 2);
-        const int e = 32 * dt + vcol;
-        const uint8_t *a = vt + r * (2 * D) + 16 * TileV<D>::perm(r, e >> 3) + 2 * (e & 7);
-        half[i] = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-            (__attribute__((address_space(3))) short4_t *)(reinterpret_cast<short4_t *>(const_cast<uint8_t *>(a))));
-      }
-      struct { short4_t a, b; } both = {half[0], half[1]};
-      auto v = __builtin_bit_cast(typename E::v8, both);
-      if constexpr (MASK) {
-        bad |= any_nonfinite<E>(v);
-        v = finite_or_zero<E>(v);
-      }
-      st.o[dt] = E::mfma(v, p[k], st.o[dt]);
+    for (int i = 0; i < kSteps - kAheadV; ++i) {
+      __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+      __builtin_amdgcn_sched_group_barrier(0x100, 2, 0);
     }
-  }
-  if constexpr (MASK) {
+    __builtin_amdgcn_sched_group_barrier(0x008, kAheadV, 0);
+    __builtin_amdgcn_sched_barrier(0);
+  } else {
+    bool bad = false;
+#pragma unroll
+    for (int i = 0; i < kSteps; ++i) {
+      bad |= any_nonfinite<E>(vf[i]);
+      st.o[i % (D / 32)] = E::mfma(finite_or_zero<E>(vf[i]), p[i / (D / 32)], st.o[i % (D / 32)]);
+    }
     if (__any(bad)) {
 #pragma unroll 1
       for (int u = 0; u < 32 * NT; ++u) {
@@ -245,8 +313,8 @@ __device__ __forceinline__ void attend(const uint8_t *kt, const uint8_t *vt, con
 #pragma unroll
           for (int r = 0; r < 16; ++r) {
             const int e = 32 * dt + 8 * (r >> 2) + 4 * h + (r & 3);
-            const float v = static_cast<float>(*reinterpret_cast<const typename E::one *>(
-                vt + u * (2 * D) + 16 * TileV<D>::perm(u, e >> 3) + 2 * (e & 7)));
+            const float v = static_cast<float>(*reinterpret_cast<const __attribute__((address_space(3))) typename E::one *>(
+                vt + u * kRow + 16 * TileV<D>::perm(u, e >> 3) + 2 * (e & 7)));
             if (!__builtin_isfinite(v)) st.o[dt][r] += w * v;
           }
       }

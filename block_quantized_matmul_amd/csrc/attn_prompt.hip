@@ -60,12 +60,12 @@ __device__ __forceinline__ bool find_tile(const PromptArgs &a, int index, int la
       const int up = __shfl_up(sum, d);
       if (lane >= d) sum += up;
     }
-    const int all = __shfl(sum, 63);
+    const int all = __builtin_amdgcn_readlane(sum, 63);
     if (index < all) {
       const int at = __builtin_ctzll(__ballot(sum > index));
-      first = __builtin_amdgcn_readfirstlane(__shfl(begin, at));
-      len = __builtin_amdgcn_readfirstlane(__shfl(n, at));
-      const int left = __builtin_amdgcn_readfirstlane(__shfl(sum, at)) - 1 - index;
+      first = __builtin_amdgcn_readlane(begin, at);
+      len = __builtin_amdgcn_readlane(n, at);
+      const int left = __builtin_amdgcn_readlane(sum, at) - 1 - index;
       tile = left;  // the sequence's last tile comes first
       return true;
     }
@@ -102,25 +102,34 @@ __global__ __launch_bounds__(kThreads, 2) void attn_prompt_kernel(PromptArgs a) 
   const int blocks = (n_keys + kKeys - 1) / kKeys;
 
   const uint32_t lds0 = lds_addr(lds);
+  const Copier<D, TileK<D>, E, kKeys, 4> copy_k(kb, a.kt, wave, lane);
+  const Copier<D, TileV<D>, E, kKeys, 4> copy_v(vb, a.vt, wave, lane);
   auto copy = [&](int b) {
-    const int n = n_keys - b * kKeys < kKeys ? n_keys - b * kKeys : kKeys;
+    const int n = n_keys - b * kKeys;
     const uint32_t at = lds0 + (b & 1) * 2 * kTile;
-    copy_tile<D, TileK<D>>(kb, a.kt, static_cast<int64_t>(b) * kKeys, n, kKeys, at, wave, 4, lane);
-    copy_tile<D, TileV<D>>(vb, a.vt, static_cast<int64_t>(b) * kKeys, n, kKeys, at + kTile, wave, 4, lane);
+    copy_k(static_cast<int64_t>(b) * kKeys, n, at, lane);
+    copy_v(static_cast<int64_t>(b) * kKeys, n, at + kTile, lane);
   };
   AttnState<D> st;
   st.clear();
   copy(0);
-  for (int b = 0; b < blocks; ++b) {
+  auto next = [&](int b) {
     wait_loads<0>();
     __syncthreads();  // block b has landed, and block b - 1's buffer is free
     if (b + 1 < blocks) copy(b + 1);
-    const uint8_t *kt = lds + (b & 1) * 2 * kTile;
-    const int key0 = b * kKeys;
-    if (key0 + kKeys - 1 <= wave_first)
-      attend<E, D, 2, false>(kt, kt + kTile, q, st, a.c, kKeys, lane);
-    else if (key0 <= wave_last)
-      attend<E, D, 2, true>(kt, kt + kTile, q, st, a.c, token + 1 - key0, lane);
+    return lds0 + (b & 1) * 2 * kTile;
+  };
+  // the blocks whose every key every row of the wavefront takes, then those
+  // on the diagonal (and, for a wavefront above it, past its rows)
+  const int full = (wave_first + 1) / kKeys;
+  int b = 0;
+  for (; b < full; ++b) {
+    const uint32_t kt = next(b);
+    attend<E, D, 2, false>(kt, kt + kTile, q, st, a.c, kKeys, lane);
+  }
+  for (; b < blocks; ++b) {
+    const uint32_t kt = next(b);
+    if (b * kKeys <= wave_last) attend<E, D, 2, true>(kt, kt + kTile, q, st, a.c, token + 1 - b * kKeys, lane);
   }
   const float l = row_sum(st);
   if (row < rows) {

@@ -84,26 +84,31 @@ __device__ __forceinline__ void prefix_piece(const SharedArgs &a, int item, uint
   const bool busy = rt * kSharedRows + wave * 32 < rows;  // the wavefront has rows
   const uint32_t lds0 = lds_addr(lds);
   const int blocks = (n_keys + kKeys - 1) / kKeys;
+  const Copier<D, TileK<D>, E, kKeys, 4> copy_k(kb, a.pkt, wave, lane);
+  const Copier<D, TileV<D>, E, kKeys, 4> copy_v(vb, a.pvt, wave, lane);
   auto copy = [&](int b) {
-    const int n = min(n_keys - b * kKeys, kKeys);
+    const int n = n_keys - b * kKeys;
     const uint32_t at = lds0 + (b & 1) * 2 * kTile;
-    copy_tile<D, TileK<D>>(kb, a.pkt, static_cast<int64_t>(b) * kKeys, n, kKeys, at, wave, 4, lane);
-    copy_tile<D, TileV<D>>(vb, a.pvt, static_cast<int64_t>(b) * kKeys, n, kKeys, at + kTile, wave, 4, lane);
+    copy_k(static_cast<int64_t>(b) * kKeys, n, at, lane);
+    copy_v(static_cast<int64_t>(b) * kKeys, n, at + kTile, lane);
   };
   AttnState<D> st;
   st.clear();
   copy(0);
-  for (int b = 0; b < blocks; ++b) {
+  auto next = [&](int b) {
     wait_loads<0>();
     __syncthreads();  // block b has landed, and block b - 1's buffer is free
     if (b + 1 < blocks) copy(b + 1);
-    if (!busy) continue;
-    const uint8_t *kt = lds + (b & 1) * 2 * kTile;
-    const int left = n_keys - b * kKeys;
-    if (left >= kKeys)
-      attend<E, D, 2, false>(kt, kt + kTile, q, st, a.c, kKeys, lane);
-    else
-      attend<E, D, 2, true>(kt, kt + kTile, q, st, a.c, left, lane);
+    return lds0 + (b & 1) * 2 * kTile;
+  };
+  const int full = n_keys / kKeys;
+  for (int b = 0; b < full; ++b) {
+    const uint32_t kt = next(b);
+    if (busy) attend<E, D, 2, false>(kt, kt + kTile, q, st, a.c, kKeys, lane);
+  }
+  if (full < blocks) {
+    const uint32_t kt = next(full);
+    if (busy) attend<E, D, 2, true>(kt, kt + kTile, q, st, a.c, n_keys - full * kKeys, lane);
   }
   const float l = row_sum(st);
   if (row < rows) store_partial<D>(a, piece, seq, head, st, l, lane);
@@ -119,7 +124,7 @@ __device__ __forceinline__ void own_piece(const SharedArgs &a, int item, uint8_t
   const int piece = item / a.n_kv / a.own_tiles / a.n_seqs;
   const int row = rt * kOwnRows + (lane & 31);  // of the group
   const int head = g * a.group + min(row, a.group - 1);
-  const int len = a.lengths[seq];
+  const int len = __builtin_amdgcn_readfirstlane(a.lengths[seq]);
   const int first = piece * a.own_step;
   // a length outside [0, own_cap] is answered by the join
   const int n_keys = len < 0 || len > a.own_cap ? 0 : min(max(len - first, 0), a.own_step);
@@ -131,26 +136,25 @@ __device__ __forceinline__ void own_piece(const SharedArgs &a, int item, uint8_t
     load_rows<E, D>(static_cast<const one *>(a.q) + seq * a.qt + head * a.qh, lane, q);
     const one *kb = static_cast<const one *>(a.k) + seq * a.ks + first * a.kt + g * a.kh;
     const one *vb = static_cast<const one *>(a.v) + seq * a.vs + first * a.vt + g * a.vh;
-    // wavefront w takes blocks w, w + 4, ...; two buffers of its own
-    const uint8_t *mine = lds + wave * 2 * kTile;
-    const uint32_t at = lds_addr(mine);
+    // wavefront w takes blocks w, w + 4, ... through its own part of LDS
+    const uint32_t at = lds_addr(lds) + wave * 2 * kTile;
     const int blocks = (n_keys + kOwnKeys - 1) / kOwnKeys;
-    auto copy = [&](int b) {
-      const int n = min(n_keys - b * kOwnKeys, kOwnKeys);
-      copy_tile<D, TileK<D>>(kb, a.kt, static_cast<int64_t>(b) * kOwnKeys, n, kOwnKeys, at, 0, 1, lane);
-      copy_tile<D, TileV<D>>(vb, a.vt, static_cast<int64_t>(b) * kOwnKeys, n, kOwnKeys, at + kTile, 0, 1, lane);
-    };
-    for (int b = wave; b < blocks; b += 4) {
-      copy(b);
+    const Copier<D, TileK<D>, E, kOwnKeys, 1> copy_k(kb, a.kt, 0, lane);
+    const Copier<D, TileV<D>, E, kOwnKeys, 1> copy_v(vb, a.vt, 0, lane);
+    auto next = [&](int b) {
+      copy_k(static_cast<int64_t>(b) * kOwnKeys, n_keys - b * kOwnKeys, at, lane);
+      copy_v(static_cast<int64_t>(b) * kOwnKeys, n_keys - b * kOwnKeys, at + kTile, lane);
       wait_loads<0>();
-      __builtin_amdgcn_wave_barrier();
-      const int left = n_keys - b * kOwnKeys;
-      if (left >= kOwnKeys)
-        attend<E, D, 1, false>(mine, mine + kTile, q, st, a.c, kOwnKeys, lane);
-      else
-        attend<E, D, 1, true>(mine, mine + kTile, q, st, a.c, left, lane);
+    };
+    int b = wave;
+    for (; b < n_keys / kOwnKeys; b += 4) {
+      next(b);
+      attend<E, D, 1, false>(at, at + kTile, q, st, a.c, kOwnKeys, lane);
       __builtin_amdgcn_s_waitcnt(0xc07f);  // lgkmcnt(0): the reads are done before the next copy
-      __builtin_amdgcn_wave_barrier();
+    }
+    if (b < blocks) {
+      next(b);
+      attend<E, D, 1, true>(at, at + kTile, q, st, a.c, n_keys - b * kOwnKeys, lane);
     }
   }
   // join the four wavefronts: the largest m, then the sums, in wavefront order
