@@ -98,7 +98,7 @@ template <int D, class Tile, class E, int ROWS, int PARTS> struct Copier {
   __device__ __forceinline__ Copier(const typename E::one *p, int64_t token_stride, int wave, int lane)
       : base(reinterpret_cast<const uint8_t *>(p)), row_bytes(token_stride * 2), part(wave) {
     const int r = part * kPer + lane / kChunks;
-    off = static_cast<uint32_t>(r * row_bytes) + 16 * Tile::perm(r, lane % kChunks);
+    off = static_cast<uint32_t>(r) * static_cast<uint32_t>(row_bytes) + 16 * Tile::perm(r, lane % kChunks);
   }
   // Rows row0 .. row0 + count - 1 (1 <= count <= ROWS). Rows past the last
   // valid one repeat it, so nothing behind it is read and whatever the
@@ -112,11 +112,13 @@ template <int D, class Tile, class E, int ROWS, int PARTS> struct Copier {
         dma_to_lds(off, bj, lds + (part + j * PARTS) * 1024);
       }
     } else {
+      int l = lane;
+      asm volatile("" : "+v"(l));  // computed here, not kept in registers through the loops around
 #pragma unroll
       for (int j = 0; j < kCount; ++j) {
-        const int r = (part + j * PARTS) * kPer + lane / kChunks;
-        const uint32_t o =
-            static_cast<uint32_t>((r < count ? r : count - 1) * row_bytes) + 16 * Tile::perm(r, lane % kChunks);
+        const int r = (part + j * PARTS) * kPer + l / kChunks;
+        const uint32_t o = static_cast<uint32_t>(r < count ? r : count - 1) * static_cast<uint32_t>(row_bytes) +
+                           16 * Tile::perm(r, l % kChunks);
         dma_to_lds(o, b, lds + (part + j * PARTS) * 1024);
       }
     }
@@ -135,7 +137,13 @@ template <int D> struct AttnState {
   }
 };
 
-__device__ __forceinline__ float other_half(float x) { return __shfl_xor(x, 32); }
+// x of lane ^ 32 and x itself, in either order.
+__device__ __forceinline__ float2_t both_halves(float x) {
+  const uint32_t u = __builtin_bit_cast(uint32_t, x);
+  const auto r = __builtin_amdgcn_permlane32_swap(u, u, false, false);
+  return float2_t{__builtin_bit_cast(float, static_cast<uint32_t>(r[0])),
+                  __builtin_bit_cast(float, static_cast<uint32_t>(r[1]))};
+}
 
 // The wavefront's rows as the B operand of S^T: element j of step ks is
 // element 16 ks + 8 h + j of the lane's row.
@@ -146,27 +154,21 @@ __device__ __forceinline__ void load_rows(const typename E::one *row, int lane, 
     q[ks] = *reinterpret_cast<const typename E::v8 *>(row + 16 * ks + 8 * (lane >> 5));
 }
 
-// True if any of the operand's 8 elements is an infinity or a NaN.
-template <class E> __device__ __forceinline__ bool any_nonfinite(typename E::v8 v) {
-  const u32x4_t u = __builtin_bit_cast(u32x4_t, v);
-  bool bad = false;
+// True, in every lane, if this wavefront's share (one of `parts`) of the
+// `bytes` of LDS at byte address a holds an infinity or a NaN.
+template <class E, int BYTES, int PARTS>
+__device__ __forceinline__ bool any_nonfinite(uint32_t a, int part, int lane) {
+  typedef uint16_t u16x2 __attribute__((ext_vector_type(2)));
+  u16x2 most = {0, 0};  // the largest magnitude, as bits
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    bad |= (u[i] & E::exp_mask) == E::exp_mask;
-    bad |= ((u[i] >> 16) & E::exp_mask) == E::exp_mask;
-  }
-  return bad;
-}
-template <class E> __device__ __forceinline__ typename E::v8 finite_or_zero(typename E::v8 v) {
-  u32x4_t u = __builtin_bit_cast(u32x4_t, v);
+  for (int i = 0; i < BYTES / PARTS / 1024; ++i) {
+    const u32x4_t u = *reinterpret_cast<const __attribute__((address_space(3))) u32x4_t *>(
+        a + (i * PARTS + part) * 1024 + 16 * lane);
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    if ((u[i] & E::exp_mask) == E::exp_mask) u[i] &= 0xFFFF0000u;
-    if (((u[i] >> 16) & E::exp_mask) == E::exp_mask) u[i] &= 0x0000FFFFu;
+    for (int j = 0; j < 4; ++j) most = __builtin_elementwise_max(most, __builtin_bit_cast(u16x2, u[j] & 0x7FFF7FFFu));
   }
-  return __builtin_bit_cast(typename E::v8, u);
+  return __any(most.x >= E::exp_mask || most.y >= E::exp_mask);
 }
-
 // Weights are kept relative to a reference m that follows the maximum only
 // when it is exceeded by more than kSlack (in base-2 units): any reference
 // gives the same quotient, and weights up to 2^kSlack neither overflow fp16
@@ -185,56 +187,61 @@ __device__ __forceinline__ short4_t lds_read_transposed(uint32_t a) {
   return __builtin_amdgcn_ds_read_tr16_b64_v4i16(reinterpret_cast<__attribute__((address_space(3))) short4_t *>(a));
 }
 
-// 32 * NT keys of the LDS tiles at byte addresses kt and vt. With MASK, a
-// lane's row takes the block's first `lim` keys only (lim may be <= 0 or past
-// the block); without it, all. `c` is scale * log2(e) > 0.
-//
-// A masked key's weight is zero, but zero times a non-finite value is a NaN:
-// with MASK, non-finite values enter the product as zeros, and where there
-// are any (no ordinary call) their contributions to the rows that do take
-// the key are added one key at a time.
-template <class E, int D, int NT, bool MASK>
-__device__ __forceinline__ void attend(uint32_t kt, uint32_t vt, const typename E::v8 q[D / 16], AttnState<D> &st,
-                                       float c, int lim, int lane) {
-  typedef typename E::v8 v8;
+// V^T's operand for keys 16 k .. + 15 and outputs 32 dt .. + 31; va is the
+// lane's address for k = dt = 0. Exclusive ors again: 64 for dt, 32 for the
+// second four keys of a lane (8 rows on).
+template <class E, int D> __device__ __forceinline__ typename E::v8 read_v(uint32_t va, int k, int dt) {
+  constexpr int kRow = 2 * D;
+  struct { short4_t a, b; } both;
+  both.a = lds_read_transposed((va ^ (64 * dt)) + k * 16 * kRow);
+  both.b = lds_read_transposed((va ^ (64 * dt) ^ 32) + k * 16 * kRow + 8 * kRow);
+  return __builtin_bit_cast(typename E::v8, both);
+}
+
+// Raw scores of 32 * NT keys, whose K tile lies at LDS byte address kt.
+template <class E, int D, int NT>
+__device__ __forceinline__ void scores(uint32_t kt, const typename E::v8 q[D / 16], float16_t s[NT], int lane) {
   constexpr int kRow = 2 * D;  // bytes of a row
   const int h = lane >> 5, col = lane & 31;
-  // K: row 32 t + col, chunk 2 ks + h: permuting is an exclusive or, so a
+  // row 32 t + col, chunk 2 ks + h: permuting is an exclusive or, so a
   // step's address is the first one's with 32 ks flipped in
   const uint32_t ka = kt + col * kRow + 16 * TileK<D>::perm(col, h);
-  v8 kf[D / 16 * NT];
-  float16_t s[NT];
+  typename E::v8 kf[D / 16 * NT];
 #pragma unroll
   for (int t = 0; t < NT; ++t) s[t] = float16_t{};
 #pragma unroll
   for (int i = 0; i < D / 16 * NT; ++i) lds_read(kf[i], (ka ^ (32 * (i / NT))) + (i % NT) * 32 * kRow);
 #pragma unroll
   for (int i = 0; i < D / 16 * NT; ++i) s[i % NT] = E::mfma(kf[i], q[i / NT], s[i % NT]);
-  // reads run kAhead operands ahead of the products
-  constexpr int kAhead = 4;
-  __builtin_amdgcn_sched_group_barrier(0x100, kAhead, 0);
-#pragma unroll
-  for (int i = 0; i < D / 16 * NT - kAhead; ++i) {
-    __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
-    __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
-  }
-  __builtin_amdgcn_sched_group_barrier(0x008, kAhead, 0);
-  __builtin_amdgcn_sched_barrier(0);
+}
 
-  if constexpr (MASK) {
-#pragma unroll
-    for (int t = 0; t < NT; ++t)
-#pragma unroll
-      for (int r = 0; r < 16; ++r)
-        if (32 * t + 8 * (r >> 2) + 4 * h + (r & 3) >= lim) s[t][r] = -__builtin_inff();
-  }
-  float mx = s[0][0];
+// The largest raw score of each lane's row.
+template <int NT> __device__ __forceinline__ float row_max(const float16_t s[NT]) {
+  float mx[2] = {s[0][0], s[0][1]};
 #pragma unroll
   for (int t = 0; t < NT; ++t)
 #pragma unroll
-    for (int r = 0; r < 16; ++r) mx = fmaxf(mx, s[t][r]);
-  mx = fmaxf(mx, other_half(mx)) * c;
-  if (__any(mx > st.m + kSlack)) {  // also the first keys of a row: m is -infinity
+    for (int r = 0; r < 16; r += 2) {
+      mx[(r >> 1) & 1] = fmaxf(fmaxf(mx[(r >> 1) & 1], s[t][r]), s[t][r + 1]);
+    }
+  const float2_t two = both_halves(fmaxf(mx[0], mx[1]));
+  return fmaxf(two.x, two.y);
+}
+
+// Keys at and past `lim` of the block take no part.
+template <int NT> __device__ __forceinline__ void mask_scores(float16_t s[NT], int lim, int lane) {
+  const int l = lim - 4 * (lane >> 5);
+#pragma unroll
+  for (int t = 0; t < NT; ++t)
+#pragma unroll
+    for (int r = 0; r < 16; ++r)
+      if (32 * t + 8 * (r >> 2) + (r & 3) >= l) s[t][r] = -__builtin_inff();
+}
+
+// Moves the reference up to the maximum mx (scaled) where some row's exceeds
+// it by more than kSlack, which is also so for a row's first keys.
+template <int D> __device__ __forceinline__ void follow_max(AttnState<D> &st, float mx) {
+  if (__any(mx > st.m + kSlack)) {
     const float m = fmaxf(st.m, mx);
     const float alpha = m == -__builtin_inff() ? 1.f : __builtin_amdgcn_exp2f(st.m - m);
     st.m = m;
@@ -244,8 +251,12 @@ __device__ __forceinline__ void attend(uint32_t kt, uint32_t vt, const typename 
 #pragma unroll
       for (int r = 0; r < 16; ++r) st.o[i][r] *= alpha;
   }
+}
+
+// Weights of the scores, rounded for the second product; their sum goes to l.
+template <class E, int D, int NT>
+__device__ __forceinline__ void weights(const float16_t s[NT], AttnState<D> &st, float c, typename E::v8 p[2 * NT]) {
   const float mu = st.m == -__builtin_inff() ? 0.f : st.m;  // no key yet: weights of zero, not NaN
-  v8 p[2 * NT];
   float sum[2] = {0.f, 0.f};
 #pragma unroll
   for (int t = 0; t < NT; ++t)
@@ -256,74 +267,170 @@ __device__ __forceinline__ void attend(uint32_t kt, uint32_t vt, const typename 
       p[2 * t + (r >> 3)][r & 7] = static_cast<typename E::one>(w);
     }
   st.l += sum[0] + sum[1];
+}
 
-  // V^T: lane column d = 32 dt + col; the 16 lanes of a read take rows key ..
-  // key + 3, columns 32 dt + 16 ((lane / 16) % 2) .. + 15. Again exclusive
-  // ors: 64 for dt, 32 for the second four keys (8 rows on)
-  const int i16 = lane & 15;
-  const int vrow = 4 * h + (i16 >> 2), vcol = 16 * ((lane >> 4) & 1) + 4 * (i16 & 3);
-  const uint32_t va = vt + vrow * kRow + 16 * TileV<D>::perm(vrow, vcol >> 3) + 2 * (vcol & 7);
-  auto read_v = [&](int k, int dt) {
-    const uint32_t a = (va ^ (64 * dt)) + k * 16 * kRow;
-    struct { short4_t a, b; } both;
-    both.a = lds_read_transposed(a);
-    both.b = lds_read_transposed((va ^ (64 * dt) ^ 32) + k * 16 * kRow + 8 * kRow);
-    return __builtin_bit_cast(v8, both);
-  };
+// The lane's address of V^T's first operand in the tile at vt: lane column
+// d = 32 dt + lane % 32; the 16 lanes of a read take rows key .. key + 3,
+// columns 32 dt + 16 ((lane / 16) % 2) .. + 15.
+template <int D> __device__ __forceinline__ uint32_t v_addr(uint32_t vt, int lane) {
+  const int row = 4 * (lane >> 5) + ((lane & 15) >> 2), col = 16 * ((lane >> 4) & 1) + 4 * (lane & 3);
+  return vt + row * (2 * D) + 16 * TileV<D>::perm(row, col >> 3) + 2 * (col & 7);
+}
+template <class E, int D, int NT>
+__device__ __forceinline__ void add_values(uint32_t va, const typename E::v8 p[2 * NT], AttnState<D> &st) {
   constexpr int kSteps = 2 * NT * (D / 32);
-  v8 vf[kSteps];
+  typename E::v8 vf[kSteps];
+#pragma unroll
+  for (int i = 0; i < kSteps; ++i) vf[i] = read_v<E, D>(va, i / (D / 32), i % (D / 32));
+#pragma unroll
+  for (int i = 0; i < kSteps; ++i) st.o[i % (D / 32)] = E::mfma(vf[i], p[i / (D / 32)], st.o[i % (D / 32)]);
+}
+// Scheduling of the instructions since the last barrier: `n` products, each
+// after the first `ahead` operands' reads (`reads` per operand), and beside
+// each product `valu` vector and `trans` transcendental instructions.
+template <int N, int AHEAD, int READS, int VALU, int TRANS> __device__ __forceinline__ void interleave() {
+  __builtin_amdgcn_sched_group_barrier(0x100, AHEAD * READS, 0);
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+    if (i < N - AHEAD) __builtin_amdgcn_sched_group_barrier(0x100, READS, 0);
+    if (VALU > 0) __builtin_amdgcn_sched_group_barrier(0x002, VALU, 0);
+    if (TRANS > 0) __builtin_amdgcn_sched_group_barrier(0x400, TRANS, 0);
+  }
   __builtin_amdgcn_sched_barrier(0);
-#pragma unroll
-  for (int i = 0; i < kSteps; ++i) vf[i] = read_v(i / (D / 32), i % (D / 32));
-  if constexpr (!MASK) {
-#pragma unroll
-    for (int i = 0; i < kSteps; ++i) st.o[i % (D / 32)] = E::mfma(vf[i], p[i / (D / 32)], st.o[i % (D / 32)]);
-    constexpr int kAheadV = 3;
-    __builtin_amdgcn_sched_group_barrier(0x100, 2 * kAheadV, 0);
-#pragma unroll
-    for (int i = 0; i < kSteps - kAheadV; ++i) {
-      __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
-      __builtin_amdgcn_sched_group_barrier(0x100, 2, 0);
+}
+
+// One block of 32 * NT keys whose K and V tiles lie at LDS byte addresses kt
+// and vt. With MASK, a lane's row takes the block's first `lim` keys only;
+// rows past them in V must be finite or attended to by the row anyway.
+template <class E, int D, int NT, bool MASK>
+__device__ __forceinline__ void attend(uint32_t kt, uint32_t vt, const typename E::v8 q[D / 16], AttnState<D> &st,
+                                       float c, int lim, int lane) {
+  float16_t s[NT];
+  typename E::v8 p[2 * NT];
+  scores<E, D, NT>(kt, q, s, lane);
+  interleave<D / 16 * NT, 4, 1, 0, 0>();
+  if (MASK) mask_scores<NT>(s, lim, lane);
+  follow_max<D>(st, row_max<NT>(s) * c);
+  weights<E, D, NT>(s, st, c, p);
+  __builtin_amdgcn_sched_barrier(0);
+  add_values<E, D, NT>(v_addr<D>(vt, lane), p, st);
+  interleave<2 * NT * (D / 32), 3, 2, 0, 0>();
+}
+
+// A workgroup of four wavefronts, 32 rows each, over keys 0 .. n_keys - 1 in
+// blocks of 64, with two buffers of a K and a V tile each in LDS.
+//
+// The two products of a block depend on each other through its weights, and
+// a wavefront alone issues a vector instruction only every 7 cycles or so,
+// so within a wavefront the products of one block run beside the vector
+// arithmetic of another: the scores of block b + 1 beside the weights of
+// block b, and the values of block b beside the maximum of block b + 1's
+// scores. The scores therefore run one block ahead: K is copied two blocks
+// ahead, V one.
+//
+// A wavefront's rows need its first `mine` blocks (>= 1); the first `full` (<
+// mine) of them are taken whole by all its rows, of the others a lane's row
+// takes keys below lim.
+//
+// A masked key's weight is zero, but zero times a non-finite value is a NaN.
+// With CAUSAL, the values of the blocks from first_masked on (at most `full`
+// of any wavefront) are therefore looked over, and true is returned where the
+// wavefront's masked blocks held an infinity or a NaN: its rows have to be
+// computed another way then. Without CAUSAL all rows share one end, behind
+// which copied rows only repeat the last.
+constexpr int kKeys = 64;
+template <int D> constexpr int attend_lds_bytes() { return 4 * kKeys * D * 2 + 32; }
+template <class E, int D, bool CAUSAL, class CopyK, class CopyV>
+__device__ __forceinline__ bool attend_blocks(uint8_t *lds, const CopyK &copy_k, const CopyV &copy_v, int n_keys,
+                                              int first_masked, int full, int mine, int lim,
+                                              const typename E::v8 q[D / 16], AttnState<D> &st, float c, int wave,
+                                              int lane) {
+  constexpr int kTile = kKeys * D * 2;
+  typedef typename E::v8 v8;
+  const int blocks = (n_keys + kKeys - 1) / kKeys;
+  const uint32_t k0 = lds_addr(lds), v0 = k0 + 2 * kTile;
+  int *nonfinite = reinterpret_cast<int *>(lds + 4 * kTile);  // [2][4], by buffer and wavefront
+  auto kt = [&](int b) { return k0 + (b & 1) * kTile; };
+  auto vt = [&](int b) { return v0 + (b & 1) * kTile; };
+  auto load_k = [&](int b) {
+    if (b < blocks) copy_k(static_cast<int64_t>(b) * kKeys, n_keys - b * kKeys, kt(b), lane);
+  };
+  auto load_v = [&](int b) {
+    if (b < blocks) copy_v(static_cast<int64_t>(b) * kKeys, n_keys - b * kKeys, vt(b), lane);
+  };
+  // Before block b: V of b and K of b + 1 have landed for all wavefronts, and
+  // the buffers of V of b - 1 and K of b are free to be filled again.
+  auto next = [&](int b) {
+    wait_loads<0>();
+    if (CAUSAL && b >= first_masked) {  // each wavefront looks at the rows it copied
+      const bool bad = any_nonfinite<E, kTile, 4>(vt(b), wave, lane);
+      if (lane == 0) nonfinite[(b & 1) * 4 + wave] = bad;
     }
-    __builtin_amdgcn_sched_group_barrier(0x008, kAheadV, 0);
+    __syncthreads();
+    load_k(b + 2);
+    load_v(b + 1);
+  };
+
+  float16_t s[2], ahead[2];
+  v8 p[4];
+  int any_bad = 0;
+  load_k(0);
+  wait_loads<0>();
+  __syncthreads();
+  load_k(1);
+  load_v(0);
+  scores<E, D, 2>(kt(0), q, s, lane);
+  interleave<D / 8, 4, 1, 0, 0>();
+  float mx = row_max<2>(s) * c;
+  auto step = [&](int b, float16_t(&now)[2], float16_t(&then)[2]) {
+    next(b);
+    follow_max<D>(st, mx);
     __builtin_amdgcn_sched_barrier(0);
-  } else {
-    bool bad = false;
-#pragma unroll
-    for (int i = 0; i < kSteps; ++i) {
-      bad |= any_nonfinite<E>(vf[i]);
-      st.o[i % (D / 32)] = E::mfma(finite_or_zero<E>(vf[i]), p[i / (D / 32)], st.o[i % (D / 32)]);
+    scores<E, D, 2>(kt(b + 1), q, then, lane);
+    weights<E, D, 2>(now, st, c, p);
+    interleave<D / 8, 4, 1, 5, 2>();
+    add_values<E, D, 2>(v_addr<D>(vt(b), lane), p, st);
+    mx = row_max<2>(then) * c;
+    interleave<D / 8, 3, 2, 2, 0>();
+  };
+  int b = 0;
+  for (; b + 1 < full; b += 2) {  // two at a time: the scores' registers swap
+    step(b, s, ahead);
+    step(b + 1, ahead, s);
+  }
+  if (b < full) {
+    step(b, s, ahead);
+    s[0] = ahead[0], s[1] = ahead[1];
+    ++b;
+  }
+  for (; b < mine; ++b) {
+    next(b);
+    mask_scores<2>(s, lim - b * kKeys, lane);
+    follow_max<D>(st, row_max<2>(s) * c);
+    weights<E, D, 2>(s, st, c, p);
+    __builtin_amdgcn_sched_barrier(0);
+    if (CAUSAL) {
+      const int *bad = nonfinite + (b & 1) * 4;
+      any_bad |= __builtin_amdgcn_readfirstlane(bad[0] | bad[1] | bad[2] | bad[3]);
     }
-    if (__any(bad)) {
-#pragma unroll 1
-      for (int u = 0; u < 32 * NT; ++u) {
-        // key u's weight: operand step u / 16, element 4 (u % 16 / 8) + u % 4, of the lanes of half (u / 4) % 2
-        const int word = 4 * (u >> 4) + 2 * ((u >> 3) & 1) + ((u >> 1) & 1);
-        uint32_t two = 0;
-#pragma unroll
-        for (int k = 0; k < 2 * NT; ++k)
-#pragma unroll
-          for (int i = 0; i < 4; ++i)
-            if (4 * k + i == word) two = __builtin_bit_cast(u32x4_t, p[k])[i];
-        two = __shfl(two, col + 32 * ((u >> 2) & 1)) >> (16 * (u & 1));
-        const float w = static_cast<float>(__builtin_bit_cast(typename E::one, static_cast<uint16_t>(two)));
-        if (u >= lim) continue;
-#pragma unroll
-        for (int dt = 0; dt < D / 32; ++dt)
-#pragma unroll
-          for (int r = 0; r < 16; ++r) {
-            const int e = 32 * dt + 8 * (r >> 2) + 4 * h + (r & 3);
-            const float v = static_cast<float>(*reinterpret_cast<const __attribute__((address_space(3))) typename E::one *>(
-                vt + u * kRow + 16 * TileV<D>::perm(u, e >> 3) + 2 * (e & 7)));
-            if (!__builtin_isfinite(v)) st.o[dt][r] += w * v;
-          }
-      }
+    __builtin_amdgcn_sched_barrier(0);
+    add_values<E, D, 2>(v_addr<D>(vt(b), lane), p, st);
+    interleave<D / 8, 3, 2, 0, 0>();
+    if (b + 1 < mine) {
+      scores<E, D, 2>(kt(b + 1), q, s, lane);
+      interleave<D / 8, 4, 1, 0, 0>();
     }
   }
+  for (; b < blocks; ++b) next(b);  // the other wavefronts' blocks
+  return any_bad != 0;
 }
 
 // The whole sum of weights of a lane's row.
-template <int D> __device__ __forceinline__ float row_sum(const AttnState<D> &st) { return st.l + other_half(st.l); }
+template <int D> __device__ __forceinline__ float row_sum(const AttnState<D> &st) {
+  const float2_t two = both_halves(st.l);
+  return two.x + two.y;
+}
 
 // Writes a lane's half of its row's D outputs, times f, to `row` (8 bytes
 // per store).

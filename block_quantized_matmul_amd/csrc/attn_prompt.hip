@@ -30,7 +30,6 @@ namespace qmm {
 namespace {
 
 constexpr int kRows = 128;   // query rows per workgroup
-constexpr int kKeys = 64;    // keys per block
 constexpr int kThreads = 256;
 
 struct PromptArgs {
@@ -74,11 +73,40 @@ __device__ __forceinline__ bool find_tile(const PromptArgs &a, int index, int la
   return false;
 }
 
+// One row over its keys 0 .. n_keys - 1, key by key, the lanes sharing the
+// head's elements: for the rows of a wavefront whose tile product would let
+// a non-finite value of a later token in (no ordinary call's does). Every
+// key it reads is one the row attends to.
+template <class E, int D>
+__device__ __forceinline__ void slow_row(const typename E::one *q, const typename E::one *k, int64_t kt,
+                                         const typename E::one *v, int64_t vt, int n_keys, float c,
+                                         typename E::one *o, int lane) {
+  constexpr int kPer = D / 64;
+  float x[kPer], acc[kPer], m = -__builtin_inff(), l = 0.f;
+#pragma unroll
+  for (int i = 0; i < kPer; ++i) x[i] = static_cast<float>(q[kPer * lane + i]) * c, acc[i] = 0.f;
+  for (int u = 0; u < n_keys; ++u) {
+    float s = 0.f;
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) s = __builtin_fmaf(x[i], static_cast<float>(k[u * kt + kPer * lane + i]), s);
+#pragma unroll
+    for (int d = 32; d > 0; d /= 2) s += __shfl_xor(s, d);
+    const float top = fmaxf(m, s);
+    const float base = top == -__builtin_inff() ? 0.f : top;
+    const float alpha = __builtin_amdgcn_exp2f(m - base), w = __builtin_amdgcn_exp2f(s - base);
+    m = top, l = l * alpha + w;
+#pragma unroll
+    for (int i = 0; i < kPer; ++i)
+      acc[i] = acc[i] * alpha + w * static_cast<float>(v[u * vt + kPer * lane + i]);
+  }
+#pragma unroll
+  for (int i = 0; i < kPer; ++i) o[kPer * lane + i] = static_cast<typename E::one>(acc[i] / l);
+}
+
 template <class E, int D>
 __global__ __launch_bounds__(kThreads, 2) void attn_prompt_kernel(PromptArgs a) {
   typedef typename E::one one;
-  constexpr int kTile = kKeys * D * 2;  // bytes of a K or V block
-  __shared__ __align__(1024) uint8_t lds[4 * kTile];
+  __shared__ __align__(1024) uint8_t lds[attend_lds_bytes<D>()];
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int g = blockIdx.x % a.n_kv;
@@ -89,9 +117,10 @@ __global__ __launch_bounds__(kThreads, 2) void attn_prompt_kernel(PromptArgs a) 
   const int rows = len * a.group;
   const int row = tile * kRows + wave * 32 + (lane & 31);
   const int row_in = row < rows ? row : rows - 1;
-  const int token = row_in / a.group, head = g * a.group + row_in % a.group;
+  const int token = row_in / a.group;
   typename E::v8 q[D / 16];
-  load_rows<E, D>(static_cast<const one *>(a.q) + (first + token) * a.qt + head * a.qh, lane, q);
+  load_rows<E, D>(static_cast<const one *>(a.q) + (first + token) * a.qt + (g * a.group + row_in - token * a.group) * a.qh,
+                  lane, q);
 
   const one *kb = static_cast<const one *>(a.k) + first * a.kt + g * a.kh;
   const one *vb = static_cast<const one *>(a.v) + first * a.vt + g * a.vh;
@@ -99,42 +128,34 @@ __global__ __launch_bounds__(kThreads, 2) void attn_prompt_kernel(PromptArgs a) 
   const int n_keys = tile_last / a.group + 1;                // keys the tile's last token sees
   const int wave_first = __builtin_amdgcn_readfirstlane(token);  // the wavefront's first and last token
   const int wave_last = __builtin_amdgcn_readlane(token, 31);
-  const int blocks = (n_keys + kKeys - 1) / kKeys;
 
-  const uint32_t lds0 = lds_addr(lds);
   const Copier<D, TileK<D>, E, kKeys, 4> copy_k(kb, a.kt, wave, lane);
   const Copier<D, TileV<D>, E, kKeys, 4> copy_v(vb, a.vt, wave, lane);
-  auto copy = [&](int b) {
-    const int n = n_keys - b * kKeys;
-    const uint32_t at = lds0 + (b & 1) * 2 * kTile;
-    copy_k(static_cast<int64_t>(b) * kKeys, n, at, lane);
-    copy_v(static_cast<int64_t>(b) * kKeys, n, at + kTile, lane);
-  };
   AttnState<D> st;
   st.clear();
-  copy(0);
-  auto next = [&](int b) {
-    wait_loads<0>();
-    __syncthreads();  // block b has landed, and block b - 1's buffer is free
-    if (b + 1 < blocks) copy(b + 1);
-    return lds0 + (b & 1) * 2 * kTile;
-  };
-  // the blocks whose every key every row of the wavefront takes, then those
-  // on the diagonal (and, for a wavefront above it, past its rows)
-  const int full = (wave_first + 1) / kKeys;
-  int b = 0;
-  for (; b < full; ++b) {
-    const uint32_t kt = next(b);
-    attend<E, D, 2, false>(kt, kt + kTile, q, st, a.c, kKeys, lane);
-  }
-  for (; b < blocks; ++b) {
-    const uint32_t kt = next(b);
-    if (b * kKeys <= wave_last) attend<E, D, 2, true>(kt, kt + kTile, q, st, a.c, token + 1 - b * kKeys, lane);
-  }
+  const int mine = wave_last / kKeys + 1;
+  const int full = min((wave_first + 1) / kKeys, mine - 1);
+  const int first_masked = (tile * kRows / a.group + 1) / kKeys;  // of the whole tile
+  const bool any_bad = attend_blocks<E, D, true>(lds, copy_k, copy_v, n_keys, min(first_masked, full), full, mine,
+                                                 token + 1, q, st, a.c, wave, lane);
   const float l = row_sum(st);
-  if (row < rows) {
-    one *o = static_cast<one *>(a.o) + (first + token) * a.ot + head * a.oh;
-    store_row<E, D>(o, st, 1.f / l, lane);
+  // the row again, from the lane: nothing of it is kept in registers meanwhile
+  int l2 = lane;
+  asm volatile("" : "+v"(l2));
+  if (!any_bad) {
+    const int row2 = tile * kRows + wave * 32 + (l2 & 31);
+    if (row2 < rows) {
+      const int t2 = row2 / a.group;
+      one *o = static_cast<one *>(a.o) + (first + t2) * a.ot + (g * a.group + row2 - t2 * a.group) * a.oh;
+      store_row<E, D>(o, st, 1.f / l, l2);
+    }
+  } else {
+    for (int r = tile * kRows + wave * 32; r < min(rows, tile * kRows + wave * 32 + 32); ++r) {
+      const int t2 = r / a.group;
+      const int64_t head = g * a.group + r - t2 * a.group;
+      slow_row<E, D>(static_cast<const one *>(a.q) + (first + t2) * a.qt + head * a.qh, kb, a.kt, vb, a.vt, t2 + 1, a.c,
+                     static_cast<one *>(a.o) + (first + t2) * a.ot + head * a.oh, l2);
+    }
   }
 }
 

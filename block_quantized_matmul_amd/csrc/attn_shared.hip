@@ -29,7 +29,6 @@ namespace qmm {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kKeys = 64;        // keys per block, prefix
 constexpr int kOwnKeys = 32;     // keys per block of one wavefront, own cache
 constexpr int kMinPiece = 256;   // keys
 constexpr int kWantGroups = 512; // workgroups: two per CU on 256 CUs
@@ -66,7 +65,6 @@ __device__ __forceinline__ void store_partial(const SharedArgs &a, int piece, in
 template <class E, int D>
 __device__ __forceinline__ void prefix_piece(const SharedArgs &a, int item, uint8_t *lds, int wave, int lane) {
   typedef typename E::one one;
-  constexpr int kTile = kKeys * D * 2;
   const int g = item % a.n_kv;
   const int rt = item / a.n_kv % a.row_tiles;
   const int piece = item / a.n_kv / a.row_tiles;
@@ -81,35 +79,12 @@ __device__ __forceinline__ void prefix_piece(const SharedArgs &a, int item, uint
   const int n_keys = min(a.prefix_step, a.prefix_len - first);
   const one *kb = static_cast<const one *>(a.pk) + first * a.pkt + g * a.pkh;
   const one *vb = static_cast<const one *>(a.pv) + first * a.pvt + g * a.pvh;
-  const bool busy = rt * kSharedRows + wave * 32 < rows;  // the wavefront has rows
-  const uint32_t lds0 = lds_addr(lds);
-  const int blocks = (n_keys + kKeys - 1) / kKeys;
   const Copier<D, TileK<D>, E, kKeys, 4> copy_k(kb, a.pkt, wave, lane);
   const Copier<D, TileV<D>, E, kKeys, 4> copy_v(vb, a.pvt, wave, lane);
-  auto copy = [&](int b) {
-    const int n = n_keys - b * kKeys;
-    const uint32_t at = lds0 + (b & 1) * 2 * kTile;
-    copy_k(static_cast<int64_t>(b) * kKeys, n, at, lane);
-    copy_v(static_cast<int64_t>(b) * kKeys, n, at + kTile, lane);
-  };
   AttnState<D> st;
   st.clear();
-  copy(0);
-  auto next = [&](int b) {
-    wait_loads<0>();
-    __syncthreads();  // block b has landed, and block b - 1's buffer is free
-    if (b + 1 < blocks) copy(b + 1);
-    return lds0 + (b & 1) * 2 * kTile;
-  };
-  const int full = n_keys / kKeys;
-  for (int b = 0; b < full; ++b) {
-    const uint32_t kt = next(b);
-    if (busy) attend<E, D, 2, false>(kt, kt + kTile, q, st, a.c, kKeys, lane);
-  }
-  if (full < blocks) {
-    const uint32_t kt = next(full);
-    if (busy) attend<E, D, 2, true>(kt, kt + kTile, q, st, a.c, n_keys - full * kKeys, lane);
-  }
+  const int blocks = (n_keys + kKeys - 1) / kKeys;
+  attend_blocks<E, D, false>(lds, copy_k, copy_v, n_keys, 0, blocks - 1, blocks, n_keys, q, st, a.c, wave, lane);
   const float l = row_sum(st);
   if (row < rows) store_partial<D>(a, piece, seq, head, st, l, lane);
 }
@@ -199,7 +174,7 @@ __device__ __forceinline__ void own_piece(const SharedArgs &a, int item, uint8_t
 
 template <class E, int D>
 __global__ __launch_bounds__(kThreads, 2) void attn_shared_kernel(SharedArgs a) {
-  __shared__ __align__(1024) uint8_t lds[4 * kKeys * D * 2];
+  __shared__ __align__(1024) uint8_t lds[attend_lds_bytes<D>()];
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int prefix_items = a.prefix_pieces * a.row_tiles * a.n_kv;
