@@ -344,8 +344,7 @@ template <int D> constexpr int attend_lds_bytes() { return 4 * kKeys * D * 2 + 3
 template <class E, int D, bool CAUSAL, class CopyK, class CopyV>
 __device__ __forceinline__ bool attend_blocks(uint8_t *lds, const CopyK &copy_k, const CopyV &copy_v, int n_keys,
                                               int first_masked, int full, int mine, int lim,
-                                              const typename E::v8 q[D / 16], AttnState<D> &st, float c, int wave,
-                                              int lane) {
+                                              typename E::v8 q[D / 16], AttnState<D> &st, float c, int wave, int lane) {
   constexpr int kTile = kKeys * D * 2;
   typedef typename E::v8 v8;
   const int blocks = (n_keys + kKeys - 1) / kKeys;
@@ -376,10 +375,13 @@ __device__ __forceinline__ bool attend_blocks(uint8_t *lds, const CopyK &copy_k,
   v8 p[4];
   int any_bad = 0;
   load_k(0);
+  load_v(0);
   wait_loads<0>();
+  // the compiler waits for its own loads of q here, while nothing else is on its way
+#pragma unroll
+  for (int i = 0; i < D / 16; ++i) asm volatile("" : "+v"(q[i]));
   __syncthreads();
   load_k(1);
-  load_v(0);
   scores<E, D, 2>(kt(0), q, s, lane);
   interleave<D / 8, 4, 1, 0, 0>();
   float mx = row_max<2>(s) * c;
@@ -432,18 +434,27 @@ template <int D> __device__ __forceinline__ float row_sum(const AttnState<D> &st
   return two.x + two.y;
 }
 
-// Writes a lane's half of its row's D outputs, times f, to `row` (8 bytes
-// per store).
+// Writes a row's D outputs, times f, from the two lanes that hold it. A lane
+// has 4 of every 8 elements; lanes l and l + 32 trade, so that l stores the 8
+// elements of one chunk and l + 32 those of the next (16 bytes per store).
+// Both lanes of a row call it, with the same `live`.
 template <class E, int D>
-__device__ __forceinline__ void store_row(typename E::one *row, const AttnState<D> &st, float f, int lane) {
+__device__ __forceinline__ void store_row(typename E::one *row, const AttnState<D> &st, float f, int lane, bool live) {
 #pragma unroll
   for (int dt = 0; dt < D / 32; ++dt)
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      typename E::v4 v;
+    for (int i = 0; i < 4; i += 2) {
+      u32x2_t two[2];
 #pragma unroll
-      for (int j = 0; j < 4; ++j) v[j] = static_cast<typename E::one>(st.o[dt][4 * i + j] * f);
-      *reinterpret_cast<typename E::v4 *>(row + 32 * dt + 8 * i + 4 * (lane >> 5)) = v;
+      for (int k = 0; k < 2; ++k) {
+        typename E::v4 v;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) v[j] = static_cast<typename E::one>(st.o[dt][4 * (i + k) + j] * f);
+        two[k] = __builtin_bit_cast(u32x2_t, v);
+      }
+      const auto x = __builtin_amdgcn_permlane32_swap(two[0].x, two[1].x, false, false);
+      const auto y = __builtin_amdgcn_permlane32_swap(two[0].y, two[1].y, false, false);
+      if (live) *reinterpret_cast<u32x4_t *>(row + 32 * dt + 8 * (i + (lane >> 5))) = u32x4_t{x[0], y[0], x[1], y[1]};
     }
 }
 

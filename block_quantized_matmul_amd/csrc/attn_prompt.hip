@@ -144,11 +144,9 @@ __global__ __launch_bounds__(kThreads, 2) void attn_prompt_kernel(PromptArgs a) 
   asm volatile("" : "+v"(l2));
   if (!any_bad) {
     const int row2 = tile * kRows + wave * 32 + (l2 & 31);
-    if (row2 < rows) {
-      const int t2 = row2 / a.group;
-      one *o = static_cast<one *>(a.o) + (first + t2) * a.ot + (g * a.group + row2 - t2 * a.group) * a.oh;
-      store_row<E, D>(o, st, 1.f / l, l2);
-    }
+    const int t2 = row2 / a.group;
+    one *o = static_cast<one *>(a.o) + (first + t2) * a.ot + (g * a.group + row2 - t2 * a.group) * a.oh;
+    store_row<E, D>(o, st, 1.f / l, l2, row2 < rows);
   } else {
     for (int r = tile * kRows + wave * 32; r < min(rows, tile * kRows + wave * 32 + 32); ++r) {
       const int t2 = r / a.group;
