@@ -83,114 +83,128 @@ def _lib():
     return _ready
 
 
+def _refuse(named):
+    """Raises what is wrong with the places of a call's (name, tensor) pairs."""
+    import torch
+    first = None
+    for name, t in named:
+        if t is None:
+            continue
+        if not isinstance(t, torch.Tensor) or not t.is_cuda:
+            raise TypeError(f"{name} must be a GPU tensor (the library has no CPU path)")
+        if first is None:
+            first = t.device
+        elif t.device != first:
+            raise ValueError(f"{name} is on {t.device}, other tensors of the call on {first}")
+    raise TypeError("a call needs GPU tensors")
+
+
 class _Place:
-    """Where a call runs: the one GPU of its tensors, made current for the
-    duration of the call, and the stream."""
-    __slots__ = ("device", "stream", "foreign", "guard")
+    """Where a call runs: the one GPU of its tensors and the stream's handle.
+    (These calls are short, so this takes the cheapest route to each answer.)"""
+    __slots__ = ("device", "handle", "foreign")
 
-    def __init__(self, stream, named):
+    def __init__(self, stream, names, tensors):
         import torch
-        device = None
-        for name, t in named:
-            if t is None:
-                continue
-            if not isinstance(t, torch.Tensor) or not t.is_cuda:
-                raise TypeError(f"{name} must be a GPU tensor (the library has no CPU path)")
-            if device is None:
-                device = t.device
-            elif t.device != device:
-                raise ValueError(f"{name} is on {t.device}, other tensors of the call on {device}")
-        current = torch.cuda.current_stream(device)
-        if stream is None:
-            stream = current
-        elif stream.device != device:
-            raise ValueError(f"the stream is on {stream.device}, the tensors on {device}")
-        self.device, self.stream = device, stream
-        self.foreign = stream.cuda_stream != current.cuda_stream
-        self.guard = None if torch.cuda.current_device() == device.index else torch.cuda.device(device)
-
-    def __enter__(self):
-        if self.guard is not None:
-            self.guard.__enter__()
-        return self
-
-    def __exit__(self, *exc):
-        if self.guard is not None:
-            self.guard.__exit__(*exc)
+        try:
+            device = tensors[0].get_device()
+            for t in tensors:
+                if t is not None and t.get_device() != device:
+                    _refuse(zip(names, tensors))
+        except AttributeError:
+            device = -1
+        if device < 0:
+            _refuse(zip(names, tensors))
+        self.device = device
+        self.handle = torch._C._cuda_getCurrentRawStream(device)
+        self.foreign = None
+        if stream is not None and stream.cuda_stream != self.handle:
+            if stream.device.index != device:
+                raise ValueError(f"the stream is on {stream.device}, the tensors on cuda:{device}")
+            self.handle, self.foreign = stream.cuda_stream, stream
 
     def empty(self, shape, dtype):
         import torch
         t = torch.empty(shape, dtype=dtype, device=self.device)
-        if self.foreign:
-            t.record_stream(self.stream)
+        if self.foreign is not None:
+            t.record_stream(self.foreign)
         return t
 
     def workspace(self, given, need, what):
-        """Pointer and size of the call's workspace: the caller's, or a new one."""
+        """The call's workspace (the caller's, or a new one), its pointer and size."""
         import torch
         if need < 0:
             raise _qmm.QmmError(int(need), what)
         if given is None:
             if need == 0:
-                return None, 0, None
+                return None, None, 0
             given = self.empty((need,), torch.uint8)
         elif given.dtype != torch.uint8 or not given.is_contiguous():
             raise TypeError("workspace must be a contiguous uint8 tensor")
-        return given.data_ptr(), given.numel(), given
+        return given, given.data_ptr(), given.numel()
+
+    def run(self, function, what, *args):
+        """The library's function with the tensors' GPU current."""
+        import torch
+        if torch._C._cuda_getDevice() == self.device:
+            status = function(*args, self.handle)
+        else:
+            with torch.cuda.device(self.device):
+                status = function(*args, self.handle)
+        if status != 0:
+            raise _qmm.QmmError(status, what)
 
 
-def _type(t, name, allowed):
+def _type(t, name):
     import torch
     code = {torch.float32: QMM_T_F32, torch.float16: QMM_T_F16, torch.bfloat16: QMM_T_BF16}.get(t.dtype)
-    if code is None or code not in allowed:
+    if code is None:
         raise TypeError(f"{name} has an unsupported type {t.dtype}")
     return code
 
 
-def _ints(t, name, shape):
-    """An int32 vector of a given length (None: any)."""
+def _ints(t, name, n):
+    """A contiguous int32 vector of n elements (None: any number)."""
     import torch
-    if t.dtype != torch.int32 or t.dim() != 1 or not t.is_contiguous():
+    if t.dtype is not torch.int32 or t.dim() != 1 or not t.is_contiguous():
         raise TypeError(f"{name} must be a contiguous 1-D int32 tensor")
-    if shape is not None and t.shape[0] != shape:
-        raise ValueError(f"{name} holds {t.shape[0]} elements, the call needs {shape}")
+    if n is not None and t.shape[0] != n:
+        raise ValueError(f"{name} holds {t.shape[0]} elements, the call needs {n}")
 
 
 def _floats(t, name, shape):
     import torch
-    if t.dtype != torch.float32 or not t.is_contiguous():
+    if t.dtype is not torch.float32 or not t.is_contiguous():
         raise TypeError(f"{name} must be a contiguous float32 tensor")
-    if tuple(t.shape) != tuple(shape):
+    if t.shape != shape:
         raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
 
 
-def _stride(t, dim):
-    # torch leaves the strides of one-element axes and empty tensors open; they are never used
-    return t.stride(dim) if t.shape[dim] > 1 and t.numel() > 0 else 0
-
-
-def _contiguous_heads(t, name):
-    if t.shape[-1] > 1 and t.stride(-1) != 1 and t.numel() > 0:
-        raise ValueError(f"the elements of one head of {name} must be contiguous")
+def _strides(t, name):
+    """A tensor's strides with contiguous heads. torch leaves the strides of
+    one-element axes and empty tensors open; they are never used, so 0."""
+    st = t.stride()
+    if st[-1] != 1 or 1 in t.shape or 0 in t.shape:
+        if t.numel() == 0:
+            return (0,) * len(st)
+        if st[-1] != 1 and t.shape[-1] > 1:
+            raise ValueError(f"the elements of one head of {name} must be contiguous")
+        st = tuple(x if n > 1 else 0 for x, n in zip(st, t.shape))
+    return st
 
 
 def _heads(t, name, shape, dtype):
     """qmm_heads of a tensor of `shape`: [tokens][heads][dim] or [seqs][tokens][heads][dim]."""
-    if t.dtype != dtype:
+    if t.dtype is not dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if tuple(t.shape) != tuple(shape):
+    if t.shape != shape:
         raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
-    _contiguous_heads(t, name)
-    return qmm_heads_desc(t.data_ptr(), _stride(t, 0) if len(shape) == 4 else 0, _stride(t, -3), _stride(t, -2))
+    st = _strides(t, name)
+    return qmm_heads_desc(t.data_ptr(), st[0] if len(st) == 4 else 0, st[-3], st[-2])
 
 
 def _ptr(t):
     return None if t is None else t.data_ptr()
-
-
-def _check(status, what):
-    if status != 0:
-        raise _qmm.QmmError(status, what)
 
 
 def qmm_lora_workspace_bytes(n_tokens: int, k: int, rank: int) -> int:
@@ -208,33 +222,34 @@ def qmm_lora(X, A, B, ids, scales=None, base=None, Y=None, workspace=None, strea
     [n_tokens][n_rows]) is allocated if None, and may be base. Without a
     workspace, one of qmm_lora_workspace_bytes bytes is allocated."""
     import torch
-    with _Place(stream, (("X", X), ("A", A), ("B", B), ("ids", ids), ("scales", scales), ("base", base), ("Y", Y),
-                         ("workspace", workspace))) as place:
-        x_type = _type(X, "X", (QMM_T_F32, QMM_T_F16))
-        if X.dim() != 2 or A.dim() != 3 or B.dim() != 3:
-            raise ValueError("X must be [n_tokens][k], A [n_adapters][rank][k], B [n_adapters][n_rows][rank]")
-        (n, k), (n_adapters, rank, ka), (nb, n_rows, rank_b) = X.shape, A.shape, B.shape
-        if ka != k or nb != n_adapters or rank_b != rank:
-            raise ValueError("X must be [n_tokens][k], A [n_adapters][rank][k], B [n_adapters][n_rows][rank]")
-        if A.dtype != torch.float16 or B.dtype != torch.float16:
-            raise TypeError("A and B must be float16")
-        if not (X.is_contiguous() and A.is_contiguous() and B.is_contiguous()):
-            raise ValueError("X, A and B must be contiguous")
-        _ints(ids, "ids", n)
-        if scales is not None:
-            _floats(scales, "scales", (n_adapters,))
-        if base is not None:
-            _floats(base, "base", (n, n_rows))
-        if Y is None:
-            Y = place.empty((n, n_rows), torch.float32)
-        else:
-            _floats(Y, "Y", (n, n_rows))
-        L = _lib()
-        ws, ws_bytes, _keep = place.workspace(workspace, L.qmm_lora_workspace_bytes(n, k, rank),
-                                              "qmm_lora_workspace_bytes")
-        _check(L.qmm_lora(X.data_ptr(), x_type, n, k, A.data_ptr(), B.data_ptr(), n_adapters, rank, n_rows,
-                          _ptr(scales), ids.data_ptr(), _ptr(base), Y.data_ptr(), ws, ws_bytes,
-                          place.stream.cuda_stream), "qmm_lora")
+    place = _Place(stream, ("X", "A", "B", "ids", "scales", "base", "Y", "workspace"),
+                   (X, A, B, ids, scales, base, Y, workspace))
+    if X.dtype is not torch.float32 and X.dtype is not torch.float16:
+        raise TypeError("X must be float32 or float16")
+    if X.dim() != 2 or A.dim() != 3 or B.dim() != 3:
+        raise ValueError("X must be [n_tokens][k], A [n_adapters][rank][k], B [n_adapters][n_rows][rank]")
+    (n, k), (n_adapters, rank, ka), (nb, n_rows, rank_b) = X.shape, A.shape, B.shape
+    if ka != k or nb != n_adapters or rank_b != rank:
+        raise ValueError("X must be [n_tokens][k], A [n_adapters][rank][k], B [n_adapters][n_rows][rank]")
+    if A.dtype is not torch.float16 or B.dtype is not torch.float16:
+        raise TypeError("A and B must be float16")
+    if not (X.is_contiguous() and A.is_contiguous() and B.is_contiguous()):
+        raise ValueError("X, A and B must be contiguous")
+    _ints(ids, "ids", n)
+    if scales is not None:
+        _floats(scales, "scales", (n_adapters,))
+    if base is not None:
+        _floats(base, "base", (n, n_rows))
+    if Y is None:
+        Y = place.empty((n, n_rows), torch.float32)
+    else:
+        _floats(Y, "Y", (n, n_rows))
+    L = _lib()
+    _keep, ws, ws_bytes = place.workspace(workspace, L.qmm_lora_workspace_bytes(n, k, rank),
+                                          "qmm_lora_workspace_bytes")
+    place.run(L.qmm_lora, "qmm_lora", X.data_ptr(), QMM_T_F32 if X.dtype is torch.float32 else QMM_T_F16, n, k,
+              A.data_ptr(), B.data_ptr(), n_adapters, rank, n_rows, _ptr(scales), ids.data_ptr(), _ptr(base),
+              Y.data_ptr(), ws, ws_bytes)
     return Y
 
 
@@ -267,46 +282,41 @@ def qmm_norm_rope(parts, positions=None, freqs=None, pairs="halves", eps=1e-6, s
         raise ValueError(f"at most {QMM_HEAD_PARTS_MAX} parts")
     if pairs not in _PAIRS:
         raise ValueError("pairs must be 'halves' or 'neighbours'")
-    named = [("positions", positions), ("slots", slots)]
-    for p in parts:
-        named += [("X", p.X), ("Y", p.Y), ("weight", p.weight)]
-    with _Place(stream, named) as place:
-        if parts[0].X.dim() != 3:
-            raise ValueError("X must be [n_tokens][n_heads][head_dim]")
-        n, _, dim = parts[0].X.shape
-        descs = (qmm_head_part_desc * len(parts))()
-        n_slots = None
-        every = (QMM_T_F32, QMM_T_F16, QMM_T_BF16)
-        for d, p in zip(descs, parts):
-            X, Y = p.X, p.Y
-            if X.dim() != 3 or Y.dim() != 3 or X.shape[0] != n or X.shape[2] != dim:
-                raise ValueError("every X must be [n_tokens][n_heads][head_dim] with one n_tokens and head_dim")
-            if Y.shape[1] != X.shape[1] or Y.shape[2] != dim or (not p.slotted and Y.shape[0] != n):
-                raise ValueError("Y must be [n_tokens][n_heads][head_dim], or [n_slots][...] if slotted")
-            if p.slotted:
-                if slots is None:
-                    raise ValueError("a slotted part needs slots")
-                if n_slots is not None and Y.shape[0] != n_slots:
-                    raise ValueError("slotted parts must have one number of slots")
-                n_slots = Y.shape[0]
-            if p.rotate and (positions is None or freqs is None):
-                raise ValueError("a rotated part needs positions and freqs")
-            if p.weight is not None:
-                if not p.norm:
-                    raise ValueError("weight needs norm")
-                _floats(p.weight, "weight", (dim,))
-            _contiguous_heads(X, "X")
-            _contiguous_heads(Y, "Y")
-            d.X, d.x_type, d.x_token_stride, d.x_head_stride = X.data_ptr(), _type(X, "X", every), _stride(X, 0), _stride(X, 1)
-            d.Y, d.y_type, d.y_row_stride, d.y_head_stride = Y.data_ptr(), _type(Y, "Y", every), _stride(Y, 0), _stride(Y, 1)
-            d.n_heads, d.norm, d.weight, d.rotate, d.slotted = X.shape[1], p.norm, _ptr(p.weight), p.rotate, p.slotted
-        if positions is not None:
-            _ints(positions, "positions", n)
-        if slots is not None:
-            _ints(slots, "slots", n)
-        fp, n_freqs, _keep = _host_doubles(freqs)
-        _check(_lib().qmm_norm_rope(descs, len(parts), n, dim, eps, _ptr(positions), fp, n_freqs, _PAIRS[pairs],
-                                    _ptr(slots), n_slots or 0, place.stream.cuda_stream), "qmm_norm_rope")
+    tensors = [t for p in parts for t in (p.X, p.Y, p.weight)] + [positions, slots]
+    place = _Place(stream, ["X", "Y", "weight"] * len(parts) + ["positions", "slots"], tensors)
+    if parts[0].X.dim() != 3:
+        raise ValueError("X must be [n_tokens][n_heads][head_dim]")
+    n, _, dim = parts[0].X.shape
+    descs = (qmm_head_part_desc * len(parts))()
+    n_slots = None
+    for i, (X, Y, norm, weight, rotate, slotted) in enumerate(parts):
+        xs, ys = X.shape, Y.shape
+        if len(xs) != 3 or xs[0] != n or xs[2] != dim:
+            raise ValueError("every X must be [n_tokens][n_heads][head_dim] with one n_tokens and head_dim")
+        if len(ys) != 3 or ys[1] != xs[1] or ys[2] != dim or (not slotted and ys[0] != n):
+            raise ValueError("Y must be [n_tokens][n_heads][head_dim], or [n_slots][...] if slotted")
+        if slotted:
+            if slots is None:
+                raise ValueError("a slotted part needs slots")
+            if n_slots is not None and ys[0] != n_slots:
+                raise ValueError("slotted parts must have one number of slots")
+            n_slots = ys[0]
+        if rotate and (positions is None or freqs is None):
+            raise ValueError("a rotated part needs positions and freqs")
+        if weight is not None:
+            if not norm:
+                raise ValueError("weight needs norm")
+            _floats(weight, "weight", (dim,))
+        xst, yst = _strides(X, "X"), _strides(Y, "Y")
+        descs[i] = qmm_head_part_desc(X.data_ptr(), _type(X, "X"), xst[0], xst[1], Y.data_ptr(), _type(Y, "Y"), yst[0],
+                                      yst[1], xs[1], bool(norm), _ptr(weight), bool(rotate), bool(slotted))
+    if positions is not None:
+        _ints(positions, "positions", n)
+    if slots is not None:
+        _ints(slots, "slots", n)
+    fp, n_freqs, _keep = _host_doubles(freqs)
+    place.run(_lib().qmm_norm_rope, "qmm_norm_rope", descs, len(parts), n, dim, eps, _ptr(positions), fp, n_freqs,
+              _PAIRS[pairs], _ptr(slots), n_slots or 0)
     return [p.Y for p in parts]
 
 
@@ -319,22 +329,21 @@ def qmm_attn_prompt(Q, K, V, seq_starts, scale=None, O=None, stream=None):
     seq_starts[i] .. seq_starts[i + 1] - 1. scale defaults to
     head_dim ** -0.5. O (like Q) is allocated if None; rows of tokens outside
     every sequence are not written."""
-    with _Place(stream, (("Q", Q), ("K", K), ("V", V), ("seq_starts", seq_starts), ("O", O))) as place:
-        if Q.dim() != 3 or K.dim() != 3:
-            raise ValueError("Q must be [n_tokens][n_q_heads][head_dim], K and V [n_tokens][n_kv_heads][head_dim]")
-        n, hq, dim = Q.shape
-        hkv = K.shape[1]
-        t = _type(Q, "Q", (QMM_T_F16, QMM_T_BF16))
-        _ints(seq_starts, "seq_starts", None)
-        if seq_starts.shape[0] < 1:
-            raise ValueError("seq_starts must hold n_seqs + 1 elements")
-        if O is None:
-            O = place.empty((n, hq, dim), Q.dtype)
-        q, k, v, o = (_heads(x, name, (n, h, dim), Q.dtype)
-                      for x, name, h in ((Q, "Q", hq), (K, "K", hkv), (V, "V", hkv), (O, "O", hq)))
-        _check(_lib().qmm_attn_prompt(t, q, k, v, o, n, hq, hkv, dim, seq_starts.data_ptr(), seq_starts.shape[0] - 1,
-                                      dim ** -0.5 if scale is None else scale, place.stream.cuda_stream),
-               "qmm_attn_prompt")
+    place = _Place(stream, ("Q", "K", "V", "seq_starts", "O"), (Q, K, V, seq_starts, O))
+    if Q.dim() != 3 or K.dim() != 3:
+        raise ValueError("Q must be [n_tokens][n_q_heads][head_dim], K and V [n_tokens][n_kv_heads][head_dim]")
+    shape, dtype = Q.shape, Q.dtype
+    n, hq, dim = shape
+    hkv = K.shape[1]
+    _ints(seq_starts, "seq_starts", None)
+    if seq_starts.shape[0] < 1:
+        raise ValueError("seq_starts must hold n_seqs + 1 elements")
+    if O is None:
+        O = place.empty(shape, dtype)
+    kv = (n, hkv, dim)
+    place.run(_lib().qmm_attn_prompt, "qmm_attn_prompt", _type(Q, "Q"), _heads(Q, "Q", shape, dtype),
+              _heads(K, "K", kv, dtype), _heads(V, "V", kv, dtype), _heads(O, "O", shape, dtype), n, hq, hkv, dim,
+              seq_starts.data_ptr(), seq_starts.shape[0] - 1, dim ** -0.5 if scale is None else scale)
     return O
 
 
@@ -356,32 +365,32 @@ def qmm_attn_shared(Q, PK, PV, K, V, lengths, scale=None, O=None, workspace=None
     of NaNs. scale defaults to head_dim ** -0.5. O (like Q) is allocated if
     None. Without a workspace, one of qmm_attn_shared_workspace_bytes bytes is
     allocated."""
-    with _Place(stream, (("Q", Q), ("PK", PK), ("PV", PV), ("K", K), ("V", V), ("lengths", lengths), ("O", O),
-                         ("workspace", workspace))) as place:
-        if (PK is None) != (PV is None) or (K is None) != (V is None) or (K is None) != (lengths is None):
-            raise ValueError("pass PK and PV together, and K, V and lengths together")
-        if Q.dim() != 3 or (PK is not None and PK.dim() != 3) or (K is not None and K.dim() != 4):
-            raise ValueError("Q must be [n_seqs][n_q_heads][head_dim], PK and PV [prefix_len][n_kv_heads][head_dim], "
-                             "K and V [n_seqs][own_cap][n_kv_heads][head_dim]")
-        n, hq, dim = Q.shape
-        if PK is None and K is None:
-            raise ValueError("pass a prefix, own caches or both")
-        prefix, cap = (0 if PK is None else PK.shape[0]), (0 if K is None else K.shape[1])
-        hkv = PK.shape[1] if PK is not None else K.shape[2]
-        t = _type(Q, "Q", (QMM_T_F16, QMM_T_BF16))
-        if O is None:
-            O = place.empty((n, hq, dim), Q.dtype)
-        q, o = _heads(Q, "Q", (n, hq, dim), Q.dtype), _heads(O, "O", (n, hq, dim), Q.dtype)
-        pk = pv = k = v = None
-        if PK is not None:
-            pk, pv = _heads(PK, "PK", (prefix, hkv, dim), Q.dtype), _heads(PV, "PV", (prefix, hkv, dim), Q.dtype)
-        if K is not None:
-            k, v = _heads(K, "K", (n, cap, hkv, dim), Q.dtype), _heads(V, "V", (n, cap, hkv, dim), Q.dtype)
-            _ints(lengths, "lengths", n)
-        L = _lib()
-        ws, ws_bytes, _keep = place.workspace(workspace, L.qmm_attn_shared_workspace_bytes(n, prefix, cap, hq, hkv, dim),
-                                              "qmm_attn_shared_workspace_bytes")
-        _check(L.qmm_attn_shared(t, q, pk, pv, prefix, k, v, cap, _ptr(lengths), o, n, hq, hkv, dim,
-                                 dim ** -0.5 if scale is None else scale, ws, ws_bytes, place.stream.cuda_stream),
-               "qmm_attn_shared")
+    place = _Place(stream, ("Q", "PK", "PV", "K", "V", "lengths", "O", "workspace"),
+                   (Q, PK, PV, K, V, lengths, O, workspace))
+    if (PK is None) != (PV is None) or (K is None) != (V is None) or (K is None) != (lengths is None):
+        raise ValueError("pass PK and PV together, and K, V and lengths together")
+    if Q.dim() != 3 or (PK is not None and PK.dim() != 3) or (K is not None and K.dim() != 4):
+        raise ValueError("Q must be [n_seqs][n_q_heads][head_dim], PK and PV [prefix_len][n_kv_heads][head_dim], "
+                         "K and V [n_seqs][own_cap][n_kv_heads][head_dim]")
+    if PK is None and K is None:
+        raise ValueError("pass a prefix, own caches or both")
+    shape, dtype = Q.shape, Q.dtype
+    n, hq, dim = shape
+    prefix, cap = (0 if PK is None else PK.shape[0]), (0 if K is None else K.shape[1])
+    hkv = PK.shape[1] if PK is not None else K.shape[2]
+    if O is None:
+        O = place.empty(shape, dtype)
+    pk = pv = k = v = None
+    if PK is not None:
+        pk, pv = _heads(PK, "PK", (prefix, hkv, dim), dtype), _heads(PV, "PV", (prefix, hkv, dim), dtype)
+    if K is not None:
+        own = (n, cap, hkv, dim)
+        k, v = _heads(K, "K", own, dtype), _heads(V, "V", own, dtype)
+        _ints(lengths, "lengths", n)
+    L = _lib()
+    _keep, ws, ws_bytes = place.workspace(workspace, L.qmm_attn_shared_workspace_bytes(n, prefix, cap, hq, hkv, dim),
+                                          "qmm_attn_shared_workspace_bytes")
+    place.run(L.qmm_attn_shared, "qmm_attn_shared", _type(Q, "Q"), _heads(Q, "Q", shape, dtype), pk, pv, prefix, k, v,
+              cap, _ptr(lengths), _heads(O, "O", shape, dtype), n, hq, hkv, dim, dim ** -0.5 if scale is None else scale,
+              ws, ws_bytes)
     return O

@@ -262,10 +262,10 @@ hipError_t launch_norm_rope(const qmm_head_part *parts, int n_parts, int64_t n_t
   a.eps = eps, a.inv_dim = 1.f / static_cast<float>(head_dim);
   // a frequency in turns per position, modulo whole turns (positions are integers)
   for (int64_t i = 0; i < n_freqs; ++i) {
-    long double t = static_cast<long double>(freqs[i]) / 6.283185307179586476925286766559L;
-    t -= floorl(t);
-    t = roundl(ldexpl(t, 64));
-    a.turn[i] = t >= ldexpl(1.0L, 64) ? 0 : static_cast<uint64_t>(t);
+    long double t = static_cast<long double>(freqs[i]) * 0.159154943091895335768883763372514362L;
+    if (t < 0.0L || t >= 1.0L) t -= floorl(t);
+    t = t * 18446744073709551616.0L + 0.5L;
+    a.turn[i] = t >= 18446744073709551616.0L ? 0 : static_cast<uint64_t>(t);
   }
   // two runs per lane, rounded up: one more unit than runs / 2 may be needed
   // where the rotated and the plain part both end in half a unit
