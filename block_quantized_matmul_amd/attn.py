@@ -58,11 +58,14 @@ class qmm_head_part(NamedTuple):
 
 
 _ready = None
+_types = {}
 
 
 def _lib():
     global _ready
     if _ready is None:
+        import torch
+        _types.update({torch.float32: QMM_T_F32, torch.float16: QMM_T_F16, torch.bfloat16: QMM_T_BF16})
         L = _qmm.lib()
         heads = ctypes.POINTER(qmm_heads_desc)
         L.qmm_lora.argtypes = [_vp, _i32, _i64, _i64, _vp, _vp, _i64, _i64, _i64, _vp, _vp, _vp, _vp, _vp, _i64, _vp]
@@ -156,8 +159,7 @@ class _Place:
 
 
 def _type(t, name):
-    import torch
-    code = {torch.float32: QMM_T_F32, torch.float16: QMM_T_F16, torch.bfloat16: QMM_T_BF16}.get(t.dtype)
+    code = _types.get(t.dtype)
     if code is None:
         raise TypeError(f"{name} has an unsupported type {t.dtype}")
     return code
@@ -181,15 +183,9 @@ def _floats(t, name, shape):
 
 
 def _strides(t, name):
-    """A tensor's strides with contiguous heads. torch leaves the strides of
-    one-element axes and empty tensors open; they are never used, so 0."""
     st = t.stride()
-    if st[-1] != 1 or 1 in t.shape or 0 in t.shape:
-        if t.numel() == 0:
-            return (0,) * len(st)
-        if st[-1] != 1 and t.shape[-1] > 1:
-            raise ValueError(f"the elements of one head of {name} must be contiguous")
-        st = tuple(x if n > 1 else 0 for x, n in zip(st, t.shape))
+    if st[-1] != 1 and t.shape[-1] > 1 and t.numel() > 0:
+        raise ValueError(f"the elements of one head of {name} must be contiguous")
     return st
 
 
@@ -287,7 +283,8 @@ def qmm_norm_rope(parts, positions=None, freqs=None, pairs="halves", eps=1e-6, s
     if parts[0].X.dim() != 3:
         raise ValueError("X must be [n_tokens][n_heads][head_dim]")
     n, _, dim = parts[0].X.shape
-    descs = (qmm_head_part_desc * len(parts))()
+    L = _lib()
+    descs = (qmm_head_part_desc * QMM_HEAD_PARTS_MAX)()
     n_slots = None
     for i, (X, Y, norm, weight, rotate, slotted) in enumerate(parts):
         xs, ys = X.shape, Y.shape
@@ -315,7 +312,7 @@ def qmm_norm_rope(parts, positions=None, freqs=None, pairs="halves", eps=1e-6, s
     if slots is not None:
         _ints(slots, "slots", n)
     fp, n_freqs, _keep = _host_doubles(freqs)
-    place.run(_lib().qmm_norm_rope, "qmm_norm_rope", descs, len(parts), n, dim, eps, _ptr(positions), fp, n_freqs,
+    place.run(L.qmm_norm_rope, "qmm_norm_rope", descs, len(parts), n, dim, eps, _ptr(positions), fp, n_freqs,
               _PAIRS[pairs], _ptr(slots), n_slots or 0)
     return [p.Y for p in parts]
 
@@ -341,7 +338,8 @@ def qmm_attn_prompt(Q, K, V, seq_starts, scale=None, O=None, stream=None):
     if O is None:
         O = place.empty(shape, dtype)
     kv = (n, hkv, dim)
-    place.run(_lib().qmm_attn_prompt, "qmm_attn_prompt", _type(Q, "Q"), _heads(Q, "Q", shape, dtype),
+    L = _lib()
+    place.run(L.qmm_attn_prompt, "qmm_attn_prompt", _type(Q, "Q"), _heads(Q, "Q", shape, dtype),
               _heads(K, "K", kv, dtype), _heads(V, "V", kv, dtype), _heads(O, "O", shape, dtype), n, hq, hkv, dim,
               seq_starts.data_ptr(), seq_starts.shape[0] - 1, dim ** -0.5 if scale is None else scale)
     return O

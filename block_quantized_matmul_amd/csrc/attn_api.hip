@@ -4,6 +4,8 @@
 // without a GPU and nothing is enqueued.
 #include <math.h>
 
+#include <utility>
+
 #include "attn.h"
 
 namespace {
@@ -11,6 +13,7 @@ namespace {
 constexpr int64_t kMaxDim = (int64_t{1} << 31) - 1;
 constexpr int64_t kMaxElems = int64_t{1} << 60;
 constexpr int64_t kMaxGroups = (int64_t{1} << 24) - 1;  // 256-thread workgroups of one launch (2^32 threads)
+constexpr int64_t kMaxCopyStride = int64_t{1} << 25;  // elements: 63 rows of a block within 32-bit byte offsets
 constexpr int64_t kMaxLoraTokens = (int64_t{1} << 25) - 1;
 constexpr int64_t kMaxLoraK = (int64_t{1} << 24) - 1;
 
@@ -22,7 +25,7 @@ bool in_dim(int64_t n) { return n >= 0 && n <= kMaxDim; }
 // Offsets of `a` rows and `b` columns under strides sa and sb stay within
 // 2^60 elements (head_dim included by the margin).
 bool span_within(int64_t a, int64_t sa, int64_t b, int64_t sb) {
-  return product_within(a, sa, kMaxElems / 4) && product_within(b, sb, kMaxElems / 4);
+  return (a <= 1 || product_within(a, sa, kMaxElems / 4)) && (b <= 1 || product_within(b, sb, kMaxElems / 4));
 }
 // No two heads of an output share elements.
 bool apart(int64_t rows, int64_t row_stride, int64_t heads, int64_t head_stride, int64_t dim) {
@@ -35,10 +38,12 @@ bool apart(int64_t rows, int64_t row_stride, int64_t heads, int64_t head_stride,
 
 int check_heads(const qmm_heads *h, int64_t seqs, int64_t tokens, int64_t heads) {
   if (h == nullptr || h->data == nullptr) return QMM_ERR_NULL;
-  if (h->seq_stride < 0 || h->token_stride < 0 || h->head_stride < 0) return QMM_ERR_STRIDE;
-  if (h->token_stride % 8 != 0 || h->head_stride % 8 != 0 || (seqs > 0 && h->seq_stride % 8 != 0)) return QMM_ERR_STRIDE;
+  // the stride of an axis of one element is never used
+  for (const auto &[n, stride] : {std::pair{seqs, h->seq_stride}, {tokens, h->token_stride}, {heads, h->head_stride}})
+    if (n > 1 && (stride < 0 || stride % 8 != 0)) return QMM_ERR_STRIDE;
+  if (h->token_stride > kMaxCopyStride && tokens > 1) return QMM_ERR_STRIDE;
   if (!span_within(tokens, h->token_stride, heads, h->head_stride) ||
-      (seqs > 0 && !product_within(seqs, h->seq_stride, kMaxElems / 4)))
+      (seqs > 1 && !product_within(seqs, h->seq_stride, kMaxElems / 4)))
     return QMM_ERR_SHAPE;
   if (!aligned(h->data, 16)) return QMM_ERR_ALIGN;
   return QMM_OK;
@@ -116,8 +121,10 @@ int qmm_norm_rope(const qmm_head_part *parts, int n_parts, int64_t n_tokens, int
     for (int t : {h.x_type, h.y_type})
       if (t != QMM_T_F32 && t != QMM_T_F16 && t != QMM_T_BF16) return QMM_ERR_TYPE;
     if (!in_dim(h.n_heads)) return QMM_ERR_SHAPE;
-    if (h.x_token_stride < 0 || h.x_head_stride < 0 || h.y_row_stride < 0 || h.y_head_stride < 0) return QMM_ERR_STRIDE;
     const int64_t rows = h.slotted ? n_slots : n_tokens;
+    if ((n_tokens > 1 && h.x_token_stride < 0) || (rows > 1 && h.y_row_stride < 0) ||
+        (h.n_heads > 1 && (h.x_head_stride < 0 || h.y_head_stride < 0)))
+      return QMM_ERR_STRIDE;
     if (!span_within(n_tokens, h.x_token_stride, h.n_heads, h.x_head_stride) ||
         !span_within(rows, h.y_row_stride, h.n_heads, h.y_head_stride))
       return QMM_ERR_SHAPE;

@@ -31,6 +31,7 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kMaxFreqs = QMM_NORM_ROPE_MAX_DIM / 2;
+constexpr int kFewFreqs = 64;  // the table travels in the kernel's arguments, so its size costs launch time
 
 struct Part {
   const void *x;
@@ -41,7 +42,7 @@ struct Part {
   int x_type, y_type;
   int norm, rotate, slotted;
 };
-struct RopeArgs {
+template <int F> struct RopeArgs {
   Part part[QMM_HEAD_PARTS_MAX];
   const int32_t *positions, *slots;
   int64_t n_tokens;
@@ -50,7 +51,7 @@ struct RopeArgs {
   int chunks;  // wavefronts per token
   int chunk;   // passes per wavefront
   float eps, inv_dim;
-  uint64_t turn[kMaxFreqs];  // f / 2 pi in units of 2^-64
+  uint64_t turn[F];  // f / 2 pi in units of 2^-64
 };
 
 typedef uint16_t u16x4_a8 __attribute__((ext_vector_type(4), aligned(8)));
@@ -119,8 +120,8 @@ __device__ __forceinline__ void sincos_turn(uint64_t t, float &sin, float &cos) 
 }
 
 // U: units per lane (a unit is two runs of V elements).
-template <int V, int U>
-__global__ __launch_bounds__(kThreads) void norm_rope_kernel(RopeArgs a) {
+template <int V, int U, int F>
+__global__ __launch_bounds__(kThreads) void norm_rope_kernel(RopeArgs<F> a) {
   const int lane = threadIdx.x & 63;
   const int64_t wave0 = static_cast<int64_t>(blockIdx.x) * (kThreads / 64) + (threadIdx.x >> 6);
   const int unit0 = lane & (a.lanes - 1), sub = lane / a.lanes, per = 64 / a.lanes;
@@ -246,12 +247,11 @@ bool run_aligned(const void *p, int type, int64_t s0, int64_t s1) {
   return reinterpret_cast<uintptr_t>(p) % bytes == 0 && s0 % 4 == 0 && s1 % 4 == 0;
 }
 
-}  // namespace
-
-hipError_t launch_norm_rope(const qmm_head_part *parts, int n_parts, int64_t n_tokens, int64_t head_dim, float eps,
-                            const int32_t *positions, const double *freqs, int64_t n_freqs, int pairs,
-                            const int32_t *slots, int64_t n_slots, hipStream_t stream) {
-  RopeArgs a{};
+template <int F>
+hipError_t run(const qmm_head_part *parts, int n_parts, int64_t n_tokens, int64_t head_dim, float eps,
+               const int32_t *positions, const double *freqs, int64_t n_freqs, int pairs, const int32_t *slots,
+               int64_t n_slots, hipStream_t stream) {
+  RopeArgs<F> a;
   bool wide = head_dim % 4 == 0 && n_freqs % (pairs == QMM_ROPE_HALVES ? 4 : 2) == 0;
   for (int p = 0; p < n_parts; ++p)
     wide = wide && run_aligned(parts[p].X, parts[p].x_type, parts[p].x_token_stride, parts[p].x_head_stride) &&
@@ -294,9 +294,18 @@ hipError_t launch_norm_rope(const qmm_head_part *parts, int n_parts, int64_t n_t
   a.chunks = static_cast<int>((passes + a.chunk - 1) / a.chunk);
   const int64_t waves = n_tokens * a.chunks;
   const dim3 grid(static_cast<unsigned>(std::min<int64_t>((waves + kThreads / 64 - 1) / (kThreads / 64), 1 << 20)));
-  if (wide) return launch(norm_rope_kernel<4, 1>, grid, dim3(kThreads), 0, stream, a);
-  if (units <= 64) return launch(norm_rope_kernel<1, 1>, grid, dim3(kThreads), 0, stream, a);
-  return launch(norm_rope_kernel<1, 4>, grid, dim3(kThreads), 0, stream, a);
+  if (wide) return launch(norm_rope_kernel<4, 1, F>, grid, dim3(kThreads), 0, stream, a);
+  if (units <= 64) return launch(norm_rope_kernel<1, 1, F>, grid, dim3(kThreads), 0, stream, a);
+  return launch(norm_rope_kernel<1, 4, F>, grid, dim3(kThreads), 0, stream, a);
+}
+
+}  // namespace
+
+hipError_t launch_norm_rope(const qmm_head_part *parts, int n_parts, int64_t n_tokens, int64_t head_dim, float eps,
+                            const int32_t *positions, const double *freqs, int64_t n_freqs, int pairs,
+                            const int32_t *slots, int64_t n_slots, hipStream_t stream) {
+  return (n_freqs <= kFewFreqs ? run<kFewFreqs> : run<kMaxFreqs>)(parts, n_parts, n_tokens, head_dim, eps, positions,
+                                                                  freqs, n_freqs, pairs, slots, n_slots, stream);
 }
 
 }  // namespace qmm

@@ -131,7 +131,8 @@ typedef struct qmm_head_part {
  *                   -1 leaves it out). Two tokens with one slot: either's
  *                   values remain, element by element.
  * Pointers are aligned to their element type (positions, slots and weight to
- * 4). Strides are >= 0, and two different heads of Y must not share
+ * 4). Strides are >= 0 (those of axes of one element are not
+ * used), and two different heads of Y must not share
  * elements: y_row_stride >= (n_heads - 1) * y_head_stride + head_dim, or
  * y_head_stride >= (rows - 1) * y_row_stride + head_dim with rows = n_slots
  * or n_tokens (QMM_ERR_STRIDE). Y may be X itself, with equal types and
@@ -147,8 +148,9 @@ int qmm_norm_rope(const qmm_head_part *parts, int n_parts, int64_t n_tokens, int
 
 /* A tensor of heads (a host struct, read during the call): element e of head
  * h of token t (of sequence b) at data + b * seq_stride + t * token_stride +
- * h * head_stride + e. Strides are in elements, >= 0 and multiples of 8, and
- * data is 16-byte aligned. seq_stride counts only where stated. */
+ * h * head_stride + e. Strides are in elements, >= 0 and multiples of 8,
+ * token_stride at most 2^25, and data is 16-byte aligned. seq_stride counts
+ * only where stated, and the stride of an axis of one element nowhere. */
 typedef struct qmm_heads {
   void *data;
   int64_t seq_stride;
@@ -174,8 +176,9 @@ typedef struct qmm_heads {
  * are not read. O must not overlap Q, K or V, nor two of its own heads each
  * other (strides as in qmm_norm_rope).
  * Numerics: scores, the softmax's maximum and sum, and the output's sum in
- * fp32; each weight is rounded to `type` (relative to the largest so far)
- * for the matrix cores, and the output once at the end. A non-finite K or V
+ * fp32; each weight, relative to a reference within a factor 2^8 of the
+ * largest so far, is rounded to `type` for the matrix cores, and the output
+ * once at the end. A non-finite K or V
  * of a later token does not reach an earlier one. n_tokens == 0 or
  * n_seqs == 0 is a no-op. n_tokens, n_seqs < 2^31 - 128 and n_tokens *
  * n_q_heads < 2^31 - 2^20.
