@@ -59,6 +59,23 @@ def test_wide_k_split_over_rounds():
     _check(x, a, b, scales, base, ids, "lora 3000 tokens of 4128")
 
 
+@pytest.mark.parametrize("n,pattern", [(512, "one"), (511, "mixed"), (513, "mixed"), (200, "runs"), (130, "late")])
+def test_tiles_by_adapter(n, pattern):
+    """Batches around the largest one whose tiles are gathered by adapter: all tokens on one adapter, adapters
+    interleaved, in runs that cross the scan's steps of 64 tokens, or first met late in the batch."""
+    ad = 7
+    x, a, b, scales, base, ids = _inputs(8, n, 96, 40, ad, 12, "f16")
+    ids = {"one": np.full(n, 3), "mixed": ids, "runs": np.arange(n) // 45 % ad,
+           "late": np.where(np.arange(n) < n - 5, -1, np.arange(n) % ad)}[pattern]
+    _check(x, a, b, scales, base, ids, f"lora {n} tokens, {pattern}")
+
+
+def test_long_k_of_few_tokens():
+    """More k than 256 ranges of the smallest size hold."""
+    x, a, b, scales, base, ids = _inputs(9, 3, 256 * 256 + 4128, 16, 2, 3, "f32")
+    _check(x, a, b, scales, base, ids, "lora k=69664")
+
+
 def test_without_base_scales_or_adapters():
     x, a, b, scales, base, ids = _inputs(3, 20, 128, 48, 4, 8, "f32")
     _check(x, a, b, None, base, ids, "lora without scales")
