@@ -15,9 +15,11 @@
 //    the earlier tokens with its id; if their number is a multiple of 16 they
 //    take t and the next 15 tokens with that id, else they leave. No launch
 //    sorts anything, and all adapters run at once;
-//  * more tokens (prompts: the tokens of a request stand together), 16
-//    consecutive tokens. A tile that does hold several adapters takes them one
-//    after another and keeps, in each token's column, its own adapter's result.
+//  * more tokens (prompts: the tokens of a request stand together), 64
+//    consecutive tokens, so that an operand of A or B serves four products. A
+//    tile that does hold several adapters takes them one after another and
+//    keeps, in each token's column, its own adapter's result. Neighbouring
+//    tiles go to one XCD, whose L2 then holds their adapters and their V.
 // Columns do not mix, so a non-finite value of another token or adapter stays
 // out in both.
 //
@@ -34,12 +36,22 @@ namespace qmm {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kTok = 16;            // tokens per tile
+constexpr int kTok = 16;            // tokens per product
+constexpr int kSub = 4;             // products' tokens per consecutive tile
 constexpr int kGroupTokens = 512;   // largest batch in tiles by adapter
 constexpr int kGroupSlab = 64;      // k per wavefront and round, tiles by adapter
 constexpr int kMaxSplits = 256;     // ranges of k, tiles by adapter
 constexpr int kRankGroup = 64;      // ranks per workgroup of the first launch
-constexpr int kTileWaves = 2048;    // wavefronts the first launch aims at, consecutive tiles
+#ifndef TG
+#define TG 512
+#endif
+#ifndef KS
+#define KS 2
+#endif
+#ifndef UG
+#define UG 1024
+#endif
+constexpr int kTileGroups = TG;    // workgroups the first launch aims at, consecutive tiles
 
 // Tiles by adapter: the tokens of workgroup `t`'s tile, by their ids' order in
 // the batch, in slot[0 .. 15] of LDS (-1 behind the last). False if t does
@@ -74,17 +86,30 @@ __device__ __forceinline__ bool group_of(const int32_t *ids, int n_tokens, int t
   return begins != 0;
 }
 
-// The adapters of a tile's tokens, one after another: f(a, mine) with mine
-// true in the lanes whose token (lane % 16) has id a. Ids outside
-// [0, n_adapters) are left out.
-template <class F> __device__ __forceinline__ void each_adapter(int id, int n_adapters, F f) {
-  uint32_t left = static_cast<uint32_t>(__ballot(id >= 0 && id < n_adapters)) & 0xFFFFu;
-  while (left != 0) {
-    const int a = __builtin_amdgcn_readlane(id, __builtin_ctz(left));
-    const bool mine = id == a;
-    left &= ~static_cast<uint32_t>(__ballot(mine));
-    f(a, mine);
-  }
+// The adapters of a tile's tokens, one after another: f(a), the lanes whose
+// token t (of TT, in column lane % 16) has adapter a being those with
+// id[t] == a. Ids outside [0, n_adapters) are left out.
+template <int TT, class F> __device__ __forceinline__ void each_adapter(const int id[TT], int n_adapters, F f) {
+  uint32_t left[TT];
+#pragma unroll
+  for (int t = 0; t < TT; ++t)
+    left[t] = static_cast<uint32_t>(__ballot(id[t] >= 0 && id[t] < n_adapters)) & 0xFFFFu;
+#pragma unroll
+  for (int t = 0; t < TT; ++t)
+    while (left[t] != 0) {
+      const int a = __builtin_amdgcn_readlane(id[t], __builtin_ctz(left[t]));
+#pragma unroll
+      for (int u = t; u < TT; ++u) left[u] &= ~static_cast<uint32_t>(__ballot(id[u] == a));
+      f(a);
+    }
+}
+// The tile of workgroup b of `chunks` per tile: each of the 8 XCDs (workgroups
+// go round them) takes neighbouring tiles.
+__device__ __forceinline__ void xcd_tile(int b, int chunks, int tiles, int &tile, int &chunk) {
+  const int per = (tiles + 7) / 8;
+  tile = b % 8 * per + b / 8 / chunks;
+  chunk = b / 8 % chunks;
+  if (b / 8 / chunks >= per) tile = tiles;
 }
 
 struct DownArgs {
@@ -93,30 +118,33 @@ struct DownArgs {
   const int32_t *ids;
   float *v;  // [splits][n_tokens][rank]
   int64_t n_tokens, k, range;  // range: k per split
-  int n_adapters, rank;
+  int n_adapters, rank, splits;
 };
 
-// V^T = A X^T on one wavefront: 16 RT ranks of one adapter, the tokens of the
-// lanes' columns, k from begin to end (multiples of 32). The C layout gives a
+// V^T = A X^T on one wavefront: 16 RT ranks of one adapter, TT tokens in each
+// of the lanes' columns, k from begin to end (multiples of 32). The C layout gives a
 // lane four consecutive ranks of token lane % 16. Operand element j of lane
 // group g = lane / 16 is the same k for both operands; which k it is does not
 // matter to the sum, so an fp32 lane takes 4 consecutive k per load and four
 // products. Loads run kSteps operands ahead.
-template <bool XF16, int RT> struct Down {
+template <bool XF16, int RT, int TT> struct Down {
   static constexpr int kStep = XF16 ? 32 : 16;  // k per load
   static constexpr int kPer = XF16 ? 8 : 4;     // k per lane and load
-  static constexpr int kSteps = 4;
+  static constexpr int kSteps = TT > 1 ? KS : 4;
   typedef typename std::conditional<XF16, half8_t, float4_t>::type xvec;
   typedef typename std::conditional<XF16, half8_t, half4_t>::type avec;
   struct Chunk {
-    xvec x[kSteps];
+    xvec x[kSteps][TT];
     avec a[kSteps][RT];
   };
-  const typename std::conditional<XF16, _Float16, float>::type *x;  // this lane's
+  typedef typename std::conditional<XF16, _Float16, float>::type xone;
+  const xone *x[TT];  // this lane's
   const _Float16 *a[RT];
 
-  __device__ __forceinline__ Down(const DownArgs &p, int64_t token, int adapter, int rank0, int lane)
-      : x(static_cast<decltype(x)>(p.x) + token * p.k + kPer * (lane >> 4)) {
+  __device__ __forceinline__ Down(const DownArgs &p, const int64_t token[TT], int adapter, int rank0, int lane) {
+#pragma unroll
+    for (int t = 0; t < TT; ++t)
+      x[t] = static_cast<const xone *>(p.x) + token[t] * p.k + kPer * (lane >> 4);
 #pragma unroll
     for (int r = 0; r < RT; ++r) {
       const int j = rank0 + 16 * r + (lane & 15);
@@ -124,31 +152,35 @@ template <bool XF16, int RT> struct Down {
     }
   }
   __device__ __forceinline__ void load(Chunk &c, int s, int64_t k) const {
-    c.x[s] = *reinterpret_cast<const xvec *>(x + k);
+#pragma unroll
+    for (int t = 0; t < TT; ++t) c.x[s][t] = *reinterpret_cast<const xvec *>(x[t] + k);
 #pragma unroll
     for (int r = 0; r < RT; ++r) c.a[s][r] = *reinterpret_cast<const avec *>(a[r] + k);
   }
-  __device__ __forceinline__ void multiply(const Chunk &c, int s, float4_t acc[RT]) const {
+  __device__ __forceinline__ void multiply(const Chunk &c, int s, float4_t (&acc)[RT][TT]) const {
 #pragma unroll
-    for (int r = 0; r < RT; ++r) {
-      if constexpr (XF16) {
-        acc[r] = __builtin_amdgcn_mfma_f32_16x16x32_f16(c.a[s][r], c.x[s], acc[r], 0, 0, 0);
-      } else {
+    for (int r = 0; r < RT; ++r)
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-          acc[r] = __builtin_amdgcn_mfma_f32_16x16x4f32(static_cast<float>(c.a[s][r][i]), c.x[s][i], acc[r], 0, 0, 0);
+      for (int t = 0; t < TT; ++t) {
+        if constexpr (XF16) {
+          acc[r][t] = __builtin_amdgcn_mfma_f32_16x16x32_f16(c.a[s][r], c.x[s][t], acc[r][t], 0, 0, 0);
+        } else {
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            acc[r][t] =
+                __builtin_amdgcn_mfma_f32_16x16x4f32(static_cast<float>(c.a[s][r][i]), c.x[s][t][i], acc[r][t], 0, 0, 0);
+        }
       }
-    }
   }
   __device__ __forceinline__ void load(Chunk &c, int64_t k) const {
 #pragma unroll
     for (int s = 0; s < kSteps; ++s) load(c, s, k + s * kStep);
   }
-  __device__ __forceinline__ void multiply(const Chunk &c, float4_t acc[RT]) const {
+  __device__ __forceinline__ void multiply(const Chunk &c, float4_t (&acc)[RT][TT]) const {
 #pragma unroll
     for (int s = 0; s < kSteps; ++s) multiply(c, s, acc);
   }
-  __device__ __forceinline__ void operator()(int64_t begin, int64_t end, float4_t acc[RT]) const {
+  __device__ __forceinline__ void operator()(int64_t begin, int64_t end, float4_t (&acc)[RT][TT]) const {
     constexpr int kChunk = kSteps * kStep;
     Chunk c[2];
     int64_t k = begin;
@@ -188,62 +220,67 @@ __device__ __forceinline__ void store_v(float *o, int j, int rank, float4_t v) {
   }
 }
 
-// Tiles by adapter: one workgroup per (token, split, ranks); its wavefronts
-// split the k range again and add up through LDS, in order.
-template <bool XF16, int RT> __global__ __launch_bounds__(kThreads) void lora_down_group_kernel(DownArgs p) {
-  __shared__ int slot[kTok];
-  __shared__ float4_t sum[4][RT][64];
-  int id;
-  if (!group_of(p.ids, static_cast<int>(p.n_tokens), blockIdx.x, slot, id)) return;
-  if (id < 0 || id >= p.n_adapters) return;  // no product: the second launch reads no V either
+// One workgroup per (tile, split, ranks); its wavefronts split the k range
+// again and add up through LDS, in order.
+template <bool XF16, int RT, bool GROUP>
+__global__ __launch_bounds__(kThreads, GROUP || RT < 4 ? 2 : 1) void lora_down_kernel(DownArgs p) {
+  constexpr int TT = GROUP ? 1 : kSub;
+  __shared__ float4_t sum[4][RT][TT][64];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int mine = slot[lane & 15];
-  const int rank0 = blockIdx.z * kRankGroup;
-  const Down<XF16, RT> down(p, mine < 0 ? blockIdx.x : mine, __builtin_amdgcn_readfirstlane(id), rank0, lane);
-  const int64_t part = p.range / 4;
-  const int64_t begin = blockIdx.y * p.range + wave * part;
-  const int64_t end = begin + part < p.k ? begin + part : p.k;
-  float4_t acc[RT];
+  const int rank0 = blockIdx.y * kRankGroup;
+  __shared__ int slot[kTok * TT];
+  int split;
+  int id[TT];
+  int64_t token[TT];
+  if constexpr (GROUP) {
+    split = blockIdx.x / static_cast<int>(p.n_tokens);
+    const int t = blockIdx.x % static_cast<int>(p.n_tokens);
+    if (!group_of(p.ids, static_cast<int>(p.n_tokens), t, slot, id[0])) return;
+    if (id[0] < 0 || id[0] >= p.n_adapters) return;  // no product: the second launch reads no V either
+    token[0] = slot[lane & 15] < 0 ? t : slot[lane & 15];
+  } else {
+    const int tiles = static_cast<int>((p.n_tokens + kTok * TT - 1) / (kTok * TT));
+    int tile;
+    xcd_tile(blockIdx.x, p.splits, tiles, tile, split);
+    if (tile >= tiles) return;
+    const int64_t t0 = static_cast<int64_t>(tile) * (kTok * TT);
+    if (threadIdx.x < kTok * TT) {
+      const int64_t t = t0 + threadIdx.x;
+      const int a = t < p.n_tokens ? p.ids[t] : -1;
+      slot[threadIdx.x] = a >= 0 && a < p.n_adapters ? static_cast<int>(t) : -1;
+    }
 #pragma unroll
-  for (int r = 0; r < RT; ++r) acc[r] = float4_t{};
-  down(begin, end, acc);
-#pragma unroll
-  for (int r = 0; r < RT; ++r) sum[wave][r][lane] = acc[r];
-  __syncthreads();
-  for (int i = threadIdx.x; i < RT * 64; i += kThreads) {
-    const int r = i >> 6, l = i & 63, t = slot[l & 15];
-    if (t < 0) continue;
-    store_v(p.v + (blockIdx.y * p.n_tokens + t) * p.rank, rank0 + 16 * r + 4 * (l >> 4), p.rank,
-            ((sum[0][r][l] + sum[1][r][l]) + sum[2][r][l]) + sum[3][r][l]);
+    for (int t = 0; t < TT; ++t) {
+      const int64_t at = t0 + kTok * t + (lane & 15);
+      token[t] = at < p.n_tokens ? at : p.n_tokens - 1;
+      id[t] = at < p.n_tokens ? p.ids[at] : -1;
+    }
   }
-}
-
-// Consecutive tiles: one wavefront per (tile, split, ranks).
-template <bool XF16, int RT> __global__ __launch_bounds__(kThreads) void lora_down_kernel(DownArgs p) {
-  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int64_t t = (static_cast<int64_t>(blockIdx.x) * 4 + wave) * kTok + (lane & 15);
-  const int64_t token = t < p.n_tokens ? t : p.n_tokens - 1;
-  const int id = t < p.n_tokens ? p.ids[token] : -1;
-  const int rank0 = blockIdx.z * kRankGroup;
-  const int64_t begin = blockIdx.y * p.range;
-  const int64_t end = begin + p.range < p.k ? begin + p.range : p.k;
-  float4_t out[RT];
-#pragma unroll
-  for (int r = 0; r < RT; ++r) out[r] = float4_t{};
-  each_adapter(id, p.n_adapters, [&](int a, bool mine) {
-    const Down<XF16, RT> down(p, token, a, rank0, lane);
-    float4_t acc[RT];
-#pragma unroll
-    for (int r = 0; r < RT; ++r) acc[r] = float4_t{};
-    down(begin, end, acc);
+  const int64_t part = p.range / 4;
+  const int64_t begin = split * p.range + wave * part;
+  const int64_t end = begin + part < p.k ? begin + part : p.k;
+  each_adapter<TT>(id, p.n_adapters, [&](int a) {
+    const Down<XF16, RT, TT> down(p, token, a, rank0, lane);
+    float4_t acc[RT][TT];
 #pragma unroll
     for (int r = 0; r < RT; ++r)
-      if (mine) out[r] = acc[r];
-  });
-  if (t >= p.n_tokens || id < 0 || id >= p.n_adapters) return;
 #pragma unroll
-  for (int r = 0; r < RT; ++r)
-    store_v(p.v + (blockIdx.y * p.n_tokens + t) * p.rank, rank0 + 16 * r + 4 * (lane >> 4), p.rank, out[r]);
+      for (int t = 0; t < TT; ++t) acc[r][t] = float4_t{};
+    down(begin, end, acc);
+#pragma unroll
+    for (int t = 0; t < TT; ++t)
+      if (id[t] == a) {
+#pragma unroll
+        for (int r = 0; r < RT; ++r) sum[wave][r][t][lane] = acc[r][t];
+      }
+  });
+  __syncthreads();
+  for (int i = threadIdx.x; i < RT * TT * 64; i += kThreads) {
+    const int r = i / (TT * 64), t = i / 64 % TT, l = i & 63, tok = slot[kTok * t + (l & 15)];
+    if (tok < 0) continue;
+    store_v(p.v + (split * p.n_tokens + tok) * p.rank, rank0 + 16 * r + 4 * (l >> 4), p.rank,
+            ((sum[0][r][t][l] + sum[1][r][t][l]) + sum[2][r][t][l]) + sum[3][r][t][l]);
+  }
 }
 
 struct UpArgs {
@@ -254,164 +291,221 @@ struct UpArgs {
   int64_t n_tokens, n_rows;
   int n_adapters, rank, splits;
   int steps, chunks;  // steps per wavefront, workgroups per token tile
-  bool b_vec, y_vec;      // rows of B, and of base and Y, allow 8- and 16-byte accesses
 };
 
-// Four values from p[0..3], of which those before `n` exist; `vec`: all or
-// none of them, at once.
-template <class V4, class T> __device__ __forceinline__ V4 load4(const T *p, int64_t n, bool vec) {
+// Four values from p[at .. at + 3] of n. VEC: n and at are multiples of 4 and
+// p allows one access; past the end the last four are read instead, without a
+// branch, so that many loads can be on their way. Otherwise those that exist,
+// and zeros.
+template <class V4, bool VEC, class T> __device__ __forceinline__ V4 load4(const T *p, int64_t at, int64_t n) {
+  if constexpr (VEC) return *reinterpret_cast<const V4 *>(p + (at < n ? at : n - 4));
   V4 v{};
-  if (vec) {
-    if (n > 0) v = *reinterpret_cast<const V4 *>(p);
-  } else {
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-      if (i < n) v[i] = p[i];
-  }
+  for (int i = 0; i < 4; ++i)
+    if (at + i < n) v[i] = p[at + i];
   return v;
 }
 
-// Y^T = B V^T: a lane holds four consecutive rows of token lane % 16; RQ: 16s
-// of the rank. The workgroup adds up its tokens' V once; then each wavefront
-// goes over its rows in steps of 16 RS, the next step's base and B on their
-// way.
-template <int RQ, bool GROUP, int RS> __global__ __launch_bounds__(kThreads) void lora_up_kernel(UpArgs p) {
+// Adds up the partial sums of V, in order, into those of the first split:
+// before the second launch on consecutive tiles, whose workgroups on one tile
+// would each read all of them again.
+__global__ __launch_bounds__(kThreads) void lora_sum_kernel(float *v, int64_t n, int splits) {
+  const int64_t stride = static_cast<int64_t>(gridDim.x) * kThreads;
+  for (int64_t i = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x; i < n; i += stride) {
+    float sum = 0.f;
+    for (int s = 0; s < splits; s += 8) {
+      float part[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) part[e] = s + e < splits ? v[(s + e) * n + i] : 0.f;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) sum += part[e];
+    }
+    v[i] = sum;
+  }
+}
+
+// Y^T = B V^T: a lane holds four consecutive rows of its tokens (columns
+// lane % 16). RQ: 16s of the rank; RS: 16s of the rows of a step, which are
+// consecutive in each token's row. The workgroup adds up its tokens' V once;
+// then each wavefront goes over its rows, the next step's base and B on their
+// way. VEC: the rows of B and V allow 8- and 16-byte accesses, those of base
+// and Y 16-byte ones.
+template <int RQ, bool GROUP, int RS, bool VEC>
+__global__ __launch_bounds__(kThreads, RQ <= 4 ? 2 : 1) void lora_up_kernel(UpArgs p) {
+  constexpr int TT = GROUP ? 1 : kSub;
   constexpr int kRow = 16 * RQ + 4;  // floats; padded so that 16 rows start on different banks
-  __shared__ __align__(16) float vs[kTok * kRow];
-  __shared__ int slot[kTok];
+  __shared__ __align__(16) float vs[kTok * TT * kRow];
+  __shared__ int slot[kTok * TT];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int col = lane & 15, grp = lane >> 4;
-  const int tile = blockIdx.x / p.chunks, chunk = blockIdx.x % p.chunks;
+  int chunk;
   if constexpr (GROUP) {
+    chunk = blockIdx.x % p.chunks;
     int id;
-    if (!group_of(p.ids, static_cast<int>(p.n_tokens), tile, slot, id)) return;
+    if (!group_of(p.ids, static_cast<int>(p.n_tokens), blockIdx.x / p.chunks, slot, id)) return;
   } else {
-    if (threadIdx.x < kTok) {
-      const int64_t t = static_cast<int64_t>(tile) * kTok + threadIdx.x;
+    const int tiles = static_cast<int>((p.n_tokens + kTok * TT - 1) / (kTok * TT));
+    int tile;
+    xcd_tile(blockIdx.x, p.chunks, tiles, tile, chunk);
+    if (tile >= tiles) return;
+    if (threadIdx.x < kTok * TT) {
+      const int64_t t = static_cast<int64_t>(tile) * (kTok * TT) + threadIdx.x;
       slot[threadIdx.x] = t < p.n_tokens ? static_cast<int>(t) : -1;
     }
     __syncthreads();
   }
   // V of the tile, scaled: thread (token, four ranks)
-  for (int i = threadIdx.x; i < kTok * 4 * RQ; i += kThreads) {
+  for (int i = threadIdx.x; i < kTok * TT * 4 * RQ; i += kThreads) {
     const int c = i / (4 * RQ), j = 4 * (i % (4 * RQ)), t = slot[c];
     const int id = t < 0 ? -1 : p.ids[t];
     float4_t v{};
     if (id >= 0 && id < p.n_adapters) {
-      const float *src = p.v + static_cast<int64_t>(t) * p.rank + j;
+      const float *src = p.v + static_cast<int64_t>(t) * p.rank;
       const int64_t step = p.n_tokens * p.rank;
       for (int s = 0; s < p.splits; s += 8) {  // eight loads on their way at once
         float4_t part[8];
 #pragma unroll
         for (int e = 0; e < 8; ++e)
-          part[e] = load4<float4_t>(src + (s + e) * step, s + e < p.splits ? p.rank - j : 0, p.rank % 4 == 0);
+          part[e] = load4<float4_t, VEC>(src + (s + e < p.splits ? s + e : p.splits - 1) * step, j, p.rank);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) v += part[e];
+        for (int e = 0; e < 8; ++e) v += s + e < p.splits ? part[e] : float4_t{};
       }
       v *= p.scales ? p.scales[id] : 1.f;
+      if (j >= p.rank) v = float4_t{};
     }
     *reinterpret_cast<float4_t *>(vs + c * kRow + j) = v;
   }
   __syncthreads();
 
-  const bool live = slot[col] >= 0;
-  const int64_t token = live ? slot[col] : slot[0];
-  const int id = live ? p.ids[token] : -1;
-  const bool valid = id >= 0 && id < p.n_adapters;
-  float4_t v[RQ];
+  int id[TT];
+  bool live[TT], valid[TT];
+  const float *base[TT];  // the lanes' token rows
+  float *out[TT];
+  constexpr bool kHold = RQ <= 4;  // V's operands fit the registers
+  float4_t held[kHold ? TT : 1][kHold ? RQ : 1];
+  int first_id = -1;  // the first valid id, -1 if there is none
+  bool one_adapter = true;
 #pragma unroll
-  for (int q = 0; q < RQ; ++q) v[q] = *reinterpret_cast<const float4_t *>(vs + col * kRow + 16 * q + 4 * grp);
-
-  const uint32_t with = static_cast<uint32_t>(__ballot(valid)) & 0xFFFFu;  // columns with an adapter
-  const int first_id = with ? __builtin_amdgcn_readlane(id, __builtin_ctz(with)) : 0;
-  const bool one_adapter = __all(!valid || id == first_id);
-  // a step: RS tiles of 16 rows, 16 RS consecutive values of each token's row
+  for (int t = 0; t < TT; ++t) {
+    const int s = slot[kTok * t + col];
+    live[t] = s >= 0;
+    const int64_t token = live[t] ? s : slot[0];
+    id[t] = live[t] ? p.ids[token] : -1;
+    valid[t] = id[t] >= 0 && id[t] < p.n_adapters;
+    base[t] = p.base ? p.base + token * p.n_rows : nullptr;
+    out[t] = p.y + token * p.n_rows;
+    const uint32_t with = static_cast<uint32_t>(__ballot(valid[t])) & 0xFFFFu;
+    if (first_id < 0 && with) first_id = __builtin_amdgcn_readlane(id[t], __builtin_ctz(with));
+    one_adapter = one_adapter && __all(!valid[t] || id[t] == first_id);
+    if constexpr (kHold) {
+#pragma unroll
+      for (int q = 0; q < RQ; ++q)
+        held[t][q] = *reinterpret_cast<const float4_t *>(vs + (kTok * t + col) * kRow + 16 * q + 4 * grp);
+    }
+  }
   struct Step {
-    float4_t y[RS];
+    float4_t y[RS][TT];
     half4_t b[RS][RQ];
   };
-  const int64_t row_base = (static_cast<int64_t>(chunk) * 4 + wave) * p.steps * (16 * RS);
-  auto load_b = [&](Step &t, int64_t row0, int a) {
+  auto load_b = [&](Step &s, int64_t row0, int a) {
 #pragma unroll
     for (int i = 0; i < RS; ++i) {
       const int64_t r = row0 + 16 * i + col;
-      const _Float16 *b = p.b + (a * p.n_rows + (r < p.n_rows ? r : p.n_rows - 1)) * p.rank + 4 * grp;
+      const _Float16 *b = p.b + (a * p.n_rows + (r < p.n_rows ? r : p.n_rows - 1)) * p.rank;
 #pragma unroll
-      for (int q = 0; q < RQ; ++q) t.b[i][q] = load4<half4_t>(b + 16 * q, p.rank - 16 * q - 4 * grp, p.b_vec);
+      for (int q = 0; q < RQ; ++q) s.b[i][q] = load4<half4_t, VEC>(b, 16 * q + 4 * grp, p.rank);
     }
   };
-  auto load = [&](Step &t, int64_t row0) {
+  auto load = [&](Step &s, int64_t row0) {
+    if (p.base) {
 #pragma unroll
-    for (int i = 0; i < RS; ++i) {
-      const int64_t r4 = row0 + 16 * i + 4 * grp;
-      t.y[i] = load4<float4_t>(p.base + token * p.n_rows + r4, p.base && live ? p.n_rows - r4 : 0, p.y_vec);
+      for (int i = 0; i < RS; ++i)
+#pragma unroll
+        for (int t = 0; t < TT; ++t) s.y[i][t] = load4<float4_t, VEC>(base[t], row0 + 16 * i + 4 * grp, p.n_rows);
+    } else {
+#pragma unroll
+      for (int i = 0; i < RS; ++i)
+#pragma unroll
+        for (int t = 0; t < TT; ++t) s.y[i][t] = float4_t{};
     }
-    if (with && one_adapter) load_b(t, row0, first_id);
+    if (first_id >= 0 && one_adapter) load_b(s, row0, first_id);
   };
-  auto add_product = [&](Step &t, bool mine) {
+  auto add_product = [&](Step &s, int a) {
 #pragma unroll
-    for (int i = 0; i < RS; ++i) {
-      float4_t acc{};
+    for (int i = 0; i < RS; ++i)
 #pragma unroll
-      for (int q = 0; q < RQ; ++q)
+      for (int t = 0; t < TT; ++t) {
+        float4_t acc{};
 #pragma unroll
-        for (int e = 0; e < 4; ++e)
-          acc = __builtin_amdgcn_mfma_f32_16x16x4f32(static_cast<float>(t.b[i][q][e]), v[q][e], acc, 0, 0, 0);
-      if (mine) t.y[i] += acc;
-    }
+        for (int q = 0; q < RQ; ++q) {
+          float4_t v;
+          if constexpr (kHold)
+            v = held[t][q];
+          else
+            v = *reinterpret_cast<const float4_t *>(vs + (kTok * t + col) * kRow + 16 * q + 4 * grp);
+          // ranks past the last meet a zero of V, and are made zeros here too (a repeated value may be infinite)
+          const half4_t w = 16 * q + 4 * grp < p.rank ? s.b[i][q] : half4_t{};
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            acc = __builtin_amdgcn_mfma_f32_16x16x4f32(static_cast<float>(w[e]), v[e], acc, 0, 0, 0);
+        }
+        if (id[t] == a) s.y[i][t] += acc;
+      }
   };
-  auto finish = [&](Step &t, int64_t row0) {
-    if (with && one_adapter)
-      add_product(t, valid);
-    else if (with)
-      each_adapter(id, p.n_adapters, [&](int a, bool mine) {
-        load_b(t, row0, a);
-        add_product(t, mine);
+  auto finish = [&](Step &s, int64_t row0) {
+    if (first_id >= 0 && one_adapter)
+      add_product(s, first_id);
+    else if (first_id >= 0)
+      each_adapter<TT>(id, p.n_adapters, [&](int a) {
+        load_b(s, row0, a);
+        add_product(s, a);
       });
 #pragma unroll
-    for (int i = 0; i < RS; ++i) {
-      if (id != -1 && !valid) {
-        const float nan = __builtin_bit_cast(float, 0x7FC00000u);
-        t.y[i] = float4_t{nan, nan, nan, nan};
-      }
-      const int64_t r4 = row0 + 16 * i + 4 * grp, left = live ? p.n_rows - r4 : 0;
-      float *o = p.y + token * p.n_rows + r4;
-      if (p.y_vec) {
-        if (left > 0) *reinterpret_cast<float4_t *>(o) = t.y[i];
-      } else {
+    for (int i = 0; i < RS; ++i)
 #pragma unroll
-        for (int e = 0; e < 4; ++e)
-          if (e < left) o[e] = t.y[i][e];
+      for (int t = 0; t < TT; ++t) {
+        if (id[t] != -1 && !valid[t]) {
+          const float nan = __builtin_bit_cast(float, 0x7FC00000u);
+          s.y[i][t] = float4_t{nan, nan, nan, nan};
+        }
+        const int64_t r4 = row0 + 16 * i + 4 * grp;
+        if constexpr (VEC) {
+          if (live[t] && r4 < p.n_rows) *reinterpret_cast<float4_t *>(out[t] + r4) = s.y[i][t];
+        } else {
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            if (live[t] && r4 + e < p.n_rows) out[t][r4 + e] = s.y[i][t][e];
+        }
       }
-    }
   };
+  const int64_t row_base = (static_cast<int64_t>(chunk) * 4 + wave) * p.steps * (16 * RS);
   const int64_t row_end = row_base + p.steps * (16 * RS) < p.n_rows ? row_base + p.steps * (16 * RS) : p.n_rows;
   if (row_base >= row_end) return;
-  Step t[2];
+  Step s[2];
   int64_t row = row_base;
-  load(t[0], row);
+  load(s[0], row);
   for (; row + 32 * RS < row_end; row += 32 * RS) {
-    load(t[1], row + 16 * RS);
-    finish(t[0], row);
-    load(t[0], row + 32 * RS);
-    finish(t[1], row + 16 * RS);
+    load(s[1], row + 16 * RS);
+    finish(s[0], row);
+    load(s[0], row + 32 * RS);
+    finish(s[1], row + 16 * RS);
   }
   if (row + 16 * RS < row_end) {
-    load(t[1], row + 16 * RS);
-    finish(t[0], row);
-    finish(t[1], row + 16 * RS);
+    load(s[1], row + 16 * RS);
+    finish(s[0], row);
+    finish(s[1], row + 16 * RS);
   } else {
-    finish(t[0], row);
+    finish(s[0], row);
   }
 }
 
 bool by_adapter(int64_t n_tokens) { return n_tokens <= kGroupTokens; }
-// k per split: a multiple of 128 (4 wavefronts of 32) by adapter, of 32 else.
+// k per split: a multiple of 128, 32 for each of a workgroup's wavefronts.
 int64_t split_range(int64_t n_tokens, int64_t k) {
-  if (by_adapter(n_tokens)) return std::max<int64_t>(4 * kGroupSlab, (k + 128 * kMaxSplits - 1) / (128 * kMaxSplits) * 128);
-  const int64_t waves = (n_tokens + kTok - 1) / kTok;
-  const int64_t want = std::min(std::max<int64_t>(1, kTileWaves / waves), std::max<int64_t>(1, k / 256));
-  return (k + 32 * want - 1) / (32 * want) * 32;
+  const int64_t tiles = (n_tokens + kTok * kSub - 1) / (kTok * kSub);
+  const int64_t want = by_adapter(n_tokens) ? std::min<int64_t>(kMaxSplits, std::max<int64_t>(1, k / (4 * kGroupSlab)))
+                                            : std::max<int64_t>(1, std::min(kTileGroups / tiles, k / 256));
+  return (k + 128 * want - 1) / (128 * want) * 128;
 }
 
 }  // namespace
@@ -426,16 +520,18 @@ hipError_t launch_lora(const void *X, bool x_f16, int64_t n_tokens, int64_t k, c
                        const float *base, float *Y, float *partial, hipStream_t stream) {
   const bool group = by_adapter(n_tokens);
   const int splits = lora_splits(n_tokens, k, rank);
-  const int64_t tiles = group ? n_tokens : (n_tokens + kTok - 1) / kTok;
+  // workgroups per split or chunk: every token's (most leave at once), or
+  // those of 8 equal ranges of tiles
+  const int64_t tiles = (n_tokens + kTok * kSub - 1) / (kTok * kSub);
+  const int64_t groups = group ? n_tokens : (tiles + 7) / 8 * 8;
   const DownArgs d{X, static_cast<const _Float16 *>(A), ids, partial, n_tokens, k, split_range(n_tokens, k),
-                   static_cast<int>(n_adapters), static_cast<int>(rank)};
-  const dim3 grid(static_cast<unsigned>(group ? tiles : (tiles + 3) / 4), splits,
-                  static_cast<unsigned>((rank + kRankGroup - 1) / kRankGroup));
+                   static_cast<int>(n_adapters), static_cast<int>(rank), splits};
+  const dim3 grid(static_cast<unsigned>(groups * splits), static_cast<unsigned>((rank + kRankGroup - 1) / kRankGroup));
   auto down = [&](auto xf16, auto rt) {
     constexpr bool X16 = decltype(xf16)::value;
     constexpr int RT = decltype(rt)::value;
-    return launch(group ? lora_down_group_kernel<X16, RT> : lora_down_kernel<X16, RT>, grid, dim3(kThreads), 0, stream,
-                  d);
+    return launch(group ? lora_down_kernel<X16, RT, true> : lora_down_kernel<X16, RT, false>, grid, dim3(kThreads), 0,
+                  stream, d);
   };
   auto by_rank = [&](auto xf16) {
     if (rank <= 16) return down(xf16, std::integral_constant<int, 1>{});
@@ -445,30 +541,41 @@ hipError_t launch_lora(const void *X, bool x_f16, int64_t n_tokens, int64_t k, c
   const hipError_t e = x_f16 ? by_rank(std::true_type{}) : by_rank(std::false_type{});
   if (e != hipSuccess) return e;
 
-  // Steps of 64 rows per wavefront (256 bytes of a token's row), of 16 where
-  // there are few; several steps where there are workgroups enough, since
-  // each workgroup first adds up its tokens' V.
-  const int64_t rs = rank > 64 || n_rows * tiles < 4096 * 64 ? 1 : 4;
+  if (!group && splits > 1) {
+    const int64_t n = n_tokens * rank;
+    const hipError_t f = launch(lora_sum_kernel, dim3(static_cast<unsigned>(std::min<int64_t>((n + kThreads - 1) / kThreads, 4096))),
+                                dim3(kThreads), 0, stream, partial, n, splits);
+    if (f != hipSuccess) return f;
+  }
+
+  // Steps of 64 rows by adapter (256 bytes of a token's row), of 16 where
+  // there are few or for consecutive tiles, whose step has 64 tokens; several
+  // steps where there are workgroups enough, since each workgroup first adds
+  // up its tokens' V.
+  const bool vec = rank % 4 == 0 && reinterpret_cast<uintptr_t>(B) % 8 == 0 && n_rows % 4 == 0 &&
+                   reinterpret_cast<uintptr_t>(Y) % 16 == 0 && reinterpret_cast<uintptr_t>(base) % 16 == 0;
+  const int64_t rs = !group || !vec || rank > 64 || n_rows * groups < 4096 * 64 ? 1 : 4;
   const int64_t all = (n_rows + 64 * rs - 1) / (64 * rs);  // steps of a workgroup's four wavefronts
-  const int64_t steps = std::max({int64_t{1}, std::min<int64_t>(16 / rs, all * tiles / 1024), (all * tiles) >> 23});
+  const int64_t steps = std::max({int64_t{1}, std::min<int64_t>(16 / rs, all * groups / UG), (all * groups) >> 23});
   const int64_t chunks = (all + steps - 1) / steps;
   const UpArgs u{static_cast<const _Float16 *>(B), partial, scales, base, ids, Y, n_tokens, n_rows,
-                 static_cast<int>(n_adapters), static_cast<int>(rank), splits, static_cast<int>(steps),
-                 static_cast<int>(chunks), rank % 4 == 0 && reinterpret_cast<uintptr_t>(B) % 8 == 0,
-                 n_rows % 4 == 0 && reinterpret_cast<uintptr_t>(Y) % 16 == 0 && reinterpret_cast<uintptr_t>(base) % 16 == 0};
-  const dim3 ugrid(static_cast<unsigned>(chunks * tiles));
-  auto up = [&](auto rq, auto r) {
-    constexpr int RQ = decltype(rq)::value, RS = decltype(r)::value;
-    return launch(group ? lora_up_kernel<RQ, true, RS> : lora_up_kernel<RQ, false, RS>, ugrid, dim3(kThreads), 0,
-                  stream, u);
+                 static_cast<int>(n_adapters), static_cast<int>(rank), group ? splits : 1, static_cast<int>(steps),
+                 static_cast<int>(chunks)};
+  const dim3 ugrid(static_cast<unsigned>(chunks * groups));
+  auto up = [&](auto rq) {
+    constexpr int RQ = decltype(rq)::value;
+    constexpr int RS = RQ <= 4 ? 4 : 1;
+    if (rs > 1) return launch(lora_up_kernel<RQ, true, RS, true>, ugrid, dim3(kThreads), 0, stream, u);
+    if (vec)
+      return launch(group ? lora_up_kernel<RQ, true, 1, true> : lora_up_kernel<RQ, false, 1, true>, ugrid,
+                    dim3(kThreads), 0, stream, u);
+    return launch(group ? lora_up_kernel<RQ, true, 1, false> : lora_up_kernel<RQ, false, 1, false>, ugrid,
+                  dim3(kThreads), 0, stream, u);
   };
-  auto by_rows = [&](auto rq) {
-    return rs == 4 ? up(rq, std::integral_constant<int, 4>{}) : up(rq, std::integral_constant<int, 1>{});
-  };
-  if (rank <= 16) return by_rows(std::integral_constant<int, 1>{});
-  if (rank <= 32) return by_rows(std::integral_constant<int, 2>{});
-  if (rank <= 64) return by_rows(std::integral_constant<int, 4>{});
-  return up(std::integral_constant<int, 16>{}, std::integral_constant<int, 1>{});
+  if (rank <= 16) return up(std::integral_constant<int, 1>{});
+  if (rank <= 32) return up(std::integral_constant<int, 2>{});
+  if (rank <= 64) return up(std::integral_constant<int, 4>{});
+  return up(std::integral_constant<int, 16>{});
 }
 
 }  // namespace qmm
