@@ -335,7 +335,7 @@ __global__ __launch_bounds__(kThreads, RQ <= 4 ? 2 : 1) void lora_up_kernel(UpAr
   constexpr int TT = GROUP ? 1 : kSub;
   constexpr int kRow = 16 * RQ + 4;  // floats; padded so that 16 rows start on different banks
   __shared__ __align__(16) float vs[kTok * TT * kRow];
-  __shared__ int slot[kTok * TT];
+  __shared__ int slot[kTok * TT], adapter[kTok * TT];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int col = lane & 15, grp = lane >> 4;
   int chunk;
@@ -343,6 +343,7 @@ __global__ __launch_bounds__(kThreads, RQ <= 4 ? 2 : 1) void lora_up_kernel(UpAr
     chunk = blockIdx.x % p.chunks;
     int id;
     if (!group_of(p.ids, static_cast<int>(p.n_tokens), blockIdx.x / p.chunks, slot, id)) return;
+    if (threadIdx.x < kTok) adapter[threadIdx.x] = slot[threadIdx.x] >= 0 ? id : -1;
   } else {
     const int tiles = static_cast<int>((p.n_tokens + kTok * TT - 1) / (kTok * TT));
     int tile;
@@ -351,38 +352,14 @@ __global__ __launch_bounds__(kThreads, RQ <= 4 ? 2 : 1) void lora_up_kernel(UpAr
     if (threadIdx.x < kTok * TT) {
       const int64_t t = static_cast<int64_t>(tile) * (kTok * TT) + threadIdx.x;
       slot[threadIdx.x] = t < p.n_tokens ? static_cast<int>(t) : -1;
+      adapter[threadIdx.x] = t < p.n_tokens ? p.ids[t] : -1;
     }
-    __syncthreads();
-  }
-  // V of the tile, scaled: thread (token, four ranks)
-  for (int i = threadIdx.x; i < kTok * TT * 4 * RQ; i += kThreads) {
-    const int c = i / (4 * RQ), j = 4 * (i % (4 * RQ)), t = slot[c];
-    const int id = t < 0 ? -1 : p.ids[t];
-    float4_t v{};
-    if (id >= 0 && id < p.n_adapters) {
-      const float *src = p.v + static_cast<int64_t>(t) * p.rank;
-      const int64_t step = p.n_tokens * p.rank;
-      for (int s = 0; s < p.splits; s += 8) {  // eight loads on their way at once
-        float4_t part[8];
-#pragma unroll
-        for (int e = 0; e < 8; ++e)
-          part[e] = load4<float4_t, VEC>(src + (s + e < p.splits ? s + e : p.splits - 1) * step, j, p.rank);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) v += s + e < p.splits ? part[e] : float4_t{};
-      }
-      v *= p.scales ? p.scales[id] : 1.f;
-      if (j >= p.rank) v = float4_t{};
-    }
-    *reinterpret_cast<float4_t *>(vs + c * kRow + j) = v;
   }
   __syncthreads();
-
   int id[TT];
   bool live[TT], valid[TT];
   const float *base[TT];  // the lanes' token rows
   float *out[TT];
-  constexpr bool kHold = RQ <= 4;  // V's operands fit the registers
-  float4_t held[kHold ? TT : 1][kHold ? RQ : 1];
   int first_id = -1;  // the first valid id, -1 if there is none
   bool one_adapter = true;
 #pragma unroll
@@ -390,18 +367,13 @@ __global__ __launch_bounds__(kThreads, RQ <= 4 ? 2 : 1) void lora_up_kernel(UpAr
     const int s = slot[kTok * t + col];
     live[t] = s >= 0;
     const int64_t token = live[t] ? s : slot[0];
-    id[t] = live[t] ? p.ids[token] : -1;
+    id[t] = adapter[kTok * t + col];
     valid[t] = id[t] >= 0 && id[t] < p.n_adapters;
     base[t] = p.base ? p.base + token * p.n_rows : nullptr;
     out[t] = p.y + token * p.n_rows;
     const uint32_t with = static_cast<uint32_t>(__ballot(valid[t])) & 0xFFFFu;
     if (first_id < 0 && with) first_id = __builtin_amdgcn_readlane(id[t], __builtin_ctz(with));
     one_adapter = one_adapter && __all(!valid[t] || id[t] == first_id);
-    if constexpr (kHold) {
-#pragma unroll
-      for (int q = 0; q < RQ; ++q)
-        held[t][q] = *reinterpret_cast<const float4_t *>(vs + (kTok * t + col) * kRow + 16 * q + 4 * grp);
-    }
   }
   struct Step {
     float4_t y[RS][TT];
@@ -430,6 +402,59 @@ __global__ __launch_bounds__(kThreads, RQ <= 4 ? 2 : 1) void lora_up_kernel(UpAr
     }
     if (first_id >= 0 && one_adapter) load_b(s, row0, first_id);
   };
+  const int64_t row_base = (static_cast<int64_t>(chunk) * 4 + wave) * p.steps * (16 * RS);
+  const int64_t row_end = row_base + p.steps * (16 * RS) < p.n_rows ? row_base + p.steps * (16 * RS) : p.n_rows;
+  Step s[2];
+  int64_t row = row_base;
+  if (row < row_end) load(s[0], row);
+
+  // V of the tile, scaled: thread (token, four ranks), all loads on their way
+  // at once (what the workspace holds for a token without an adapter is read
+  // too, and dropped)
+  constexpr int kItems = kTok * TT * 4 * RQ, kEach = (kItems + kThreads - 1) / kThreads;
+  constexpr int kParts = GROUP ? 8 : 1;  // partial sums per round
+  float4_t sum[kEach];
+#pragma unroll
+  for (int e = 0; e < kEach; ++e) sum[e] = float4_t{};
+  const int64_t v_step = p.n_tokens * p.rank;
+  for (int part = 0; part < p.splits; part += kParts) {
+    float4_t add[kEach][kParts];
+#pragma unroll
+    for (int e = 0; e < kEach; ++e) {
+      const int i = threadIdx.x + e * kThreads < kItems ? threadIdx.x + e * kThreads : 0;
+      const int t = slot[i / (4 * RQ)] < 0 ? slot[0] : slot[i / (4 * RQ)];
+#pragma unroll
+      for (int u = 0; u < kParts; ++u)
+        add[e][u] = load4<float4_t, VEC>(
+            p.v + (part + u < p.splits ? part + u : p.splits - 1) * v_step + static_cast<int64_t>(t) * p.rank,
+            4 * (i % (4 * RQ)), p.rank);
+    }
+#pragma unroll
+    for (int e = 0; e < kEach; ++e)
+#pragma unroll
+      for (int u = 0; u < kParts; ++u) sum[e] += part + u < p.splits ? add[e][u] : float4_t{};
+  }
+#pragma unroll
+  for (int e = 0; e < kEach; ++e) {
+    const int i = threadIdx.x + e * kThreads, c = i / (4 * RQ), j = 4 * (i % (4 * RQ));
+    if (i < kItems) {
+      const int a = adapter[c];
+      const bool with = a >= 0 && a < p.n_adapters && j < p.rank;
+      const float scale = with && p.scales ? p.scales[a] : 1.f;
+      *reinterpret_cast<float4_t *>(vs + c * kRow + j) = with ? sum[e] * scale : float4_t{};
+    }
+  }
+  __syncthreads();
+  if (row >= row_end) return;
+  constexpr bool kHold = RQ <= 4;  // V's operands fit the registers
+  float4_t held[kHold ? TT : 1][kHold ? RQ : 1];
+  if constexpr (kHold) {
+#pragma unroll
+    for (int t = 0; t < TT; ++t)
+#pragma unroll
+      for (int q = 0; q < RQ; ++q)
+        held[t][q] = *reinterpret_cast<const float4_t *>(vs + (kTok * t + col) * kRow + 16 * q + 4 * grp);
+  }
   auto add_product = [&](Step &s, int a) {
 #pragma unroll
     for (int i = 0; i < RS; ++i)
@@ -478,12 +503,6 @@ __global__ __launch_bounds__(kThreads, RQ <= 4 ? 2 : 1) void lora_up_kernel(UpAr
         }
       }
   };
-  const int64_t row_base = (static_cast<int64_t>(chunk) * 4 + wave) * p.steps * (16 * RS);
-  const int64_t row_end = row_base + p.steps * (16 * RS) < p.n_rows ? row_base + p.steps * (16 * RS) : p.n_rows;
-  if (row_base >= row_end) return;
-  Step s[2];
-  int64_t row = row_base;
-  load(s[0], row);
   for (; row + 32 * RS < row_end; row += 32 * RS) {
     load(s[1], row + 16 * RS);
     finish(s[0], row);
