@@ -42,16 +42,7 @@ constexpr int kGroupTokens = 512;   // largest batch in tiles by adapter
 constexpr int kGroupSlab = 64;      // k per wavefront and round, tiles by adapter
 constexpr int kMaxSplits = 256;     // ranges of k, tiles by adapter
 constexpr int kRankGroup = 64;      // ranks per workgroup of the first launch
-#ifndef TG
-#define TG 512
-#endif
-#ifndef KS
-#define KS 2
-#endif
-#ifndef UG
-#define UG 1024
-#endif
-constexpr int kTileGroups = TG;    // workgroups the first launch aims at, consecutive tiles
+constexpr int kTileGroups = 512;    // workgroups the first launch aims at, consecutive tiles
 
 // Tiles by adapter: the tokens of workgroup `t`'s tile, by their ids' order in
 // the batch, in slot[0 .. 15] of LDS (-1 behind the last). False if t does
@@ -94,14 +85,16 @@ template <int TT, class F> __device__ __forceinline__ void each_adapter(const in
 #pragma unroll
   for (int t = 0; t < TT; ++t)
     left[t] = static_cast<uint32_t>(__ballot(id[t] >= 0 && id[t] < n_adapters)) & 0xFFFFu;
+  for (;;) {
+    int a = -1;
 #pragma unroll
-  for (int t = 0; t < TT; ++t)
-    while (left[t] != 0) {
-      const int a = __builtin_amdgcn_readlane(id[t], __builtin_ctz(left[t]));
+    for (int t = 0; t < TT; ++t)
+      if (a < 0 && left[t] != 0) a = __builtin_amdgcn_readlane(id[t], __builtin_ctz(left[t]));
+    if (a < 0) return;
 #pragma unroll
-      for (int u = t; u < TT; ++u) left[u] &= ~static_cast<uint32_t>(__ballot(id[u] == a));
-      f(a);
-    }
+    for (int t = 0; t < TT; ++t) left[t] &= ~static_cast<uint32_t>(__ballot(id[t] == a));
+    f(a);
+  }
 }
 // The tile of workgroup b of `chunks` per tile: each of the 8 XCDs (workgroups
 // go round them) takes neighbouring tiles.
@@ -130,7 +123,7 @@ struct DownArgs {
 template <bool XF16, int RT, int TT> struct Down {
   static constexpr int kStep = XF16 ? 32 : 16;  // k per load
   static constexpr int kPer = XF16 ? 8 : 4;     // k per lane and load
-  static constexpr int kSteps = TT > 1 ? KS : 4;
+  static constexpr int kSteps = TT > 1 ? 2 : 4;
   typedef typename std::conditional<XF16, half8_t, float4_t>::type xvec;
   typedef typename std::conditional<XF16, half8_t, half4_t>::type avec;
   struct Chunk {
@@ -175,10 +168,12 @@ template <bool XF16, int RT, int TT> struct Down {
   __device__ __forceinline__ void load(Chunk &c, int64_t k) const {
 #pragma unroll
     for (int s = 0; s < kSteps; ++s) load(c, s, k + s * kStep);
+    __builtin_amdgcn_sched_barrier(0);  // the loads go out before the products of the other buffer
   }
   __device__ __forceinline__ void multiply(const Chunk &c, float4_t (&acc)[RT][TT]) const {
 #pragma unroll
     for (int s = 0; s < kSteps; ++s) multiply(c, s, acc);
+    __builtin_amdgcn_sched_barrier(0);
   }
   __device__ __forceinline__ void operator()(int64_t begin, int64_t end, float4_t (&acc)[RT][TT]) const {
     constexpr int kChunk = kSteps * kStep;
@@ -401,6 +396,7 @@ __global__ __launch_bounds__(kThreads, RQ <= 4 ? 2 : 1) void lora_up_kernel(UpAr
         for (int t = 0; t < TT; ++t) s.y[i][t] = float4_t{};
     }
     if (first_id >= 0 && one_adapter) load_b(s, row0, first_id);
+    __builtin_amdgcn_sched_barrier(0);
   };
   const int64_t row_base = (static_cast<int64_t>(chunk) * 4 + wave) * p.steps * (16 * RS);
   const int64_t row_end = row_base + p.steps * (16 * RS) < p.n_rows ? row_base + p.steps * (16 * RS) : p.n_rows;
@@ -575,7 +571,7 @@ hipError_t launch_lora(const void *X, bool x_f16, int64_t n_tokens, int64_t k, c
                    reinterpret_cast<uintptr_t>(Y) % 16 == 0 && reinterpret_cast<uintptr_t>(base) % 16 == 0;
   const int64_t rs = !group || !vec || rank > 64 || n_rows * groups < 4096 * 64 ? 1 : 4;
   const int64_t all = (n_rows + 64 * rs - 1) / (64 * rs);  // steps of a workgroup's four wavefronts
-  const int64_t steps = std::max({int64_t{1}, std::min<int64_t>(16 / rs, all * groups / UG), (all * groups) >> 23});
+  const int64_t steps = std::max({int64_t{1}, std::min<int64_t>(16 / rs, all * groups / 1024), (all * groups) >> 23});
   const int64_t chunks = (all + steps - 1) / steps;
   const UpArgs u{static_cast<const _Float16 *>(B), partial, scales, base, ids, Y, n_tokens, n_rows,
                  static_cast<int>(n_adapters), static_cast<int>(rank), group ? splits : 1, static_cast<int>(steps),
