@@ -334,8 +334,8 @@ __device__ __forceinline__ void attend(uint32_t kt, uint32_t vt, const typename 
 // takes keys below lim.
 //
 // A masked key's weight is zero, but zero times a non-finite value is a NaN.
-// With CAUSAL, the values of the blocks from first_masked on (at most `full`
-// of any wavefront) are therefore looked over, and true is returned where the
+// With CAUSAL, the values of the blocks from first_masked on (at most any
+// wavefront's `full`, and the same for all) are therefore looked over, and true is returned where the
 // wavefront's masked blocks held an infinity or a NaN: its rows have to be
 // computed another way then. Without CAUSAL all rows share one end, behind
 // which copied rows only repeat the last.

@@ -135,9 +135,12 @@ __global__ __launch_bounds__(kThreads, 2) void attn_prompt_kernel(PromptArgs a) 
   st.clear();
   const int mine = wave_last / kKeys + 1;
   const int full = min((wave_first + 1) / kKeys, mine - 1);
-  const int first_masked = (tile * kRows / a.group + 1) / kKeys;  // of the whole tile
-  const bool any_bad = attend_blocks<E, D, true>(lds, copy_k, copy_v, n_keys, min(first_masked, full), full, mine,
-                                                 token + 1, q, st, a.c, wave, lane);
+  // The first block that any wavefront of the tile may treat as masked, the
+  // same for all of them, since each looks at its share of a block: that of
+  // the first token's diagonal, or the one before, if it is a wavefront's last.
+  const int first_masked = (tile * kRows / a.group + 1) / kKeys - 1;
+  const bool any_bad = attend_blocks<E, D, true>(lds, copy_k, copy_v, n_keys, first_masked, full, mine, token + 1,
+                                                 q, st, a.c, wave, lane);
   const float l = row_sum(st);
   // the row again, from the lane: nothing of it is kept in registers meanwhile
   int l2 = lane;

@@ -61,17 +61,44 @@ def test_many_sequences_and_an_offset_start(dim):
     _check(q, k, v, _starts(lens, 5), "f16", f"prompt 150 sequences dim={dim}")
 
 
-def test_long_sequence_sampled_rows():
-    """2300 tokens: rows in every block, compared one by one."""
-    n, hq, hkv, dim, kind = 2300, 8, 2, 128, "f16"
+@pytest.mark.parametrize("n,hq,hkv,dim,kind", [(2300, 8, 2, 128, "f16"), (2300, 8, 2, 64, "bf16"),
+                                               (4700, 32, 8, 128, "bf16"), (5003, 32, 8, 64, "f16")])
+def test_long_sequence_sampled_rows(n, hq, hkv, dim, kind):
+    """Rows in every block of a long sequence, compared one by one: few tiles, and more than run at once."""
     q, k, v = _inputs(3, n, hq, hkv, dim, kind)
-    say("prompt one sequence of 2300")
+    say(f"prompt one sequence of {n}, heads {hq}/{hkv} of {dim}")
     o = f64(_run(q, k, v, [0, n]))
     qn, kn, vn = f64(q), f64(k), f64(v)
-    for t in list(range(0, n, 61)) + [n - 1]:
-        for h in (0, 3, 4, 7):
-            want, err = O.attend(qn[t, h], kn[:t + 1, h // 4], vn[:t + 1, h // 4], dim ** -0.5, kind)
+    for t in list(range(0, n, n // 37)) + [n - 1]:
+        for h in (0, 3, 4, hq - 1):
+            g = h * hkv // hq
+            want, err = O.attend(qn[t, h], kn[:t + 1, g], vn[:t + 1, g], dim ** -0.5, kind)
             assert (np.abs(o[t, h] - want) <= err).all(), (t, h)
+
+
+@pytest.mark.parametrize("dim", [64, 128])
+def test_many_short_sequences(dim):
+    """More tiles than run at once, each with one block."""
+    lens = [1 + i % 3 for i in range(700)]
+    n = sum(lens)
+    q, k, v = _inputs(12, n + 2, 4, 2, dim, "f16")
+    _check(q, k, v, _starts(lens), "f16", f"prompt 700 short sequences dim={dim}")
+
+
+@pytest.mark.parametrize("dim", [64, 128])
+def test_many_tiles_with_masked_ends(dim):
+    """The same with ragged lengths around block and tile borders."""
+    lens = [63, 64, 65, 127, 128, 129, 1, 200] * 6
+    n = sum(lens)
+    q, k, v = _inputs(13, n, 64, 16, dim, "bf16")
+    say(f"prompt 48 ragged sequences dim={dim}")
+    o = f64(_run(q, k, v, _starts(lens)))
+    qn, kn, vn = f64(q), f64(k), f64(v)
+    for i, (b, e) in enumerate(zip(_starts(lens)[:-1], _starts(lens)[1:])):
+        for t in {b, (b + e) // 2, e - 1}:
+            for h in (0, 5 + i % 50, 63):
+                want, err = O.attend(qn[t, h], kn[b:t + 1, h // 4], vn[b:t + 1, h // 4], dim ** -0.5, "bf16")
+                assert (np.abs(o[t, h] - want) <= err).all(), (t, h)
 
 
 @pytest.mark.parametrize("layout", ["interleaved", "head-major", "wide rows"])
@@ -118,19 +145,20 @@ def test_scores_that_grow_and_fall_along_the_keys():
 
 @pytest.mark.parametrize("kind", ["f16", "bf16"])
 @pytest.mark.parametrize("bad", [float("nan"), float("inf"), -float("inf")])
-def test_nonfinite_values_of_later_tokens_stay_there(kind, bad):
+@pytest.mark.parametrize("more", [0, 600])
+def test_nonfinite_values_of_later_tokens_stay_there(kind, bad, more):
     """A non-finite key or value reaches the rows from its token on, of its KV
     head, and no other; the tokens behind the last sequence reach none."""
     n, hq, hkv, dim = 140, 4, 2, 128
-    q, k, v = _inputs(7, n + 20, hq, hkv, dim, kind)
-    starts = [0, 50, n]
+    q, k, v = _inputs(7, n + 20 + more, hq, hkv, dim, kind)
+    starts = [0, 50, n] + list(range(n + 21, n + 21 + more))  # further sequences of one token
     clean, err = O.attn_prompt(f64(q), f64(k), f64(v), starts, dim ** -0.5, kind)
     for which, t in ((v, 77), (v, 130), (k, 90), (v, 20)):
         keep = which[t, 1].clone()
         which[t, 1, 5] = bad
         for x in (q, k, v):
-            x[n:] = bad
-        say(f"prompt {kind} {bad} at token {t}")
+            x[n:n + 20] = bad
+        say(f"prompt {kind} {bad} at token {t}, {more} more sequences")
         o = f64(_run(q, k, v, starts))
         end = 50 if t < 50 else n
         free = np.ones((n, hq), bool)
