@@ -66,6 +66,9 @@ template <int N> __device__ __forceinline__ void wait_loads() {
   asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory");
 }
 
+// This wavefront's LDS reads are done, so what they read may be overwritten.
+__device__ __forceinline__ void wait_reads() { asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory"); }
+
 // A tile of rows of D elements in LDS: chunk c (16 bytes) of row r at slot
 // perm(r, c) of the row. K reads take one chunk of 32 consecutive rows: the
 // permutation puts any 16 consecutive rows (8 pairs for D = 64, whose rows

@@ -92,6 +92,7 @@ __device__ __forceinline__ void prefix_piece(const SharedArgs &a, int item, uint
 template <class E, int D>
 __device__ __forceinline__ void own_piece(const SharedArgs &a, int item, uint8_t *lds, int wave, int lane) {
   typedef typename E::one one;
+  typedef typename E::v8 v8;
   constexpr int kTile = kOwnKeys * D * 2;
   const int g = item % a.n_kv;
   const int rt = item / a.n_kv % a.own_tiles;
@@ -111,25 +112,46 @@ __device__ __forceinline__ void own_piece(const SharedArgs &a, int item, uint8_t
     load_rows<E, D>(static_cast<const one *>(a.q) + seq * a.qt + head * a.qh, lane, q);
     const one *kb = static_cast<const one *>(a.k) + seq * a.ks + first * a.kt + g * a.kh;
     const one *vb = static_cast<const one *>(a.v) + seq * a.vs + first * a.vt + g * a.vh;
-    // wavefront w takes blocks w, w + 4, ... through its own part of LDS
+    // Wavefront w takes blocks w, w + 4, ... through its own part of LDS, no
+    // barrier needed: the next block's K is copied while this one's weights
+    // are computed, its V while its scores are.
     const uint32_t at = lds_addr(lds) + wave * 2 * kTile;
+    constexpr int kCopies = kTile / 1024;  // copy instructions of a K or a V tile
     const int blocks = (n_keys + kOwnKeys - 1) / kOwnKeys;
     const Copier<D, TileK<D>, E, kOwnKeys, 1> copy_k(kb, a.kt, 0, lane);
     const Copier<D, TileV<D>, E, kOwnKeys, 1> copy_v(vb, a.vt, 0, lane);
-    auto next = [&](int b) {
-      copy_k(static_cast<int64_t>(b) * kOwnKeys, n_keys - b * kOwnKeys, at, lane);
-      copy_v(static_cast<int64_t>(b) * kOwnKeys, n_keys - b * kOwnKeys, at + kTile, lane);
-      wait_loads<0>();
+    auto load_k = [&](int b) {
+      if (b < blocks) copy_k(b * kOwnKeys, n_keys - b * kOwnKeys, at, lane);
     };
-    int b = wave;
-    for (; b < n_keys / kOwnKeys; b += 4) {
-      next(b);
-      attend<E, D, 1, false>(at, at + kTile, q, st, a.c, kOwnKeys, lane);
-      __builtin_amdgcn_s_waitcnt(0xc07f);  // lgkmcnt(0): the reads are done before the next copy
-    }
-    if (b < blocks) {
-      next(b);
-      attend<E, D, 1, true>(at, at + kTile, q, st, a.c, n_keys - b * kOwnKeys, lane);
+    auto load_v = [&](int b) {
+      if (b < blocks) copy_v(b * kOwnKeys, n_keys - b * kOwnKeys, at + kTile, lane);
+    };
+    load_k(wave);
+    load_v(wave);
+    for (int b = wave; b < blocks; b += 4) {
+      const bool more = b + 4 < blocks;
+      wait_loads<kCopies>();  // K has landed, V may be on its way
+#pragma unroll
+      for (int i = 0; i < D / 16; ++i) asm volatile("" : "+v"(q[i]));
+      float16_t s[1];
+      v8 p[2];
+      scores<E, D, 1>(at, q, s, lane);
+      interleave<D / 16, 4, 1, 0, 0>();
+      wait_reads();
+      load_k(b + 4);
+      const int left = n_keys - b * kOwnKeys;
+      if (left < kOwnKeys) mask_scores<1>(s, left, lane);
+      follow_max<D>(st, row_max<1>(s) * a.c);
+      weights<E, D, 1>(s, st, a.c, p);
+      if (more)
+        wait_loads<kCopies>();  // V has landed, the next K may be on its way
+      else
+        wait_loads<0>();
+      __builtin_amdgcn_sched_barrier(0);
+      add_values<E, D, 1>(v_addr<D>(at + kTile, lane), p, st);
+      interleave<2 * (D / 32), 3, 2, 0, 0>();
+      wait_reads();
+      load_v(b + 4);
     }
   }
   // join the four wavefronts: the largest m, then the sums, in wavefront order
@@ -185,26 +207,55 @@ __global__ __launch_bounds__(kThreads, 2) void attn_shared_kernel(SharedArgs a) 
     own_piece<E, D>(a, item - prefix_items, lds, wave, lane);
 }
 
-// One workgroup of D threads per (sequence, query head): the weighted sum of
-// its pieces, in order.
-template <class E, int D> __global__ __launch_bounds__(D) void attn_join_kernel(SharedArgs a) {
-  typedef typename E::one one;
+// One workgroup per (sequence, query head): the weighted sum of its pieces.
+// Thread (part, four elements): every kParts-th piece, eight on their way at
+// once, then the parts through LDS; all in a fixed order.
+template <class E, int D> __global__ __launch_bounds__(kThreads) void attn_join_kernel(SharedArgs a) {
+  constexpr int kFours = D / 4, kParts = kThreads / kFours;
+  __shared__ float4_t sums[kParts][kFours];
+  __shared__ float weights[kParts];
   const int seq = blockIdx.x / a.n_heads, head = blockIdx.x % a.n_heads;
   const int64_t rows = static_cast<int64_t>(a.n_seqs) * a.n_heads;
   const int pieces = a.prefix_pieces + a.own_pieces;
+  const int part = threadIdx.x / kFours, e = threadIdx.x % kFours;
   const int len = a.own_cap > 0 ? a.lengths[seq] : 0;
+  const int lane = threadIdx.x & 63;
   float top = -__builtin_inff();
-  for (int i = 0; i < pieces; ++i) top = fmaxf(top, a.part_l[i * rows + blockIdx.x]);
+  for (int i = lane; i < pieces; i += 64) top = fmaxf(top, a.part_l[i * rows + blockIdx.x]);
+#pragma unroll
+  for (int d = 32; d > 0; d /= 2) top = fmaxf(top, __shfl_xor(top, d));
   const float base = top == -__builtin_inff() ? 0.f : top;
-  float sum = 0.f, o = 0.f;
-  for (int i = 0; i < pieces; ++i) {
-    const float w = __builtin_amdgcn_exp2f(a.part_l[i * rows + blockIdx.x] - base);
-    sum += w;
-    o += w * a.part_o[(i * rows + blockIdx.x) * D + threadIdx.x];
+  float sum = 0.f;
+  float4_t o{};
+  for (int i0 = part; i0 < pieces; i0 += 8 * kParts) {
+    float w[8];
+    float4_t x[8];
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      const int64_t at = (i0 + k * kParts < pieces ? i0 + k * kParts : part) * rows + blockIdx.x;
+      w[k] = a.part_l[at];
+      x[k] = *reinterpret_cast<const float4_t *>(a.part_o + at * D + 4 * e);
+    }
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      if (i0 + k * kParts >= pieces) continue;
+      const float f = __builtin_amdgcn_exp2f(w[k] - base);
+      sum += f;
+      o += f * x[k];
+    }
   }
-  o = sum == 0.f ? 0.f : o / sum;
-  if (len < 0 || len > a.own_cap) o = __builtin_bit_cast(float, 0x7FC00000u);
-  static_cast<one *>(a.o)[seq * a.ot + head * a.oh + threadIdx.x] = static_cast<one>(o);
+  sums[part][e] = o;
+  if (e == 0) weights[part] = sum;
+  __syncthreads();
+  if (part != 0) return;
+#pragma unroll
+  for (int k = 1; k < kParts; ++k) o += sums[k][e], sum += weights[k];
+  const float f = sum == 0.f ? 0.f : 1.f / sum;
+  const bool bad = len < 0 || len > a.own_cap;
+  typename E::v4 out;
+#pragma unroll
+  for (int k = 0; k < 4; ++k) out[k] = static_cast<typename E::one>(bad ? __builtin_bit_cast(float, 0x7FC00000u) : o[k] * f);
+  *reinterpret_cast<typename E::v4 *>(static_cast<typename E::one *>(a.o) + seq * a.ot + head * a.oh + 4 * e) = out;
 }
 
 template <class E, int D> hipError_t run(const SharedArgs &a, int64_t items, hipStream_t stream) {
@@ -213,7 +264,7 @@ template <class E, int D> hipError_t run(const SharedArgs &a, int64_t items, hip
         launch(attn_shared_kernel<E, D>, dim3(static_cast<unsigned>(items)), dim3(kThreads), 0, stream, a);
     if (e != hipSuccess) return e;
   }
-  return launch(attn_join_kernel<E, D>, dim3(static_cast<unsigned>(a.n_seqs * a.n_heads)), dim3(D), 0, stream, a);
+  return launch(attn_join_kernel<E, D>, dim3(static_cast<unsigned>(a.n_seqs * a.n_heads)), dim3(kThreads), 0, stream, a);
 }
 
 }  // namespace
