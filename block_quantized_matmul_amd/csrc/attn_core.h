@@ -332,8 +332,8 @@ __device__ __forceinline__ void attend(uint32_t kt, uint32_t vt, const typename 
 // scores. The scores therefore run one block ahead: K is copied two blocks
 // ahead, V one.
 //
-// A wavefront's rows need its first `mine` blocks (>= 1); the first `full` (<
-// mine) of them are taken whole by all its rows, of the others a lane's row
+// A wavefront's rows need its first `mine` blocks (>= 1; without CAUSAL also
+// 0, for a wavefront that only copies); the first `full` (< mine) of them are taken whole by all its rows, of the others a lane's row
 // takes keys below lim.
 //
 // A masked key's weight is zero, but zero times a non-finite value is a NaN.
@@ -385,9 +385,12 @@ __device__ __forceinline__ bool attend_blocks(uint8_t *lds, const CopyK &copy_k,
   for (int i = 0; i < D / 16; ++i) asm volatile("" : "+v"(q[i]));
   __syncthreads();
   load_k(1);
-  scores<E, D, 2>(kt(0), q, s, lane);
-  interleave<D / 8, 4, 1, 0, 0>();
-  float mx = row_max<2>(s) * c;
+  float mx = 0.f;
+  if (CAUSAL || mine > 0) {
+    scores<E, D, 2>(kt(0), q, s, lane);
+    interleave<D / 8, 4, 1, 0, 0>();
+    mx = row_max<2>(s) * c;
+  }
   auto step = [&](int b, float16_t(&now)[2], float16_t(&then)[2]) {
     next(b);
     follow_max<D>(st, mx);

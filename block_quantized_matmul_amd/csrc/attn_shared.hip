@@ -8,16 +8,16 @@
 //
 // The prefix is read once for all sequences: the rows of all sequences and of
 // the heads that share a KV head are flattened (row x: sequence x / group,
-// head g group + x % group) into tiles of 128, four wavefronts of 32 rows on
-// blocks of 64 keys, as the prompt kernel runs without its mask. A sequence's
+// head g group + x % group) into equal tiles of at most 128, four wavefronts of 32
+// rows on blocks of 64 keys, as the prompt kernel runs without its mask. A sequence's
 // own cache serves only `group` rows, so there a workgroup's four wavefronts
 // share one tile of 32 rows and split the piece's keys, each with blocks of
 // 32 keys of its own (copied into its own part of LDS, no barrier), and join
 // at the end through LDS.
 //
-// Both kinds of pieces are workgroups of one launch: the prefix's are bound
-// by the matrix cores, the caches' by memory. A second launch joins the
-// pieces.
+// Both kinds of pieces are workgroups of one launch and alternate in it, since
+// the prefix's are bound by the matrix cores and the caches' by memory. A
+// second launch joins the pieces.
 #include "attn.h"
 #include "attn_core.h"
 #include "launch.h"
@@ -41,7 +41,7 @@ struct SharedArgs {
   float *part_o;  // [pieces][n_seqs * n_q_heads][D]
   float *part_l;  // [pieces][n_seqs * n_q_heads]
   int n_seqs, n_heads, group, n_kv, prefix_len, own_cap;
-  int row_tiles, prefix_pieces, prefix_step, own_tiles, own_pieces, own_step;
+  int row_tiles, tile_rows, prefix_pieces, prefix_step, own_tiles, own_pieces, own_step;
   float c;  // scale * log2(e)
 };
 
@@ -63,13 +63,13 @@ __device__ __forceinline__ void store_partial(const SharedArgs &a, int piece, in
 }
 
 template <class E, int D>
-__device__ __forceinline__ void prefix_piece(const SharedArgs &a, int item, uint8_t *lds, int wave, int lane) {
+__device__ __forceinline__ void prefix_piece(const SharedArgs &a, int item, int g, uint8_t *lds, int wave, int lane) {
   typedef typename E::one one;
-  const int g = item % a.n_kv;
-  const int rt = item / a.n_kv % a.row_tiles;
-  const int piece = item / a.n_kv / a.row_tiles;
+  const int rt = item % a.row_tiles;
+  const int piece = item / a.row_tiles;
   const int rows = a.n_seqs * a.group;
-  const int row = rt * kSharedRows + wave * 32 + (lane & 31);
+  const int row = rt * a.tile_rows + wave * 32 + (lane & 31);
+  const bool busy = wave * 32 < a.tile_rows && rt * a.tile_rows + wave * 32 < rows;  // else it only copies
   const int row_in = row < rows ? row : rows - 1;
   const int seq = row_in / a.group, head = g * a.group + row_in % a.group;
   typename E::v8 q[D / 16];
@@ -84,20 +84,20 @@ __device__ __forceinline__ void prefix_piece(const SharedArgs &a, int item, uint
   AttnState<D> st;
   st.clear();
   const int blocks = (n_keys + kKeys - 1) / kKeys;
-  attend_blocks<E, D, false>(lds, copy_k, copy_v, n_keys, 0, blocks - 1, blocks, n_keys, q, st, a.c, wave, lane);
+  attend_blocks<E, D, false>(lds, copy_k, copy_v, n_keys, 0, busy ? blocks - 1 : -1, busy ? blocks : 0, n_keys, q, st, a.c,
+                             wave, lane);
   const float l = row_sum(st);
-  if (row < rows) store_partial<D>(a, piece, seq, head, st, l, lane);
+  if (busy && row < rows) store_partial<D>(a, piece, seq, head, st, l, lane);
 }
 
 template <class E, int D>
-__device__ __forceinline__ void own_piece(const SharedArgs &a, int item, uint8_t *lds, int wave, int lane) {
+__device__ __forceinline__ void own_piece(const SharedArgs &a, int item, int g, uint8_t *lds, int wave, int lane) {
   typedef typename E::one one;
   typedef typename E::v8 v8;
   constexpr int kTile = kOwnKeys * D * 2;
-  const int g = item % a.n_kv;
-  const int rt = item / a.n_kv % a.own_tiles;
-  const int seq = item / a.n_kv / a.own_tiles % a.n_seqs;
-  const int piece = item / a.n_kv / a.own_tiles / a.n_seqs;
+  const int rt = item % a.own_tiles;
+  const int seq = item / a.own_tiles % a.n_seqs;
+  const int piece = item / a.own_tiles / a.n_seqs;
   const int row = rt * kOwnRows + (lane & 31);  // of the group
   const int head = g * a.group + min(row, a.group - 1);
   const int len = __builtin_amdgcn_readfirstlane(a.lengths[seq]);
@@ -199,12 +199,16 @@ __global__ __launch_bounds__(kThreads, 2) void attn_shared_kernel(SharedArgs a) 
   __shared__ __align__(1024) uint8_t lds[attend_lds_bytes<D>()];
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int prefix_items = a.prefix_pieces * a.row_tiles * a.n_kv;
-  const int item = blockIdx.x;
-  if (item < prefix_items)
-    prefix_piece<E, D>(a, item, lds, wave, lane);
+  // KV heads are the fastest index (their keys stay in one XCD's L2); the two
+  // kinds of pieces alternate, in proportion
+  const int g = blockIdx.x % a.n_kv;
+  const int64_t unit = blockIdx.x / a.n_kv;
+  const int prefix_units = a.prefix_pieces * a.row_tiles, units = prefix_units + a.own_pieces * a.n_seqs * a.own_tiles;
+  const int before = static_cast<int>(unit * prefix_units / units);
+  if (static_cast<int>((unit + 1) * prefix_units / units) > before)
+    prefix_piece<E, D>(a, before, g, lds, wave, lane);
   else
-    own_piece<E, D>(a, item - prefix_items, lds, wave, lane);
+    own_piece<E, D>(a, static_cast<int>(unit) - before, g, lds, wave, lane);
 }
 
 // One workgroup per (sequence, query head): the weighted sum of its pieces.
@@ -305,7 +309,11 @@ hipError_t launch_attn_shared(int type, const qmm_heads &Q, const qmm_heads &PK,
   a.n_seqs = static_cast<int>(n_seqs), a.n_heads = static_cast<int>(n_q_heads);
   a.group = static_cast<int>(n_q_heads / n_kv_heads), a.n_kv = static_cast<int>(n_kv_heads);
   a.prefix_len = static_cast<int>(prefix_len), a.own_cap = static_cast<int>(own_cap);
-  a.row_tiles = static_cast<int>(p.row_tiles), a.prefix_pieces = static_cast<int>(p.prefix_pieces);
+  // equal tiles, of whole wavefronts' rows
+  const int64_t row_waves = (n_seqs * a.group + 31) / 32;
+  a.row_tiles = static_cast<int>(p.row_tiles);
+  a.tile_rows = static_cast<int>((row_waves + p.row_tiles - 1) / p.row_tiles) * 32;
+  a.prefix_pieces = static_cast<int>(p.prefix_pieces);
   a.prefix_step = static_cast<int>(p.prefix_step), a.own_tiles = static_cast<int>(p.own_tiles);
   a.own_pieces = static_cast<int>(p.own_pieces), a.own_step = static_cast<int>(p.own_step);
   a.c = scale * 1.4426950408889634f;
