@@ -27,6 +27,7 @@ hipError_t launch_attn_prompt(int type, const qmm_heads &Q, const qmm_heads &K, 
 // qmm_attn_shared's split: the keys of the prefix and of the own caches in
 // pieces, each of which leaves its rows' partial result in the workspace.
 struct SharedPlan {
+  bool direct;            // few keys: no pieces, no workspace
   int64_t row_tiles;      // tiles of kSharedRows of the n_seqs * group rows of one KV head
   int64_t prefix_pieces;  // pieces of the prefix, prefix_step keys each
   int64_t prefix_step;

@@ -32,6 +32,14 @@ constexpr int kThreads = 256;
 constexpr int kOwnKeys = 32;     // keys per block of one wavefront, own cache
 constexpr int kMinPiece = 256;   // keys
 constexpr int kWantGroups = 512; // workgroups: two per CU on 256 CUs
+constexpr int kWantBoth = 384;   // of each kind of piece, where there are both
+// No pieces (attn_direct_kernel) up to so many keys and so many reads of prefix
+// keys by all sequences. Measured with 32 heads on 8 KV heads of 128, us
+// without and with pieces: 4 sequences on 500 + 192 keys 11.3 / 17.2, on 1000
+// + 192 15.1 / 18.2, on 2000 + 192 24.1 / 16.8; 48 on 500 + 256 18.6 / 23.2,
+// on 1000 + 256 24.0 / 21.9; 128 on 500 + 256 43.7 / 47.3.
+constexpr int64_t kDirectKeys = 1024;
+constexpr int64_t kDirectReads = 65536;
 
 struct SharedArgs {
   const void *q, *pk, *pv, *k, *v;
@@ -90,75 +98,62 @@ __device__ __forceinline__ void prefix_piece(const SharedArgs &a, int item, int 
   if (busy && row < rows) store_partial<D>(a, piece, seq, head, st, l, lane);
 }
 
+// 32 rows over keys 0 .. n_keys - 1, on one of four wavefronts: this one takes
+// blocks wave, wave + 4, ... of 32 keys through its own part of LDS, no
+// barrier needed. The next block's K is copied while this one's weights are
+// computed, its V while its scores are.
 template <class E, int D>
-__device__ __forceinline__ void own_piece(const SharedArgs &a, int item, int g, uint8_t *lds, int wave, int lane) {
-  typedef typename E::one one;
-  typedef typename E::v8 v8;
-  constexpr int kTile = kOwnKeys * D * 2;
-  const int rt = item % a.own_tiles;
-  const int seq = item / a.own_tiles % a.n_seqs;
-  const int piece = item / a.own_tiles / a.n_seqs;
-  const int row = rt * kOwnRows + (lane & 31);  // of the group
-  const int head = g * a.group + min(row, a.group - 1);
-  const int len = __builtin_amdgcn_readfirstlane(a.lengths[seq]);
-  const int first = piece * a.own_step;
-  // a length outside [0, own_cap] is answered by the join
-  const int n_keys = len < 0 || len > a.own_cap ? 0 : min(max(len - first, 0), a.own_step);
-
-  AttnState<D> st;
-  st.clear();
-  if (n_keys > 0) {
-    typename E::v8 q[D / 16];
-    load_rows<E, D>(static_cast<const one *>(a.q) + seq * a.qt + head * a.qh, lane, q);
-    const one *kb = static_cast<const one *>(a.k) + seq * a.ks + first * a.kt + g * a.kh;
-    const one *vb = static_cast<const one *>(a.v) + seq * a.vs + first * a.vt + g * a.vh;
-    // Wavefront w takes blocks w, w + 4, ... through its own part of LDS, no
-    // barrier needed: the next block's K is copied while this one's weights
-    // are computed, its V while its scores are.
-    const uint32_t at = lds_addr(lds) + wave * 2 * kTile;
-    constexpr int kCopies = kTile / 1024;  // copy instructions of a K or a V tile
-    const int blocks = (n_keys + kOwnKeys - 1) / kOwnKeys;
-    const Copier<D, TileK<D>, E, kOwnKeys, 1> copy_k(kb, a.kt, 0, lane);
-    const Copier<D, TileV<D>, E, kOwnKeys, 1> copy_v(vb, a.vt, 0, lane);
-    auto load_k = [&](int b) {
-      if (b < blocks) copy_k(b * kOwnKeys, n_keys - b * kOwnKeys, at, lane);
-    };
-    auto load_v = [&](int b) {
-      if (b < blocks) copy_v(b * kOwnKeys, n_keys - b * kOwnKeys, at + kTile, lane);
-    };
-    load_k(wave);
-    load_v(wave);
-    for (int b = wave; b < blocks; b += 4) {
-      const bool more = b + 4 < blocks;
-      wait_loads<kCopies>();  // K has landed, V may be on its way
+__device__ __forceinline__ void own_blocks(const typename E::one *kb, int64_t k_stride, const typename E::one *vb,
+                                           int64_t v_stride, int n_keys, typename E::v8 q[D / 16], AttnState<D> &st,
+                                           float c, uint8_t *lds, int wave, int lane) {
+  constexpr int kTile = kOwnKeys * D * 2, kCopies = kTile / 1024;  // copies: instructions of a K or a V tile
+  const uint32_t at = lds_addr(lds) + wave * 2 * kTile;
+  const int blocks = (n_keys + kOwnKeys - 1) / kOwnKeys;
+  const Copier<D, TileK<D>, E, kOwnKeys, 1> copy_k(kb, k_stride, 0, lane);
+  const Copier<D, TileV<D>, E, kOwnKeys, 1> copy_v(vb, v_stride, 0, lane);
+  auto load_k = [&](int b) {
+    if (b < blocks) copy_k(b * kOwnKeys, n_keys - b * kOwnKeys, at, lane);
+  };
+  auto load_v = [&](int b) {
+    if (b < blocks) copy_v(b * kOwnKeys, n_keys - b * kOwnKeys, at + kTile, lane);
+  };
+  load_k(wave);
+  load_v(wave);
+  for (int b = wave; b < blocks; b += 4) {
+    wait_loads<kCopies>();  // K has landed, V may be on its way
 #pragma unroll
-      for (int i = 0; i < D / 16; ++i) asm volatile("" : "+v"(q[i]));
-      float16_t s[1];
-      v8 p[2];
-      scores<E, D, 1>(at, q, s, lane);
-      interleave<D / 16, 4, 1, 0, 0>();
-      wait_reads();
-      load_k(b + 4);
-      const int left = n_keys - b * kOwnKeys;
-      if (left < kOwnKeys) mask_scores<1>(s, left, lane);
-      follow_max<D>(st, row_max<1>(s) * a.c);
-      weights<E, D, 1>(s, st, a.c, p);
-      if (more)
-        wait_loads<kCopies>();  // V has landed, the next K may be on its way
-      else
-        wait_loads<0>();
-      __builtin_amdgcn_sched_barrier(0);
-      add_values<E, D, 1>(v_addr<D>(at + kTile, lane), p, st);
-      interleave<2 * (D / 32), 3, 2, 0, 0>();
-      wait_reads();
-      load_v(b + 4);
-    }
+    for (int i = 0; i < D / 16; ++i) asm volatile("" : "+v"(q[i]));
+    float16_t s[1];
+    typename E::v8 p[2];
+    scores<E, D, 1>(at, q, s, lane);
+    interleave<D / 16, 4, 1, 0, 0>();
+    wait_reads();
+    load_k(b + 4);
+    const int left = n_keys - b * kOwnKeys;
+    if (left < kOwnKeys) mask_scores<1>(s, left, lane);
+    follow_max<D>(st, row_max<1>(s) * c);
+    weights<E, D, 1>(s, st, c, p);
+    if (b + 4 < blocks)
+      wait_loads<kCopies>();  // V has landed, the next K may be on its way
+    else
+      wait_loads<0>();
+    __builtin_amdgcn_sched_barrier(0);
+    add_values<E, D, 1>(v_addr<D>(at + kTile, lane), p, st);
+    interleave<2 * (D / 32), 3, 2, 0, 0>();
+    wait_reads();
+    load_v(b + 4);
   }
-  // join the four wavefronts: the largest m, then the sums, in wavefront order
+}
+
+// Joins the states of four wavefronts on the same rows through LDS: the
+// largest m, then the sums in wavefront order. Wavefront 3 ends up with the
+// whole, and its l is the row's, not a lane's half.
+template <int D>
+__device__ __forceinline__ void join_wavefronts(AttnState<D> &st, uint8_t *lds, int wave, int lane) {
   float l = row_sum(st);
   __syncthreads();
-  float *ml = reinterpret_cast<float *>(lds);           // [4][32][2]
-  float *os = reinterpret_cast<float *>(lds) + 256;     // [32][D + 1], added to in turn
+  float *ml = reinterpret_cast<float *>(lds);        // [4][32][2]
+  float *os = reinterpret_cast<float *>(lds) + 256;  // [32][D + 1], added to in turn
   if (lane < 32) {
     ml[(wave * 32 + lane) * 2] = st.m;
     ml[(wave * 32 + lane) * 2 + 1] = l;
@@ -174,6 +169,7 @@ __device__ __forceinline__ void own_piece(const SharedArgs &a, int item, int g, 
   for (int w = 0; w < 4; ++w)
     l += ml[(w * 32 + col) * 2 + 1] * __builtin_amdgcn_exp2f(ml[(w * 32 + col) * 2] - base);
   const float f = __builtin_amdgcn_exp2f(st.m - base);
+  st.m = top, st.l = l;
 #pragma unroll
   for (int w = 0; w < 4; ++w) {
     if (wave == w) {
@@ -183,15 +179,66 @@ __device__ __forceinline__ void own_piece(const SharedArgs &a, int item, int g, 
         for (int r = 0; r < 16; ++r) {
           float *x = os + col * (D + 1) + 32 * dt + 8 * (r >> 2) + 4 * (lane >> 5) + (r & 3);
           st.o[dt][r] = st.o[dt][r] * f + (w > 0 ? *x : 0.f);
-          *x = st.o[dt][r];
+          if (w < 3) *x = st.o[dt][r];
         }
     }
-    __syncthreads();
+    if (w < 3) __syncthreads();
   }
-  if (wave == 3 && row < a.group) {
-    st.m = top;
-    store_partial<D>(a, a.prefix_pieces + piece, seq, head, st, l, lane);
+}
+
+template <class E, int D>
+__device__ __forceinline__ void own_piece(const SharedArgs &a, int item, int g, uint8_t *lds, int wave, int lane) {
+  typedef typename E::one one;
+  const int rt = item % a.own_tiles;
+  const int seq = item / a.own_tiles % a.n_seqs;
+  const int piece = item / a.own_tiles / a.n_seqs;
+  const int row = rt * kOwnRows + (lane & 31);  // of the group
+  const int head = g * a.group + min(row, a.group - 1);
+  const int len = __builtin_amdgcn_readfirstlane(a.lengths[seq]);
+  const int first = piece * a.own_step;
+  // a length outside [0, own_cap] is answered by the join
+  const int n_keys = len < 0 || len > a.own_cap ? 0 : min(max(len - first, 0), a.own_step);
+  AttnState<D> st;
+  st.clear();
+  if (n_keys > 0) {
+    typename E::v8 q[D / 16];
+    load_rows<E, D>(static_cast<const one *>(a.q) + seq * a.qt + head * a.qh, lane, q);
+    own_blocks<E, D>(static_cast<const one *>(a.k) + seq * a.ks + first * a.kt + g * a.kh, a.kt,
+                     static_cast<const one *>(a.v) + seq * a.vs + first * a.vt + g * a.vh, a.vt, n_keys, q, st, a.c,
+                     lds, wave, lane);
   }
+  join_wavefronts<D>(st, lds, wave, lane);
+  if (wave == 3 && row < a.group) store_partial<D>(a, a.prefix_pieces + piece, seq, head, st, st.l, lane);
+}
+
+// Few keys: one workgroup per (sequence, KV head, 32 rows of the group) goes
+// over the prefix and the cache and writes the result, without partial
+// results to join. It reads the prefix once per sequence (from L2), so this is
+// for short prefixes and small batches.
+template <class E, int D> __global__ __launch_bounds__(kThreads, 2) void attn_direct_kernel(SharedArgs a) {
+  typedef typename E::one one;
+  __shared__ __align__(1024) uint8_t lds[4 * 2 * kOwnKeys * D * 2];
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int g = blockIdx.x % a.n_kv, rt = blockIdx.x / a.n_kv % a.own_tiles, seq = blockIdx.x / a.n_kv / a.own_tiles;
+  const int row = rt * kOwnRows + (lane & 31);
+  const int head = g * a.group + min(row, a.group - 1);
+  const int len = a.own_cap > 0 ? __builtin_amdgcn_readfirstlane(a.lengths[seq]) : 0;
+  const bool bad = len < 0 || len > a.own_cap;
+  AttnState<D> st;
+  st.clear();
+  typename E::v8 q[D / 16];
+  load_rows<E, D>(static_cast<const one *>(a.q) + seq * a.qt + head * a.qh, lane, q);
+  if (a.prefix_len > 0)
+    own_blocks<E, D>(static_cast<const one *>(a.pk) + g * a.pkh, a.pkt, static_cast<const one *>(a.pv) + g * a.pvh,
+                     a.pvt, a.prefix_len, q, st, a.c, lds, wave, lane);
+  if (len > 0 && !bad)
+    own_blocks<E, D>(static_cast<const one *>(a.k) + seq * a.ks + g * a.kh, a.kt,
+                     static_cast<const one *>(a.v) + seq * a.vs + g * a.vh, a.vt, len, q, st, a.c, lds, wave, lane);
+  join_wavefronts<D>(st, lds, wave, lane);
+  if (wave != 3) return;
+  const float f = bad ? __builtin_bit_cast(float, 0x7FC00000u) : st.l == 0.f ? 0.f : 1.f / st.l;
+  store_row<E, D>(static_cast<one *>(a.o) + seq * a.ot + head * a.oh, st, f, lane, row < a.group);
 }
 
 template <class E, int D>
@@ -262,7 +309,9 @@ template <class E, int D> __global__ __launch_bounds__(kThreads) void attn_join_
   *reinterpret_cast<typename E::v4 *>(static_cast<typename E::one *>(a.o) + seq * a.ot + head * a.oh + 4 * e) = out;
 }
 
-template <class E, int D> hipError_t run(const SharedArgs &a, int64_t items, hipStream_t stream) {
+template <class E, int D> hipError_t run(const SharedArgs &a, int64_t items, bool direct, hipStream_t stream) {
+  if (direct)
+    return launch(attn_direct_kernel<E, D>, dim3(static_cast<unsigned>(items)), dim3(kThreads), 0, stream, a);
   if (items > 0) {
     const hipError_t e =
         launch(attn_shared_kernel<E, D>, dim3(static_cast<unsigned>(items)), dim3(kThreads), 0, stream, a);
@@ -280,9 +329,15 @@ SharedPlan shared_plan(int64_t n_seqs, int64_t prefix_len, int64_t own_cap, int6
   SharedPlan p{};
   p.row_tiles = (n_seqs * group + kSharedRows - 1) / kSharedRows;
   p.own_tiles = (group + kOwnRows - 1) / kOwnRows;
-  auto cut = [](int64_t keys, int64_t items, int64_t block, int64_t &pieces, int64_t &step) {
+  // (without a prefix, a workgroup per cache is as good where they fill the
+  // GPU: 64 caches of 2000 94 / 99 us)
+  p.direct = (prefix_len + own_cap <= kDirectKeys && prefix_len * n_seqs <= kDirectReads) ||
+             (prefix_len == 0 && n_seqs * n_kv_heads * p.own_tiles >= kWantGroups);
+  if (p.direct) return p;
+  const int64_t groups = prefix_len > 0 && own_cap > 0 ? kWantBoth : kWantGroups;
+  auto cut = [groups](int64_t keys, int64_t items, int64_t block, int64_t &pieces, int64_t &step) {
     if (keys == 0) return;
-    const int64_t want = std::max<int64_t>(1, std::min((kWantGroups + items - 1) / items, keys / kMinPiece));
+    const int64_t want = std::max<int64_t>(1, std::min((groups + items - 1) / items, keys / kMinPiece));
     step = ((keys + want - 1) / want + block - 1) / block * block;
     pieces = (keys + step - 1) / step;
   };
@@ -317,9 +372,13 @@ hipError_t launch_attn_shared(int type, const qmm_heads &Q, const qmm_heads &PK,
   a.prefix_step = static_cast<int>(p.prefix_step), a.own_tiles = static_cast<int>(p.own_tiles);
   a.own_pieces = static_cast<int>(p.own_pieces), a.own_step = static_cast<int>(p.own_step);
   a.c = scale * 1.4426950408889634f;
-  const int64_t items = p.prefix_pieces * p.row_tiles * n_kv_heads + p.own_pieces * n_seqs * p.own_tiles * n_kv_heads;
-  if (type == QMM_T_F16) return head_dim == 128 ? run<ElemF16, 128>(a, items, stream) : run<ElemF16, 64>(a, items, stream);
-  return head_dim == 128 ? run<ElemBF16, 128>(a, items, stream) : run<ElemBF16, 64>(a, items, stream);
+  const int64_t items = (p.direct ? n_seqs * p.own_tiles
+                                  : p.prefix_pieces * p.row_tiles + p.own_pieces * n_seqs * p.own_tiles) * n_kv_heads;
+  auto by_dim = [&](auto elem) {
+    typedef decltype(elem) E;
+    return head_dim == 128 ? run<E, 128>(a, items, p.direct, stream) : run<E, 64>(a, items, p.direct, stream);
+  };
+  return type == QMM_T_F16 ? by_dim(ElemF16{}) : by_dim(ElemBF16{});
 }
 
 }  // namespace qmm

@@ -43,6 +43,10 @@ def _check(q, pk, pv, k, v, lengths, kind, what, o=None):
     (1, 1, 1, [0], 1, 1), (1, 0, 5, [5], 4, 1), (3, 0, 40, [0, 1, 40], 2, 2), (2, 63, 33, [32, 33], 8, 2),
     (5, 64, 31, [0, 1, 7, 30, 31], 4, 4), (4, 65, 300, [300, 0, 129, 257], 7, 1), (33, 130, 8, None, 4, 1),
     (2, 700, 700, [699, 13], 6, 2), (3, 257, 64, [64, 3, 0], 40, 1), (40, 300, 3, None, 8, 8),
+    # more keys than are taken without pieces
+    (1, 1025, 0, [0], 4, 2), (3, 1087, 1, [1, 0, 1], 40, 1), (33, 1030, 5, None, 4, 1), (2, 1, 1100, [1100, 0], 6, 2),
+    (5, 64, 1000, [0, 1000, 33, 256, 257], 4, 4), (3, 0, 1500, [1500, 0, 700], 7, 1), (17, 1024, 40, None, 8, 2),
+    (70, 0, 40, None, 8, 8),
 ])
 def test_against_the_definition(kind, dim, b, prefix, cap, lengths, hq, hkv):
     lengths = [i % (cap + 1) for i in range(b)] if lengths is None else lengths
@@ -66,9 +70,10 @@ def test_long_ranges_in_many_pieces():
 
 
 @pytest.mark.parametrize("bad", [float("nan"), float("inf")])
-def test_nothing_past_a_length_counts(bad):
+@pytest.mark.parametrize("prefix", [90, 1090])
+def test_nothing_past_a_length_counts(bad, prefix):
     """What the cache holds past a sequence's length, and what other sequences hold, does not reach it."""
-    b, prefix, cap, hq, hkv, dim = 4, 90, 70, 4, 2, 64
+    b, cap, hq, hkv, dim = 4, 70, 4, 2, 64
     q, pk, pv, k, v = _inputs(3, b, prefix, cap, hq, hkv, dim, "f16")
     lengths = [0, 33, 69, 70]
     for i, n in enumerate(lengths):
@@ -86,12 +91,14 @@ def test_nothing_past_a_length_counts(bad):
 
 
 def test_lengths_outside_the_cache_give_nan_rows():
-    q, pk, pv, k, v = _inputs(4, 5, 40, 16, 2, 1, 64, "f16")
-    _check(q, pk, pv, k, v, [3, -1, 17, 16, 2 ** 31 - 1], "f16", "shared bad lengths")
+    for prefix in (40, 1040):
+        q, pk, pv, k, v = _inputs(4, 5, prefix, 16, 2, 1, 64, "f16")
+        _check(q, pk, pv, k, v, [3, -1, 17, 16, 2 ** 31 - 1], "f16", f"shared bad lengths, prefix {prefix}")
 
 
-def test_strides_and_a_given_workspace():
-    b, prefix, cap, hq, hkv, dim = 3, 100, 50, 4, 2, 64
+@pytest.mark.parametrize("prefix", [100, 1100])
+def test_strides_and_a_given_workspace(prefix):
+    b, cap, hq, hkv, dim = 3, 50, 4, 2, 64
     q, pk, pv, k, v = _inputs(5, b, prefix, cap, hq, hkv, dim, "f16")
     lengths = [50, 0, 21]
     say("shared strides")
