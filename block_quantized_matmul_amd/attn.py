@@ -29,6 +29,7 @@ __all__ = ["QMM_T_F32", "QMM_T_F16", "QMM_T_BF16", "QMM_ROPE_HALVES", "QMM_ROPE_
            "qmm_lora", "qmm_lora_workspace_bytes", "qmm_norm_rope", "qmm_attn_prompt", "qmm_attn_shared",
            "qmm_attn_shared_workspace_bytes"]
 
+_PART_NAMES = ("X", "Y", "weight") + ("positions", "slots") + ("X", "Y", "weight") * (QMM_HEAD_PARTS_MAX - 1)
 _PAIRS = {"halves": QMM_ROPE_HALVES, "neighbours": QMM_ROPE_NEIGHBOURS}
 _vp, _i32, _i64, _f32 = ctypes.c_void_p, ctypes.c_int, ctypes.c_int64, ctypes.c_float
 
@@ -105,7 +106,7 @@ def _refuse(named):
 class _Place:
     """Where a call runs: the one GPU of its tensors and the stream's handle.
     (These calls are short, so this takes the cheapest route to each answer.)"""
-    __slots__ = ("device", "handle", "foreign")
+    __slots__ = ("device", "handle", "foreign", "like")
 
     def __init__(self, stream, names, tensors):
         import torch
@@ -118,7 +119,7 @@ class _Place:
             device = -1
         if device < 0:
             _refuse(zip(names, tensors))
-        self.device = device
+        self.device, self.like = device, tensors[0]
         self.handle = torch._C._cuda_getCurrentRawStream(device)
         self.foreign = None
         if stream is not None and stream.cuda_stream != self.handle:
@@ -127,8 +128,7 @@ class _Place:
             self.handle, self.foreign = stream.cuda_stream, stream
 
     def empty(self, shape, dtype):
-        import torch
-        t = torch.empty(shape, dtype=dtype, device=self.device)
+        t = self.like.new_empty(shape, dtype=dtype)
         if self.foreign is not None:
             t.record_stream(self.foreign)
         return t
@@ -141,7 +141,7 @@ class _Place:
         if given is None:
             if need == 0:
                 return None, None, 0
-            given = self.empty((need,), torch.uint8)
+            given = self.empty(need, torch.uint8)
         elif given.dtype != torch.uint8 or not given.is_contiguous():
             raise TypeError("workspace must be a contiguous uint8 tensor")
         return given, given.data_ptr(), given.numel()
@@ -168,10 +168,11 @@ def _type(t, name):
 def _ints(t, name, n):
     """A contiguous int32 vector of n elements (None: any number)."""
     import torch
-    if t.dtype is not torch.int32 or t.dim() != 1 or not t.is_contiguous():
+    shape = t.shape
+    if t.dtype is not torch.int32 or len(shape) != 1 or not t.is_contiguous():
         raise TypeError(f"{name} must be a contiguous 1-D int32 tensor")
-    if n is not None and t.shape[0] != n:
-        raise ValueError(f"{name} holds {t.shape[0]} elements, the call needs {n}")
+    if n is not None and shape[0] != n:
+        raise ValueError(f"{name} holds {shape[0]} elements, the call needs {n}")
 
 
 def _floats(t, name, shape):
@@ -278,11 +279,12 @@ def qmm_norm_rope(parts, positions=None, freqs=None, pairs="halves", eps=1e-6, s
         raise ValueError(f"at most {QMM_HEAD_PARTS_MAX} parts")
     if pairs not in _PAIRS:
         raise ValueError("pairs must be 'halves' or 'neighbours'")
-    tensors = [t for p in parts for t in (p.X, p.Y, p.weight)] + [positions, slots]
-    place = _Place(stream, ["X", "Y", "weight"] * len(parts) + ["positions", "slots"], tensors)
+    place = _Place(stream, _PART_NAMES, [parts[0].X, parts[0].Y, parts[0].weight, positions, slots]
+                   + [t for p in parts[1:] for t in (p.X, p.Y, p.weight)])
     if parts[0].X.dim() != 3:
         raise ValueError("X must be [n_tokens][n_heads][head_dim]")
     n, _, dim = parts[0].X.shape
+    vector = (dim,)
     L = _lib()
     descs = (qmm_head_part_desc * QMM_HEAD_PARTS_MAX)()
     n_slots = None
@@ -303,7 +305,7 @@ def qmm_norm_rope(parts, positions=None, freqs=None, pairs="halves", eps=1e-6, s
         if weight is not None:
             if not norm:
                 raise ValueError("weight needs norm")
-            _floats(weight, "weight", (dim,))
+            _floats(weight, "weight", vector)
         xst, yst = _strides(X, "X"), _strides(Y, "Y")
         descs[i] = qmm_head_part_desc(X.data_ptr(), _type(X, "X"), xst[0], xst[1], Y.data_ptr(), _type(Y, "Y"), yst[0],
                                       yst[1], xs[1], bool(norm), _ptr(weight), bool(rotate), bool(slotted))

@@ -14,6 +14,7 @@ constexpr int64_t kMaxDim = (int64_t{1} << 31) - 1;
 constexpr int64_t kMaxElems = int64_t{1} << 60;
 constexpr int64_t kMaxGroups = (int64_t{1} << 24) - 1;  // 256-thread workgroups of one launch (2^32 threads)
 constexpr int64_t kMaxCopyStride = int64_t{1} << 25;  // elements: 63 rows of a block within 32-bit byte offsets
+constexpr double kMaxFreq = 64.;  // radians per position: what qmm_norm_rope's fixed point stays accurate for
 constexpr int64_t kMaxLoraTokens = (int64_t{1} << 25) - 1;
 constexpr int64_t kMaxLoraK = (int64_t{1} << 24) - 1;
 
@@ -113,7 +114,7 @@ int qmm_norm_rope(const qmm_head_part *parts, int n_parts, int64_t n_tokens, int
   if (pairs != QMM_ROPE_HALVES && pairs != QMM_ROPE_NEIGHBOURS) return QMM_ERR_TYPE;
   if (n_freqs > 0 && freqs == nullptr) return QMM_ERR_NULL;
   for (int64_t i = 0; i < n_freqs; ++i)
-    if (!isfinite(freqs[i])) return QMM_ERR_SHAPE;
+    if (!(fabs(freqs[i]) <= kMaxFreq)) return QMM_ERR_SHAPE;
   if (!aligned(positions, 4) || !aligned(slots, 4)) return QMM_ERR_ALIGN;
   int64_t heads = 0;
   for (int p = 0; p < n_parts; ++p) {

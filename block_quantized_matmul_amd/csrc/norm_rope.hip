@@ -13,15 +13,13 @@
 // An angle p f (position times radians per position) matters modulo a turn
 // only: f / 2 pi is rounded to 64-bit fixed point on the host, and the
 // product with the integer position, modulo 2^64, is the fraction of a turn
-// (error below |p| 2^-64). Its top bits choose the quadrant, the rest is an
+// (error below |p| (2^-64 + |f| 2^-67)). Its top bits choose the quadrant, the rest is an
 // angle in [-pi/4, pi/4] for the Taylor polynomials of sine and cosine. A
 // wavefront computes its lanes' sines once per token and then goes over the
 // heads of the token.
 #include "attn.h"
 #include "common.h"
 #include "launch.h"
-
-#include <math.h>
 
 #include <algorithm>
 
@@ -247,6 +245,21 @@ bool run_aligned(const void *p, int type, int64_t s0, int64_t s1) {
   return reinterpret_cast<uintptr_t>(p) % bytes == 0 && s0 % 4 == 0 && s1 % 4 == 0;
 }
 
+// f / 2 pi in units of 2^-64, modulo 1, to within a unit: f is m 2^e with a
+// 53-bit integer m, and m 2^65 / pi an integer product of 117 bits.
+uint64_t to_turn(double f) {
+  const uint64_t bits = __builtin_bit_cast(uint64_t, f);
+  const int e = static_cast<int>(bits >> 52 & 0x7FF);
+  if (e == 0) return 0;  // zero, or far below any angle
+  const uint64_t m = (bits & 0xFFFFFFFFFFFFFull) | 0x10000000000000ull;
+  const unsigned __int128 product = static_cast<unsigned __int128>(m) * 0xA2F9836E4E44152Aull;  // 2^65 / pi
+  const int shift = 1077 - e;  // f = m 2^(e - 1075); 64 fraction bits, and 66 in the constant
+  uint64_t t = 0;
+  if (shift < 128)  // and above 47, |f| being at most 64
+    t = static_cast<uint64_t>((product + (static_cast<unsigned __int128>(1) << (shift - 1))) >> shift);
+  return f < 0 ? 0 - t : t;
+}
+
 template <int F>
 hipError_t run(const qmm_head_part *parts, int n_parts, int64_t n_tokens, int64_t head_dim, float eps,
                const int32_t *positions, const double *freqs, int64_t n_freqs, int pairs, const int32_t *slots,
@@ -261,12 +274,7 @@ hipError_t run(const qmm_head_part *parts, int n_parts, int64_t n_tokens, int64_
   a.neighbours = pairs == QMM_ROPE_NEIGHBOURS, a.n_slots = static_cast<int>(n_slots);
   a.eps = eps, a.inv_dim = 1.f / static_cast<float>(head_dim);
   // a frequency in turns per position, modulo whole turns (positions are integers)
-  for (int64_t i = 0; i < n_freqs; ++i) {
-    long double t = static_cast<long double>(freqs[i]) * 0.159154943091895335768883763372514362L;
-    if (t < 0.0L || t >= 1.0L) t -= floorl(t);
-    t = t * 18446744073709551616.0L + 0.5L;
-    a.turn[i] = t >= 18446744073709551616.0L ? 0 : static_cast<uint64_t>(t);
-  }
+  for (int64_t i = 0; i < n_freqs; ++i) a.turn[i] = to_turn(freqs[i]);
   // two runs per lane, rounded up: one more unit than runs / 2 may be needed
   // where the rotated and the plain part both end in half a unit
   const int v = wide ? 4 : 1;

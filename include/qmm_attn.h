@@ -124,7 +124,7 @@ typedef struct qmm_head_part {
  *   eps             >= 0, finite
  *   positions       int32 [n_tokens], any value; needed if a part rotates
  *   freqs           HOST array of n_freqs doubles, radians per position,
- *                   finite; read during the call
+ *                   magnitudes at most 64; read during the call
  *   n_freqs         0 .. head_dim / 2; at least 1 if a part rotates
  *   slots, n_slots  int32 [n_tokens]; needed if a part is slotted. A token
  *                   whose slot lies outside [0, n_slots) is not stored (so
@@ -138,7 +138,7 @@ typedef struct qmm_head_part {
  * or n_tokens (QMM_ERR_STRIDE). Y may be X itself, with equal types and
  * strides and not slotted; otherwise no Y overlaps any X or another Y.
  * Numerics: fp32, the norm's sum included; an angle is reduced to a turn in
- * 64-bit fixed point (error below 2^-32 of a turn at any position) before
+ * 64-bit fixed point (error below 2^-30 of a turn at any position) before
  * sine and cosine. n_tokens == 0 is a no-op. n_tokens, n_slots < 2^31;
  * every offset <= 2^60 elements.
  */
@@ -208,7 +208,7 @@ int qmm_attn_prompt(int type, const qmm_heads *Q, const qmm_heads *K, const qmm_
  *   scale        finite and > 0
  *   workspace    at least qmm_attn_shared_workspace_bytes(...) bytes, 16-byte
  *                aligned; partial results, overwritten; two calls in flight
- *                must not share one
+ *                must not share one. May be NULL when that size is 0.
  * Numerics as qmm_attn_prompt; partial results are joined in fp32 in a fixed
  * order. n_seqs == 0 is a no-op. n_seqs, prefix_len, own_cap < 2^31 - 2^20,
  * n_seqs * n_q_heads < 2^31 - 2^20.
