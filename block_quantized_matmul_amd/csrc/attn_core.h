@@ -303,24 +303,6 @@ template <int N, int AHEAD, int READS, int VALU, int TRANS> __device__ __forcein
   __builtin_amdgcn_sched_barrier(0);
 }
 
-// One block of 32 * NT keys whose K and V tiles lie at LDS byte addresses kt
-// and vt. With MASK, a lane's row takes the block's first `lim` keys only;
-// rows past them in V must be finite or attended to by the row anyway.
-template <class E, int D, int NT, bool MASK>
-__device__ __forceinline__ void attend(uint32_t kt, uint32_t vt, const typename E::v8 q[D / 16], AttnState<D> &st,
-                                       float c, int lim, int lane) {
-  float16_t s[NT];
-  typename E::v8 p[2 * NT];
-  scores<E, D, NT>(kt, q, s, lane);
-  interleave<D / 16 * NT, 4, 1, 0, 0>();
-  if (MASK) mask_scores<NT>(s, lim, lane);
-  follow_max<D>(st, row_max<NT>(s) * c);
-  weights<E, D, NT>(s, st, c, p);
-  __builtin_amdgcn_sched_barrier(0);
-  add_values<E, D, NT>(v_addr<D>(vt, lane), p, st);
-  interleave<2 * NT * (D / 32), 3, 2, 0, 0>();
-}
-
 // A workgroup of four wavefronts, 32 rows each, over keys 0 .. n_keys - 1 in
 // blocks of 64, with two buffers of a K and a V tile each in LDS.
 //

@@ -237,7 +237,8 @@ template <class E, int D> __global__ __launch_bounds__(kThreads, 2) void attn_di
                      static_cast<const one *>(a.v) + seq * a.vs + g * a.vh, a.vt, len, q, st, a.c, lds, wave, lane);
   join_wavefronts<D>(st, lds, wave, lane);
   if (wave != 3) return;
-  const float f = bad ? __builtin_bit_cast(float, 0x7FC00000u) : st.l == 0.f ? 0.f : 1.f / st.l;
+  // without a key a row of zeros; with keys, but no weight (every score -infinity), 0 / 0
+  const float f = bad ? __builtin_bit_cast(float, 0x7FC00000u) : a.prefix_len == 0 && len == 0 ? 0.f : 1.f / st.l;
   store_row<E, D>(static_cast<one *>(a.o) + seq * a.ot + head * a.oh, st, f, lane, row < a.group);
 }
 
@@ -301,7 +302,7 @@ template <class E, int D> __global__ __launch_bounds__(kThreads) void attn_join_
   if (part != 0) return;
 #pragma unroll
   for (int k = 1; k < kParts; ++k) o += sums[k][e], sum += weights[k];
-  const float f = sum == 0.f ? 0.f : 1.f / sum;
+  const float f = a.prefix_len == 0 && len == 0 ? 0.f : 1.f / sum;  // with keys, but no weight, 0 / 0
   const bool bad = len < 0 || len > a.own_cap;
   typename E::v4 out;
 #pragma unroll

@@ -90,6 +90,23 @@ def test_nothing_past_a_length_counts(bad, prefix):
     assert (np.abs(o - want)[ok] <= err[ok]).all()
 
 
+@pytest.mark.parametrize("prefix,cap", [(90, 70), (1090, 70), (200, 1000)])
+def test_scores_of_minus_infinity(prefix, cap):
+    """A key whose score is -infinity has no weight; a row with keys, but without any weight, is 0 / 0."""
+    b, hq, hkv, dim = 4, 4, 2, 64
+    q, pk, pv, k, v = _inputs(7, b, prefix, cap, hq, hkv, dim, "f16")
+    q[:, :, 0] = 1.0
+    pk[:, :, 0] = -float("inf")
+    lengths = [0, 1, 33, 70]
+    want, err = O.attn_shared(f64(q), None, None, f64(k), f64(v), lengths, 0.125, "f16")
+    want[0] = np.nan
+    say(f"shared scores of -inf, prefix {prefix}")
+    assert_within(_run(q, pk, pv, k, v, lengths), want, err, "no weight in the prefix")
+    k[2, :, :, 0] = -float("inf")
+    want[2] = np.nan
+    assert_within(_run(q, pk, pv, k, v, lengths), want, err, "no weight at all")
+
+
 def test_lengths_outside_the_cache_give_nan_rows():
     for prefix in (40, 1040):
         q, pk, pv, k, v = _inputs(4, 5, prefix, 16, 2, 1, 64, "f16")
