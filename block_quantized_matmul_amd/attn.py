@@ -5,8 +5,9 @@ binding that only marshals arguments, like the package's other functions:
 tensors supply pointers, strides and sizes, and the library checks and runs.
 All tensors of a call are on one GPU, which need not be the current one; work
 is enqueued on `stream`, or on that GPU's current stream. Memory a call
-allocates (an output or a workspace that was not passed) is kept from reuse
-until the stream has passed the call.
+allocates (an output or a workspace that was not passed) belongs to the call's
+stream, and an output may also be used on the current one (after waiting for
+the call).
 """
 from __future__ import annotations
 
@@ -128,9 +129,13 @@ class _Place:
             self.handle, self.foreign = stream.cuda_stream, stream
 
     def empty(self, shape, dtype):
-        t = self.like.new_empty(shape, dtype=dtype)
-        if self.foreign is not None:
-            t.record_stream(self.foreign)
+        import torch
+        if self.foreign is None:
+            return self.like.new_empty(shape, dtype=dtype)
+        # memory of the call's stream: what the current one freed may still be written by work enqueued there
+        with torch.cuda.stream(self.foreign):
+            t = self.like.new_empty(shape, dtype=dtype)
+        t.record_stream(torch.cuda.current_stream(self.device))
         return t
 
     def workspace(self, given, need, what):

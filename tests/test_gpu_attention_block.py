@@ -198,3 +198,27 @@ def test_two_streams_at_once():
     for res in results:
         for got, want in zip(res, alone):
             assert torch.equal(got, want)
+
+
+def test_memory_of_another_stream():
+    """What a call on another stream allocates is not memory that pending work of the current stream still writes."""
+    r = rng(12)
+    x = torch.from_numpy(r.standard_normal((700, 512)).astype(np.float32)).cuda()
+    a = torch.from_numpy(r.standard_normal((2, 8, 512)) / 20).half().cuda()
+    b = torch.from_numpy(r.standard_normal((2, 1024, 8))).half().cuda()
+    ids = _ints(r.integers(0, 2, 700))
+    say("another stream's memory")
+    want = qmm.qmm_lora(x, a, b, ids)
+    torch.cuda.synchronize()
+    torch.cuda.empty_cache()
+    s = torch.cuda.Stream()
+    dropped = [torch.empty(700, 1024, device="cuda") for _ in range(4)]
+    dropped += [torch.empty(qmm.qmm_lora_workspace_bytes(700, 512, 8), dtype=torch.uint8, device="cuda")
+                for _ in range(4)]
+    torch.cuda._sleep(30_000_000)  # some 15 ms
+    for t in dropped:
+        t.fill_(7)
+    del dropped, t
+    got = qmm.qmm_lora(x, a, b, ids, stream=s)
+    torch.cuda.synchronize()
+    assert torch.equal(got, want)
