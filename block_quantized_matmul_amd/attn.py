@@ -12,6 +12,7 @@ the call).
 from __future__ import annotations
 
 import ctypes
+import struct
 from typing import NamedTuple, Optional
 
 import block_quantized_matmul_amd as _qmm
@@ -61,10 +62,14 @@ class qmm_head_part(NamedTuple):
 
 _ready = None
 _types = {}
+_calls = {}
+torch = None  # imported with the library, at the first call
+_part_bytes = struct.Struct("@PiqqPiqqqiPii0P").pack  # a qmm_head_part_desc's
+_heads_bytes = struct.Struct("@Pqqq").pack  # a qmm_heads_desc's
 
 
 def _lib():
-    global _ready
+    global _ready, torch
     if _ready is None:
         import torch
         _types.update({torch.float32: QMM_T_F32, torch.float16: QMM_T_F16, torch.bfloat16: QMM_T_BF16})
@@ -84,13 +89,17 @@ def _lib():
         L.qmm_attn_shared.restype = _i32
         L.qmm_attn_shared_workspace_bytes.argtypes = [_i64] * 6
         L.qmm_attn_shared_workspace_bytes.restype = _i64
+        # the same functions for this module, which passes host structs as bytes
+        for name in ("qmm_norm_rope", "qmm_attn_prompt", "qmm_attn_shared"):
+            f = _calls[name] = L[name]
+            f.argtypes = [_vp if issubclass(t, ctypes._Pointer) else t for t in getattr(L, name).argtypes]
+            f.restype = _i32
         _ready = L
     return _ready
 
 
 def _refuse(named):
     """Raises what is wrong with the places of a call's (name, tensor) pairs."""
-    import torch
     first = None
     for name, t in named:
         if t is None:
@@ -110,7 +119,6 @@ class _Place:
     __slots__ = ("device", "handle", "foreign", "like")
 
     def __init__(self, stream, names, tensors):
-        import torch
         try:
             device = tensors[0].get_device()
             for t in tensors:
@@ -129,7 +137,6 @@ class _Place:
             self.handle, self.foreign = stream.cuda_stream, stream
 
     def empty(self, shape, dtype):
-        import torch
         if self.foreign is None:
             return self.like.new_empty(shape, dtype=dtype)
         # memory of the call's stream: what the current one freed may still be written by work enqueued there
@@ -140,7 +147,6 @@ class _Place:
 
     def workspace(self, given, need, what):
         """The call's workspace (the caller's, or a new one), its pointer and size."""
-        import torch
         if need < 0:
             raise _qmm.QmmError(int(need), what)
         if given is None:
@@ -153,7 +159,6 @@ class _Place:
 
     def run(self, function, what, *args):
         """The library's function with the tensors' GPU current."""
-        import torch
         if torch._C._cuda_getDevice() == self.device:
             status = function(*args, self.handle)
         else:
@@ -172,7 +177,6 @@ def _type(t, name):
 
 def _ints(t, name, n):
     """A contiguous int32 vector of n elements (None: any number)."""
-    import torch
     shape = t.shape
     if t.dtype is not torch.int32 or len(shape) != 1 or not t.is_contiguous():
         raise TypeError(f"{name} must be a contiguous 1-D int32 tensor")
@@ -181,7 +185,6 @@ def _ints(t, name, n):
 
 
 def _floats(t, name, shape):
-    import torch
     if t.dtype is not torch.float32 or not t.is_contiguous():
         raise TypeError(f"{name} must be a contiguous float32 tensor")
     if t.shape != shape:
@@ -196,13 +199,13 @@ def _strides(t, name):
 
 
 def _heads(t, name, shape, dtype):
-    """qmm_heads of a tensor of `shape`: [tokens][heads][dim] or [seqs][tokens][heads][dim]."""
+    """qmm_heads (as bytes) of a tensor of `shape`: [tokens][heads][dim] or [seqs][tokens][heads][dim]."""
     if t.dtype is not dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
     if t.shape != shape:
         raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
     st = _strides(t, name)
-    return qmm_heads_desc(t.data_ptr(), st[0] if len(st) == 4 else 0, st[-3], st[-2])
+    return _heads_bytes(t.data_ptr(), st[0] if len(st) == 4 else 0, st[-3], st[-2])
 
 
 def _ptr(t):
@@ -223,7 +226,7 @@ def qmm_lora(X, A, B, ids, scales=None, base=None, Y=None, workspace=None, strea
     1, base fp32 [n_tokens][n_rows] or None for zeros; all contiguous. Y (fp32
     [n_tokens][n_rows]) is allocated if None, and may be base. Without a
     workspace, one of qmm_lora_workspace_bytes bytes is allocated."""
-    import torch
+    L = _lib()
     place = _Place(stream, ("X", "A", "B", "ids", "scales", "base", "Y", "workspace"),
                    (X, A, B, ids, scales, base, Y, workspace))
     if X.dtype is not torch.float32 and X.dtype is not torch.float16:
@@ -246,7 +249,6 @@ def qmm_lora(X, A, B, ids, scales=None, base=None, Y=None, workspace=None, strea
         Y = place.empty((n, n_rows), torch.float32)
     else:
         _floats(Y, "Y", (n, n_rows))
-    L = _lib()
     _keep, ws, ws_bytes = place.workspace(workspace, L.qmm_lora_workspace_bytes(n, k, rank),
                                           "qmm_lora_workspace_bytes")
     place.run(L.qmm_lora, "qmm_lora", X.data_ptr(), QMM_T_F32 if X.dtype is torch.float32 else QMM_T_F16, n, k,
@@ -257,7 +259,6 @@ def qmm_lora(X, A, B, ids, scales=None, base=None, Y=None, workspace=None, strea
 
 def _host_doubles(freqs):
     """(pointer, count, object that owns the memory) of the host table of frequencies."""
-    import torch
     if freqs is None:
         return None, 0, None
     if isinstance(freqs, torch.Tensor):
@@ -277,6 +278,7 @@ def qmm_norm_rope(parts, positions=None, freqs=None, pairs="halves", eps=1e-6, s
     sequence), read during the call; pairs "halves" or "neighbours"; slots
     int32 [n_tokens], the rows of the slotted parts' Y (one outside it: the
     token is not stored). Returns the Ys."""
+    _lib()
     parts = [p if isinstance(p, qmm_head_part) else qmm_head_part(*p) for p in parts]
     if not parts:
         return []
@@ -290,10 +292,9 @@ def qmm_norm_rope(parts, positions=None, freqs=None, pairs="halves", eps=1e-6, s
         raise ValueError("X must be [n_tokens][n_heads][head_dim]")
     n, _, dim = parts[0].X.shape
     vector = (dim,)
-    L = _lib()
-    descs = (qmm_head_part_desc * QMM_HEAD_PARTS_MAX)()
+    descs = b""
     n_slots = None
-    for i, (X, Y, norm, weight, rotate, slotted) in enumerate(parts):
+    for X, Y, norm, weight, rotate, slotted in parts:
         xs, ys = X.shape, Y.shape
         if len(xs) != 3 or xs[0] != n or xs[2] != dim:
             raise ValueError("every X must be [n_tokens][n_heads][head_dim] with one n_tokens and head_dim")
@@ -311,15 +312,20 @@ def qmm_norm_rope(parts, positions=None, freqs=None, pairs="halves", eps=1e-6, s
             if not norm:
                 raise ValueError("weight needs norm")
             _floats(weight, "weight", vector)
-        xst, yst = _strides(X, "X"), _strides(Y, "Y")
-        descs[i] = qmm_head_part_desc(X.data_ptr(), _type(X, "X"), xst[0], xst[1], Y.data_ptr(), _type(Y, "Y"), yst[0],
-                                      yst[1], xs[1], bool(norm), _ptr(weight), bool(rotate), bool(slotted))
+        xst, yst = X.stride(), Y.stride()
+        if xst[2] != 1 or yst[2] != 1:
+            _strides(X, "X"), _strides(Y, "Y")
+        xt, yt = _types.get(X.dtype), _types.get(Y.dtype)
+        if xt is None or yt is None:
+            _type(X, "X"), _type(Y, "Y")
+        descs += _part_bytes(X.data_ptr(), xt, xst[0], xst[1], Y.data_ptr(), yt, yst[0], yst[1], xs[1], bool(norm),
+                             0 if weight is None else weight.data_ptr(), bool(rotate), bool(slotted))
     if positions is not None:
         _ints(positions, "positions", n)
     if slots is not None:
         _ints(slots, "slots", n)
     fp, n_freqs, _keep = _host_doubles(freqs)
-    place.run(L.qmm_norm_rope, "qmm_norm_rope", descs, len(parts), n, dim, eps, _ptr(positions), fp, n_freqs,
+    place.run(_calls["qmm_norm_rope"], "qmm_norm_rope", descs, len(parts), n, dim, eps, _ptr(positions), fp, n_freqs,
               _PAIRS[pairs], _ptr(slots), n_slots or 0)
     return [p.Y for p in parts]
 
@@ -333,6 +339,7 @@ def qmm_attn_prompt(Q, K, V, seq_starts, scale=None, O=None, stream=None):
     seq_starts[i] .. seq_starts[i + 1] - 1. scale defaults to
     head_dim ** -0.5. O (like Q) is allocated if None; rows of tokens outside
     every sequence are not written."""
+    _lib()
     place = _Place(stream, ("Q", "K", "V", "seq_starts", "O"), (Q, K, V, seq_starts, O))
     if Q.dim() != 3 or K.dim() != 3:
         raise ValueError("Q must be [n_tokens][n_q_heads][head_dim], K and V [n_tokens][n_kv_heads][head_dim]")
@@ -345,8 +352,7 @@ def qmm_attn_prompt(Q, K, V, seq_starts, scale=None, O=None, stream=None):
     if O is None:
         O = place.empty(shape, dtype)
     kv = (n, hkv, dim)
-    L = _lib()
-    place.run(L.qmm_attn_prompt, "qmm_attn_prompt", _type(Q, "Q"), _heads(Q, "Q", shape, dtype),
+    place.run(_calls["qmm_attn_prompt"], "qmm_attn_prompt", _type(Q, "Q"), _heads(Q, "Q", shape, dtype),
               _heads(K, "K", kv, dtype), _heads(V, "V", kv, dtype), _heads(O, "O", shape, dtype), n, hq, hkv, dim,
               seq_starts.data_ptr(), seq_starts.shape[0] - 1, dim ** -0.5 if scale is None else scale)
     return O
@@ -370,6 +376,7 @@ def qmm_attn_shared(Q, PK, PV, K, V, lengths, scale=None, O=None, workspace=None
     of NaNs. scale defaults to head_dim ** -0.5. O (like Q) is allocated if
     None. Without a workspace, one of qmm_attn_shared_workspace_bytes bytes is
     allocated."""
+    L = _lib()
     place = _Place(stream, ("Q", "PK", "PV", "K", "V", "lengths", "O", "workspace"),
                    (Q, PK, PV, K, V, lengths, O, workspace))
     if (PK is None) != (PV is None) or (K is None) != (V is None) or (K is None) != (lengths is None):
@@ -392,10 +399,9 @@ def qmm_attn_shared(Q, PK, PV, K, V, lengths, scale=None, O=None, workspace=None
         own = (n, cap, hkv, dim)
         k, v = _heads(K, "K", own, dtype), _heads(V, "V", own, dtype)
         _ints(lengths, "lengths", n)
-    L = _lib()
     _keep, ws, ws_bytes = place.workspace(workspace, L.qmm_attn_shared_workspace_bytes(n, prefix, cap, hq, hkv, dim),
                                           "qmm_attn_shared_workspace_bytes")
-    place.run(L.qmm_attn_shared, "qmm_attn_shared", _type(Q, "Q"), _heads(Q, "Q", shape, dtype), pk, pv, prefix, k, v,
-              cap, _ptr(lengths), _heads(O, "O", shape, dtype), n, hq, hkv, dim, dim ** -0.5 if scale is None else scale,
-              ws, ws_bytes)
+    place.run(_calls["qmm_attn_shared"], "qmm_attn_shared", _type(Q, "Q"), _heads(Q, "Q", shape, dtype), pk, pv,
+              prefix, k, v, cap, _ptr(lengths), _heads(O, "O", shape, dtype), n, hq, hkv, dim,
+              dim ** -0.5 if scale is None else scale, ws, ws_bytes)
     return O

@@ -315,14 +315,14 @@ template <int N, int AHEAD, int READS, int VALU, int TRANS> __device__ __forcein
 // ahead, V one.
 //
 // A wavefront's rows need its first `mine` blocks (>= 1; without CAUSAL also
-// 0, for a wavefront that only copies); the first `full` (< mine) of them are taken whole by all its rows, of the others a lane's row
-// takes keys below lim.
+// 0, for a wavefront that only copies); the first `full` (< mine) of them are
+// taken whole by all its rows, of the others a lane's row takes keys below lim.
 //
 // A masked key's weight is zero, but zero times a non-finite value is a NaN.
 // With CAUSAL, the values of the blocks from first_masked on (at most any
-// wavefront's `full`, and the same for all) are therefore looked over, and true is returned where the
-// wavefront's masked blocks held an infinity or a NaN: its rows have to be
-// computed another way then. Without CAUSAL all rows share one end, behind
+// wavefront's `full`, and the same for all) are therefore looked over, and
+// true is returned where the wavefront's masked blocks held an infinity or a
+// NaN: its rows have to be computed another way then. Without CAUSAL all rows share one end, behind
 // which copied rows only repeat the last.
 constexpr int kKeys = 64;
 template <int D> constexpr int attend_lds_bytes() { return 4 * kKeys * D * 2 + 32; }

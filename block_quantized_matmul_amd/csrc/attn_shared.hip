@@ -8,12 +8,12 @@
 //
 // The prefix is read once for all sequences: the rows of all sequences and of
 // the heads that share a KV head are flattened (row x: sequence x / group,
-// head g group + x % group) into equal tiles of at most 128, four wavefronts of 32
-// rows on blocks of 64 keys, as the prompt kernel runs without its mask. A sequence's
-// own cache serves only `group` rows, so there a workgroup's four wavefronts
-// share one tile of 32 rows and split the piece's keys, each with blocks of
-// 32 keys of its own (copied into its own part of LDS, no barrier), and join
-// at the end through LDS.
+// head g group + x % group) into equal tiles of at most 128, four wavefronts
+// of 32 rows on blocks of 64 keys, as the prompt kernel runs without its mask.
+// A sequence's own cache serves only `group` rows, so there a workgroup's four
+// wavefronts share one tile of 32 rows and split the piece's keys, each with
+// blocks of 32 keys of its own (copied into its own part of LDS, no barrier),
+// and join at the end through LDS.
 //
 // Both kinds of pieces are workgroups of one launch and alternate in it, since
 // the prefix's are bound by the matrix cores and the caches' by memory. A

@@ -77,9 +77,9 @@ extern "C" {
  * Numerics: A, B and an fp16 X are multiplied exactly and summed in fp32; an
  * fp32 X is not rounded; V stays in fp32. Non-finite values of one token's
  * X or of an adapter stay in the rows of the tokens that use them.
- * n_tokens == 0 or n_rows == 0 is a no-op. Sizes: n_tokens, k, n_rows,
- * n_adapters < 2^31, n_tokens * k, n_tokens * n_rows,
- * n_adapters * rank * k, n_adapters * n_rows * rank <= 2^60 (QMM_ERR_SHAPE).
+ * n_tokens == 0 or n_rows == 0 is a no-op. Sizes: n_tokens < 2^25, k < 2^24,
+ * n_rows, n_adapters < 2^31, n_tokens * n_rows, n_adapters * rank * k,
+ * n_adapters * n_rows * rank <= 2^60 (QMM_ERR_SHAPE).
  */
 int qmm_lora(const void *X, int x_type, int64_t n_tokens, int64_t k, const uint16_t *A, const uint16_t *B,
              int64_t n_adapters, int64_t rank, int64_t n_rows, const float *scales, const int32_t *ids,
@@ -131,15 +131,16 @@ typedef struct qmm_head_part {
  *                   -1 leaves it out). Two tokens with one slot: either's
  *                   values remain, element by element.
  * Pointers are aligned to their element type (positions, slots and weight to
- * 4). Strides are >= 0 (those of axes of one element are not
- * used), and two different heads of Y must not share
- * elements: y_row_stride >= (n_heads - 1) * y_head_stride + head_dim, or
+ * 4). Strides are >= 0 (those of axes of one element are not used), and two
+ * different heads of Y must not share elements:
+ * y_row_stride >= (n_heads - 1) * y_head_stride + head_dim, or
  * y_head_stride >= (rows - 1) * y_row_stride + head_dim with rows = n_slots
  * or n_tokens (QMM_ERR_STRIDE). Y may be X itself, with equal types and
  * strides and not slotted; otherwise no Y overlaps any X or another Y.
- * Numerics: fp32, the norm's sum included; an angle is reduced to a turn in
- * 64-bit fixed point (error below 2^-30 of a turn at any position) before
- * sine and cosine. n_tokens == 0 is a no-op. n_tokens, n_slots < 2^31;
+ * Numerics: fp32, the norm's sum included (a head whose squares leave fp32's
+ * range is normed as if by infinity or by sqrt(eps)); an angle is reduced to
+ * a turn in 64-bit fixed point (error below 2^-30 of a turn at any position)
+ * before sine and cosine. n_tokens == 0 is a no-op. n_tokens, n_slots < 2^31;
  * every offset <= 2^60 elements.
  */
 int qmm_norm_rope(const qmm_head_part *parts, int n_parts, int64_t n_tokens, int64_t head_dim, float eps,
@@ -170,7 +171,8 @@ typedef struct qmm_heads {
  *   head_dim     64 or 128
  *   seq_starts   int32 [n_seqs + 1], non-decreasing within [0, n_tokens].
  *                Device data: a sequence whose two ends are not so is left
- *                out. Sequences may be empty.
+ *                out, and where others then overlap, their tokens' rows are
+ *                undefined. Sequences may be empty.
  *   scale        finite and > 0 (usually 1 / sqrt(head_dim))
  * Tokens outside every sequence keep their rows of O, and their Q, K and V
  * are not read. O must not overlap Q, K or V, nor two of its own heads each
@@ -178,10 +180,10 @@ typedef struct qmm_heads {
  * Numerics: scores, the softmax's maximum and sum, and the output's sum in
  * fp32; each weight, relative to a reference within a factor 2^8 of the
  * largest so far, is rounded to `type` for the matrix cores, and the output
- * once at the end. A non-finite K or V
- * of a later token does not reach an earlier one. n_tokens == 0 or
- * n_seqs == 0 is a no-op. n_tokens, n_seqs < 2^31 - 128 and n_tokens *
- * n_q_heads < 2^31 - 2^20.
+ * once at the end. A non-finite K or V of a later token does not reach an
+ * earlier one; where one is attended to, the outputs it enters are not finite
+ * (infinite or NaN). n_tokens == 0 or n_seqs == 0 is a no-op. n_tokens,
+ * n_seqs < 2^31 - 128 and n_tokens * n_q_heads < 2^31 - 2^20.
  */
 int qmm_attn_prompt(int type, const qmm_heads *Q, const qmm_heads *K, const qmm_heads *V, const qmm_heads *O,
                     int64_t n_tokens, int64_t n_q_heads, int64_t n_kv_heads, int64_t head_dim,
@@ -199,7 +201,7 @@ int qmm_attn_prompt(int type, const qmm_heads *Q, const qmm_heads *K, const qmm_
  *   PK, PV       [prefix_len], n_kv_heads heads; may be NULL if prefix_len is 0
  *   K, V         sequence b at seq_stride * b, own_cap tokens, n_kv_heads
  *                heads; may be NULL if own_cap is 0
- *   lengths      int32 [n_seqs]; may be NULL if own_cap is 0. A length of 0
+ *   lengths      int32 [n_seqs]; not read if own_cap is 0. A length of 0
  *                with prefix_len 0 gives a row of zeros. Device data: a
  *                length outside [0, own_cap] gives that sequence rows of
  *                quiet NaNs, and its cache is not read. Nothing at or past a
