@@ -17,14 +17,23 @@
 //    sorts anything, and all adapters run at once;
 //  * more tokens (prompts: the tokens of a request stand together), 64
 //    consecutive tokens, so that an operand of A or B serves four products. A
-//    tile that does hold several adapters takes them one after another and
-//    keeps, in each token's column, its own adapter's result. Neighbouring
-//    tiles go to one XCD, whose L2 then holds their adapters and their V.
+//    tile that does hold several adapters deals them to two workgroups, which
+//    take theirs one after another and keep, in each token's column, its own
+//    adapter's result.
 // Columns do not mix, so a non-finite value of another token or adapter stays
 // out in both.
 //
 // The first launch splits k and leaves partial sums of V in the workspace,
-// which the second adds in order (no atomics).
+// which the second adds in order (no atomics; for consecutive tiles a launch
+// between them does).
+//
+// Measured: 1 token, 4096 x 4096, rank 16, fp32 X 7 us for both launches in a
+// graph (latency); 64 tokens on 32 adapters, 4096 to 11008 rows, 16 us (22 MB,
+// of which 15 are the adapters: 4.5 us at a copy's rate; the rest is the two
+// launches' latencies: ids, then operands, then the sum); 2048 fp16 tokens of
+// 9 requests, 11008 to 4096 rows, rank 64, 61 us: down 25 (45 MB, 1.8 TB/s),
+// sum 5, up 32 (67 MB, 2.1 TB/s; its fp32 products alone are 7); 8192 fp32
+// tokens, 4096 x 4096, rank 32, 119 us (402 MB, 3.4 TB/s).
 #include "attn.h"
 #include "common.h"
 #include "launch.h"
@@ -41,6 +50,11 @@ constexpr int kSub = 4;             // products' tokens per consecutive tile
 constexpr int kGroupTokens = 512;   // largest batch in tiles by adapter
 constexpr int kGroupSlab = 64;      // k per wavefront and round, tiles by adapter
 constexpr int kMaxSplits = 256;     // ranges of k, tiles by adapter
+// Workgroups among which a consecutive tile's adapters are dealt: most tiles
+// have one adapter, and those where requests meet two. 2048 tokens of 9
+// requests 61 us, with one workgroup for all of a tile's adapters 66, with four
+// 67 (the workgroups that leave at once cost more than they save).
+constexpr int kShares = 2;
 constexpr int kRankGroup = 64;      // ranks per workgroup of the first launch
 constexpr int kTileGroups = 512;    // workgroups the first launch aims at, consecutive tiles
 
@@ -96,13 +110,28 @@ template <int TT, class F> __device__ __forceinline__ void each_adapter(const in
     f(a);
   }
 }
-// The tile of workgroup b of `chunks` per tile: each of the 8 XCDs (workgroups
-// go round them) takes neighbouring tiles.
-__device__ __forceinline__ void xcd_tile(int b, int chunks, int tiles, int &tile, int &chunk) {
-  const int per = (tiles + 7) / 8;
-  tile = b % 8 * per + b / 8 / chunks;
-  chunk = b / 8 % chunks;
-  if (b / 8 / chunks >= per) tile = tiles;
+// Consecutive tiles: the tokens (as bits) whose adapters fall to this share of
+// a tile's workgroups, the tile's adapters being dealt to its kShares shares
+// in the order of their first tokens. Lane l of the wavefront has token l's id.
+__device__ __forceinline__ uint64_t share_of(int id, int n_adapters, int share) {
+  static_assert(kTok * kSub == 64, "a lane per token");
+  uint64_t left = __ballot(id >= 0 && id < n_adapters), mine = 0;
+  for (int j = 0; left != 0; j = (j + 1) % kShares) {
+    const uint64_t with = __ballot(id == __builtin_amdgcn_readlane(id, __builtin_ctzll(left)));
+    if (j == share) mine |= with;
+    left &= ~with;
+  }
+  return mine;
+}
+// Consecutive tiles: workgroup b's share, tile and part of the tile's work, of
+// `parts` (padded). The parts are the fastest index, so that one XCD
+// (workgroups go round them) gets the same parts of all tiles: its L2 then
+// holds those of the adapters, and the XCDs have equal work. The last share
+// comes first: where a tile has one adapter, its workgroups leave at once.
+__device__ __forceinline__ void tile_of(int b, int parts, int tiles, int &share, int &tile, int &part) {
+  part = b % parts;
+  tile = b / parts % tiles;
+  share = kShares - 1 - b / parts / tiles;
 }
 
 struct DownArgs {
@@ -112,11 +141,12 @@ struct DownArgs {
   float *v;  // [splits][n_tokens][rank]
   int64_t n_tokens, k, range;  // range: k per split
   int n_adapters, rank, splits;
+  int parts;  // consecutive tiles: splits, padded
 };
 
 // V^T = A X^T on one wavefront: 16 RT ranks of one adapter, TT tokens in each
-// of the lanes' columns, k from begin to end (multiples of 32). The C layout gives a
-// lane four consecutive ranks of token lane % 16. Operand element j of lane
+// of the lanes' columns, k from begin to end (multiples of 32). The C layout
+// gives a lane four consecutive ranks of token lane % 16. Operand element j of lane
 // group g = lane / 16 is the same k for both operands; which k it is does not
 // matter to the sum, so an fp32 lane takes 4 consecutive k per load and four
 // products. Loads run kSteps operands ahead.
@@ -160,8 +190,8 @@ template <bool XF16, int RT, int TT> struct Down {
         } else {
 #pragma unroll
           for (int i = 0; i < 4; ++i)
-            acc[r][t] =
-                __builtin_amdgcn_mfma_f32_16x16x4f32(static_cast<float>(c.a[s][r][i]), c.x[s][t][i], acc[r][t], 0, 0, 0);
+            acc[r][t] = __builtin_amdgcn_mfma_f32_16x16x4f32(static_cast<float>(c.a[s][r][i]), c.x[s][t][i],
+                                                             acc[r][t], 0, 0, 0);
         }
       }
   }
@@ -235,20 +265,20 @@ __global__ __launch_bounds__(kThreads, GROUP || RT < 4 ? 2 : 1) void lora_down_k
     token[0] = slot[lane & 15] < 0 ? t : slot[lane & 15];
   } else {
     const int tiles = static_cast<int>((p.n_tokens + kTok * TT - 1) / (kTok * TT));
-    int tile;
-    xcd_tile(blockIdx.x, p.splits, tiles, tile, split);
-    if (tile >= tiles) return;
+    int tile, share;
+    tile_of(blockIdx.x, p.parts, tiles, share, tile, split);
+    if (split >= p.splits) return;
     const int64_t t0 = static_cast<int64_t>(tile) * (kTok * TT);
-    if (threadIdx.x < kTok * TT) {
-      const int64_t t = t0 + threadIdx.x;
-      const int a = t < p.n_tokens ? p.ids[t] : -1;
-      slot[threadIdx.x] = a >= 0 && a < p.n_adapters ? static_cast<int>(t) : -1;
-    }
+    const int own = t0 + lane < p.n_tokens ? p.ids[t0 + lane] : -1;
+    const uint64_t mine = share_of(own, p.n_adapters, share);
+    if (mine == 0) return;
+    if (wave == 0) slot[lane] = mine >> lane & 1 ? static_cast<int>(t0) + lane : -1;
 #pragma unroll
     for (int t = 0; t < TT; ++t) {
-      const int64_t at = t0 + kTok * t + (lane & 15);
-      token[t] = at < p.n_tokens ? at : p.n_tokens - 1;
-      id[t] = at < p.n_tokens ? p.ids[at] : -1;
+      const int at = kTok * t + (lane & 15);
+      const int a = __shfl(own, at);
+      id[t] = mine >> at & 1 ? a : -1;
+      token[t] = t0 + (mine >> at & 1 ? at : __builtin_ctzll(mine));
     }
   }
   const int64_t part = p.range / 4;
@@ -286,6 +316,7 @@ struct UpArgs {
   int64_t n_tokens, n_rows;
   int n_adapters, rank, splits;
   int steps, chunks;  // steps per wavefront, workgroups per token tile
+  int parts;          // consecutive tiles: chunks, padded
 };
 
 // Four values from p[at .. at + 3] of n. VEC: n and at are multiples of 4 and
@@ -334,21 +365,29 @@ __global__ __launch_bounds__(kThreads, RQ <= 4 ? 2 : 1) void lora_up_kernel(UpAr
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int col = lane & 15, grp = lane >> 4;
   int chunk;
+  int any;  // one of the tile's tokens
   if constexpr (GROUP) {
     chunk = blockIdx.x % p.chunks;
+    any = blockIdx.x / p.chunks;
     int id;
-    if (!group_of(p.ids, static_cast<int>(p.n_tokens), blockIdx.x / p.chunks, slot, id)) return;
+    if (!group_of(p.ids, static_cast<int>(p.n_tokens), any, slot, id)) return;
     if (threadIdx.x < kTok) adapter[threadIdx.x] = slot[threadIdx.x] >= 0 ? id : -1;
   } else {
     const int tiles = static_cast<int>((p.n_tokens + kTok * TT - 1) / (kTok * TT));
-    int tile;
-    xcd_tile(blockIdx.x, p.chunks, tiles, tile, chunk);
-    if (tile >= tiles) return;
-    if (threadIdx.x < kTok * TT) {
-      const int64_t t = static_cast<int64_t>(tile) * (kTok * TT) + threadIdx.x;
-      slot[threadIdx.x] = t < p.n_tokens ? static_cast<int>(t) : -1;
-      adapter[threadIdx.x] = t < p.n_tokens ? p.ids[t] : -1;
+    int tile, share;
+    tile_of(blockIdx.x, p.parts, tiles, share, tile, chunk);
+    if (chunk >= p.chunks) return;
+    const int64_t t = static_cast<int64_t>(tile) * (kTok * TT) + lane;
+    const int own = t < p.n_tokens ? p.ids[t] : -1;
+    uint64_t mine = share_of(own, p.n_adapters, share);
+    // tokens without a product go with the first share
+    if (share == 0) mine |= __ballot(t < p.n_tokens && (own < 0 || own >= p.n_adapters));
+    if (mine == 0) return;
+    if (wave == 0) {
+      slot[lane] = mine >> lane & 1 ? static_cast<int>(t) : -1;
+      adapter[lane] = mine >> lane & 1 ? own : -1;
     }
+    any = static_cast<int>(t) - lane + __builtin_ctzll(mine);
   }
   __syncthreads();
   int id[TT];
@@ -361,7 +400,7 @@ __global__ __launch_bounds__(kThreads, RQ <= 4 ? 2 : 1) void lora_up_kernel(UpAr
   for (int t = 0; t < TT; ++t) {
     const int s = slot[kTok * t + col];
     live[t] = s >= 0;
-    const int64_t token = live[t] ? s : slot[0];
+    const int64_t token = live[t] ? s : any;
     id[t] = adapter[kTok * t + col];
     valid[t] = id[t] >= 0 && id[t] < p.n_adapters;
     base[t] = p.base ? p.base + token * p.n_rows : nullptr;
@@ -418,7 +457,7 @@ __global__ __launch_bounds__(kThreads, RQ <= 4 ? 2 : 1) void lora_up_kernel(UpAr
 #pragma unroll
     for (int e = 0; e < kEach; ++e) {
       const int i = threadIdx.x + e * kThreads < kItems ? threadIdx.x + e * kThreads : 0;
-      const int t = slot[i / (4 * RQ)] < 0 ? slot[0] : slot[i / (4 * RQ)];
+      const int t = slot[i / (4 * RQ)] < 0 ? any : slot[i / (4 * RQ)];
 #pragma unroll
       for (int u = 0; u < kParts; ++u)
         add[e][u] = load4<float4_t, VEC>(
@@ -514,6 +553,12 @@ __global__ __launch_bounds__(kThreads, RQ <= 4 ? 2 : 1) void lora_up_kernel(UpAr
   }
 }
 
+// Workgroups per tile, such that those of a part fall to one XCD of eight, or
+// to as few as they can.
+int64_t padded(int64_t parts) {
+  if (parts >= 8) return (parts + 7) / 8 * 8;
+  return parts > 4 ? 8 : parts > 2 ? 4 : parts;
+}
 bool by_adapter(int64_t n_tokens) { return n_tokens <= kGroupTokens; }
 // k per split: a multiple of 128, 32 for each of a workgroup's wavefronts.
 int64_t split_range(int64_t n_tokens, int64_t k) {
@@ -535,13 +580,13 @@ hipError_t launch_lora(const void *X, bool x_f16, int64_t n_tokens, int64_t k, c
                        const float *base, float *Y, float *partial, hipStream_t stream) {
   const bool group = by_adapter(n_tokens);
   const int splits = lora_splits(n_tokens, k, rank);
-  // workgroups per split or chunk: every token's (most leave at once), or
-  // those of 8 equal ranges of tiles
-  const int64_t tiles = (n_tokens + kTok * kSub - 1) / (kTok * kSub);
-  const int64_t groups = group ? n_tokens : (tiles + 7) / 8 * 8;
+  // workgroups per split or chunk: every token's (most leave at once), or every tile's
+  const int64_t groups = group ? n_tokens : (n_tokens + kTok * kSub - 1) / (kTok * kSub);
+  const int64_t parts = padded(splits);
   const DownArgs d{X, static_cast<const _Float16 *>(A), ids, partial, n_tokens, k, split_range(n_tokens, k),
-                   static_cast<int>(n_adapters), static_cast<int>(rank), splits};
-  const dim3 grid(static_cast<unsigned>(groups * splits), static_cast<unsigned>((rank + kRankGroup - 1) / kRankGroup));
+                   static_cast<int>(n_adapters), static_cast<int>(rank), splits, static_cast<int>(parts)};
+  const dim3 grid(static_cast<unsigned>(group ? groups * splits : groups * parts * kShares),
+                  static_cast<unsigned>((rank + kRankGroup - 1) / kRankGroup));
   auto down = [&](auto xf16, auto rt) {
     constexpr bool X16 = decltype(xf16)::value;
     constexpr int RT = decltype(rt)::value;
@@ -558,25 +603,29 @@ hipError_t launch_lora(const void *X, bool x_f16, int64_t n_tokens, int64_t k, c
 
   if (!group && splits > 1) {
     const int64_t n = n_tokens * rank;
-    const hipError_t f = launch(lora_sum_kernel, dim3(static_cast<unsigned>(std::min<int64_t>((n + kThreads - 1) / kThreads, 4096))),
-                                dim3(kThreads), 0, stream, partial, n, splits);
+    const int64_t blocks = std::min<int64_t>((n + kThreads - 1) / kThreads, 4096);
+    const hipError_t f =
+        launch(lora_sum_kernel, dim3(static_cast<unsigned>(blocks)), dim3(kThreads), 0, stream, partial, n, splits);
     if (f != hipSuccess) return f;
   }
 
   // Steps of 64 rows by adapter (256 bytes of a token's row), of 16 where
   // there are few or for consecutive tiles, whose step has 64 tokens; several
   // steps where there are workgroups enough, since each workgroup first adds
-  // up its tokens' V.
+  // up its tokens' V. On consecutive tiles V is little for ranks up to 32, and
+  // more workgroups balance better: 2048 tokens, 11008 rows, rank 16 72 us with
+  // 2048 wanted, 64 with 4096; 4096 rows, rank 64 60 with 2048, 53 with 1024.
   const bool vec = rank % 4 == 0 && reinterpret_cast<uintptr_t>(B) % 8 == 0 && n_rows % 4 == 0 &&
                    reinterpret_cast<uintptr_t>(Y) % 16 == 0 && reinterpret_cast<uintptr_t>(base) % 16 == 0;
   const int64_t rs = !group || !vec || rank > 64 || n_rows * groups < 4096 * 64 ? 1 : 4;
   const int64_t all = (n_rows + 64 * rs - 1) / (64 * rs);  // steps of a workgroup's four wavefronts
-  const int64_t steps = std::max({int64_t{1}, std::min<int64_t>(16 / rs, all * groups / 1024), (all * groups) >> 23});
+  const int64_t want = group || rank > 32 ? 1024 : 4096;
+  const int64_t steps = std::max({int64_t{1}, std::min<int64_t>(16 / rs, all * groups / want), (all * groups) >> 22});
   const int64_t chunks = (all + steps - 1) / steps;
   const UpArgs u{static_cast<const _Float16 *>(B), partial, scales, base, ids, Y, n_tokens, n_rows,
                  static_cast<int>(n_adapters), static_cast<int>(rank), group ? splits : 1, static_cast<int>(steps),
-                 static_cast<int>(chunks)};
-  const dim3 ugrid(static_cast<unsigned>(chunks * groups));
+                 static_cast<int>(chunks), static_cast<int>(padded(chunks))};
+  const dim3 ugrid(static_cast<unsigned>(group ? groups * chunks : groups * padded(chunks) * kShares));
   auto up = [&](auto rq) {
     constexpr int RQ = decltype(rq)::value;
     constexpr int RS = RQ <= 4 ? 4 : 1;

@@ -110,6 +110,21 @@ def test_in_place_on_base_and_unaligned_rows():
         assert torch.equal(off, y) and torch.equal(other, y)
 
 
+@pytest.mark.parametrize("kind", ["f32", "f16"])
+@pytest.mark.parametrize("rank", [7, 16, 64, 100])
+def test_tiles_of_several_adapters(kind, rank):
+    """Prompts whose tiles of 64 tokens hold none, one, two, three and many adapters, with tokens without an adapter
+    or with an id outside the stack among them, and a last tile that is not full."""
+    n, k, rows, ad = 700, 288, 68, 7
+    x, a, b, scales, base, ids = _inputs(9, n, k, rows, ad, rank, kind)
+    t = np.arange(n)
+    ids = np.where(t < 300, t // 45 % ad, np.where(t < 500, t // 20 % ad, ids))
+    ids[:64], ids[64:130] = -1, 3
+    ids[[5, 70, 199, 320]] = [ad, ad + 9, -7, 2 ** 31 - 1]
+    ids[[64, 310, 640]] = -1
+    _check(x, a, b, scales, base, ids, f"lora {kind} rank={rank}, tiles of several adapters")
+
+
 @pytest.mark.parametrize("bad", [float("nan"), float("inf")])
 def test_nonfinite_values_stay_with_their_tokens(bad):
     """A token's own non-finite activation, or an adapter's, reaches the rows that use it and no other."""
