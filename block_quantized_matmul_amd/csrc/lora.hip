@@ -48,7 +48,6 @@ constexpr int kThreads = 256;
 constexpr int kTok = 16;            // tokens per product
 constexpr int kSub = 4;             // products' tokens per consecutive tile
 constexpr int kGroupTokens = 512;   // largest batch in tiles by adapter
-constexpr int kGroupSlab = 64;      // k per wavefront and round, tiles by adapter
 constexpr int kMaxSplits = 256;     // ranges of k, tiles by adapter
 // Workgroups among which a consecutive tile's adapters are dealt: most tiles
 // have one adapter, and those where requests meet two. 2048 tokens of 9
@@ -560,18 +559,28 @@ int64_t padded(int64_t parts) {
   return parts > 4 ? 8 : parts > 2 ? 4 : parts;
 }
 bool by_adapter(int64_t n_tokens) { return n_tokens <= kGroupTokens; }
-// k per split: a multiple of 128, 32 for each of a workgroup's wavefronts.
-int64_t split_range(int64_t n_tokens, int64_t k) {
+// k per split: a multiple of 128, 32 for each of a workgroup's wavefronts. By
+// adapter, each split is a partial sum that the second launch's workgroups
+// read, a round of eight at a time: two rounds of loads of 64 k per wavefront,
+// or one where ranks are many and k short. 8 tokens, 4096 to 11008 rows, rank
+// 16 8.9 us with 512 k per split, 9.7 with 256, 9.9 with 1024; 1 token, the
+// same with rank 64 11.1, 9.6, 14.7; 8 tokens, 11008 to 4096, rank 64 15.4,
+// 16.6, 18.4.
+int64_t split_range(int64_t n_tokens, int64_t k, int64_t rank) {
   const int64_t tiles = (n_tokens + kTok * kSub - 1) / (kTok * kSub);
-  const int64_t want = by_adapter(n_tokens) ? std::min<int64_t>(kMaxSplits, std::max<int64_t>(1, k / (4 * kGroupSlab)))
-                                            : std::max<int64_t>(1, std::min(kTileGroups / tiles, k / 256));
+  int64_t want;
+  if (by_adapter(n_tokens))
+    want = std::min<int64_t>(kMaxSplits, rank > 32 ? std::max(k / 512, std::min<int64_t>(k / 256, 16)) : k / 512);
+  else
+    want = std::min(kTileGroups / tiles, k / 256);
+  want = std::max<int64_t>(want, 1);
   return (k + 128 * want - 1) / (128 * want) * 128;
 }
 
 }  // namespace
 
-int lora_splits(int64_t n_tokens, int64_t k, int64_t) {
-  const int64_t range = split_range(n_tokens, k);
+int lora_splits(int64_t n_tokens, int64_t k, int64_t rank) {
+  const int64_t range = split_range(n_tokens, k, rank);
   return static_cast<int>((k + range - 1) / range);
 }
 
@@ -583,7 +592,7 @@ hipError_t launch_lora(const void *X, bool x_f16, int64_t n_tokens, int64_t k, c
   // workgroups per split or chunk: every token's (most leave at once), or every tile's
   const int64_t groups = group ? n_tokens : (n_tokens + kTok * kSub - 1) / (kTok * kSub);
   const int64_t parts = padded(splits);
-  const DownArgs d{X, static_cast<const _Float16 *>(A), ids, partial, n_tokens, k, split_range(n_tokens, k),
+  const DownArgs d{X, static_cast<const _Float16 *>(A), ids, partial, n_tokens, k, split_range(n_tokens, k, rank),
                    static_cast<int>(n_adapters), static_cast<int>(rank), splits, static_cast<int>(parts)};
   const dim3 grid(static_cast<unsigned>(group ? groups * splits : groups * parts * kShares),
                   static_cast<unsigned>((rank + kRankGroup - 1) / kRankGroup));
