@@ -17,17 +17,17 @@
 // beside the other's matrix products.
 //
 // The grid covers an upper bound of the tiles (the starts are device data);
-// each wavefront finds its tile by a scan over the starts, 64 sequences at a
-// time. KV heads are the fastest index, so that with 8 of them (or a
-// multiple) each XCD's L2 holds the keys of its own heads only; the tiles of
-// a sequence go from its last (the longest) to its first.
+// each wavefront finds its tile by a search over the starts, 64 sequences at a
+// time, which orders the tiles by length. KV heads are the fastest index, so
+// that with 8 of them (or a multiple) each XCD's L2 holds the keys of its own
+// heads only.
 //
 // Measured, 32 heads on 8 KV heads of 128: 8192 tokens bf16 480 to 500 us
 // (550 GFLOP, 1.1 PFLOP/s where a large library product reaches 1.26; matrix
 // cores busy in 66 % of the cycles, vector units in 56 %); 16 prompts of up to
 // 950 tokens 80 us (0.55 PFLOP/s: of a tile's 17 us, 4 are its search and
 // first loads, 2 the masked block and 2 the store). 16 heads of 64, three
-// prompts of up to 2001 tokens, 33 us: half of a block's time is exponentials
+// prompts of up to 2001 tokens, 32 us: half of a block's time is exponentials
 // and other vector work, and the last third of the time only the longest
 // tiles run. Eight wavefronts that split a tile's keys in two took as long
 // there and longer elsewhere (8 x 1024 tokens 97 / 123 us).
@@ -41,6 +41,10 @@ namespace {
 
 constexpr int kRows = 128;   // query rows per workgroup
 constexpr int kThreads = 256;
+// Tiles per band (find_tile). Against whole sequences one after the other: two
+// prompts of 1024 36 / 30 us, 16 heads of 64 on prompts of up to 2001 35 / 32,
+// 16 x 512 65 / 65; bands of one tile lose the keys' neighbours: 30, 32, 73.
+constexpr int kBand = 8;
 
 struct PromptArgs {
   const void *q, *k, *v;
@@ -51,8 +55,33 @@ struct PromptArgs {
   float c;  // scale * log2(e)
 };
 
+// f over the lanes up to this one, where f(0, x) = x and x >= 0: in rows of 16
+// lanes by shifts of 1, 2, 4 and 8, then the last lanes of rows 0 and 2 into the
+// rows behind them, and lane 31 into the upper half (register moves, no trip
+// through LDS).
+template <class F> __device__ __forceinline__ int scan_lanes(int x, F f) {
+  x = f(__builtin_amdgcn_update_dpp(0, x, 0x111, 0xF, 0xF, false), x);
+  x = f(__builtin_amdgcn_update_dpp(0, x, 0x112, 0xF, 0xF, false), x);
+  x = f(__builtin_amdgcn_update_dpp(0, x, 0x114, 0xF, 0xF, false), x);
+  x = f(__builtin_amdgcn_update_dpp(0, x, 0x118, 0xF, 0xF, false), x);
+  x = f(__builtin_amdgcn_update_dpp(0, x, 0x142, 0xA, 0xF, false), x);
+  x = f(__builtin_amdgcn_update_dpp(0, x, 0x143, 0xC, 0xF, false), x);
+  return x;
+}
+__device__ __forceinline__ int scan_sum(int x) {
+  return scan_lanes(x, [](int a, int b) { return a + b; });
+}
+__device__ __forceinline__ int lane_sum(int x) { return __builtin_amdgcn_readlane(scan_sum(x), 63); }
+__device__ __forceinline__ int lane_max(int x) {
+  return __builtin_amdgcn_readlane(scan_lanes(x, [](int a, int b) { return max(a, b); }), 63);
+}
+
 // The tile with number `index` over all sequences: its sequence's first token
-// and length, and its own number in it. False past the last one.
+// and length, and its own number in it. False past the last one. Sequences
+// are gone through 64 at a time. Among those, tiles go by bands of kBand of
+// their numbers, the highest (the longest tiles) first, so that the launch
+// ends with short ones; in a band by sequence, so that neighbours share keys,
+// and in a sequence downwards.
 __device__ __forceinline__ bool find_tile(const PromptArgs &a, int index, int lane, int &first, int &len, int &tile) {
   for (int s0 = 0; s0 < a.n_seqs; s0 += 64) {
     const int s = s0 + lane;
@@ -63,22 +92,29 @@ __device__ __forceinline__ bool find_tile(const PromptArgs &a, int index, int la
       if (begin >= 0 && end >= begin && end <= a.n_tokens) n = end - begin;
       tiles = (n * a.group + kRows - 1) / kRows;
     }
-    int sum = tiles;  // inclusive scan over the lanes
-#pragma unroll
-    for (int d = 1; d < 64; d *= 2) {
-      const int up = __shfl_up(sum, d);
-      if (lane >= d) sum += up;
+    const int all = lane_sum(tiles);
+    if (index >= all) {
+      index -= all;
+      continue;
     }
-    const int all = __builtin_amdgcn_readlane(sum, 63);
-    if (index < all) {
-      const int at = __builtin_ctzll(__ballot(sum > index));
-      first = __builtin_amdgcn_readlane(begin, at);
-      len = __builtin_amdgcn_readlane(n, at);
-      const int left = __builtin_amdgcn_readlane(sum, at) - 1 - index;
-      tile = left;  // the sequence's last tile comes first
-      return true;
+    // tiles in bands >= j: the sum over the sequences of those past j kBand;
+    // the largest j for which there are more than `index`
+    int low = 0, high = (lane_max(tiles) + kBand - 1) / kBand, above = 0;
+    while (high - low > 1) {
+      const int j = low + (high - low) / 2;
+      const int more = lane_sum(max(tiles - j * kBand, 0));
+      if (more > index) {
+        low = j;
+      } else {
+        high = j, above = more;
+      }
     }
-    index -= all;
+    const int sum = scan_sum(min(max(tiles - low * kBand, 0), kBand));
+    const int at = __builtin_ctzll(__ballot(sum > index - above));
+    first = __builtin_amdgcn_readlane(begin, at);
+    len = __builtin_amdgcn_readlane(n, at);
+    tile = low * kBand + __builtin_amdgcn_readlane(sum, at) - 1 - (index - above);
+    return true;
   }
   return false;
 }

@@ -171,6 +171,23 @@ def test_nonfinite_values_of_later_tokens_stay_there(kind, bad, more):
         which[t, 1] = keep
 
 
+@pytest.mark.parametrize("hq,hkv,dim", [(4, 1, 64), (2, 2, 128)])
+def test_sequences_of_many_and_few_tiles(hq, hkv, dim):
+    """Tiles are taken in order of their length across 64 sequences at a time: every one exactly once."""
+    lens = [300, 0, 1, 611, 64, 40, 259] + [3] * 60 + [290, 0, 128] + [1, 33] * 5
+    q, k, v = _inputs(11, sum(lens) + 5, hq, hkv, dim, "f16")
+    starts = [0]
+    for n in lens:
+        starts.append(starts[-1] + n)
+    say(f"prompt many and few tiles {hq}/{hkv} dim={dim}")
+    o = torch.full(q.shape, 7.0, dtype=q.dtype, device="cuda")
+    qmm.qmm_attn_prompt(q.cuda(), k.cuda(), v.cuda(), torch.tensor(starts, dtype=torch.int32).cuda(), O=o)
+    torch.cuda.synchronize()
+    want, err = O.attn_prompt(f64(q), f64(k), f64(v), starts, dim ** -0.5, "f16")
+    assert bool((o[starts[-1]:] == 7.0).all())
+    assert_within(o[:starts[-1]], want[:starts[-1]], err[:starts[-1]], "many and few tiles")
+
+
 def test_rows_outside_and_bad_starts():
     """A sequence whose ends are out of order or outside the tokens is left out; its rows stay."""
     n = 60
