@@ -25,12 +25,12 @@
 // Measured, 32 heads on 8 KV heads of 128: 8192 tokens bf16 480 to 500 us
 // (550 GFLOP, 1.1 PFLOP/s where a large library product reaches 1.26; matrix
 // cores busy in 66 % of the cycles, vector units in 56 %); 16 prompts of up to
-// 950 tokens 80 us (0.55 PFLOP/s: of a tile's 17 us, 4 are its search and
+// 950 tokens 82 us (0.54 PFLOP/s: of a tile's 17 us, 4 are its search and
 // first loads, 2 the masked block and 2 the store). 16 heads of 64, three
 // prompts of up to 2001 tokens, 32 us: half of a block's time is exponentials
 // and other vector work, and the last third of the time only the longest
 // tiles run. Eight wavefronts that split a tile's keys in two took as long
-// there and longer elsewhere (8 x 1024 tokens 97 / 123 us).
+// there and longer elsewhere (8 x 1024 tokens 123 us instead of 97).
 #include "attn.h"
 #include "attn_core.h"
 #include "launch.h"

@@ -28,7 +28,7 @@
 // between them does).
 //
 // Measured: 1 token, 4096 x 4096, rank 16, fp32 X 7 us for both launches in a
-// graph (latency); 64 tokens on 32 adapters, 4096 to 11008 rows, 16 us (22 MB,
+// graph (latency); 64 tokens on 32 adapters, 4096 to 11008 rows, 15 us (22 MB,
 // of which 15 are the adapters: 4.5 us at a copy's rate; the rest is the two
 // launches' latencies: ids, then operands, then the sum); 2048 fp16 tokens of
 // 9 requests, 11008 to 4096 rows, rank 64, 61 us: down 25 (45 MB, 1.8 TB/s),
