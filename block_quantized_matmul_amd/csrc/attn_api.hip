@@ -54,7 +54,7 @@ int check_attention(int type, int64_t tokens, int64_t n_q_heads, int64_t n_kv_he
   if (!in_dim(tokens) || n_q_heads <= 0 || n_kv_heads <= 0 || n_q_heads > kMaxDim || n_q_heads % n_kv_heads != 0)
     return QMM_ERR_SHAPE;
   if (head_dim != 64 && head_dim != 128) return QMM_ERR_SHAPE;
-  if (!(scale > 0.f) || isinf(scale)) return QMM_ERR_SHAPE;
+  if (!(scale > 0.f) || !(scale < 0x1p127f)) return QMM_ERR_SHAPE;  // (the kernels take scale log2(e))
   if (tokens > kMaxDim - (1 << 20) || !product_within(tokens, n_q_heads, kMaxDim - (1 << 20))) return QMM_ERR_SHAPE;
   return QMM_OK;
 }

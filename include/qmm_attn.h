@@ -173,14 +173,14 @@ typedef struct qmm_heads {
  *                Device data: a sequence whose two ends are not so is left
  *                out, and where others then overlap, their tokens' rows are
  *                undefined. Sequences may be empty.
- *   scale        finite and > 0 (usually 1 / sqrt(head_dim))
+ *   scale        > 0 and < 2^127 (usually 1 / sqrt(head_dim))
  * Tokens outside every sequence keep their rows of O, and their Q, K and V
  * are not read. O must not overlap Q, K or V, nor two of its own heads each
  * other (strides as in qmm_norm_rope).
- * Numerics: scores, the softmax's maximum and sum, and the output's sum in
- * fp32; each weight, relative to a reference within a factor 2^8 of the
- * largest so far, is rounded to `type` for the matrix cores, and the output
- * once at the end. A non-finite K or V of a later token does not reach an
+ * Numerics: scores (infinite beyond fp32's range), the softmax's maximum and
+ * sum, and the output's sum in fp32; each weight, relative to a reference
+ * within a factor 2^8 of the largest so far, is rounded to `type` for the
+ * matrix cores, and the output once at the end. A non-finite K or V of a later token does not reach an
  * earlier one; where one is attended to, the outputs it enters are not finite
  * (infinite or NaN). n_tokens == 0 or n_seqs == 0 is a no-op. n_tokens,
  * n_seqs < 2^31 - 128 and n_tokens * n_q_heads < 2^31 - 2^20.
@@ -207,7 +207,7 @@ int qmm_attn_prompt(int type, const qmm_heads *Q, const qmm_heads *K, const qmm_
  *                quiet NaNs, and its cache is not read. Nothing at or past a
  *                length is read.
  *   head_dim     64 or 128
- *   scale        finite and > 0
+ *   scale        > 0 and < 2^127
  *   workspace    at least qmm_attn_shared_workspace_bytes(...) bytes, 16-byte
  *                aligned; partial results, overwritten; two calls in flight
  *                must not share one. May be NULL when that size is 0.

@@ -163,6 +163,12 @@ def _shared(L, t=1, Q=None, PK=None, PV=None, prefix=100, K=None, V=None, cap=20
                              hq, hkv, dim, scale, ws, ws_bytes, NULL)
 
 
+def test_scale_times_log2_e_has_to_fit(L):
+    for scale in (2.0 ** 127, 3e38):
+        assert _prompt(L, scale=scale) == qmm.QMM_ERR_SHAPE
+        assert _shared(L, scale=scale) == qmm.QMM_ERR_SHAPE
+
+
 def test_attn_shared_validation(L):
     E = qmm
     assert _shared(L, t=0) == E.QMM_ERR_TYPE
