@@ -172,8 +172,10 @@ int64_t qmm_attn_shared_workspace_bytes(int64_t n_seqs, int64_t prefix_len, int6
     return QMM_ERR_SHAPE;
   if (n_seqs == 0) return 0;
   if (!shared_fits(n_seqs, prefix_len, own_cap, n_q_heads, n_kv_heads)) return QMM_ERR_SHAPE;
-  return qmm::shared_plan(n_seqs, prefix_len, own_cap, n_q_heads, n_kv_heads).pieces() * n_seqs * n_q_heads *
-         (head_dim + 1) * 4;
+  // a piece's row is head_dim outputs and a reference; the sums of weights
+  // follow, as a further row for every head_dim + 1 pieces
+  const int64_t pieces = qmm::shared_plan(n_seqs, prefix_len, own_cap, n_q_heads, n_kv_heads).pieces();
+  return (pieces + (pieces + head_dim) / (head_dim + 1)) * n_seqs * n_q_heads * (head_dim + 1) * 4;
 }
 
 int qmm_attn_shared(int type, const qmm_heads *Q, const qmm_heads *PK, const qmm_heads *PV, int64_t prefix_len,

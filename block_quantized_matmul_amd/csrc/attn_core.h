@@ -5,6 +5,8 @@
 // running state over the keys seen so far is m = max s_u, l = sum 2^(s_u - m)
 // and o = sum 2^(s_u - m) v_u; a block of keys updates it in one pass:
 //   m' = max(m, max_block s),  (l, o) = 2^(m - m') (l, o) + block's sums.
+// s_u = c x_u with the raw score x_u = q . k_u, and c = scale log2(e) is applied
+// where a difference is taken (Reference, below).
 //
 // Both products run on v_mfma_f32_32x32x16 with the query row along the
 // columns: S^T = K Q^T and O^T = V^T P^T. A lane then owns one query row
@@ -128,15 +130,43 @@ template <int D, class Tile, class E, int ROWS, int PARTS> struct Copier {
   }
 };
 
+// What a row's weights are relative to: the weight of raw score x is
+// 2^(c x - c m) for the row's reference m, itself a raw score. It is computed as
+// 2^fma(x - sub, c, -mu) with one of
+//   mu = c m rounded, sub = 0: one instruction. The rounding of c m only moves
+//     the reference, by at most 2^-4 where |c m| < kLarge;
+//   mu = 0, sub = m: where c m is larger, its rounding could be off by so much
+//     that the weights leave their type's range, or all vanish.
+// An infinite m has neither (mu = sub = 0): -infinity stands for no key, whose
+// weights are zeros, and infinity for rows that come out as infinity or NaN.
+constexpr float kLarge = 0x1p20f;
+struct Reference {
+  float mu, sub;
+  __device__ __forceinline__ Reference(float m, float c) {
+    const float scaled = m * c;
+    const bool large = !(__builtin_fabsf(scaled) < kLarge);
+    mu = large ? 0.f : scaled;
+    sub = large && __builtin_fabsf(m) < __builtin_inff() ? m : 0.f;
+  }
+};
+// The factor that takes sums relative to m over to those relative to `to`.
+__device__ __forceinline__ float rescaling(float m, float to, float c) {
+  const Reference a(m, c), b(to, c);
+  return m == -__builtin_inff() ? 0.f : __builtin_amdgcn_exp2f(__builtin_fmaf(a.sub - b.sub, c, a.mu - b.mu));
+}
+
 // The state of a wavefront's 32 rows (a lane's column lane % 32).
 template <int D> struct AttnState {
   float16_t o[D / 32];
-  float m, l;  // l: this lane's half of the sum
+  float m, l;  // m: the reference, a raw score; l: this lane's half of the sum
+  float mu;    // Reference(m, c).mu
+  bool large;  // some row of the wavefront has had a Reference with a sub
   __device__ __forceinline__ void clear() {
 #pragma unroll
     for (int i = 0; i < D / 32; ++i) o[i] = float16_t{};
     m = -__builtin_inff();
-    l = 0.f;
+    l = mu = 0.f;
+    large = false;
   }
 };
 
@@ -172,7 +202,7 @@ __device__ __forceinline__ bool any_nonfinite(uint32_t a, int part, int lane) {
   }
   return __any(most.x >= E::exp_mask || most.y >= E::exp_mask);
 }
-// Weights are kept relative to a reference m that follows the maximum only
+// Weights are kept relative to a reference that follows the maximum only
 // when it is exceeded by more than kSlack (in base-2 units): any reference
 // gives the same quotient, and weights up to 2^kSlack neither overflow fp16
 // nor cost precision, while rescaling the outputs (64 multiplies at D = 128)
@@ -241,31 +271,41 @@ template <int NT> __device__ __forceinline__ void mask_scores(float16_t s[NT], i
       if (32 * t + 8 * (r >> 2) + (r & 3) >= l) s[t][r] = -__builtin_inff();
 }
 
-// Moves the reference up to the maximum mx (scaled) where some row's exceeds
-// it by more than kSlack, which is also so for a row's first keys.
-template <int D> __device__ __forceinline__ void follow_max(AttnState<D> &st, float mx) {
-  if (__any(mx > st.m + kSlack)) {
+// Moves the reference up to the block's largest raw score mx where some row's
+// exceeds it by more than kSlack, which is also so for a row's first keys; then
+// makes the scores s ready for weights().
+template <int D, int NT>
+__device__ __forceinline__ void follow_max(AttnState<D> &st, float mx, float c, float16_t s[NT]) {
+  if (__any((mx - st.m) * c > kSlack)) {
     const float m = fmaxf(st.m, mx);
-    const float alpha = m == -__builtin_inff() ? 1.f : __builtin_amdgcn_exp2f(st.m - m);
-    st.m = m;
+    const float alpha = rescaling(st.m, m, c);
+    const Reference ref(m, c);
+    st.m = m, st.mu = ref.mu;
+    st.large = st.large || __any(ref.sub != 0.f);
     st.l *= alpha;
 #pragma unroll
     for (int i = 0; i < D / 32; ++i)
 #pragma unroll
       for (int r = 0; r < 16; ++r) st.o[i][r] *= alpha;
   }
+  if (st.large) {
+    const float sub = Reference(st.m, c).sub;
+#pragma unroll
+    for (int t = 0; t < NT; ++t)
+#pragma unroll
+      for (int r = 0; r < 16; ++r) s[t][r] -= sub;
+  }
 }
 
 // Weights of the scores, rounded for the second product; their sum goes to l.
 template <class E, int D, int NT>
 __device__ __forceinline__ void weights(const float16_t s[NT], AttnState<D> &st, float c, typename E::v8 p[2 * NT]) {
-  const float mu = st.m == -__builtin_inff() ? 0.f : st.m;  // no key yet: weights of zero, not NaN
   float sum[2] = {0.f, 0.f};
 #pragma unroll
   for (int t = 0; t < NT; ++t)
 #pragma unroll
     for (int r = 0; r < 16; ++r) {
-      const float w = __builtin_amdgcn_exp2f(__builtin_fmaf(s[t][r], c, -mu));
+      const float w = __builtin_amdgcn_exp2f(__builtin_fmaf(s[t][r], c, -st.mu));
       sum[r & 1] += w;
       p[2 * t + (r >> 3)][r & 7] = static_cast<typename E::one>(w);
     }
@@ -371,17 +411,17 @@ __device__ __forceinline__ bool attend_blocks(uint8_t *lds, const CopyK &copy_k,
   if (CAUSAL || mine > 0) {
     scores<E, D, 2>(kt(0), q, s, lane);
     interleave<D / 8, 4, 1, 0, 0>();
-    mx = row_max<2>(s) * c;
+    mx = row_max<2>(s);
   }
   auto step = [&](int b, float16_t(&now)[2], float16_t(&then)[2]) {
     next(b);
-    follow_max<D>(st, mx);
+    follow_max<D, 2>(st, mx, c, now);
     __builtin_amdgcn_sched_barrier(0);
     scores<E, D, 2>(kt(b + 1), q, then, lane);
     weights<E, D, 2>(now, st, c, p);
     interleave<D / 8, 4, 1, 5, 2>();
     add_values<E, D, 2>(v_addr<D>(vt(b), lane), p, st);
-    mx = row_max<2>(then) * c;
+    mx = row_max<2>(then);
     interleave<D / 8, 3, 2, 2, 0>();
   };
   int b = 0;
@@ -397,7 +437,7 @@ __device__ __forceinline__ bool attend_blocks(uint8_t *lds, const CopyK &copy_k,
   for (; b < mine; ++b) {
     next(b);
     mask_scores<2>(s, lim - b * kKeys, lane);
-    follow_max<D>(st, row_max<2>(s) * c);
+    follow_max<D, 2>(st, row_max<2>(s), c, s);
     weights<E, D, 2>(s, st, c, p);
     __builtin_amdgcn_sched_barrier(0);
     if (CAUSAL) {

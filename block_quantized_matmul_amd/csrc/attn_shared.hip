@@ -2,9 +2,10 @@
 // cache (qmm_attn_shared).
 //
 // One softmax over both key ranges; it is computed in pieces of keys. A piece
-// leaves, for every row (sequence, query head), its normalised output O_i and
-// the base-2 logarithm L_i of its sum of weights, and the join is
-//   O = sum_i 2^(L_i - L) O_i,  L = log2 sum_i 2^L_i.
+// leaves, for every row (sequence, query head), its normalised output O_i, its
+// reference m_i and its sum of weights l_i relative to that, and the join is
+//   O = sum_i f_i O_i / sum_i f_i,  f_i = l_i 2^(c m_i - c m),  m = max_i m_i.
+// (One logarithm of c m_i + log2 l_i would lose l_i where scores are large.)
 //
 // The prefix is read once for all sequences: the rows of all sequences and of
 // the heads that share a KV head are flattened (row x: sequence x / group,
@@ -51,13 +52,14 @@ struct SharedArgs {
   int64_t qt, qh, pkt, pkh, pvt, pvh, ks, kt, kh, vs, vt, vh, ot, oh;
   const int32_t *lengths;
   float *part_o;  // [pieces][n_seqs * n_q_heads][D]
-  float *part_l;  // [pieces][n_seqs * n_q_heads]
+  float *part_m;  // [pieces][n_seqs * n_q_heads], and the same for l
+  float *part_l;
   int n_seqs, n_heads, group, n_kv, prefix_len, own_cap;
   int row_tiles, tile_rows, prefix_pieces, prefix_step, own_tiles, own_pieces, own_step;
   float c;  // scale * log2(e)
 };
 
-// A row's partial result; an empty piece (no keys) has L = -infinity and
+// A row's partial result; an empty piece (no keys) has m = -infinity, l = 0 and
 // zeros for its output.
 template <int D>
 __device__ __forceinline__ void store_partial(const SharedArgs &a, int piece, int seq, int head,
@@ -71,7 +73,7 @@ __device__ __forceinline__ void store_partial(const SharedArgs &a, int piece, in
     for (int i = 0; i < 4; ++i)
       *reinterpret_cast<float4_t *>(o + 32 * dt + 8 * i + 4 * (lane >> 5)) =
           float4_t{st.o[dt][4 * i] * f, st.o[dt][4 * i + 1] * f, st.o[dt][4 * i + 2] * f, st.o[dt][4 * i + 3] * f};
-  if (lane < 32) a.part_l[at] = l == 0.f ? -__builtin_inff() : st.m + __builtin_amdgcn_logf(l);
+  if (lane < 32) a.part_m[at] = st.m, a.part_l[at] = l;
 }
 
 template <class E, int D>
@@ -135,7 +137,7 @@ __device__ __forceinline__ void own_blocks(const typename E::one *kb, int64_t k_
     load_k(b + 4);
     const int left = n_keys - b * kOwnKeys;
     if (left < kOwnKeys) mask_scores<1>(s, left, lane);
-    follow_max<D>(st, row_max<1>(s) * c);
+    follow_max<D, 1>(st, row_max<1>(s), c, s);
     weights<E, D, 1>(s, st, c, p);
     if (b + 4 < blocks)
       wait_loads<kCopies>();  // V has landed, the next K may be on its way
@@ -153,7 +155,7 @@ __device__ __forceinline__ void own_blocks(const typename E::one *kb, int64_t k_
 // largest m, then the sums in wavefront order. Wavefront 3 ends up with the
 // whole, and its l is the row's, not a lane's half.
 template <int D>
-__device__ __forceinline__ void join_wavefronts(AttnState<D> &st, uint8_t *lds, int wave, int lane) {
+__device__ __forceinline__ void join_wavefronts(AttnState<D> &st, float c, uint8_t *lds, int wave, int lane) {
   float l = row_sum(st);
   __syncthreads();
   float *ml = reinterpret_cast<float *>(lds);        // [4][32][2]
@@ -167,12 +169,10 @@ __device__ __forceinline__ void join_wavefronts(AttnState<D> &st, uint8_t *lds, 
   float top = -__builtin_inff();
 #pragma unroll
   for (int w = 0; w < 4; ++w) top = fmaxf(top, ml[(w * 32 + col) * 2]);
-  const float base = top == -__builtin_inff() ? 0.f : top;
   l = 0.f;
 #pragma unroll
-  for (int w = 0; w < 4; ++w)
-    l += ml[(w * 32 + col) * 2 + 1] * __builtin_amdgcn_exp2f(ml[(w * 32 + col) * 2] - base);
-  const float f = __builtin_amdgcn_exp2f(st.m - base);
+  for (int w = 0; w < 4; ++w) l += ml[(w * 32 + col) * 2 + 1] * rescaling(ml[(w * 32 + col) * 2], top, c);
+  const float f = rescaling(st.m, top, c);
   st.m = top, st.l = l;
 #pragma unroll
   for (int w = 0; w < 4; ++w) {
@@ -211,7 +211,7 @@ __device__ __forceinline__ void own_piece(const SharedArgs &a, int item, int g, 
                      static_cast<const one *>(a.v) + seq * a.vs + first * a.vt + g * a.vh, a.vt, n_keys, q, st, a.c,
                      lds, wave, lane);
   }
-  join_wavefronts<D>(st, lds, wave, lane);
+  join_wavefronts<D>(st, a.c, lds, wave, lane);
   if (wave == 3 && row < a.group) store_partial<D>(a, a.prefix_pieces + piece, seq, head, st, st.l, lane);
 }
 
@@ -239,7 +239,7 @@ template <class E, int D> __global__ __launch_bounds__(kThreads, 2) void attn_di
   if (len > 0 && !bad)
     own_blocks<E, D>(static_cast<const one *>(a.k) + seq * a.ks + g * a.kh, a.kt,
                      static_cast<const one *>(a.v) + seq * a.vs + g * a.vh, a.vt, len, q, st, a.c, lds, wave, lane);
-  join_wavefronts<D>(st, lds, wave, lane);
+  join_wavefronts<D>(st, a.c, lds, wave, lane);
   if (wave != 3) return;
   // without a key a row of zeros; with keys, but no weight (every score -infinity), 0 / 0
   const float f = bad ? __builtin_bit_cast(float, 0x7FC00000u) : a.prefix_len == 0 && len == 0 ? 0.f : 1.f / st.l;
@@ -277,25 +277,24 @@ template <class E, int D> __global__ __launch_bounds__(kThreads) void attn_join_
   const int len = a.own_cap > 0 ? a.lengths[seq] : 0;
   const int lane = threadIdx.x & 63;
   float top = -__builtin_inff();
-  for (int i = lane; i < pieces; i += 64) top = fmaxf(top, a.part_l[i * rows + blockIdx.x]);
+  for (int i = lane; i < pieces; i += 64) top = fmaxf(top, a.part_m[i * rows + blockIdx.x]);
 #pragma unroll
   for (int d = 32; d > 0; d /= 2) top = fmaxf(top, __shfl_xor(top, d));
-  const float base = top == -__builtin_inff() ? 0.f : top;
   float sum = 0.f;
   float4_t o{};
   for (int i0 = part; i0 < pieces; i0 += 8 * kParts) {
-    float w[8];
+    float m[8], l[8];
     float4_t x[8];
 #pragma unroll
     for (int k = 0; k < 8; ++k) {
       const int64_t at = (i0 + k * kParts < pieces ? i0 + k * kParts : part) * rows + blockIdx.x;
-      w[k] = a.part_l[at];
+      m[k] = a.part_m[at], l[k] = a.part_l[at];
       x[k] = *reinterpret_cast<const float4_t *>(a.part_o + at * D + 4 * e);
     }
 #pragma unroll
     for (int k = 0; k < 8; ++k) {
       if (i0 + k * kParts >= pieces) continue;
-      const float f = __builtin_amdgcn_exp2f(w[k] - base);
+      const float f = l[k] * rescaling(m[k], top, a.c);
       sum += f;
       o += f * x[k];
     }
@@ -367,7 +366,8 @@ hipError_t launch_attn_shared(int type, const qmm_heads &Q, const qmm_heads &PK,
   a.ot = O.token_stride, a.oh = O.head_stride;
   a.lengths = lengths;
   a.part_o = static_cast<float *>(workspace);
-  a.part_l = a.part_o + p.pieces() * n_seqs * n_q_heads * head_dim;
+  a.part_m = a.part_o + p.pieces() * n_seqs * n_q_heads * head_dim;
+  a.part_l = a.part_m + p.pieces() * n_seqs * n_q_heads;
   a.n_seqs = static_cast<int>(n_seqs), a.n_heads = static_cast<int>(n_q_heads);
   a.group = static_cast<int>(n_q_heads / n_kv_heads), a.n_kv = static_cast<int>(n_kv_heads);
   a.prefix_len = static_cast<int>(prefix_len), a.own_cap = static_cast<int>(own_cap);
