@@ -122,7 +122,8 @@ __device__ __forceinline__ bool find_tile(const PromptArgs &a, int index, int la
 // One row over its keys 0 .. n_keys - 1, key by key, the lanes sharing the
 // head's elements: for the rows of a wavefront whose tile product would let
 // a non-finite value of a later token in (no ordinary call's does). Every
-// key it reads is one the row attends to.
+// key it reads is one the row attends to. Scores are raw until their difference
+// is taken, as in the tiles.
 template <class E, int D>
 __device__ __forceinline__ void slow_row(const typename E::one *q, const typename E::one *k, int64_t kt,
                                          const typename E::one *v, int64_t vt, int n_keys, float c,
@@ -130,7 +131,7 @@ __device__ __forceinline__ void slow_row(const typename E::one *q, const typenam
   constexpr int kPer = D / 64;
   float x[kPer], acc[kPer], m = -__builtin_inff(), l = 0.f;
 #pragma unroll
-  for (int i = 0; i < kPer; ++i) x[i] = static_cast<float>(q[kPer * lane + i]) * c, acc[i] = 0.f;
+  for (int i = 0; i < kPer; ++i) x[i] = static_cast<float>(q[kPer * lane + i]), acc[i] = 0.f;
   for (int u = 0; u < n_keys; ++u) {
     float s = 0.f;
 #pragma unroll
@@ -139,7 +140,7 @@ __device__ __forceinline__ void slow_row(const typename E::one *q, const typenam
     for (int d = 32; d > 0; d /= 2) s += __shfl_xor(s, d);
     const float top = fmaxf(m, s);
     const float base = top == -__builtin_inff() ? 0.f : top;
-    const float alpha = __builtin_amdgcn_exp2f(m - base), w = __builtin_amdgcn_exp2f(s - base);
+    const float alpha = __builtin_amdgcn_exp2f((m - base) * c), w = __builtin_amdgcn_exp2f((s - base) * c);
     m = top, l = l * alpha + w;
 #pragma unroll
     for (int i = 0; i < kPer; ++i)

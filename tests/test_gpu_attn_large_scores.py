@@ -169,3 +169,21 @@ def test_large_beside_ordinary_scores(kind, dim, large_first):
     assert_within(direct[0], o, e, "direct")
     # four times the keys: sums of four times the terms
     assert_within(pieces[0], o, e + 9 * n * O.E32 * np.abs(v).max(0), "pieces")
+
+
+@pytest.mark.parametrize("power", [20, 60])
+def test_large_scale_beside_a_nonfinite_later_value(power):
+    """A scale that takes the queries (not the scores) to 2^90, or out of fp32's range, in rows that are computed key by
+    key because a later token's value is not finite."""
+    n, dim, starts = 100, 64, [0, 100]
+    r = rng(24)
+    q = rounded(2.0 ** 70 * r.standard_normal((n, 2, dim)), "bf16")
+    k = rounded(2.0 ** (-70 - power) * r.standard_normal((n, 1, dim)), "bf16")
+    v = rounded(r.standard_normal((n, 1, dim)), "bf16")
+    scale = 2.0 ** power / 8
+    want, err = O.attn_prompt(q.double().numpy(), k.double().numpy(), v.double().numpy(), starts, scale, "bf16")
+    v[n - 1, 0, 3] = float("inf")
+    say(f"prompt, scale {scale} beside an infinite later value")
+    o = qmm.qmm_attn_prompt(q.cuda(), k.cuda(), v.cuda(), torch.tensor(starts, dtype=torch.int32).cuda(), scale=scale)
+    torch.cuda.synchronize()
+    assert_within(o[:n - 1], want[:n - 1], err[:n - 1], "rows before it")
