@@ -16,8 +16,10 @@
 // registers let two workgroups share a CU, so that one's exponentials run
 // beside the other's matrix products.
 //
-// The grid covers an upper bound of the tiles (the starts are device data);
-// each wavefront finds its tile by a search over the starts, 64 sequences at a
+// The grid covers an upper bound of the tiles (the starts are device data) of
+// sequences that share no token, as starts in order make them. Where starts
+// are not in order, there may be more tiles, and workgroups that have seen so
+// take several, one after another (attn_prompt_kernel). Each wavefront finds its tile by a search over the starts, 64 sequences at a
 // time, which orders the tiles by length. KV heads are the fastest index, so
 // that with 8 of them (or a multiple) each XCD's L2 holds the keys of its own
 // heads only.
@@ -77,26 +79,34 @@ __device__ __forceinline__ int lane_max(int x) {
 }
 
 // The tile with number `index` over all sequences: its sequence's first token
-// and length, and its own number in it. False past the last one. Sequences
-// are gone through 64 at a time. Among those, tiles go by bands of kBand of
+// and length, and its own number in it. False past the last one. `ahead`: the
+// number of tiles ahead of the first 64 sequences gone through of which one's
+// ends are not in order, or -1. Sequences are gone through 64 at a time. Among those, tiles go by bands of kBand of
 // their numbers, the highest (the longest tiles) first, so that the launch
 // ends with short ones; in a band by sequence, so that neighbours share keys,
 // and in a sequence downwards.
-__device__ __forceinline__ bool find_tile(const PromptArgs &a, int index, int lane, int &first, int &len, int &tile) {
+__device__ __forceinline__ bool find_tile(const PromptArgs &a, int64_t number, int lane, int &first, int &len, int &tile,
+                                          int64_t &ahead) {
+  int64_t left = number;
+  ahead = -1;
   for (int s0 = 0; s0 < a.n_seqs; s0 += 64) {
     const int s = s0 + lane;
     int begin = 0, n = 0, tiles = 0;
+    bool in_order = true;
     if (s < a.n_seqs) {
       begin = a.starts[s];
       const int end = a.starts[s + 1];
-      if (begin >= 0 && end >= begin && end <= a.n_tokens) n = end - begin;
+      in_order = begin >= 0 && end >= begin && end <= a.n_tokens;
+      if (in_order) n = end - begin;
       tiles = (n * a.group + kRows - 1) / kRows;
     }
+    if (__builtin_expect(ahead < 0 && !__all(in_order), 0)) ahead = number - left;
     const int all = lane_sum(tiles);
-    if (index >= all) {
-      index -= all;
+    if (left >= all) {
+      left -= all;
       continue;
     }
+    const int index = static_cast<int>(left);
     // tiles in bands >= j: the sum over the sequences of those past j kBand;
     // the largest j for which there are more than `index`
     int low = 0, high = (lane_max(tiles) + kBand - 1) / kBand, above = 0;
@@ -150,15 +160,16 @@ __device__ __forceinline__ void slow_row(const typename E::one *q, const typenam
   for (int i = 0; i < kPer; ++i) o[kPer * lane + i] = static_cast<typename E::one>(acc[i] / l);
 }
 
+// The tile with number `number` (find_tile). False if there is none.
 template <class E, int D>
-__global__ __launch_bounds__(kThreads, 2) void attn_prompt_kernel(PromptArgs a) {
+__device__ __forceinline__ bool prompt_tile(const PromptArgs &a, int64_t number, uint8_t *lds, uint32_t thread,
+                                            int64_t &ahead) {
   typedef typename E::one one;
-  __shared__ __align__(1024) uint8_t lds[attend_lds_bytes<D>()];
-  const int lane = threadIdx.x & 63;
-  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int lane = thread & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(thread >> 6);
   const int g = blockIdx.x % a.n_kv;
   int first, len, tile;
-  if (!find_tile(a, blockIdx.x / a.n_kv, lane, first, len, tile)) return;
+  if (!find_tile(a, number, lane, first, len, tile, ahead)) return false;
 
   // this lane's row; rows past the sequence's last repeat it and are not stored
   const int rows = len * a.group;
@@ -205,6 +216,31 @@ __global__ __launch_bounds__(kThreads, 2) void attn_prompt_kernel(PromptArgs a) 
                      static_cast<one *>(a.o) + (first + t2) * a.ot + head * a.oh, l2);
     }
   }
+  return true;
+}
+
+template <class E, int D>
+__global__ __launch_bounds__(kThreads, 2) void attn_prompt_kernel(PromptArgs a) {
+  __shared__ __align__(1024) uint8_t lds[attend_lds_bytes<D>()];
+  int64_t number = blockIdx.x / a.n_kv, ahead;
+  if (!prompt_tile<E, D>(a, number, lds, threadIdx.x, ahead)) return;
+  if (__builtin_expect(ahead < 0, 1)) return;
+  // Starts that are not in order. Up to where they are, sequences have no more
+  // tiles than the grid; the tiles from there on are shared out among the
+  // workgroups whose first one was among them, since those before have not seen
+  // it. (If there are no such workgroups, every token was a sequence of its own
+  // before, and what follows only shares their tokens.) The arguments are read
+  // again, so that this costs the first tile no registers.
+  do {
+    auto *p = (const __attribute__((address_space(4))) PromptArgs *)__builtin_amdgcn_kernarg_segment_ptr();
+    uint32_t thread = threadIdx.x;
+    asm volatile("" : "+s"(p), "+v"(thread));
+    const PromptArgs again{p->q,  p->k,  p->v,  p->o,      p->qt,     p->qh,       p->kt,    p->kh,   p->vt,
+                           p->vh, p->ot, p->oh, p->starts, p->n_seqs, p->n_tokens, p->group, p->n_kv, p->c};
+    number += gridDim.x / again.n_kv - ahead;
+    __syncthreads();  // the next tile's copies go where this one's may still be read
+    if (!prompt_tile<E, D>(again, number, lds, thread, ahead)) return;
+  } while (true);
 }
 
 }  // namespace

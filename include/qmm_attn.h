@@ -171,8 +171,8 @@ typedef struct qmm_heads {
  *   head_dim     64 or 128
  *   seq_starts   int32 [n_seqs + 1], non-decreasing within [0, n_tokens].
  *                Device data: a sequence whose two ends are not so is left
- *                out, and where others then overlap, their tokens' rows are
- *                undefined. Sequences may be empty.
+ *                out, and where others then overlap, the rows of the tokens
+ *                that they share are undefined. Sequences may be empty.
  *   scale        > 0 and < 2^127 (usually 1 / sqrt(head_dim))
  * Tokens outside every sequence keep their rows of O, and their Q, K and V
  * are not read. O must not overlap Q, K or V, nor two of its own heads each
