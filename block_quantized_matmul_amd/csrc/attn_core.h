@@ -43,6 +43,13 @@ struct ElemF16 {
   __device__ static __forceinline__ float16_t mfma(v8 a, v8 b, float16_t c) {
     return __builtin_amdgcn_mfma_f32_32x32x16_f16(a, b, c, 0, 0, 0);
   }
+  // An output is a mean of values with rounded weights over the sum of the
+  // unrounded ones, and may thus pass the largest value by a half step, hence
+  // the type's range: x within it, but for infinities and NaN.
+  static constexpr float largest = 65504.f;
+  __device__ static __forceinline__ float limit(float x) {
+    return __builtin_fabsf(x) < __builtin_inff() ? __builtin_amdgcn_fmed3f(x, -largest, largest) : x;
+  }
 };
 struct ElemBF16 {
   typedef __bf16 one;
@@ -52,6 +59,9 @@ struct ElemBF16 {
   __device__ static __forceinline__ float16_t mfma(v8 a, v8 b, float16_t c) {
     return __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, c, 0, 0, 0);
   }
+  // fp32 has no room for sums of values that large either.
+  static constexpr float largest = __builtin_inff();
+  __device__ static __forceinline__ float limit(float x) { return x; }
 };
 
 __device__ __forceinline__ uint32_t lds_addr(const void *p) {
@@ -467,7 +477,21 @@ template <int D> __device__ __forceinline__ float row_sum(const AttnState<D> &st
 // elements of one chunk and l + 32 those of the next (16 bytes per store).
 // Both lanes of a row call it, with the same `live`.
 template <class E, int D>
-__device__ __forceinline__ void store_row(typename E::one *row, const AttnState<D> &st, float f, int lane, bool live) {
+__device__ __forceinline__ void store_row(typename E::one *row, AttnState<D> &st, float f, int lane, bool live) {
+  if (E::largest < __builtin_inff()) {
+    float top = 0.f;
+#pragma unroll
+    for (int dt = 0; dt < D / 32; ++dt)
+#pragma unroll
+      for (int r = 0; r < 16; ++r) top = fmaxf(top, __builtin_fabsf(st.o[dt][r]));
+    if (__builtin_expect(__any(top * f > E::largest), 0)) {
+#pragma unroll
+      for (int dt = 0; dt < D / 32; ++dt)
+#pragma unroll
+        for (int r = 0; r < 16; ++r) st.o[dt][r] = E::limit(st.o[dt][r] * f);
+      f = 1.f;
+    }
+  }
 #pragma unroll
   for (int dt = 0; dt < D / 32; ++dt)
 #pragma unroll

@@ -157,7 +157,7 @@ __device__ __forceinline__ void slow_row(const typename E::one *q, const typenam
       acc[i] = acc[i] * alpha + w * static_cast<float>(v[u * vt + kPer * lane + i]);
   }
 #pragma unroll
-  for (int i = 0; i < kPer; ++i) o[kPer * lane + i] = static_cast<typename E::one>(acc[i] / l);
+  for (int i = 0; i < kPer; ++i) o[kPer * lane + i] = static_cast<typename E::one>(E::limit(acc[i] / l));
 }
 
 // The tile with number `number` (find_tile). False if there is none.

@@ -310,7 +310,7 @@ template <class E, int D> __global__ __launch_bounds__(kThreads) void attn_join_
   typename E::v4 out;
 #pragma unroll
   for (int k = 0; k < 4; ++k)
-    out[k] = static_cast<typename E::one>(bad ? __builtin_bit_cast(float, 0x7FC00000u) : o[k] * f);
+    out[k] = static_cast<typename E::one>(bad ? __builtin_bit_cast(float, 0x7FC00000u) : E::limit(o[k] * f));
   *reinterpret_cast<typename E::v4 *>(static_cast<typename E::one *>(a.o) + seq * a.ot + head * a.oh + 4 * e) = out;
 }
 

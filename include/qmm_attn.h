@@ -180,7 +180,10 @@ typedef struct qmm_heads {
  * Numerics: scores (infinite beyond fp32's range), the softmax's maximum and
  * sum, and the output's sum in fp32; each weight, relative to a reference
  * within a factor 2^8 of the largest so far, is rounded to `type` for the
- * matrix cores, and the output once at the end. A non-finite K or V of a later token does not reach an
+ * matrix cores, and the output once at the end. The sum of the values times
+ * these weights has to stay within fp32's range: bf16 values below 2^118 over
+ * the number of keys do, and all fp16 ones, whose outputs are never beyond the
+ * largest finite fp16. A non-finite K or V of a later token does not reach an
  * earlier one; where one is attended to, the outputs it enters are not finite
  * (infinite or NaN). n_tokens == 0 or n_seqs == 0 is a no-op. n_tokens,
  * n_seqs < 2^31 - 128 and n_tokens * n_q_heads < 2^31 - 2^20.
