@@ -28,8 +28,8 @@ QMM_NORM_ROPE_MAX_DIM = 512
 
 __all__ = ["QMM_T_F32", "QMM_T_F16", "QMM_T_BF16", "QMM_ROPE_HALVES", "QMM_ROPE_NEIGHBOURS", "QMM_LORA_MAX_RANK",
            "QMM_HEAD_PARTS_MAX", "QMM_NORM_ROPE_MAX_DIM", "qmm_head_part", "qmm_heads_desc", "qmm_head_part_desc",
-           "qmm_lora", "qmm_lora_workspace_bytes", "qmm_norm_rope", "qmm_attn_prompt", "qmm_attn_shared",
-           "qmm_attn_shared_workspace_bytes"]
+           "qmm_lora", "qmm_lora_workspace_bytes", "qmm_lora_workspace_max_bytes", "qmm_norm_rope", "qmm_attn_prompt",
+           "qmm_attn_shared", "qmm_attn_shared_workspace_bytes", "qmm_attn_shared_workspace_max_bytes"]
 
 _PART_NAMES = ("X", "Y", "weight") + ("positions", "slots") + ("X", "Y", "weight") * (QMM_HEAD_PARTS_MAX - 1)
 _PAIRS = {"halves": QMM_ROPE_HALVES, "neighbours": QMM_ROPE_NEIGHBOURS}
@@ -216,6 +216,15 @@ def qmm_lora_workspace_bytes(n_tokens: int, k: int, rank: int) -> int:
     return int(_lib().qmm_lora_workspace_bytes(int(n_tokens), int(k), int(rank)))
 
 
+def qmm_lora_workspace_max_bytes(max_tokens: int, max_k: int, max_rank: int) -> int:
+    """What no qmm_lora call of at most these sizes needs more than: for a workspace kept for calls of different sizes
+    (qmm_lora_workspace_bytes may be larger for fewer tokens). The header's inline function."""
+    rows = min(max_tokens, 512) * min(max(max_k // 512, 16), 256)
+    if max_tokens > 512:
+        rows = max(rows, 32768)
+    return max(rows, max_tokens) * max_rank * 4
+
+
 def qmm_lora(X, A, B, ids, scales=None, base=None, Y=None, workspace=None, stream=None):
     """Low-rank adapters of many requests beside a shared projection (C: qmm_lora):
     Y[t] = base[t] + scales[a] * B[a] (A[a] X[t]) with a = ids[t].
@@ -362,6 +371,13 @@ def qmm_attn_shared_workspace_bytes(n_seqs: int, prefix_len: int, own_cap: int, 
                                     head_dim: int) -> int:
     return int(_lib().qmm_attn_shared_workspace_bytes(int(n_seqs), int(prefix_len), int(own_cap), int(n_q_heads),
                                                       int(n_kv_heads), int(head_dim)))
+
+
+def qmm_attn_shared_workspace_max_bytes(max_seqs: int, n_q_heads: int, head_dim: int) -> int:
+    """What no qmm_attn_shared call of at most max_seqs sequences needs more than, whatever the prefix and the caches: for
+    a workspace kept for calls of different sizes (qmm_attn_shared_workspace_bytes may be larger for fewer sequences or
+    keys). The header's inline function."""
+    return (512 * (128 + 32) + 3 * max_seqs * n_q_heads) * (head_dim + 2) * 4
 
 
 def qmm_attn_shared(Q, PK, PV, K, V, lengths, scale=None, O=None, workspace=None, stream=None):

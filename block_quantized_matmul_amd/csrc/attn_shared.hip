@@ -329,7 +329,9 @@ template <class E, int D> hipError_t run(const SharedArgs &a, int64_t items, boo
 }  // namespace
 
 // Pieces: enough workgroups to fill the GPU, but at least kMinPiece keys in
-// each, since every piece costs its rows' partial result.
+// each, since every piece costs its rows' partial result. (The header's
+// qmm_attn_shared_workspace_max_bytes follows from kWantGroups and the tiles'
+// rows.)
 SharedPlan shared_plan(int64_t n_seqs, int64_t prefix_len, int64_t own_cap, int64_t n_q_heads, int64_t n_kv_heads) {
   const int64_t group = n_q_heads / n_kv_heads;
   SharedPlan p{};

@@ -565,7 +565,7 @@ bool by_adapter(int64_t n_tokens) { return n_tokens <= kGroupTokens; }
 // or one where ranks are many and k short. 8 tokens, 4096 to 11008 rows, rank
 // 16 8.9 us with 512 k per split, 9.7 with 256, 9.9 with 1024; 1 token, the
 // same with rank 64 11.1, 9.6, 14.7; 8 tokens, 11008 to 4096, rank 64 15.4,
-// 16.6, 18.4.
+// 16.6, 18.4. (The header's qmm_lora_workspace_max_bytes follows from these.)
 int64_t split_range(int64_t n_tokens, int64_t k, int64_t rank) {
   const int64_t tiles = (n_tokens + kTok * kSub - 1) / (kTok * kSub);
   int64_t want;

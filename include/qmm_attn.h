@@ -86,8 +86,22 @@ int qmm_lora(const void *X, int x_type, int64_t n_tokens, int64_t k, const uint1
              const float *base, float *Y, void *workspace, int64_t workspace_bytes, void *stream);
 
 /* qmm_lora_workspace_bytes - the workspace qmm_lora needs for these sizes, or
- * QMM_ERR_SHAPE. The same on every device. */
+ * QMM_ERR_SHAPE. The same on every device. Fewer tokens may need more (2048 of
+ * k 4096 more than 2049): a workspace kept for calls of different sizes is as
+ * large as qmm_lora_workspace_max_bytes says. */
 int64_t qmm_lora_workspace_bytes(int64_t n_tokens, int64_t k, int64_t rank);
+
+/* qmm_lora_workspace_max_bytes - what no call of at most these sizes needs
+ * more than; never decreases with any of them. Up to 512 tokens V is kept in at
+ * most max_k / 512 (but 16 to 256) partial sums, beyond in as many as make
+ * 32768 rows, or in one. */
+static inline int64_t qmm_lora_workspace_max_bytes(int64_t max_tokens, int64_t max_k, int64_t max_rank) {
+  const int64_t sums = max_k / 512 < 16 ? 16 : max_k / 512 > 256 ? 256 : max_k / 512;
+  int64_t rows = (max_tokens < 512 ? max_tokens : 512) * sums;
+  if (max_tokens > 512 && rows < 32768) rows = 32768;
+  if (rows < max_tokens) rows = max_tokens;
+  return rows * max_rank * 4;
+}
 
 /* One group of heads of a qmm_norm_rope call (a host struct, read during the
  * call). Strides are in elements; the elements of one head are contiguous. */
@@ -224,9 +238,21 @@ int qmm_attn_shared(int type, const qmm_heads *Q, const qmm_heads *PK, const qmm
                     float scale, void *workspace, int64_t workspace_bytes, void *stream);
 
 /* qmm_attn_shared_workspace_bytes - the workspace qmm_attn_shared needs for
- * these sizes, or QMM_ERR_SHAPE. The same on every device. */
+ * these sizes, or QMM_ERR_SHAPE. The same on every device. Fewer sequences or
+ * keys may need more (32 sequences on a prefix of 32000 more than 48): a
+ * workspace kept for calls of different sizes is as large as
+ * qmm_attn_shared_workspace_max_bytes says. */
 int64_t qmm_attn_shared_workspace_bytes(int64_t n_seqs, int64_t prefix_len, int64_t own_cap, int64_t n_q_heads,
                                         int64_t n_kv_heads, int64_t head_dim);
+
+/* qmm_attn_shared_workspace_max_bytes - what no call of at most max_seqs
+ * sequences needs more than, whatever prefix_len, own_cap and n_kv_heads; never
+ * decreases with any of its arguments. Pieces of the prefix make at most 512 x
+ * 128 rows of partial results, or one for every row of Q, those of the caches
+ * 512 x 32, or one likewise. */
+static inline int64_t qmm_attn_shared_workspace_max_bytes(int64_t max_seqs, int64_t n_q_heads, int64_t head_dim) {
+  return (512 * (128 + 32) + 3 * max_seqs * n_q_heads) * (head_dim + 2) * 4;
+}
 
 #ifdef __cplusplus
 }
