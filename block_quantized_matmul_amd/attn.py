@@ -13,6 +13,7 @@ from __future__ import annotations
 
 import ctypes
 import struct
+import threading
 from typing import NamedTuple, Optional
 
 import block_quantized_matmul_amd as _qmm
@@ -61,6 +62,7 @@ class qmm_head_part(NamedTuple):
 
 
 _ready = None
+_loading = threading.Lock()
 _types = {}
 _calls = {}
 torch = None  # imported with the library, at the first call
@@ -69,32 +71,39 @@ _heads_bytes = struct.Struct("@Pqqq").pack  # a qmm_heads_desc's
 
 
 def _lib():
+    return _ready or _load()
+
+
+def _load():
+    """Declares the functions, once, whichever thread comes first: what others find is complete."""
     global _ready, torch
-    if _ready is None:
-        import torch
-        _types.update({torch.float32: QMM_T_F32, torch.float16: QMM_T_F16, torch.bfloat16: QMM_T_BF16})
-        L = _qmm.lib()
-        heads = ctypes.POINTER(qmm_heads_desc)
-        L.qmm_lora.argtypes = [_vp, _i32, _i64, _i64, _vp, _vp, _i64, _i64, _i64, _vp, _vp, _vp, _vp, _vp, _i64, _vp]
-        L.qmm_lora.restype = _i32
-        L.qmm_lora_workspace_bytes.argtypes = [_i64, _i64, _i64]
-        L.qmm_lora_workspace_bytes.restype = _i64
-        L.qmm_norm_rope.argtypes = [ctypes.POINTER(qmm_head_part_desc), _i32, _i64, _i64, _f32, _vp, _vp, _i64, _i32,
-                                    _vp, _i64, _vp]
-        L.qmm_norm_rope.restype = _i32
-        L.qmm_attn_prompt.argtypes = [_i32, heads, heads, heads, heads, _i64, _i64, _i64, _i64, _vp, _i64, _f32, _vp]
-        L.qmm_attn_prompt.restype = _i32
-        L.qmm_attn_shared.argtypes = [_i32, heads, heads, heads, _i64, heads, heads, _i64, _vp, heads, _i64, _i64,
-                                      _i64, _i64, _f32, _vp, _i64, _vp]
-        L.qmm_attn_shared.restype = _i32
-        L.qmm_attn_shared_workspace_bytes.argtypes = [_i64] * 6
-        L.qmm_attn_shared_workspace_bytes.restype = _i64
-        # the same functions for this module, which passes host structs as bytes
-        for name in ("qmm_norm_rope", "qmm_attn_prompt", "qmm_attn_shared"):
-            f = _calls[name] = L[name]
-            f.argtypes = [_vp if issubclass(t, ctypes._Pointer) else t for t in getattr(L, name).argtypes]
-            f.restype = _i32
-        _ready = L
+    with _loading:
+        if _ready is None:
+            import torch
+            _types.update({torch.float32: QMM_T_F32, torch.float16: QMM_T_F16, torch.bfloat16: QMM_T_BF16})
+            L = _qmm.lib()
+            heads = ctypes.POINTER(qmm_heads_desc)
+            L.qmm_lora.argtypes = [_vp, _i32, _i64, _i64, _vp, _vp, _i64, _i64, _i64, _vp, _vp, _vp, _vp, _vp, _i64, _vp]
+            L.qmm_lora.restype = _i32
+            L.qmm_lora_workspace_bytes.argtypes = [_i64, _i64, _i64]
+            L.qmm_lora_workspace_bytes.restype = _i64
+            L.qmm_norm_rope.argtypes = [ctypes.POINTER(qmm_head_part_desc), _i32, _i64, _i64, _f32, _vp, _vp, _i64, _i32,
+                                        _vp, _i64, _vp]
+            L.qmm_norm_rope.restype = _i32
+            L.qmm_attn_prompt.argtypes = [_i32, heads, heads, heads, heads, _i64, _i64, _i64, _i64, _vp, _i64, _f32, _vp]
+            L.qmm_attn_prompt.restype = _i32
+            L.qmm_attn_shared.argtypes = [_i32, heads, heads, heads, _i64, heads, heads, _i64, _vp, heads, _i64, _i64,
+                                          _i64, _i64, _f32, _vp, _i64, _vp]
+            L.qmm_attn_shared.restype = _i32
+            L.qmm_attn_shared_workspace_bytes.argtypes = [_i64] * 6
+            L.qmm_attn_shared_workspace_bytes.restype = _i64
+            # the same functions for this module, which passes host structs as bytes
+            for name in ("qmm_norm_rope", "qmm_attn_prompt", "qmm_attn_shared"):
+                f = L[name]
+                f.argtypes = [_vp if issubclass(t, ctypes._Pointer) else t for t in getattr(L, name).argtypes]
+                f.restype = _i32
+                _calls[name] = f
+            _ready = L
     return _ready
 
 
