@@ -140,10 +140,11 @@ class _Place:
         self.device, self.like = device, tensors[0]
         self.handle = torch._C._cuda_getCurrentRawStream(device)
         self.foreign = None
-        if stream is not None and stream.cuda_stream != self.handle:
-            if stream.device.index != device:
+        if stream is not None:
+            if stream.device.index != device:  # (whose handle may be the same: default streams')
                 raise ValueError(f"the stream is on {stream.device}, the tensors on cuda:{device}")
-            self.handle, self.foreign = stream.cuda_stream, stream
+            if stream.cuda_stream != self.handle:
+                self.handle, self.foreign = stream.cuda_stream, stream
 
     def empty(self, shape, dtype):
         if self.foreign is None:

@@ -1,6 +1,10 @@
-"""The attention operators' binding: its first use from several threads."""
+"""The attention operators' binding: its first use from several threads, and the
+streams it refuses (no GPU needed: calls stop before the library)."""
 import threading
 import time
+from types import SimpleNamespace
+
+import pytest
 
 import block_quantized_matmul_amd as qmm
 from block_quantized_matmul_amd import attn
@@ -44,3 +48,22 @@ def test_first_use_from_several_threads(monkeypatch):
     for t in threads:
         t.join()
     assert not failed, failed
+
+
+def test_a_stream_of_another_gpu_is_refused(monkeypatch):
+    """Also where its handle is that of the tensors' current stream, as those of two GPUs' default streams are."""
+    attn._lib()
+    monkeypatch.setattr(attn, "torch", SimpleNamespace(_C=SimpleNamespace(_cuda_getCurrentRawStream=lambda device: 0)))
+    tensor = SimpleNamespace(get_device=lambda: 0)
+
+    def stream(index, handle):
+        return SimpleNamespace(device=SimpleNamespace(index=index), cuda_stream=handle)
+
+    for handle in (0, 77):
+        with pytest.raises(ValueError, match="stream"):
+            attn._Place(stream(1, handle), ("X",), [tensor])
+    place = attn._Place(stream(0, 0), ("X",), [tensor])
+    assert place.handle == 0 and place.foreign is None
+    own = stream(0, 77)
+    place = attn._Place(own, ("X",), [tensor])
+    assert place.handle == 77 and place.foreign is own
