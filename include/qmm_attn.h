@@ -155,7 +155,7 @@ typedef struct qmm_head_part {
  * range is normed as if by infinity or by sqrt(eps)); an angle is reduced to
  * a turn in 64-bit fixed point (error below 2^-30 of a turn at any position)
  * before sine and cosine. n_tokens == 0 is a no-op. n_tokens, n_slots < 2^31;
- * every offset <= 2^60 elements.
+ * at most 2^24 heads in all parts; every offset <= 2^60 elements.
  */
 int qmm_norm_rope(const qmm_head_part *parts, int n_parts, int64_t n_tokens, int64_t head_dim, float eps,
                   const int32_t *positions, const double *freqs, int64_t n_freqs, int pairs, const int32_t *slots,
@@ -200,7 +200,9 @@ typedef struct qmm_heads {
  * largest finite fp16. A non-finite K or V of a later token does not reach an
  * earlier one; where one is attended to, the outputs it enters are not finite
  * (infinite or NaN). n_tokens == 0 or n_seqs == 0 is a no-op. n_tokens,
- * n_seqs < 2^31 - 128 and n_tokens * n_q_heads < 2^31 - 2^20.
+ * n_seqs < 2^31 - 128 and n_tokens * n_q_heads < 2^31 - 2^20, and
+ * (n_tokens * (n_q_heads / n_kv_heads) / 128 + min(n_seqs, n_tokens)) *
+ * n_kv_heads < 2^24, the workgroups of a launch (QMM_ERR_SHAPE).
  */
 int qmm_attn_prompt(int type, const qmm_heads *Q, const qmm_heads *K, const qmm_heads *V, const qmm_heads *O,
                     int64_t n_tokens, int64_t n_q_heads, int64_t n_kv_heads, int64_t head_dim,
@@ -229,8 +231,9 @@ int qmm_attn_prompt(int type, const qmm_heads *Q, const qmm_heads *K, const qmm_
  *                aligned; partial results, overwritten; two calls in flight
  *                must not share one. May be NULL when that size is 0.
  * Numerics as qmm_attn_prompt; partial results are joined in fp32 in a fixed
- * order. n_seqs == 0 is a no-op. n_seqs, prefix_len, own_cap < 2^31 - 2^20,
- * n_seqs * n_q_heads < 2^31 - 2^20.
+ * order. n_seqs == 0 is a no-op. prefix_len, own_cap < 2^31 - 2^20. n_seqs *
+ * n_q_heads up to 2^22 is taken with any of these; from 2^24 on, and before
+ * where a launch would have more than 2^24 workgroups, it is QMM_ERR_SHAPE.
  */
 int qmm_attn_shared(int type, const qmm_heads *Q, const qmm_heads *PK, const qmm_heads *PV, int64_t prefix_len,
                     const qmm_heads *K, const qmm_heads *V, int64_t own_cap, const int32_t *lengths,
