@@ -230,6 +230,8 @@ int qmm_attn_prompt(int type, const qmm_heads *Q, const qmm_heads *K, const qmm_
  *   workspace    at least qmm_attn_shared_workspace_bytes(...) bytes, 16-byte
  *                aligned; partial results, overwritten; two calls in flight
  *                must not share one. May be NULL when that size is 0.
+ * O must not overlap K, V, PK, PV or the workspace, nor two of its own heads
+ * each other; it may be Q itself, with equal strides.
  * Numerics as qmm_attn_prompt; partial results are joined in fp32 in a fixed
  * order. n_seqs == 0 is a no-op. prefix_len, own_cap < 2^31 - 2^20. n_seqs *
  * n_q_heads up to 2^22 is taken with any of these; from 2^24 on, and before

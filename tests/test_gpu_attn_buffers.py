@@ -1,4 +1,5 @@
-"""One workspace, sized for the largest batch, through calls of falling sizes."""
+"""Buffers of the attention operators: one workspace, sized for the largest batch,
+through calls of falling sizes, and an output in place of the queries."""
 import numpy as np
 import pytest
 import torch
@@ -38,3 +39,17 @@ def test_lora():
         got, want = qmm.qmm_lora(*args, workspace=ws), qmm.qmm_lora(*args)
         torch.cuda.synchronize()
         assert torch.equal(got, want)
+
+
+@pytest.mark.parametrize("prefix,cap", [(100, 50), (3000, 50), (0, 2000)])
+def test_output_in_place_of_the_queries(prefix, cap):
+    r = rng(52)
+    q = _normal(r, 9, 8, 64).half()
+    pk, pv = (_normal(r, prefix, 2, 64).half() if prefix else None for _ in range(2))
+    k, v = (_normal(r, 9, cap, 2, 64).half() for _ in range(2))
+    lengths = torch.tensor([i * cap // 8 for i in range(9)], dtype=torch.int32).cuda()
+    say(f"shared, O in place of Q, prefix {prefix}, caches of {cap}")
+    want = qmm.qmm_attn_shared(q, pk, pv, k, v, lengths)
+    got = qmm.qmm_attn_shared(q, pk, pv, k, v, lengths, O=q)
+    torch.cuda.synchronize()
+    assert got is q and torch.equal(got, want)

@@ -187,3 +187,31 @@ def test_large_scale_beside_a_nonfinite_later_value(power):
     o = qmm.qmm_attn_prompt(q.cuda(), k.cuda(), v.cuda(), torch.tensor(starts, dtype=torch.int32).cuda(), scale=scale)
     torch.cuda.synchronize()
     assert_within(o[:n - 1], want[:n - 1], err[:n - 1], "rows before it")
+
+
+@pytest.mark.parametrize("kind", ["f16", "bf16"])
+@pytest.mark.parametrize("dim", [64, 128])
+def test_large_scores_beside_infinite_and_nonfinite(kind, dim):
+    """Keys whose score is -infinity among large ones, and rows computed key by key for a later token's value."""
+    n, mag = 150, 8000.0 if kind == "f16" else 2.0 ** 40
+    signs = rng(25, dim).choice([-1, 1], n)
+    c = ties(kind, dim, mag, signs, 26)
+    c.k[5::7] = -float("inf")
+    c.scores[5::7] = -np.inf
+    v = c.v.clone()
+    v[n - 1, 3] = float("nan")
+    say(f"{kind} dim={dim}, large and infinite scores")
+    args = c.q.expand(n, 2, dim).contiguous().cuda(), c.k[:, None].cuda()
+    starts = torch.tensor([0, n], dtype=torch.int32).cuda()
+    prompt = qmm.qmm_attn_prompt(*args, c.v[:, None].cuda(), starts)
+    by_key = qmm.qmm_attn_prompt(*args, v[:, None].cuda(), starts)
+    direct = qmm.qmm_attn_shared(args[0][:1], args[1], c.v[:, None].cuda(), None, None, None)
+    pieces = qmm.qmm_attn_shared(args[0][:1], args[1].repeat(8, 1, 1), c.v[:, None].cuda().repeat(8, 1, 1), None, None, None)
+    torch.cuda.synchronize()
+    v = c.v.double().numpy()
+    rows = [_attend(c.scores[:t + 1], v[:t + 1], kind) for t in range(n)]
+    want, err = (np.repeat(np.array([r[i] for r in rows])[:, None], 2, 1) for i in (0, 1))
+    assert_within(prompt, want, err, "tiles")
+    assert_within(by_key[:n - 1], want[:n - 1], err[:n - 1], "key by key")
+    assert_within(direct[0], want[-1], err[-1], "direct")
+    assert_within(pieces[0], want[-1], err[-1] + 21 * n * O.E32 * np.abs(v).max(0), "pieces")
