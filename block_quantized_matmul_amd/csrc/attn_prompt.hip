@@ -19,14 +19,14 @@
 // The grid covers an upper bound of the tiles (the starts are device data) of
 // sequences that share no token, as starts in order make them. Where starts
 // are not in order, there may be more tiles, and workgroups that have seen so
-// take several, one after another (attn_prompt_kernel). Each wavefront finds its tile by a search over the starts, 64 sequences at a
-// time, which orders the tiles by length. KV heads are the fastest index, so
-// that with 8 of them (or a multiple) each XCD's L2 holds the keys of its own
-// heads only.
+// take several, one after another (attn_prompt_kernel). Each wavefront finds its
+// tile by a search over the starts, 64 sequences at a time, which orders the
+// tiles by length. KV heads are the fastest index, so that with 8 of them (or a
+// multiple) each XCD's L2 holds the keys of its own heads only.
 //
-// Measured, 32 heads on 8 KV heads of 128: 8192 tokens bf16 480 to 500 us
-// (550 GFLOP, 1.1 PFLOP/s where a large library product reaches 1.26; matrix
-// cores busy in 66 % of the cycles, vector units in 56 %); 16 prompts of up to
+// Measured, 32 heads on 8 KV heads of 128: 8192 tokens bf16 490 to 520 us
+// by box (550 GFLOP, 1.1 PFLOP/s where a large library product reaches 1.26;
+// matrix cores busy in 65 % of the cycles, vector units in 56 %); 16 prompts of up to
 // 950 tokens 82 us (0.54 PFLOP/s: of a tile's 17 us, 4 are its search and
 // first loads, 2 the masked block and 2 the store). 16 heads of 64, three
 // prompts of up to 2001 tokens, 32 us: half of a block's time is exponentials

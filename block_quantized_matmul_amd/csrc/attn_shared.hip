@@ -21,7 +21,7 @@
 // second launch joins the pieces.
 //
 // Measured, 32 heads on 8 KV heads of 128, bf16: 48 sequences on a prefix of
-// 32000 and caches of up to 2047 92 us, 6 of them the join (332 MB, 3.6 TB/s);
+// 32000 and caches of up to 2047 93 us, 6 of them the join (332 MB, 3.6 TB/s);
 // 4 sequences on 500 + 130 keys 11 us in one launch (latency).
 #include "attn.h"
 #include "attn_core.h"
@@ -329,7 +329,12 @@ template <class E, int D> hipError_t run(const SharedArgs &a, int64_t items, boo
 }  // namespace
 
 // Pieces: enough workgroups to fill the GPU, but at least kMinPiece keys in
-// each, since every piece costs its rows' partial result. (The header's
+// each, since every piece costs its rows' partial result. Lengths are device
+// data, so the pieces of the caches follow from their number, not from how long
+// each is: from kWantGroups (or kWantBoth) caches and KV heads on, a cache is one
+// workgroup's, and a long one among short ones is that workgroup's chain while
+// the GPU is otherwise idle (32 heads on 8 of 128: 64 caches of 500 25 us, with
+// one of 32000 among them 312). (The header's
 // qmm_attn_shared_workspace_max_bytes follows from kWantGroups and the tiles'
 // rows.)
 SharedPlan shared_plan(int64_t n_seqs, int64_t prefix_len, int64_t own_cap, int64_t n_q_heads, int64_t n_kv_heads) {
@@ -337,8 +342,9 @@ SharedPlan shared_plan(int64_t n_seqs, int64_t prefix_len, int64_t own_cap, int6
   SharedPlan p{};
   p.row_tiles = (n_seqs * group + kSharedRows - 1) / kSharedRows;
   p.own_tiles = (group + kOwnRows - 1) / kOwnRows;
-  // (without a prefix, a workgroup per cache is as good where they fill the
-  // GPU: 64 caches of 2000 94 / 99 us)
+  // (without a prefix, where the caches fill the GPU there would be one piece of
+  // each, which only adds the join; us without and with it: 64 caches of 2000
+  // 96 / 101, of 8000 356 / 362, of 32000 1392 / 1400, of 500 25 / 30)
   p.direct = (prefix_len + own_cap <= kDirectKeys && prefix_len * n_seqs <= kDirectReads) ||
              (prefix_len == 0 && n_seqs * n_kv_heads * p.own_tiles >= kWantGroups);
   if (p.direct) return p;

@@ -47,15 +47,28 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kTok = 16;            // tokens per product
 constexpr int kSub = 4;             // products' tokens per consecutive tile
-constexpr int kGroupTokens = 512;   // largest batch in tiles by adapter
-constexpr int kMaxSplits = 256;     // ranges of k, tiles by adapter
+// Largest batch in tiles by adapter. The host does not know the ids, so this
+// weighs decode batches of many adapters against prompts. 4096 x 4096, rank 16,
+// us by adapter / in consecutive tiles: 200 tokens on 32 adapters at random 17 /
+// 39, on 8 17 / 18, in 9 runs 17 / 14, on one 20 / 12; 512 tokens 29 / 48, 28 /
+// 22, 29 / 14, 53 / 14; 1000 tokens 49 / 84, 48 / 35, 51 / 19, 89 / 17. What is
+// left is a step up for batches of many adapters at random: 512 tokens on 32
+// 29 us, 513 59.
+constexpr int kGroupTokens = 512;
+// Ranges of k, tiles by adapter: bounds the workspace, for k beyond 131072 only.
+// 1 token of 262144 to 1024 rows 22 us, 14 with 64 ranges, 38 with 1024; of
+// 1048576 26, 27, 72.
+constexpr int kMaxSplits = 256;
 // Workgroups among which a consecutive tile's adapters are dealt: most tiles
 // have one adapter, and those where requests meet two. 2048 tokens of 9
 // requests 61 us, with one workgroup for all of a tile's adapters 66, with four
 // 67 (the workgroups that leave at once cost more than they save).
 constexpr int kShares = 2;
 constexpr int kRankGroup = 64;      // ranks per workgroup of the first launch
-constexpr int kTileGroups = 512;    // workgroups the first launch aims at, consecutive tiles
+// Workgroups the first launch aims at, consecutive tiles: 2048 tokens, 11008 to
+// 4096 rows, rank 64 63 us, 64 with 256, 72 with 1024; 8192 tokens, 4096 x 4096,
+// rank 32 119, 124, 117.
+constexpr int kTileGroups = 512;
 
 // Tiles by adapter: the tokens of workgroup `t`'s tile, by their ids' order in
 // the batch, in slot[0 .. 15] of LDS (-1 behind the last). False if t does
@@ -619,7 +632,10 @@ hipError_t launch_lora(const void *X, bool x_f16, int64_t n_tokens, int64_t k, c
   }
 
   // Steps of 64 rows by adapter (256 bytes of a token's row), of 16 where
-  // there are few or for consecutive tiles, whose step has 64 tokens; several
+  // there are few or for consecutive tiles, whose step has 64 tokens (rank 16,
+  // us in steps of 64 / 16: 64 tokens to 11008 rows 15.6 / 17.4, 256 to 4096
+  // 24.6 / 26.5, up to 16 tokens the same; rank 64: 64 to 11008 46.5 / 40.6, 8 to
+  // 11008 16.2 / 14.8); several
   // steps where there are workgroups enough, since each workgroup first adds
   // up its tokens' V. On consecutive tiles V is little for ranks up to 32, and
   // more workgroups balance better: 2048 tokens, 11008 rows, rank 16 72 us with

@@ -101,8 +101,9 @@ template <int V> __device__ __forceinline__ void store_run(void *y, int64_t at, 
   }
 }
 
-// Sine and cosine of 2 pi t / 2^64. The Taylor polynomials' first omitted
-// terms are below 2e-9 on [-pi/4, pi/4].
+// Sine and cosine of 2 pi t / 2^64. On [-pi/4, pi/4] the Taylor polynomials'
+// first omitted terms are at most 1.8e-9 for the sine (x^11 / 11!) and 2.5e-8,
+// 0.4 of a half step of fp32 at 1, for the cosine (x^10 / 10!).
 __device__ __forceinline__ void sincos_turn(uint64_t t, float &sin, float &cos) {
   const uint32_t quadrant = static_cast<uint32_t>((t + (uint64_t{1} << 61)) >> 62);
   const int32_t r = static_cast<int32_t>((t - (static_cast<uint64_t>(quadrant) << 62)) >> 32);

@@ -77,6 +77,10 @@ extern "C" {
  * Numerics: A, B and an fp16 X are multiplied exactly and summed in fp32; an
  * fp32 X is not rounded; V stays in fp32. Non-finite values of one token's
  * X or of an adapter stay in the rows of the tokens that use them.
+ * Time: up to 512 tokens are gathered by their adapters, wherever they stand.
+ * Beyond, 64 consecutive tokens take theirs one after another, as suits prompts
+ * (1000 tokens of 4096 to 4096 rows, rank 16: 19 us in 9 runs, 84 us where 32
+ * adapters alternate at random).
  * n_tokens == 0 or n_rows == 0 is a no-op. Sizes: n_tokens < 2^25, k < 2^24,
  * n_rows, n_adapters < 2^31, n_tokens * n_rows, n_adapters * rank * k,
  * n_adapters * n_rows * rank <= 2^60 (QMM_ERR_SHAPE).
@@ -232,6 +236,9 @@ int qmm_attn_prompt(int type, const qmm_heads *Q, const qmm_heads *K, const qmm_
  *                must not share one. May be NULL when that size is 0.
  * O must not overlap K, V, PK, PV or the workspace, nor two of its own heads
  * each other; it may be Q itself, with equal strides.
+ * Time: the work is divided by own_cap and the number of sequences, since the
+ * host does not know the lengths. Of many sequences with one much longer cache
+ * than the others', that one decides the time.
  * Numerics as qmm_attn_prompt; partial results are joined in fp32 in a fixed
  * order. n_seqs == 0 is a no-op. prefix_len, own_cap < 2^31 - 2^20. n_seqs *
  * n_q_heads up to 2^22 is taken with any of these; from 2^24 on, and before
