@@ -26,8 +26,8 @@
 //
 // Measured, 32 heads on 8 KV heads of 128: 8192 tokens bf16 490 to 520 us
 // by box (550 GFLOP, 1.1 PFLOP/s where a large library product reaches 1.26;
-// matrix cores busy in 65 % of the cycles, vector units in 56 %); 16 prompts of up to
-// 950 tokens 82 us (0.54 PFLOP/s: of a tile's 17 us, 4 are its search and
+// matrix cores busy in 65 % of the cycles, vector units in 56 %); 16 prompts of
+// up to 950 tokens 82 us (0.54 PFLOP/s: of a tile's 17 us, 4 are its search and
 // first loads, 2 the masked block and 2 the store). 16 heads of 64, three
 // prompts of up to 2001 tokens, 32 us: half of a block's time is exponentials
 // and other vector work, and the last third of the time only the longest
@@ -78,13 +78,13 @@ __device__ __forceinline__ int lane_max(int x) {
   return __builtin_amdgcn_readlane(scan_lanes(x, [](int a, int b) { return max(a, b); }), 63);
 }
 
-// The tile with number `index` over all sequences: its sequence's first token
-// and length, and its own number in it. False past the last one. `ahead`: the
-// number of tiles ahead of the first 64 sequences gone through of which one's
-// ends are not in order, or -1. Sequences are gone through 64 at a time. Among those, tiles go by bands of kBand of
-// their numbers, the highest (the longest tiles) first, so that the launch
-// ends with short ones; in a band by sequence, so that neighbours share keys,
-// and in a sequence downwards.
+// The tile with number `number` over all sequences: its sequence's first token
+// and length, and its own number in it. False past the last one. Sequences are
+// gone through 64 at a time. Among those, tiles go by bands of kBand of their
+// numbers, the highest (the longest tiles) first, so that the launch ends with
+// short ones; in a band by sequence, so that neighbours share keys, and in a
+// sequence downwards. `ahead`: the number of tiles ahead of the first 64
+// sequences of which one's ends are not in order; -1 if none was met.
 __device__ __forceinline__ bool find_tile(const PromptArgs &a, int64_t number, int lane, int &first, int &len, int &tile,
                                           int64_t &ahead) {
   int64_t left = number;
