@@ -15,10 +15,11 @@ border decides: codes, expert choices, cumulative probabilities), or, where
 `own` is set, by the library's entry points. exact() is the definition in 64
 bits, row by row.
 
-A page of the cache holds `page` tokens of every KV head, head by head: K
-codes [page][dim / 2 bytes], K scales fp16 [dim / 32][page], V codes, V scales.
-Element e of a K row is nibble n of dword g (dim / 32) + b, with b = e / 32,
-g = e % 32 / 8, n = e % 8; of a V row, nibble e. A value is d (code - 8).
+A page of the cache holds `page` tokens of every KV head, head by head, in tiles
+of 16 tokens: K codes, V codes [16][dim / 2 bytes], K scales, V scales, both fp16
+[dim / 32][16]. Element e of token t's K is nibble e % 8 of dword
+(16 (e % 32 / 8) + t) (dim / 32) + e / 32 of the tile's K codes, of its V nibble e
+of its row. A value is d (code - 8).
 """
 import math
 
@@ -112,18 +113,18 @@ def _page_bytes(page, hkv, dim):
 def _cache(n_pages, c, gen):
     """A cache with keys and values in every place: codes like those of normal values, scales as their blocks have."""
     page, hkv, dim = c["page"], c["hkv"], c["dim"]
-    pages = torch.empty(n_pages, hkv, 2, page * dim * 9 // 16, dtype=torch.uint8, device="cuda")
+    pages = torch.empty(n_pages, hkv * page // 16, 18 * dim, dtype=torch.uint8, device="cuda")
 
     def codes(*shape):
         return (torch.randn(*shape, generator=gen, device="cuda") * 3.4 + 8.5).clamp_(0, 15).to(torch.uint8)
 
-    for lo in range(0, n_pages, 2048):  # in parts, for the memory of the random numbers
-        part = pages[lo:lo + 2048]
-        shape = (*part.shape[:3], page * dim // 2)
-        part[..., :page * dim // 2] = codes(*shape) | codes(*shape) << 4
-        d = 0.27 * (0.6 + 0.8 * torch.rand(*part.shape[:3], page * dim // 32, generator=gen, device="cuda"))
+    for lo in range(0, n_pages, 1024):  # in parts, for the memory of the random numbers
+        part = pages[lo:lo + 1024]
+        shape = (*part.shape[:2], 16 * dim)
+        part[..., :16 * dim] = codes(*shape) | codes(*shape) << 4
+        d = 0.27 * (0.6 + 0.8 * torch.rand(*part.shape[:2], dim, generator=gen, device="cuda"))
         sign = torch.where(torch.rand(d.shape, generator=gen, device="cuda") < 0.5, -1.0, 1.0)
-        part[..., page * dim // 2:] = (d * sign).half().view(torch.uint8)
+        part[..., 16 * dim:] = (d * sign).half().view(torch.uint8)
     return pages.view(n_pages, -1)
 
 
@@ -264,14 +265,14 @@ def _plain_append(s):
 
 def _plain_pages(pages, page, hkv, dim):
     """Keys and values of pages [..., bytes], each [..., page, hkv, dim] in 32 bits."""
-    flat = pages.unflatten(-1, (hkv, 2, page * dim * 9 // 16))
-    codes, scales = flat[..., : page * dim // 2], flat[..., page * dim // 2:].contiguous().view(torch.float16)
-    codes = torch.stack([codes & 15, codes >> 4], -1).flatten(-2).unflatten(-1, (page, dim)).float() - 8.0
-    scales = scales.unflatten(-1, (dim // 32, page)).transpose(-1, -2).float()
-    k, v = codes.select(-3, 0), codes.select(-3, 1)  # [..., hkv, page, dim]
-    k = k.unflatten(-1, (4, dim // 32, 8)).transpose(-2, -3) * scales.select(-3, 0)[..., None, None]
-    v = v.unflatten(-1, (dim // 32, 32)) * scales.select(-3, 1)[..., None]
-    return k.flatten(-3).transpose(-2, -3), v.flatten(-2).transpose(-2, -3)
+    tiles = pages.unflatten(-1, (hkv, page // 16, 18 * dim))
+    codes, scales = tiles[..., : 16 * dim], tiles[..., 16 * dim:].contiguous().view(torch.float16).float()
+    codes = (torch.stack([codes & 15, codes >> 4], -1).flatten(-2).float() - 8.0).unflatten(-1, (2, 16 * dim))
+    k = codes.select(-2, 0).unflatten(-1, (4, 16, dim // 32, 8)).movedim(-4, -2)  # [..., token, block, 4, 8]
+    v = codes.select(-2, 1).unflatten(-1, (16, dim // 32, 4, 8))
+    scales = scales.unflatten(-1, (2, dim // 32, 16)).transpose(-1, -2)[..., None, None]  # [..., 2, token, block, 1, 1]
+    # [..., hkv, tile, token, dim] to [..., page, hkv, dim]
+    return tuple((x * scales.select(-5, i)).flatten(-3).flatten(-3, -2).transpose(-2, -3) for i, x in enumerate((k, v)))
 
 
 def _plain_attn(s):
@@ -389,16 +390,19 @@ def _exact_codes(x):
     return out
 
 
-def _exact_page_value(head, which, page, dim):
-    """Keys (0) or values (1) of one head's bytes of pages, [pages][page][dim]."""
-    n = page * dim
-    codes = head[:, which, : n // 2].reshape(-1, page, dim // 2)
-    d = head[:, which, n // 2:].contiguous().view(torch.float16).view(-1, dim // 32, page).double()
-    out = torch.empty(head.shape[0], page, dim, dtype=torch.float64, device=head.device)
-    for e in range(dim):
-        nibble = e if which == 1 else (e % 32 // 8 * (dim // 32) + e // 32) * 8 + e % 8
-        out[..., e] = ((codes[..., nibble // 2] >> 4 * (nibble % 2) & 15).double() - 8.0) * d[:, e // 32]
-    return out
+def _exact_page_value(head, which, dim):
+    """Keys (0) or values (1) of one head's tiles [pages][tiles][bytes], [pages][page][dim]."""
+    codes = head[..., 8 * dim * which: 8 * dim * (which + 1)]
+    d = head[..., dim * (16 + which): dim * (17 + which)].contiguous().view(torch.float16).double()
+    out = torch.empty(*head.shape[:2], 16, dim, dtype=torch.float64, device=head.device)
+    for t in range(16):
+        for e in range(dim):
+            if which == 0:
+                nibble = ((e % 32 // 8 * 16 + t) * (dim // 32) + e // 32) * 8 + e % 8
+            else:
+                nibble = t * dim + e
+            out[..., t, e] = ((codes[..., nibble // 2] >> 4 * (nibble % 2) & 15).double() - 8.0) * d[..., e // 32 * 16 + t]
+    return out.flatten(1, 2)
 
 
 def _exact_weights(w, qtype):
@@ -441,10 +445,10 @@ def exact(case, seed):
         return {"k": _exact_codes(y), "v": _exact_codes(s["v"])}
     if c["op"] == "attn":
         g, dim, page = c["hq"] // c["hkv"], c["dim"], c["page"]
-        heads = s["cache"].view(-1, c["hkv"], 2, page * dim * 9 // 16)
+        heads = s["cache"].view(-1, c["hkv"], page // 16, 18 * dim)
         o = torch.zeros(c["seqs"], c["hq"], dim, dtype=torch.float64, device="cuda")
         for h in range(c["hkv"]):
-            k, v = (_exact_page_value(heads[:, h], i, page, dim) for i in (0, 1))
+            k, v = (_exact_page_value(heads[:, h], i, dim) for i in (0, 1))
             for i, n in enumerate(s["lens"]):
                 mine = s["tables"][i, : -(-n // page)].long()
                 if n:
