@@ -402,3 +402,4 @@ def qmm_matmul_batch_ws(items, workspace, stream=None):
 
 
 from .attn import *  # noqa: E402,F401,F403 - the operators of include/qmm_attn.h
+from .serve import *  # noqa: E402,F401,F403 - the operators of include/qmm_serve.h

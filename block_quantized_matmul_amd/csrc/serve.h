@@ -1,0 +1,41 @@
+// Internal launch interface between the C ABI of the serving-step operators
+// (serve_api.hip) and their kernels. Arguments have been validated.
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "qmm_serve.h"
+
+namespace qmm {
+
+// A 4-bit paged cache: the place of a token's tile, and what lies where in it.
+struct Kv4Cache {
+  uint8_t *data;
+  int64_t n_pages, page_bytes;
+  int page_tokens, page_shift;  // 2^page_shift tokens
+};
+constexpr int kKv4Tile = 16;  // tokens per tile
+__host__ __device__ constexpr int64_t kv4_tile_bytes(int64_t head_dim) { return 18 * head_dim; }
+
+hipError_t launch_kv4_append(int type, const qmm_heads &K, const qmm_heads &V, int64_t n_tokens, int64_t n_kv_heads,
+                             int64_t head_dim, bool norm, const float *weight, double eps, const int32_t *positions,
+                             const double *freqs, int64_t n_freqs, int pairs, const int32_t *slots,
+                             const Kv4Cache &cache, hipStream_t stream);
+hipError_t launch_kv4_read(int type, const qmm_heads &K, const qmm_heads &V, int64_t n_rows, int64_t n_kv_heads,
+                           int64_t head_dim, const int32_t *slots, const Kv4Cache &cache, hipStream_t stream);
+
+// qmm_attn_kv4's split: every row and KV head in `splits` ranges of keys (fewer
+// where a sequence is short), `tiles` workgroups for the heads of a group.
+struct Kv4Plan {
+  int64_t tiles;
+  int64_t columns;  // column tiles of a workgroup, 1 or 2
+  int64_t splits;
+};
+Kv4Plan kv4_plan(int64_t n_rows, int64_t n_q_heads, int64_t n_kv_heads, int64_t head_dim, int64_t cap);
+hipError_t launch_attn_kv4(int type, const qmm_heads &Q, const qmm_heads &O, int64_t n_rows, int64_t n_q_heads,
+                           int64_t n_kv_heads, int64_t head_dim, const Kv4Cache &cache, const int32_t *tables,
+                           int64_t table_stride, int64_t table_width, const int32_t *lengths, float scale,
+                           void *workspace, hipStream_t stream);
+
+}  // namespace qmm

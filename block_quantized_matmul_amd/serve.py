@@ -1,0 +1,180 @@
+"""The operators that complete a served decode step (C: include/qmm_serve.h).
+
+qmm_kv4_append, qmm_kv4_read and qmm_attn_kv4 (a 4-bit paged cache), in the
+same manner as attn.py: tensors supply pointers, strides and sizes, and the
+library checks and runs. All tensors of a call are on one GPU, which need not
+be the current one; work is enqueued on `stream`, or on that GPU's current
+stream.
+"""
+from __future__ import annotations
+
+import ctypes
+import threading
+
+import block_quantized_matmul_amd as _qmm
+from . import attn as _attn
+from .attn import _PAIRS, _Place, _floats, _heads, _host_doubles, _ints, _ptr, _type
+
+QMM_KV4_MAX_PAGE_TOKENS = 256
+
+__all__ = ["QMM_KV4_MAX_PAGE_TOKENS", "qmm_kv4_page_bytes", "qmm_kv4_append", "qmm_kv4_read", "qmm_attn_kv4",
+           "qmm_attn_kv4_workspace_bytes"]
+
+_vp, _i32, _i64, _f32, _f64 = ctypes.c_void_p, ctypes.c_int, ctypes.c_int64, ctypes.c_float, ctypes.c_double
+_ready = None
+_loading = threading.Lock()
+torch = None  # imported with the library, at the first call
+
+_SIGNATURES = {  # restype, then the arguments; host structs travel as bytes
+    "qmm_kv4_page_bytes": (_i64, [_i64] * 3),
+    "qmm_kv4_append": (_i32, [_i32, _vp, _vp, _i64, _i64, _i64, _i32, _vp, _f64, _vp, _vp, _i64, _i32, _vp, _vp, _i64,
+                              _i64, _vp]),
+    "qmm_kv4_read": (_i32, [_i32, _vp, _vp, _i64, _i64, _i64, _vp, _vp, _i64, _i64, _vp]),
+    "qmm_attn_kv4": (_i32, [_i32, _vp, _vp, _i64, _i64, _i64, _i64, _vp, _i64, _i64, _vp, _i64, _i64, _vp, _f32, _vp,
+                            _i64, _vp]),
+    "qmm_attn_kv4_workspace_bytes": (_i64, [_i64] * 6),
+}
+
+
+def _lib():
+    return _ready or _load()
+
+
+def _load():
+    """Declares the functions, once, whichever thread comes first: what others find is complete."""
+    global _ready, torch
+    with _loading:
+        if _ready is None:
+            _attn._lib()
+            import torch
+            L = _qmm.lib()
+            for name, (res, args) in _SIGNATURES.items():
+                f = getattr(L, name)
+                f.argtypes, f.restype = args, res
+            _ready = L
+    return _ready
+
+
+def _pages(cache, page_tokens, n_kv_heads, head_dim):
+    """The number of pages of a cache: a contiguous uint8 tensor [n_pages][qmm_kv4_page_bytes(...)]."""
+    if cache.dtype is not torch.uint8 or cache.dim() != 2 or not cache.is_contiguous():
+        raise TypeError("cache must be a contiguous 2-D uint8 tensor")
+    size = _ready.qmm_kv4_page_bytes(page_tokens, n_kv_heads, head_dim)
+    if size < 0:
+        raise _qmm.QmmError(int(size), "qmm_kv4_page_bytes")
+    if cache.shape[1] != size:
+        raise ValueError(f"a page of the cache holds {cache.shape[1]} bytes, the call needs {size}")
+    return cache.shape[0]
+
+
+def qmm_kv4_page_bytes(page_tokens: int, n_kv_heads: int, head_dim: int) -> int:
+    """Bytes of a page of a 4-bit cache with room for page_tokens tokens (16, 32, 64, 128 or 256)."""
+    size = int(_lib().qmm_kv4_page_bytes(int(page_tokens), int(n_kv_heads), int(head_dim)))
+    if size < 0:
+        raise _qmm.QmmError(size, "qmm_kv4_page_bytes")
+    return size
+
+
+def qmm_kv4_append(K, V, cache, page_tokens, slots, positions=None, freqs=None, pairs="halves", norm=False, weight=None,
+                   eps=1e-6, stream=None):
+    """Keys (normed, rotated) and values into a 4-bit paged cache (C: qmm_kv4_append).
+
+    K and V [n_tokens][n_kv_heads][head_dim], fp32, fp16 or bf16, any strides with
+    contiguous heads; cache uint8 [n_pages][qmm_kv4_page_bytes(...)]; slots int32
+    [n_tokens]: page * page_tokens + place, or outside the cache for a token that
+    is not stored. positions int32 [n_tokens] and freqs (the host table of radians
+    per position, as for qmm_norm_rope) rotate the keys, norm and weight (fp32
+    [head_dim]) norm them first. Returns the cache."""
+    L = _lib()
+    place = _Place(stream, ("K", "V", "cache", "slots", "positions", "weight"), (K, V, cache, slots, positions, weight))
+    if K.dim() != 3:
+        raise ValueError("K and V must be [n_tokens][n_kv_heads][head_dim]")
+    shape, dtype = K.shape, K.dtype
+    n, heads, dim = shape
+    n_pages = _pages(cache, page_tokens, heads, dim)
+    if pairs not in _PAIRS:
+        raise ValueError("pairs must be 'halves' or 'neighbours'")
+    if weight is not None:
+        if not norm:
+            raise ValueError("weight needs norm")
+        _floats(weight, "weight", (dim,))
+    if (positions is None) != (freqs is None):
+        raise ValueError("pass positions and freqs together")
+    if positions is not None:
+        _ints(positions, "positions", n)
+    _ints(slots, "slots", n)
+    fp, n_freqs, _keep = _host_doubles(freqs)
+    place.run(L.qmm_kv4_append, "qmm_kv4_append", _type(K, "K"), _heads(K, "K", shape, dtype),
+              _heads(V, "V", shape, dtype), n, heads, dim, bool(norm), _ptr(weight), eps, _ptr(positions), fp, n_freqs,
+              _PAIRS[pairs], slots.data_ptr(), cache.data_ptr(), n_pages, page_tokens)
+    return cache
+
+
+def qmm_kv4_read(cache, page_tokens, slots, n_kv_heads=None, head_dim=None, dtype=None, K=None, V=None, stream=None):
+    """The keys and values at slots of a 4-bit paged cache (C: qmm_kv4_read).
+
+    Outputs [n][n_kv_heads][head_dim] fp32, fp16 or bf16: those that are passed,
+    or both, new, of n_kv_heads, head_dim and dtype (float32). A slot outside the
+    cache reads as NaNs. Returns (K, V), None for one that was not asked for."""
+    L = _lib()
+    place = _Place(stream, ("cache", "slots", "K", "V"), (cache, slots, K, V))
+    _ints(slots, "slots", None)
+    n = slots.shape[0]
+    if K is None and V is None:
+        if n_kv_heads is None or head_dim is None:
+            raise ValueError("pass K, V or both, or n_kv_heads and head_dim")
+        dtype = dtype or torch.float32
+        K, V = (place.empty((n, n_kv_heads, head_dim), dtype) for _ in range(2))
+    like = K if K is not None else V
+    if like.dim() != 3:
+        raise ValueError("K and V must be [n][n_kv_heads][head_dim]")
+    _, heads, dim = like.shape
+    n_pages = _pages(cache, page_tokens, heads, dim)
+    shape = (n, heads, dim)
+    place.run(L.qmm_kv4_read, "qmm_kv4_read", _type(like, "K"),
+              None if K is None else _heads(K, "K", shape, like.dtype),
+              None if V is None else _heads(V, "V", shape, like.dtype), n, heads, dim, slots.data_ptr(),
+              cache.data_ptr(), n_pages, page_tokens)
+    return K, V
+
+
+def qmm_attn_kv4_workspace_bytes(n_rows: int, n_q_heads: int, n_kv_heads: int, head_dim: int, table_width: int,
+                                 page_tokens: int) -> int:
+    return int(_lib().qmm_attn_kv4_workspace_bytes(int(n_rows), int(n_q_heads), int(n_kv_heads), int(head_dim),
+                                                   int(table_width), int(page_tokens)))
+
+
+def qmm_attn_kv4(Q, cache, page_tokens, n_kv_heads, tables, lengths, scale=None, O=None, workspace=None, stream=None):
+    """Attention of a decode batch over a 4-bit paged cache (C: qmm_attn_kv4).
+
+    Q [n_rows][n_q_heads][head_dim], fp16 or bf16, any strides (multiples of 8
+    elements) with contiguous heads; cache as qmm_kv4_append fills it; tables int32
+    [n_rows][table_width], the pages of each row's sequence in order (rows of any
+    stride, so an expanded table serves several tokens of one sequence); lengths
+    int32 [n_rows], the tokens each row attends to. A length outside the table, or
+    a page outside the cache, gives that row NaNs; a length of 0 zeros. scale
+    defaults to head_dim ** -0.5. O (like Q) is allocated if None. Without a
+    workspace, one of qmm_attn_kv4_workspace_bytes bytes is allocated."""
+    L = _lib()
+    place = _Place(stream, ("Q", "cache", "tables", "lengths", "O", "workspace"),
+                   (Q, cache, tables, lengths, O, workspace))
+    if Q.dim() != 3:
+        raise ValueError("Q must be [n_rows][n_q_heads][head_dim]")
+    shape, dtype = Q.shape, Q.dtype
+    n, hq, dim = shape
+    n_pages = _pages(cache, page_tokens, n_kv_heads, dim)
+    if tables.dtype is not torch.int32 or tables.dim() != 2 or (tables.shape[1] > 1 and tables.stride(1) != 1):
+        raise TypeError("tables must be a 2-D int32 tensor with contiguous rows")
+    if tables.shape[0] != n:
+        raise ValueError(f"tables holds {tables.shape[0]} rows, the call needs {n}")
+    _ints(lengths, "lengths", n)
+    if O is None:
+        O = place.empty(shape, dtype)
+    width = tables.shape[1]
+    _keep, ws, ws_bytes = place.workspace(workspace,
+                                          L.qmm_attn_kv4_workspace_bytes(n, hq, n_kv_heads, dim, width, page_tokens),
+                                          "qmm_attn_kv4_workspace_bytes")
+    place.run(L.qmm_attn_kv4, "qmm_attn_kv4", _type(Q, "Q"), _heads(Q, "Q", shape, dtype), _heads(O, "O", shape, dtype), n,
+              hq, n_kv_heads, dim, cache.data_ptr(), n_pages, page_tokens, tables.data_ptr(), tables.stride(0), width,
+              lengths.data_ptr(), dim ** -0.5 if scale is None else scale, ws, ws_bytes)
+    return O

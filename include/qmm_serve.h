@@ -1,0 +1,141 @@
+/*
+ * qmm_serve.h - C ABI of the operators that complete a decode step of a served
+ * transformer on the AMD MI355X (gfx950), in the same libqmm.so as qmm.h and
+ * qmm_attn.h:
+ *
+ *   qmm_kv4_append  keys (normed and rotated) and values rounded to 4-bit
+ *                   blocks and stored in a paged cache;
+ *   qmm_kv4_read    the values that places of such a cache hold;
+ *   qmm_attn_kv4    attention of a decode batch over such a cache.
+ *
+ * Conventions are those of qmm_attn.h: every pointer is device memory owned by
+ * the caller unless stated otherwise, nothing is retained or allocated, work
+ * is enqueued on `stream` (a hipStream_t of the current device, or NULL) and
+ * the call returns without waiting; every check runs on the host before
+ * anything is enqueued and returns a QMM_ERR_* status. There is no global
+ * state: calls on different streams may run concurrently as long as their
+ * workspaces and outputs differ. Every call may be captured into a HIP graph.
+ * Results repeat bit for bit for the same arguments on the same device.
+ */
+#ifndef QMM_SERVE_H
+#define QMM_SERVE_H
+
+#include <stdint.h>
+
+#include "qmm_attn.h"
+
+#ifdef __cplusplus
+extern "C" {
+#endif
+
+/*
+ * The 4-bit paged cache ("kv4"): n_pages pages of qmm_kv4_page_bytes(...) bytes
+ * one after another, 16-byte aligned, in one buffer for keys and values. A page
+ * has room for page_tokens tokens (16, 32, 64, 128 or 256) of n_kv_heads heads
+ * of head_dim (64 or 128) elements; slot s is place s % page_tokens of page
+ * s / page_tokens. Values are Q4_0 blocks of 32 elements, w = d (code - 8) with
+ * a binary16 d and codes 0 .. 15, laid out for the attention's loads: a page is
+ * [n_kv_heads][page_tokens / 16] tiles of 18 * head_dim bytes, each with
+ *   8 head_dim bytes  key codes: element e of the tile's token t is nibble e % 8
+ *                     of dword (16 (e % 32 / 8) + t) (head_dim / 32) + e / 32
+ *   8 head_dim bytes  value codes: [16][head_dim / 2], element e is nibble e % 2
+ *                     (low first) of byte e / 2 of token t's row
+ *   head_dim bytes    key scales, binary16 [head_dim / 32][16 tokens]
+ *   head_dim bytes    value scales, likewise.
+ * A page of zeros is valid (it holds zeros).
+ */
+#define QMM_KV4_MAX_PAGE_TOKENS 256
+
+/* qmm_kv4_page_bytes - bytes of a page, or QMM_ERR_SHAPE. */
+int64_t qmm_kv4_page_bytes(int64_t page_tokens, int64_t n_kv_heads, int64_t head_dim);
+
+/*
+ * qmm_kv4_append - for every token t with a slot, and every KV head:
+ *   key:    x = K[t][h]; norm: x = x / sqrt(mean_e x[e]^2 + eps) * weight[e];
+ *           rotated by positions[t] as qmm_norm_rope rotates (n_freqs 0: not);
+ *   value:  x = V[t][h];
+ *   both:   x rounded to fp32, then for each block of 32 elements
+ *             m = its element of largest magnitude (the first of several),
+ *             d = binary16(m / -8),  code = floor(x / d + 8.5) within 0 .. 15
+ *           (d +0 and the codes 8 where d is zero), stored at slots[t].
+ *   type          QMM_T_F32, QMM_T_F16 or QMM_T_BF16, of K and V
+ *   K, V          n_kv_heads heads, [n_tokens] in the token axis (seq_stride
+ *                 unused); strides are any >= 0, data aligned to the type
+ *   norm          1: norm the keys; weight (fp32 [head_dim]) then may be given
+ *   positions     int32 [n_tokens], any value; needed if n_freqs > 0
+ *   freqs         HOST array of n_freqs doubles, radians per position,
+ *                 magnitudes at most 64; read during the call
+ *   n_freqs       0 .. head_dim / 2; pairs: QMM_ROPE_HALVES or _NEIGHBOURS
+ *   slots         int32 [n_tokens]. A token whose slot lies outside
+ *                 [0, n_pages * page_tokens) is not stored (so -1 leaves it out).
+ *                 Two tokens with one slot leave a mixture of the two there;
+ *                 other places are never touched.
+ * Numerics: norm, angles and rotation in 64 bits, so the codes are those of the
+ * formula (a code is decided at a border, where an fp32 rotation would choose
+ * the other neighbour now and then). A block that holds an infinity, a NaN or
+ * an element whose d leaves binary16's range is stored as NaNs (d a quiet NaN,
+ * codes 8). K and V do not overlap the cache.
+ * n_tokens, n_pages * page_tokens < 2^31; n_tokens * n_kv_heads <= 2^40.
+ */
+int qmm_kv4_append(int type, const qmm_heads *K, const qmm_heads *V, int64_t n_tokens, int64_t n_kv_heads,
+                   int64_t head_dim, int norm, const float *weight, double eps, const int32_t *positions,
+                   const double *freqs, int64_t n_freqs, int pairs, const int32_t *slots, void *cache,
+                   int64_t n_pages, int64_t page_tokens, void *stream);
+
+/*
+ * qmm_kv4_read - K[i], V[i] = the keys and values at slots[i], each rounded
+ * once to `type` (QMM_T_F32 is exact). A slot outside the cache reads as NaNs.
+ * Either output may be NULL. Outputs have strides >= 0, are aligned to their
+ * type, and their heads must not share elements (as in qmm_norm_rope).
+ */
+int qmm_kv4_read(int type, const qmm_heads *K, const qmm_heads *V, int64_t n_rows, int64_t n_kv_heads,
+                 int64_t head_dim, const int32_t *slots, const void *cache, int64_t n_pages, int64_t page_tokens,
+                 void *stream);
+
+/*
+ * qmm_attn_kv4 - attention of n_rows query tokens, each over the first
+ * lengths[i] tokens of the sequence whose pages tables[i] lists:
+ *   O[i][h] = sum_u w_u V_u[g],  w = softmax_u(scale * Q[i][h] . K_u[g]),
+ * u = 0 .. lengths[i] - 1 at place u % page_tokens of page
+ * tables[i * table_stride + u / page_tokens], g = h / (n_q_heads / n_kv_heads).
+ * One query token per sequence is a decode step. Several tokens of one sequence
+ * (a few drafted ones) are several rows with the same pages and lengths of their
+ * own, appended first; table_stride 0 gives all rows one table.
+ *   type          QMM_T_F16 or QMM_T_BF16, of Q and O
+ *   Q, O          n_q_heads heads, [n_rows] in the token axis (seq_stride unused);
+ *                 strides multiples of 8, 16-byte aligned
+ *   n_kv_heads    a divisor of n_q_heads; head_dim 64 or 128
+ *   tables        int32, table_width entries per row; table_stride >= 0
+ *   lengths       int32 [n_rows]. A length of 0 gives a row of zeros
+ *   scale         > 0 and < 2^127
+ *   workspace     at least qmm_attn_kv4_workspace_bytes(...) bytes, 16-byte
+ *                 aligned; overwritten; two calls in flight must not share one.
+ *                 May be NULL when that size is 0.
+ * Device data: a length outside [0, table_width * page_tokens], or a page
+ * outside [0, n_pages) among those that the length reaches, gives that row
+ * NaNs, and such a page is not read. Table entries past a length are not used,
+ * and places past it do not reach the output whatever they hold.
+ * O may be Q itself, with equal strides; otherwise it overlaps nothing.
+ * Numerics: codes and Q are multiplied exactly (a Q's element below 2^-25 of the
+ * row's largest counts as less than its rounding); scores, maximum and sums in
+ * fp32; each weight times its value's scale is rounded to binary16 relative to a
+ * reference, and the output once at the end. A Q with an infinity or a NaN gives
+ * NaNs.
+ * n_rows < 2^24, n_rows * n_q_heads < 2^24, table_width * page_tokens < 2^31,
+ * n_pages >= 1 (QMM_ERR_SHAPE).
+ */
+int qmm_attn_kv4(int type, const qmm_heads *Q, const qmm_heads *O, int64_t n_rows, int64_t n_q_heads,
+                 int64_t n_kv_heads, int64_t head_dim, const void *cache, int64_t n_pages, int64_t page_tokens,
+                 const int32_t *tables, int64_t table_stride, int64_t table_width, const int32_t *lengths, float scale,
+                 void *workspace, int64_t workspace_bytes, void *stream);
+
+/* qmm_attn_kv4_workspace_bytes - the workspace qmm_attn_kv4 needs for these
+ * sizes, or QMM_ERR_SHAPE. The same on every device. */
+int64_t qmm_attn_kv4_workspace_bytes(int64_t n_rows, int64_t n_q_heads, int64_t n_kv_heads, int64_t head_dim,
+                                     int64_t table_width, int64_t page_tokens);
+
+#ifdef __cplusplus
+}
+#endif
+
+#endif /* QMM_SERVE_H */
