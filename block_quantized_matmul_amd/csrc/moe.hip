@@ -1,0 +1,647 @@
+// A whole mixture-of-experts layer for a few tokens (qmm_moe).
+//
+//   r = softmax(R x), the `used` largest;  y = sum_e r_e D_e h_e,
+//   h_e = silu(G_e x) * (U_e x)
+//
+// Bound by memory: the chosen experts' blocks are read once. Four launches:
+// the router's logits and the activations' operands; the choice; gate and up
+// with the activation; down with the sum over experts.
+//
+// Tokens are columns. Every chosen expert computes all (at most 16) tokens, since
+// columns that the matrix cores have anyway cost nothing; a token that did not
+// choose it gets a zero in h. With the routing weight multiplied into h, the
+// last step is one product along (expert, n_ff): y = [D_e1 D_e2 ..] [h_e1; h_e2; ..],
+// whose sums need no order between experts and no output per expert.
+//
+// Operands. v_mfma_f32_16x16x32_f16 sums a block of 32 weights of 16 rows with 16
+// columns. An activation x takes two columns, hi = fp16(x) and lo = fp16(2^11 (x -
+// hi)), so that it is not rounded (to 2^-22, or absolutely to 2^-35); they are
+// prepared once, in operand order, by the launch before. A 4-bit code n becomes a
+// half by a shift and a mask, 16 + n (n in the upper bits of the mantissa; in the
+// lower ones it would be 1024 + n or a subnormal, and the sums a hundred times
+// less exact); -(16 + 8) times the activations' sum, one more product that the
+// rows' groups share, starts a Q4_0 row's sum. A block's scale multiplies the
+// block's 16 x 16 sums in fp32.
+//
+// Weights are copied to LDS as they lie in memory, 16 bytes per lane, a quad of
+// blocks (256 weights) of a wavefront's 16 or 32 rows at a time, several quads
+// ahead, and read from there as operands; no wavefront waits for another until
+// the partial sums of those that share rows are added, in order, at the end.
+#include "attn_core.h"
+#include "gemv_common.h"
+#include "launch.h"
+#include "serve.h"
+
+#include <algorithm>
+
+namespace qmm {
+
+namespace {
+
+constexpr int kThreads = 512;
+constexpr int kWaves = kThreads / 64;
+constexpr int kMaxTokens = QMM_MOE_MAX_TOKENS;
+constexpr int kRouteThreads = 1024;
+constexpr int kLogitThreads = 256;
+constexpr int kLogitTokens = 4;  // tokens of a logit workgroup
+constexpr float kLoScale = 2048.f;
+
+// ------------------------------------------------------------- operands
+
+// Where element i of a block stands among the operands: place j of lane group g.
+struct Spot {
+  int g, j;
+};
+__device__ __forceinline__ Spot spot_of(int qtype, int i) {
+  if (qtype == QMM_TYPE_Q4_K) return {i / 8, (i & 4) | (i & 1) << 1 | (i >> 1 & 1)};
+  if (qtype == QMM_TYPE_Q4_0 || qtype == QMM_TYPE_Q4_1) return {i % 16 / 4, (i & 1) << 2 | (i >> 1 & 1) | (i / 16) << 1};
+  if (qtype == QMM_TYPE_Q8_0) return {i / 8, i & 7};
+  return {i % 16 / 4, (i & 3) | (i / 16) << 2};
+}
+// The two halves of an activation.
+__device__ __forceinline__ void split(float x, _Float16 &hi, _Float16 &lo) {
+  hi = static_cast<_Float16>(x);
+  // (an infinite hi makes the sum it enters infinite or NaN by itself)
+  const float rest = (x - static_cast<float>(hi)) * kLoScale;
+  lo = static_cast<_Float16>(__builtin_fabsf(rest) < __builtin_inff() ? rest : 0.f);
+}
+// Operand halves: [block][column][g][j], columns 2 t and 2 t + 1 of token t.
+__device__ __forceinline__ int64_t operand_at(int64_t block, int columns, int column, int g) {
+  return ((block * columns + column) * 4 + g) * 8;
+}
+
+template <int QT> struct Quad {
+  static constexpr int chunks = Block<QT>::bytes / 2;  // 16-byte pieces of a row's 8 blocks
+  static constexpr int row = chunks * 16;
+};
+
+// One block's codes as an operand, with its scale (and its term of the columns' sums).
+struct BlockOp {
+  half8_t codes;
+  float d, m;
+};
+// Four-bit codes n as the halves 16 + n (n in the mantissa's upper bits): those
+// whose nibbles lie `up` bits below the place, or above it if negative.
+template <int UP> __device__ __forceinline__ uint32_t codes_at(uint32_t v) {
+  return ((UP > 0 ? v << (UP & 31) : v >> (-UP & 31)) & 0x03C003C0u) | 0x4C004C00u;
+}
+// A dword's nibbles in the order 0, 4, 1, 5, 2, 6, 3, 7.
+__device__ __forceinline__ half8_t nibbles(uint32_t v) {
+  return __builtin_bit_cast(half8_t, u32x4_t{codes_at<6>(v), codes_at<2>(v), codes_at<-2>(v), codes_at<-6>(v)});
+}
+// The two blocks of pair u of the row at rb (LDS), for lane group g.
+template <int QT> __device__ __forceinline__ void pair_ops(const uint8_t *rb, int u, int g, BlockOp op[2]) {
+  auto ld = [&](int off) { return *reinterpret_cast<const uint32_t *>(rb + off); };
+  if constexpr (QT == QMM_TYPE_Q4_K) {
+    const uint32_t h0 = ld(0), s0 = ld(4), s1 = ld(8), s2 = ld(12);
+    const float d = half_bits_to_float(h0 & 0xFFFFu), dmin = half_bits_to_float(h0 >> 16);
+    const uint32_t a0 = ld(16 + 32 * u + 8 * g), a1 = ld(20 + 32 * u + 8 * g);
+    op[0].codes = __builtin_bit_cast(half8_t, u32x4_t{codes_at<6>(a0), codes_at<-2>(a0), codes_at<6>(a1), codes_at<-2>(a1)});
+    op[1].codes = __builtin_bit_cast(half8_t, u32x4_t{codes_at<2>(a0), codes_at<-6>(a0), codes_at<2>(a1), codes_at<-6>(a1)});
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      uint32_t sc, mn;
+      q4k_scale_min(s0, s1, s2, 2 * u + h, sc, mn);
+      op[h].d = d * static_cast<float>(sc);
+      op[h].m = __builtin_fmaf(-dmin, static_cast<float>(mn), -16.f * op[h].d);
+    }
+  } else {
+    const uint8_t *p = rb + u * (2 * Block<QT>::bytes);
+    auto lp = [&](int off) { return *reinterpret_cast<const uint32_t *>(p + off); };
+    if constexpr (QT == QMM_TYPE_Q4_0) {
+      const uint32_t a0 = lp(4 * g), a1 = lp(4 * g + 4), b = lp(20 + 4 * g), d0 = lp(0), d1 = lp(16);
+      op[0].codes = nibbles(shift16(a0, a1)), op[1].codes = nibbles(b);
+      op[0].d = half_bits_to_float(d0 & 0xFFFFu), op[1].d = half_bits_to_float(d1 >> 16);
+    } else if constexpr (QT == QMM_TYPE_Q4_1) {
+      const uint32_t a = lp(4 + 4 * g), b = lp(24 + 4 * g), dm0 = lp(0), dm1 = lp(20);
+      op[0].codes = nibbles(a), op[1].codes = nibbles(b);
+      op[0].d = half_bits_to_float(dm0 & 0xFFFFu), op[1].d = half_bits_to_float(dm1 & 0xFFFFu);
+      op[0].m = __builtin_fmaf(-16.f, op[0].d, half_bits_to_float(dm0 >> 16));
+      op[1].m = __builtin_fmaf(-16.f, op[1].d, half_bits_to_float(dm1 >> 16));
+    } else if constexpr (QT == QMM_TYPE_Q5_0) {
+      const uint32_t w0 = lp(0), w1 = lp(4), a0 = lp(4 + 4 * g), a1 = lp(8 + 4 * g);
+      const uint32_t w5 = lp(20), h1 = lp(24), b = lp(28 + 4 * g);
+      op[0].codes = gemv_codes5<QT>(shift16(a0, a1), shift16(w0, w1), 4 * g);
+      op[1].codes = gemv_codes5<QT>(b, h1, 4 * g);
+      op[0].d = half_bits_to_float(w0 & 0xFFFFu), op[1].d = half_bits_to_float(w5 >> 16);
+    } else if constexpr (QT == QMM_TYPE_Q5_1) {
+      const uint32_t dm0 = lp(0), h0 = lp(4), a = lp(8 + 4 * g), dm1 = lp(24), h1 = lp(28), b = lp(32 + 4 * g);
+      op[0].codes = gemv_codes5<QT>(a, h0, 4 * g), op[1].codes = gemv_codes5<QT>(b, h1, 4 * g);
+      op[0].d = half_bits_to_float(dm0 & 0xFFFFu), op[0].m = half_bits_to_float(dm0 >> 16);
+      op[1].d = half_bits_to_float(dm1 & 0xFFFFu), op[1].m = half_bits_to_float(dm1 >> 16);
+    } else {
+      const uint32_t a0 = lp(8 * g), a1 = lp(8 * g + 4), a2 = lp(8 * g + 8);
+      const uint32_t b0 = lp(36 + 8 * g), b1 = lp(40 + 8 * g), d0 = lp(0), d1 = lp(32);
+      op[0].codes = gemv_codes<QT>(shift16(a0, a1), shift16(a1, a2)), op[1].codes = gemv_codes<QT>(b0, b1);
+      op[0].d = half_bits_to_float(d0 & 0xFFFFu), op[1].d = half_bits_to_float(d1 >> 16);
+    }
+  }
+}
+// The constant operand whose product with the activations is what a Q4_0 row's sum
+// starts with, -(16 + 8) times their sum, or what a minimum multiplies, their sum.
+template <int QT> __device__ __forceinline__ half8_t sum_operand() {
+  const _Float16 c = static_cast<_Float16>(QT == QMM_TYPE_Q4_0 ? -24.f : 1.f);
+  return half8_t{c, c, c, c, c, c, c, c};
+}
+template <int QT> constexpr bool has_min() { return QTraits<QT>::has_min || QTraits<QT>::kquant; }
+
+// --------------------------------------------------------------- streaming
+
+// A wavefront's rows: G groups of 16, from which a lane copies piece lane + 64 j
+// of every quad. Rows past the last repeat it.
+template <int QT, int MT, int G> struct Rows {
+  static constexpr int kPieces = 16 * G * Quad<QT>::chunks;
+  static constexpr int kCopies = (kPieces + 63) / 64;
+  static constexpr int kStage = kPieces * 16;                      // bytes of LDS
+  static constexpr int kStages = kStage > 6000 ? 2 : G == 1 ? 4 : 3;  // quads on their way, the one in use among them
+  static constexpr int kXLoads = 8 * MT;
+  int64_t off[kCopies];  // from the expert's matrix (group 0's), of this lane's pieces in quad 0
+  bool on_last;          // whether this lane has a piece in the last copy
+  int64_t nb1;
+
+  // With two groups they are the same rows of two matrices, `apart` bytes from each other.
+  __device__ __forceinline__ Rows(int64_t nb1_, int row0, int n_rows, int64_t apart, int lane) : nb1(nb1_) {
+#pragma unroll
+    for (int j = 0; j < kCopies; ++j) {
+      const int c = min(64 * j + lane, kPieces - 1), r = c / Quad<QT>::chunks;
+      const int group = r / 16;
+      const int64_t row = min(row0 + r % 16, n_rows - 1);
+      off[j] = row * nb1 + 16 * (c % Quad<QT>::chunks) + (group ? apart : 0);
+    }
+    on_last = 64 * (kCopies - 1) + lane < kPieces;
+  }
+  __device__ __forceinline__ void copy(const uint8_t *w, int q, uint32_t lds) const {
+    const uint8_t *p = w + static_cast<int64_t>(q) * Quad<QT>::row;
+#pragma unroll
+    for (int j = 0; j < kCopies; ++j) {
+      if (j < kCopies - 1 || kPieces % 64 == 0 || on_last) {
+        const uint8_t *from = p + off[j];
+        asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, off" ::"v"(from), "s"(lds + 1024 * j)
+                     : "memory", "m0");
+      }
+    }
+  }
+};
+
+template <int MT> struct Activations {
+  half8_t x[8][MT];
+};
+// The operands of quad q's blocks (those below `blocks`; zeros beyond, and in columns that no token has).
+template <int MT>
+__device__ __forceinline__ void load_activations(Activations<MT> &a, const _Float16 *ops, int q, int blocks, int columns,
+                                                 int lane) {
+#pragma unroll
+  for (int i = 0; i < 8; ++i)
+#pragma unroll
+    for (int t = 0; t < MT; ++t) {
+      const int column = 16 * t + (lane & 15);
+      a.x[i][t] = half8_t{};
+      if (column < columns && 8 * q + i < blocks)
+        a.x[i][t] = *reinterpret_cast<const half8_t *>(ops + operand_at(8 * q + i, columns, column, lane >> 4));
+    }
+}
+
+// A quad in LDS times its activations, into the rows' sums. `valid`: blocks that exist.
+template <int QT, int MT, int G>
+__device__ __forceinline__ void take_quad(const uint8_t *stage, const Activations<MT> &a, int valid, float4_t acc[G][MT],
+                                          int lane) {
+  const int g = lane >> 4;
+  const uint8_t *rb = stage + (lane & 15) * Quad<QT>::row;
+#pragma unroll
+  for (int u = 0; u < 4; ++u) {
+    if (2 * u >= valid) break;
+    BlockOp op[G][2];
+#pragma unroll
+    for (int k = 0; k < G; ++k) pair_ops<QT>(rb + k * 16 * Quad<QT>::row, u, g, op[k]);
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      if (2 * u + h >= valid) break;
+#pragma unroll
+      for (int t = 0; t < MT; ++t) {
+        const half8_t x = a.x[2 * u + h][t];
+        float4_t start{}, sums{};
+        if constexpr (QT == QMM_TYPE_Q4_0) start = __builtin_amdgcn_mfma_f32_16x16x32_f16(x, sum_operand<QT>(), start, 0, 0, 0);
+        if constexpr (has_min<QT>()) sums = __builtin_amdgcn_mfma_f32_16x16x32_f16(x, sum_operand<QT>(), sums, 0, 0, 0);
+#pragma unroll
+        for (int k = 0; k < G; ++k) {
+          const float4_t part = __builtin_amdgcn_mfma_f32_16x16x32_f16(x, op[k][h].codes, start, 0, 0, 0);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            acc[k][t][e] = __builtin_fmaf(op[k][h].d, part[e], acc[k][t][e]);
+            if constexpr (has_min<QT>()) acc[k][t][e] = __builtin_fmaf(op[k][h].m, sums[e], acc[k][t][e]);
+          }
+        }
+      }
+    }
+  }
+}
+
+// The blocks behind the last whole quad, copied dword by dword so that nothing
+// behind a row's last dword is read.
+template <int QT, int MT, int G>
+__device__ __forceinline__ void take_tail(const uint8_t *w, int64_t nb1, int row0, int n_rows, int64_t apart, int blocks,
+                                          const _Float16 *ops, int columns, uint8_t *stage, float4_t acc[G][MT], int lane) {
+  const int q = blocks / 8, valid = blocks % 8;
+  const int dwords = (valid * Block<QT>::bytes + 3) / 4;
+  Activations<MT> a;
+  load_activations<MT>(a, ops, q, blocks, columns, lane);
+  wait_reads();  // of what lay in this place before
+  for (int i = lane; i < 16 * G * dwords; i += 64) {
+    const int r = i / dwords, at = i % dwords;
+    const int64_t row = min(row0 + r % 16, n_rows - 1);
+    const uint8_t *from = w + row * nb1 + (r >= 16 ? apart : 0) + static_cast<int64_t>(q) * Quad<QT>::row + 4 * at;
+    *reinterpret_cast<uint32_t *>(stage + r * Quad<QT>::row + 4 * at) = *reinterpret_cast<const uint32_t *>(from);
+  }
+  wait_reads();
+  take_quad<QT, MT, G>(stage, a, valid, acc, lane);
+}
+
+// Stages 0 .. n - 1 through LDS: at(i) gives stage i's matrix, quad and operands.
+template <int QT, int MT, int G, class At>
+__device__ __forceinline__ void stream(const Rows<QT, MT, G> &rows, const At &at, int n, int blocks, int columns,
+                                       uint8_t *ring, float4_t acc[G][MT], int lane) {
+  typedef Rows<QT, MT, G> R;
+  if (n <= 0) return;
+  const uint32_t lds = lds_addr(ring);
+  auto copy = [&](int i, int slot) {
+    const auto s = at(i);
+    rows.copy(s.w, s.q, lds + slot * R::kStage);
+  };
+  Activations<MT> a;
+  {
+    const auto s = at(0);
+    load_activations<MT>(a, s.ops, s.q, blocks, columns, lane);
+  }
+#pragma unroll
+  for (int i = 0; i < R::kStages - 1; ++i)
+    if (i < n) copy(i, i);
+  int slot = 0, ahead = R::kStages - 1;
+  for (int i = 0; i < n; ++i) {
+    Activations<MT> next = a;
+    if (i + 1 < n) {
+      const auto s = at(i + 1);
+      load_activations<MT>(next, s.ops, s.q, blocks, columns, lane);
+    }
+    if (i + R::kStages - 1 < n) {
+      copy(i + R::kStages - 1, ahead);
+      // later than stage i's copies: those of the stages behind it and the loads just above
+      wait_loads<(R::kStages - 1) * R::kCopies + R::kXLoads>();
+    } else {
+      wait_loads<0>();
+    }
+    take_quad<QT, MT, G>(ring + slot * R::kStage, a, 8, acc, lane);
+    wait_reads();
+    a = next;
+    slot = slot + 1 == R::kStages ? 0 : slot + 1;
+    ahead = ahead + 1 == R::kStages ? 0 : ahead + 1;
+  }
+}
+
+// Adds the partial sums of the `split` wavefronts that share rows, in order; the
+// first of them has the result. (The ring is free: every wavefront is done with it.)
+template <int MT, int G> __device__ __forceinline__ void add_parts(float4_t acc[G][MT], uint8_t *lds, int split, int wave, int lane) {
+  if (split == 1) return;
+  __syncthreads();
+  float4_t *at = reinterpret_cast<float4_t *>(lds) + lane;
+#pragma unroll
+  for (int k = 0; k < G; ++k)
+#pragma unroll
+    for (int t = 0; t < MT; ++t) at[((wave * G + k) * MT + t) * 64] = acc[k][t];
+  __syncthreads();
+  if (wave % split != 0) return;
+  for (int s = 1; s < split; ++s)
+#pragma unroll
+    for (int k = 0; k < G; ++k)
+#pragma unroll
+      for (int t = 0; t < MT; ++t) acc[k][t] += at[(((wave + s) * G + k) * MT + t) * 64];
+}
+
+// ----------------------------------------------------------------- kernels
+
+struct Table {  // what the choice leaves for the products
+  int n_active;
+  int pad[3];
+};
+struct MoeArgs {
+  const void *x;
+  const float *router;
+  const uint8_t *gate, *down;
+  int64_t up_apart;  // up - gate, in bytes
+  int64_t nb1_in, nb2_in, nb1_out, nb2_out;
+  float *y;
+  int32_t *ids;
+  float *weights;
+  // workspace
+  double *logits;     // [n_tokens][n_experts]
+  Table *table;
+  int32_t *active;    // [most active] experts, in order
+  float *share;       // [most active][kMaxTokens] routing weights
+  _Float16 *x_ops, *h_ops;  // operands of x, and of h expert by expert
+  int64_t h_step;     // halves of one expert's h
+  int n_tokens, k, n_ff, n_experts, n_used, renormalise, x_f16, type_in, type_out;
+  int logit_groups;   // workgroups of the first launch that compute logits; the others prepare operands
+  int split_in, split_out;
+};
+
+__device__ __forceinline__ float load_x(const MoeArgs &a, int64_t at) {
+  return a.x_f16 ? static_cast<float>(static_cast<const _Float16 *>(a.x)[at]) : static_cast<const float *>(a.x)[at];
+}
+
+// Logits in 64 bits (a choice is decided at a border), and x as operands.
+__global__ __launch_bounds__(kLogitThreads) void moe_prepare_kernel(MoeArgs a) {
+  __shared__ double sums[kLogitThreads / 64][kLogitTokens];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  if (static_cast<int>(blockIdx.x) < a.logit_groups) {
+    const int e = blockIdx.x % a.n_experts, t0 = blockIdx.x / a.n_experts * kLogitTokens;
+    const float *r = a.router + static_cast<int64_t>(e) * a.k;
+    double s[kLogitTokens] = {};
+    for (int i = 4 * threadIdx.x; i < a.k; i += 4 * kLogitThreads) {
+      const float4_a4 w = *reinterpret_cast<const float4_a4 *>(r + i);
+#pragma unroll
+      for (int t = 0; t < kLogitTokens; ++t) {
+        const int64_t at = static_cast<int64_t>(min(t0 + t, a.n_tokens - 1)) * a.k + i;
+        float x[4];
+        if (a.x_f16) {
+          const half4_a4 h = *reinterpret_cast<const half4_a4 *>(static_cast<const _Float16 *>(a.x) + at);
+#pragma unroll
+          for (int j = 0; j < 4; ++j) x[j] = static_cast<float>(h[j]);
+        } else {
+          const float4_a4 f = *reinterpret_cast<const float4_a4 *>(static_cast<const float *>(a.x) + at);
+#pragma unroll
+          for (int j = 0; j < 4; ++j) x[j] = f[j];
+        }
+#pragma unroll
+        for (int j = 0; j < 4; ++j) s[t] = __builtin_fma(static_cast<double>(w[j]), static_cast<double>(x[j]), s[t]);
+      }
+    }
+#pragma unroll
+    for (int t = 0; t < kLogitTokens; ++t) {
+#pragma unroll
+      for (int d = 32; d > 0; d /= 2) s[t] += __shfl_xor(s[t], d);
+      if (lane == 0) sums[wave][t] = s[t];
+    }
+    __syncthreads();
+    const int t = threadIdx.x;
+    if (t < kLogitTokens && t0 + t < a.n_tokens) {
+      double total = 0.;
+#pragma unroll
+      for (int w = 0; w < kLogitThreads / 64; ++w) total += sums[w][t];
+      a.logits[static_cast<int64_t>(t0 + t) * a.n_experts + e] = total;
+    }
+    return;
+  }
+  // a thread: one element of a block, all tokens' in turn
+  const int64_t i = static_cast<int64_t>(blockIdx.x - a.logit_groups) * kLogitThreads + threadIdx.x;
+  if (i >= static_cast<int64_t>(a.k) * a.n_tokens) return;
+  const int t = static_cast<int>(i / a.k), e = static_cast<int>(i % a.k);
+  const Spot s = spot_of(a.type_in, e % 32);
+  _Float16 hi, lo;
+  split(load_x(a, i), hi, lo);
+  a.x_ops[operand_at(e / 32, 2 * a.n_tokens, 2 * t, s.g) + s.j] = hi;
+  a.x_ops[operand_at(e / 32, 2 * a.n_tokens, 2 * t + 1, s.g) + s.j] = lo;
+}
+
+// The choice, by one workgroup: an expert's rank among a token's is the number of
+// larger logits, of equal ones before it (a NaN is below all others), and those
+// of rank below n_used are chosen.
+__global__ __launch_bounds__(kRouteThreads) void moe_route_kernel(MoeArgs a) {
+  extern __shared__ __align__(16) uint8_t smem[];
+  const int n = a.n_tokens, experts = a.n_experts, items = n * experts;
+  double *l = reinterpret_cast<double *>(smem);                    // [n][experts], NaN as -infinity
+  float *w = reinterpret_cast<float *>(l + items);                 // [n][n_used]
+  int *id = reinterpret_cast<int *>(w + n * a.n_used);             // [n][n_used]
+  int *place = id + n * a.n_used;                                  // [experts]
+  for (int i = threadIdx.x; i < items; i += kRouteThreads) {
+    const double v = a.logits[i];
+    l[i] = v != v ? -__builtin_inf() : v;
+  }
+  for (int i = threadIdx.x; i < experts; i += kRouteThreads) place[i] = 0;
+  __syncthreads();
+  for (int i = threadIdx.x; i < items; i += kRouteThreads) {
+    const int t = i / experts, e = i % experts;
+    const double mine = l[i], *row = l + t * experts;
+    int rank = 0;
+    for (int k = 0; k < experts; ++k) rank += row[k] > mine || (row[k] == mine && k < e);
+    if (rank < a.n_used) {
+      id[t * a.n_used + rank] = e;
+      place[e] = 1;  // (any of several writes the same)
+    }
+  }
+  __syncthreads();
+  // weights: a wavefront per token
+  const int lane = threadIdx.x & 63;
+  for (int t = threadIdx.x >> 6; t < n; t += kRouteThreads / 64) {
+    const double *row = a.logits + static_cast<int64_t>(t) * experts;
+    const double top = l[t * experts + id[t * a.n_used]];
+    float sum = 0.f;
+    if (a.renormalise) {
+      for (int k = lane; k < a.n_used; k += 64) sum += expf(static_cast<float>(row[id[t * a.n_used + k]] - top));
+    } else {
+      for (int k = lane; k < experts; k += 64) sum += expf(static_cast<float>(row[k] - top));
+    }
+#pragma unroll
+    for (int d = 32; d > 0; d /= 2) sum += __shfl_xor(sum, d);
+    for (int k = lane; k < a.n_used; k += 64) {
+      const int e = id[t * a.n_used + k];
+      const float v = expf(static_cast<float>(row[e] - top)) / sum;
+      w[t * a.n_used + k] = v;
+      if (a.ids) a.ids[t * a.n_used + k] = e;
+      if (a.weights) a.weights[t * a.n_used + k] = v;
+    }
+  }
+  __syncthreads();
+  // the active experts in order, by the first wavefront
+  if (threadIdx.x < 64) {
+    int before = 0;
+    for (int e0 = 0; e0 < experts; e0 += 64) {
+      const int e = e0 + lane;
+      const bool on = e < experts && place[e];
+      const uint64_t mask = __ballot(on);
+      if (on) {
+        const int at = before + __popcll(mask & ((uint64_t{1} << lane) - 1));
+        place[e] = at;
+        a.active[at] = e;
+      }
+      before += __popcll(mask);
+    }
+    if (lane == 0) a.table->n_active = before;
+    id[n * a.n_used + experts] = before;  // (behind place)
+  }
+  __syncthreads();
+  const int n_active = id[n * a.n_used + experts];
+  for (int i = threadIdx.x; i < n_active * kMaxTokens; i += kRouteThreads) a.share[i] = 0.f;
+  __syncthreads();
+  for (int i = threadIdx.x; i < n * a.n_used; i += kRouteThreads) {
+    // a zero share stands for "not chosen"; a chosen weight that underflowed to it is as good as that
+    a.share[place[id[i]] * kMaxTokens + i / a.n_used] = w[i];
+  }
+}
+
+struct Stage {
+  const uint8_t *w;
+  int q;
+  const _Float16 *ops;
+};
+
+// Columns 4 g + e of a tile: hi and lo of tokens 8 t + 2 g and 8 t + 2 g + 1.
+__device__ __forceinline__ float token_value(const float4_t &acc, int which) {
+  return __builtin_fmaf(acc[2 * which + 1], 1.f / kLoScale, acc[2 * which]);
+}
+
+// gate, up and their product: blockIdx.y is the active expert, a unit 16 rows of both.
+template <int QT, int MT> __global__ __launch_bounds__(kThreads, 2) void moe_inner_kernel(MoeArgs a) {
+  typedef Rows<QT, MT, 2> R;
+  extern __shared__ __align__(1024) uint8_t smem[];
+  if (static_cast<int>(blockIdx.y) >= a.table->n_active) return;
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int split = a.split_in, part = wave % split;
+  const int unit = blockIdx.x * (kWaves / split) + wave / split;
+  const int row0 = 16 * unit;
+  const bool live = row0 < a.n_ff;
+  const int blocks = a.k / 32, quads = blocks / 8, columns = 2 * a.n_tokens;
+  const uint8_t *w = a.gate + static_cast<int64_t>(__builtin_amdgcn_readfirstlane(a.active[blockIdx.y])) * a.nb2_in;
+  uint8_t *ring = smem + wave * (R::kStages * R::kStage);
+  float4_t acc[2][MT] = {};
+  if (live) {
+    const int lo = quads * part / split, hi = quads * (part + 1) / split;
+    const R rows(a.nb1_in, row0, a.n_ff, a.up_apart, lane);
+    stream<QT, MT, 2>(rows, [&](int i) { return Stage{w, lo + i, a.x_ops}; }, hi - lo, blocks, columns, ring, acc, lane);
+    if (blocks % 8 != 0 && part == split - 1)
+      take_tail<QT, MT, 2>(w, a.nb1_in, row0, a.n_ff, a.up_apart, blocks, a.x_ops, columns, ring, acc, lane);
+  }
+  add_parts<MT, 2>(acc, smem, split, wave, lane);
+  if (part != 0 || !live) return;
+  const int row = row0 + (lane & 15), g = lane >> 4;
+  if (row >= a.n_ff) return;
+  const Spot s = spot_of(a.type_out, row % 32);
+  _Float16 *h = a.h_ops + blockIdx.y * a.h_step;
+#pragma unroll
+  for (int t = 0; t < MT; ++t)
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      const int token = 8 * t + 2 * g + k;
+      if (token >= a.n_tokens) continue;
+      const float share = a.share[blockIdx.y * kMaxTokens + token];
+      const float gate = token_value(acc[0][t], k), up = token_value(acc[1][t], k);
+      const float v = share == 0.f ? 0.f : gate / (1.f + expf(-gate)) * up * share;
+      _Float16 hi, lo;
+      qmm::split(v, hi, lo);
+      h[operand_at(row / 32, columns, 2 * token, s.g) + s.j] = hi;
+      h[operand_at(row / 32, columns, 2 * token + 1, s.g) + s.j] = lo;
+    }
+}
+
+// down: 16 rows over all active experts' quads, split evenly between wavefronts.
+template <int QT, int MT> __global__ __launch_bounds__(kThreads, 2) void moe_outer_kernel(MoeArgs a) {
+  typedef Rows<QT, MT, 1> R;
+  extern __shared__ __align__(1024) uint8_t smem[];
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int split = a.split_out, part = wave % split;
+  const int row0 = 16 * (blockIdx.x * (kWaves / split) + wave / split);
+  const bool live = row0 < a.k;
+  const int n_active = __builtin_amdgcn_readfirstlane(a.table->n_active);
+  const int blocks = a.n_ff / 32, quads = blocks / 8, columns = 2 * a.n_tokens;
+  uint8_t *ring = smem + wave * (R::kStages * R::kStage);
+  float4_t acc[1][MT] = {};
+  if (live) {
+    const int64_t all = static_cast<int64_t>(n_active) * quads;
+    const int lo = static_cast<int>(all * part / split), hi = static_cast<int>(all * (part + 1) / split);
+    const R rows(a.nb1_out, row0, a.k, 0, lane);
+    auto expert = [&](int i) {
+      return a.down + static_cast<int64_t>(__builtin_amdgcn_readfirstlane(a.active[i])) * a.nb2_out;
+    };
+    auto at = [&](int i) {
+      const int e = (lo + i) / quads;
+      return Stage{expert(e), lo + i - e * quads, a.h_ops + e * a.h_step};
+    };
+    stream<QT, MT, 1>(rows, at, hi - lo, blocks, columns, ring, acc, lane);
+    if (blocks % 8 != 0)
+      for (int e = part; e < n_active; e += split)
+        take_tail<QT, MT, 1>(expert(e), a.nb1_out, row0, a.k, 0, blocks, a.h_ops + e * a.h_step, columns, ring, acc, lane);
+  }
+  add_parts<MT, 1>(acc, smem, split, wave, lane);
+  const int row = row0 + (lane & 15), g = lane >> 4;
+  if (part != 0 || row >= a.k) return;
+#pragma unroll
+  for (int t = 0; t < MT; ++t)
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      const int token = 8 * t + 2 * g + k;
+      if (token < a.n_tokens) a.y[static_cast<int64_t>(token) * a.k + row] = token_value(acc[0][t], k);
+    }
+}
+
+int64_t round16(int64_t n) { return (n + 15) / 16 * 16; }
+int64_t most_active(int64_t n_tokens, int64_t n_experts, int64_t n_used) { return std::min(n_experts, n_tokens * n_used); }
+
+template <class R> constexpr size_t ring_bytes() { return static_cast<size_t>(kWaves) * R::kStages * R::kStage; }
+
+// Wavefronts that share a unit's rows: as few as give every CU about two workgroups.
+int split_for(int64_t units, int64_t want) {
+  int split = 1;
+  while (split < kWaves && units * split < want * kWaves) split *= 2;
+  return split;
+}
+
+template <int QT, int MT> hipError_t run_inner(const MoeArgs &a, int64_t most, hipStream_t stream) {
+  const int64_t units = (a.n_ff + 15) / 16, per = kWaves / a.split_in;
+  const dim3 grid(static_cast<unsigned>((units + per - 1) / per), static_cast<unsigned>(most));
+  return launch(moe_inner_kernel<QT, MT>, grid, dim3(kThreads), ring_bytes<Rows<QT, MT, 2>>(), stream, a);
+}
+template <int QT, int MT> hipError_t run_outer(const MoeArgs &a, hipStream_t stream) {
+  const int64_t units = (a.k + 15) / 16, per = kWaves / a.split_out;
+  const dim3 grid(static_cast<unsigned>((units + per - 1) / per));
+  return launch(moe_outer_kernel<QT, MT>, grid, dim3(kThreads), ring_bytes<Rows<QT, MT, 1>>(), stream, a);
+}
+
+}  // namespace
+
+int64_t moe_workspace_bytes(int64_t n_tokens, int64_t k, int64_t n_ff, int64_t n_experts, int64_t n_used) {
+  const int64_t most = most_active(n_tokens, n_experts, n_used);
+  return round16(n_tokens * n_experts * 8) + 16 + round16(most * 4) + most * kMaxTokens * 4 + n_tokens * k * 4 +
+         most * n_tokens * n_ff * 4;
+}
+
+hipError_t launch_moe(const MoeLayer &m, void *workspace, hipStream_t stream) {
+  const int64_t most = most_active(m.n_tokens, m.n_experts, m.n_used);
+  MoeArgs a{};
+  a.x = m.X, a.x_f16 = m.x_f16, a.router = m.router;
+  a.gate = static_cast<const uint8_t *>(m.gate), a.down = static_cast<const uint8_t *>(m.down);
+  a.up_apart = static_cast<const uint8_t *>(m.up) - a.gate;
+  a.nb1_in = m.nb1_in, a.nb2_in = m.nb2_in, a.nb1_out = m.nb1_out, a.nb2_out = m.nb2_out;
+  a.y = m.Y, a.ids = m.ids, a.weights = m.weights;
+  uint8_t *p = static_cast<uint8_t *>(workspace);
+  a.logits = reinterpret_cast<double *>(p), p += round16(m.n_tokens * m.n_experts * 8);
+  a.table = reinterpret_cast<Table *>(p), p += 16;
+  a.active = reinterpret_cast<int32_t *>(p), p += round16(most * 4);
+  a.share = reinterpret_cast<float *>(p), p += most * kMaxTokens * 4;
+  a.x_ops = reinterpret_cast<_Float16 *>(p), p += m.n_tokens * m.k * 4;
+  a.h_ops = reinterpret_cast<_Float16 *>(p);
+  a.h_step = m.n_tokens * m.n_ff * 2;
+  a.n_tokens = static_cast<int>(m.n_tokens), a.k = static_cast<int>(m.k), a.n_ff = static_cast<int>(m.n_ff);
+  a.n_experts = static_cast<int>(m.n_experts), a.n_used = static_cast<int>(m.n_used), a.renormalise = m.renormalise;
+  a.type_in = m.type_in, a.type_out = m.type_out;
+  a.split_in = split_for(most * ((m.n_ff + 15) / 16), 384);
+  a.split_out = split_for((m.k + 15) / 16, 256);
+  a.logit_groups = static_cast<int>(m.n_experts * ((m.n_tokens + kLogitTokens - 1) / kLogitTokens));
+  const unsigned first = static_cast<unsigned>(a.logit_groups + (m.k * m.n_tokens + kLogitThreads - 1) / kLogitThreads);
+  hipError_t e = launch(moe_prepare_kernel, dim3(first), dim3(kLogitThreads), 0, stream, a);
+  if (e != hipSuccess) return e;
+  const size_t lds = static_cast<size_t>(m.n_tokens * (m.n_experts + m.n_used) * 8 + (m.n_experts + 1) * 4);
+  e = launch(moe_route_kernel, dim3(1), dim3(kRouteThreads), lds, stream, a);
+  if (e != hipSuccess) return e;
+  const bool one = m.n_tokens <= 8;
+  e = by_qtype_k(m.type_in, [&](auto q) {
+    constexpr int QT = decltype(q)::value;
+    return one ? run_inner<QT, 1>(a, most, stream) : run_inner<QT, 2>(a, most, stream);
+  });
+  if (e != hipSuccess) return e;
+  return by_qtype_k(m.type_out, [&](auto q) {
+    constexpr int QT = decltype(q)::value;
+    return one ? run_outer<QT, 1>(a, stream) : run_outer<QT, 2>(a, stream);
+  });
+}
+
+}  // namespace qmm

@@ -38,4 +38,21 @@ hipError_t launch_attn_kv4(int type, const qmm_heads &Q, const qmm_heads &O, int
                            int64_t table_stride, int64_t table_width, const int32_t *lengths, float scale,
                            void *workspace, hipStream_t stream);
 
+// qmm_moe. The parts of its workspace (bytes from its start).
+struct MoeLayer {
+  const void *X;
+  bool x_f16;
+  int64_t n_tokens, k, n_ff, n_experts, n_used;
+  const float *router;
+  const void *gate, *up, *down;
+  int type_in, type_out;
+  int64_t nb1_in, nb2_in, nb1_out, nb2_out;  // row and expert strides
+  bool renormalise;
+  float *Y;
+  int32_t *ids;    // may be null
+  float *weights;  // may be null
+};
+int64_t moe_workspace_bytes(int64_t n_tokens, int64_t k, int64_t n_ff, int64_t n_experts, int64_t n_used);
+hipError_t launch_moe(const MoeLayer &m, void *workspace, hipStream_t stream);
+
 }  // namespace qmm

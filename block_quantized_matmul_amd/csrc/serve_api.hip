@@ -57,6 +57,17 @@ int check_cache(const void *cache, int64_t n_pages, int64_t page_tokens, int64_t
   return QMM_OK;
 }
 
+constexpr int64_t kMaxMoeDim = (int64_t{1} << 24) - 32;
+
+// A stack of n_experts matrices of n_rows rows of k weights.
+int check_stack(int qtype, int64_t n_rows, int64_t k, int64_t n_experts, int64_t nb1, int64_t nb2) {
+  const int64_t dense = qmm_row_bytes(qtype, k);
+  if (dense < 0) return static_cast<int>(dense);
+  if (nb1 < dense || nb1 % 4 != 0 || nb1 > kMaxElems / kMaxMoeDim || nb2 % 4 != 0 || nb2 < n_rows * nb1) return QMM_ERR_STRIDE;
+  if (!product_within(n_experts, nb2, kMaxElems)) return QMM_ERR_SHAPE;
+  return QMM_OK;
+}
+
 }  // namespace
 
 extern "C" {
@@ -150,6 +161,41 @@ int qmm_attn_kv4(int type, const qmm_heads *Q, const qmm_heads *O, int64_t n_row
   return status_of(qmm::launch_attn_kv4(type, *Q, *O, n_rows, n_q_heads, n_kv_heads, head_dim, c, tables,
                                         n_rows > 1 ? table_stride : 0, table_width, lengths, scale, workspace,
                                         static_cast<hipStream_t>(stream)));
+}
+
+int64_t qmm_moe_workspace_bytes(int64_t n_tokens, int64_t k, int64_t n_ff, int64_t n_experts, int64_t n_used) {
+  if (n_tokens < 0 || n_tokens > QMM_MOE_MAX_TOKENS || n_experts <= 0 || n_experts > QMM_MOE_MAX_EXPERTS) return QMM_ERR_SHAPE;
+  if (n_used <= 0 || n_used > n_experts || n_used > QMM_MOE_MAX_USED) return QMM_ERR_SHAPE;
+  if (k <= 0 || k % 32 != 0 || k > kMaxMoeDim || n_ff <= 0 || n_ff % 32 != 0 || n_ff > kMaxMoeDim) return QMM_ERR_SHAPE;
+  return n_tokens == 0 ? 0 : qmm::moe_workspace_bytes(n_tokens, k, n_ff, n_experts, n_used);
+}
+
+int qmm_moe(const void *X, int x_type, int64_t n_tokens, int64_t k, const float *router, int64_t n_experts,
+            int64_t n_used, int renormalise, const void *gate, const void *up, int type_in, int64_t n_ff,
+            int64_t row_stride_in, int64_t expert_stride_in, const void *down, int type_out, int64_t row_stride_out,
+            int64_t expert_stride_out, float *Y, int32_t *ids, float *weights, void *workspace,
+            int64_t workspace_bytes, void *stream) {
+  if (x_type != QMM_T_F32 && x_type != QMM_T_F16) return QMM_ERR_TYPE;
+  const int64_t need = qmm_moe_workspace_bytes(n_tokens, k, n_ff, n_experts, n_used);
+  if (need < 0) return static_cast<int>(need);
+  int st = check_stack(type_in, n_ff, k, n_experts, row_stride_in, expert_stride_in);
+  if (st == QMM_OK) st = check_stack(type_out, k, n_ff, n_experts, row_stride_out, expert_stride_out);
+  if (st != QMM_OK) return st;
+  if (n_tokens == 0) return QMM_OK;
+  if (X == nullptr || router == nullptr || gate == nullptr || up == nullptr || down == nullptr || Y == nullptr)
+    return QMM_ERR_NULL;
+  for (const void *p : {X, static_cast<const void *>(router), gate, up, down, static_cast<const void *>(Y),
+                        static_cast<const void *>(ids), static_cast<const void *>(weights)})
+    if (!aligned(p, 4)) return QMM_ERR_ALIGN;
+  if (workspace == nullptr || workspace_bytes < need) return QMM_ERR_WORKSPACE;
+  if (!aligned(workspace, 16)) return QMM_ERR_ALIGN;
+  qmm::MoeLayer m{};
+  m.X = X, m.x_f16 = x_type == QMM_T_F16, m.n_tokens = n_tokens, m.k = k, m.n_ff = n_ff;
+  m.n_experts = n_experts, m.n_used = n_used, m.router = router, m.gate = gate, m.up = up, m.down = down;
+  m.type_in = type_in, m.type_out = type_out, m.nb1_in = row_stride_in, m.nb2_in = expert_stride_in;
+  m.nb1_out = row_stride_out, m.nb2_out = expert_stride_out, m.renormalise = renormalise != 0;
+  m.Y = Y, m.ids = ids, m.weights = weights;
+  return status_of(qmm::launch_moe(m, workspace, static_cast<hipStream_t>(stream)));
 }
 
 }  // extern "C"

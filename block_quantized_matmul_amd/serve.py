@@ -1,7 +1,7 @@
 """The operators that complete a served decode step (C: include/qmm_serve.h).
 
-qmm_kv4_append, qmm_kv4_read and qmm_attn_kv4 (a 4-bit paged cache), in the
-same manner as attn.py: tensors supply pointers, strides and sizes, and the
+qmm_kv4_append, qmm_kv4_read and qmm_attn_kv4 (a 4-bit paged cache) and qmm_moe
+(a mixture-of-experts layer), in the same manner as attn.py: tensors supply pointers, strides and sizes, and the
 library checks and runs. All tensors of a call are on one GPU, which need not
 be the current one; work is enqueued on `stream`, or on that GPU's current
 stream.
@@ -16,9 +16,13 @@ from . import attn as _attn
 from .attn import _PAIRS, _Place, _floats, _heads, _host_doubles, _ints, _ptr, _type
 
 QMM_KV4_MAX_PAGE_TOKENS = 256
+QMM_MOE_MAX_TOKENS = 16
+QMM_MOE_MAX_EXPERTS = 512
+QMM_MOE_MAX_USED = 32
 
-__all__ = ["QMM_KV4_MAX_PAGE_TOKENS", "qmm_kv4_page_bytes", "qmm_kv4_append", "qmm_kv4_read", "qmm_attn_kv4",
-           "qmm_attn_kv4_workspace_bytes"]
+__all__ = ["QMM_KV4_MAX_PAGE_TOKENS", "QMM_MOE_MAX_TOKENS", "QMM_MOE_MAX_EXPERTS", "QMM_MOE_MAX_USED",
+           "qmm_kv4_page_bytes", "qmm_kv4_append", "qmm_kv4_read", "qmm_attn_kv4", "qmm_attn_kv4_workspace_bytes",
+           "qmm_moe", "qmm_moe_workspace_bytes"]
 
 _vp, _i32, _i64, _f32, _f64 = ctypes.c_void_p, ctypes.c_int, ctypes.c_int64, ctypes.c_float, ctypes.c_double
 _ready = None
@@ -33,6 +37,9 @@ _SIGNATURES = {  # restype, then the arguments; host structs travel as bytes
     "qmm_attn_kv4": (_i32, [_i32, _vp, _vp, _i64, _i64, _i64, _i64, _vp, _i64, _i64, _vp, _i64, _i64, _vp, _f32, _vp,
                             _i64, _vp]),
     "qmm_attn_kv4_workspace_bytes": (_i64, [_i64] * 6),
+    "qmm_moe": (_i32, [_vp, _i32, _i64, _i64, _vp, _i64, _i64, _i32, _vp, _vp, _i32, _i64, _i64, _i64, _vp, _i32, _i64,
+                       _i64, _vp, _vp, _vp, _vp, _i64, _vp]),
+    "qmm_moe_workspace_bytes": (_i64, [_i64] * 5),
 }
 
 
@@ -178,3 +185,74 @@ def qmm_attn_kv4(Q, cache, page_tokens, n_kv_heads, tables, lengths, scale=None,
               hq, n_kv_heads, dim, cache.data_ptr(), n_pages, page_tokens, tables.data_ptr(), tables.stride(0), width,
               lengths.data_ptr(), dim ** -0.5 if scale is None else scale, ws, ws_bytes)
     return O
+
+
+def qmm_moe_workspace_bytes(n_tokens: int, k: int, n_ff: int, n_experts: int, n_used: int) -> int:
+    return int(_lib().qmm_moe_workspace_bytes(int(n_tokens), int(k), int(n_ff), int(n_experts), int(n_used)))
+
+
+def _stack(W, name, n_experts, n_rows):
+    """(row stride, expert stride) of a uint8 tensor [n_experts][n_rows][bytes] with contiguous rows."""
+    if W.dtype is not torch.uint8 or W.dim() != 3:
+        raise TypeError(f"{name} must be a uint8 tensor [n_experts][n_rows][row bytes]")
+    if W.shape[0] != n_experts or W.shape[1] != n_rows:
+        raise ValueError(f"{name} must hold {n_experts} experts of {n_rows} rows, got {list(W.shape)}")
+    if W.shape[2] > 1 and W.stride(2) != 1:
+        raise ValueError(f"the bytes of one row of {name} must be contiguous")
+    nb1 = W.stride(1) if n_rows > 1 else max(W.stride(1), W.shape[2])
+    nb2 = W.stride(0) if n_experts > 1 else max(W.stride(0), n_rows * nb1)
+    return nb1, nb2
+
+
+def _row_fits(W, name, qtype, k):
+    """The rows hold k weights of the type, and the two bytes behind an odd number of 2-byte-aligned blocks."""
+    need = _qmm.qmm_row_bytes(qtype, k)
+    if need >= 0 and W.shape[2] < (need + 3) // 4 * 4:
+        raise ValueError(f"a row of {name} holds {W.shape[2]} bytes, {k} weights need {(need + 3) // 4 * 4}")
+
+
+def qmm_moe(X, router, gate, up, type_in, down, type_out, n_used, renormalise=True, Y=None, ids=None, weights=None,
+            workspace=None, stream=None):
+    """A mixture-of-experts layer of up to QMM_MOE_MAX_TOKENS tokens (C: qmm_moe):
+    Y[t] = sum over the n_used experts of largest logits router X[t] of
+    w down_e (silu(gate_e X[t]) * (up_e X[t])).
+
+    X fp32 or fp16 [n_tokens][k], router fp32 [n_experts][k], both contiguous;
+    gate and up uint8 [n_experts][n_ff][row bytes], blocks of type_in, with one
+    pair of strides; down uint8 [n_experts][k][row bytes], blocks of type_out;
+    their rows and experts at any strides that are multiples of 4 bytes. ids
+    (int32) and weights (fp32) [n_tokens][n_used], if given, receive the choice.
+    Y (fp32 [n_tokens][k]) is allocated if None; without a workspace, one of
+    qmm_moe_workspace_bytes bytes is allocated. Returns Y."""
+    L = _lib()
+    place = _Place(stream, ("X", "router", "gate", "up", "down", "Y", "ids", "weights", "workspace"),
+                   (X, router, gate, up, down, Y, ids, weights, workspace))
+    if X.dtype is not torch.float32 and X.dtype is not torch.float16:
+        raise TypeError("X must be float32 or float16")
+    if X.dim() != 2 or not X.is_contiguous() or router.dim() != 2:
+        raise ValueError("X must be contiguous [n_tokens][k], router [n_experts][k]")
+    (n, k), experts = X.shape, router.shape[0]
+    _floats(router, "router", (experts, k))
+    if gate.dim() != 3:
+        raise TypeError("gate must be a uint8 tensor [n_experts][n_ff][row bytes]")
+    ff = gate.shape[1]
+    strides = _stack(gate, "gate", experts, ff)
+    if _stack(up, "up", experts, ff) != strides:
+        raise ValueError("gate and up must have the same strides")
+    out_strides = _stack(down, "down", experts, k)
+    for W, name, qtype, width in ((gate, "gate", type_in, k), (up, "up", type_in, k), (down, "down", type_out, ff)):
+        _row_fits(W, name, qtype, width)
+    if Y is None:
+        Y = place.empty((n, k), torch.float32)
+    else:
+        _floats(Y, "Y", (n, k))
+    if ids is not None and (ids.dtype is not torch.int32 or ids.shape != (n, n_used) or not ids.is_contiguous()):
+        raise TypeError("ids must be a contiguous int32 tensor [n_tokens][n_used]")
+    if weights is not None:
+        _floats(weights, "weights", (n, n_used))
+    _keep, ws, ws_bytes = place.workspace(workspace, L.qmm_moe_workspace_bytes(n, k, ff, experts, n_used),
+                                          "qmm_moe_workspace_bytes")
+    place.run(L.qmm_moe, "qmm_moe", X.data_ptr(), _attn.QMM_T_F32 if X.dtype is torch.float32 else _attn.QMM_T_F16, n, k,
+              router.data_ptr(), experts, n_used, bool(renormalise), gate.data_ptr(), up.data_ptr(), type_in, ff, *strides,
+              down.data_ptr(), type_out, *out_strides, Y.data_ptr(), _ptr(ids), _ptr(weights), ws, ws_bytes)
+    return Y

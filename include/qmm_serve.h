@@ -6,7 +6,9 @@
  *   qmm_kv4_append  keys (normed and rotated) and values rounded to 4-bit
  *                   blocks and stored in a paged cache;
  *   qmm_kv4_read    the values that places of such a cache hold;
- *   qmm_attn_kv4    attention of a decode batch over such a cache.
+ *   qmm_attn_kv4    attention of a decode batch over such a cache;
+ *   qmm_moe         a whole mixture-of-experts layer for a few tokens, its
+ *                   experts in the block types of the MUL_MATs.
  *
  * Conventions are those of qmm_attn.h: every pointer is device memory owned by
  * the caller unless stated otherwise, nothing is retained or allocated, work
@@ -45,6 +47,10 @@ extern "C" {
  * A page of zeros is valid (it holds zeros).
  */
 #define QMM_KV4_MAX_PAGE_TOKENS 256
+
+#define QMM_MOE_MAX_TOKENS 16
+#define QMM_MOE_MAX_EXPERTS 512
+#define QMM_MOE_MAX_USED 32
 
 /* qmm_kv4_page_bytes - bytes of a page, or QMM_ERR_SHAPE. */
 int64_t qmm_kv4_page_bytes(int64_t page_tokens, int64_t n_kv_heads, int64_t head_dim);
@@ -133,6 +139,49 @@ int qmm_attn_kv4(int type, const qmm_heads *Q, const qmm_heads *O, int64_t n_row
  * sizes, or QMM_ERR_SHAPE. The same on every device. */
 int64_t qmm_attn_kv4_workspace_bytes(int64_t n_rows, int64_t n_q_heads, int64_t n_kv_heads, int64_t head_dim,
                                      int64_t table_width, int64_t page_tokens);
+
+/*
+ * qmm_moe - a mixture-of-experts layer of up to QMM_MOE_MAX_TOKENS tokens:
+ *   r = softmax(router X[t]) over the experts; the n_used experts of largest
+ *   logits are chosen (of equal ones the first; a NaN is below all others), with
+ *   weights w = r, divided by their sum if renormalise;
+ *   Y[t] = sum over them of w down_e (silu(gate_e X[t]) * (up_e X[t])),
+ *   silu(z) = z / (1 + e^-z).
+ * More tokens are a matter for qmm_matmul_id, whose matrix-core route serves them.
+ *   X           fp32 or fp16 (x_type QMM_T_F32 / QMM_T_F16) [n_tokens][k]
+ *   router      fp32 [n_experts][k]
+ *   n_experts   1 .. QMM_MOE_MAX_EXPERTS; n_used 1 .. QMM_MOE_MAX_USED, and at
+ *               most n_experts
+ *   gate, up    n_experts matrices of n_ff rows of k weights each, blocks of
+ *               type_in as for qmm_matmul: row r of expert e at e *
+ *               expert_stride_in + r * row_stride_in. They may be one matrix.
+ *   down        n_experts matrices of k rows of n_ff weights, blocks of type_out
+ *   strides     bytes, multiples of 4 (rows of an odd number of 18-, 22- or
+ *               34-byte blocks are padded by two bytes, which may be read but do
+ *               not count); expert strides at least the rows'
+ *   k, n_ff     positive multiples of 32 (256 for the side that a Q4_K row has),
+ *               below 2^24
+ *   Y           fp32 [n_tokens][k], overwritten
+ *   ids, weights  int32 and fp32 [n_tokens][n_used], the choice in order of
+ *               falling logits; each may be NULL
+ *   workspace   at least qmm_moe_workspace_bytes(...) bytes, 16-byte aligned;
+ *               overwritten; two calls in flight must not share one
+ * All pointers are 4-byte aligned; outputs and workspace overlap nothing else.
+ * Numerics: logits are summed in 64 bits. Activations, also those between the two
+ * products, are taken as two binary16 numbers each (error at most 2^-22 of the
+ * value, or 2^-35), codes are exact, sums and scales fp32. An activation beyond
+ * 65504, of X or of w silu(gate) up, makes its token's outputs non-finite, as in
+ * qmm_matmul; non-finite values of one token stay in its row.
+ */
+int qmm_moe(const void *X, int x_type, int64_t n_tokens, int64_t k, const float *router, int64_t n_experts,
+            int64_t n_used, int renormalise, const void *gate, const void *up, int type_in, int64_t n_ff,
+            int64_t row_stride_in, int64_t expert_stride_in, const void *down, int type_out, int64_t row_stride_out,
+            int64_t expert_stride_out, float *Y, int32_t *ids, float *weights, void *workspace,
+            int64_t workspace_bytes, void *stream);
+
+/* qmm_moe_workspace_bytes - the workspace qmm_moe needs for these sizes, or
+ * QMM_ERR_SHAPE; grows with each of them. The same on every device. */
+int64_t qmm_moe_workspace_bytes(int64_t n_tokens, int64_t k, int64_t n_ff, int64_t n_experts, int64_t n_used);
 
 #ifdef __cplusplus
 }

@@ -163,3 +163,54 @@ def attn_kv4(q, cache, page, heads, tables, lengths, scale, kind):
             with np.errstate(invalid="ignore", over="ignore"):
                 o[i, h], err[i, h] = attend(q[i, h], k[:, x], v[:, x], dk[:, x], dv[:, x], scale, kind)
     return o, err
+
+
+# ------------------------------------------------------ the expert layer
+
+def choice(x, router, n_used, renormalise=True):
+    """ids and weights [n][n_used]: logits in 80 bits (64 suffice, but for ties), the first of equal ones first."""
+    logits = np.asarray(x, np.longdouble) @ np.asarray(router, np.longdouble).T
+    with np.errstate(invalid="ignore", over="ignore"):
+        key = np.where(np.isnan(logits), -np.inf, logits)
+        ids = np.argsort(-key, axis=-1, kind="stable")[:, :n_used]
+        top = np.take_along_axis(key, ids[:, :1], -1)
+        w = np.exp(np.take_along_axis(logits, ids, -1) - top)
+        total = w.sum(-1, keepdims=True) if renormalise else np.exp(logits - top).sum(-1, keepdims=True)
+        return ids, np.asarray(w / total, np.float64)
+
+
+def moe(x, router, gate, up, down, n_used, renormalise=True):
+    """Y, its bound, ids and weights. gate, up, down: float64 [experts][rows][k].
+
+    A product's sums: 32 terms in a block and then block by block, k / 32 + 40
+    roundings of sums whose terms are at most 16 times the block's largest weight
+    (4-bit codes are taken with an offset of 16, whose sum is taken off again).
+    Activations, h among them, are off by 2^-22 and 2^-32. A routing weight's
+    difference of logits is rounded to fp32 after 64-bit sums, its exponential and
+    quotient are a few steps."""
+    n, k = x.shape
+    ids, w = choice(x, router, n_used, renormalise)
+    y, err = np.zeros((n, k)), np.zeros((n, k))
+    ff = gate.shape[1]
+
+    def product(m, v, v_err, terms):
+        size = np.repeat(np.abs(m).reshape(m.shape[0], -1, 32).max(-1), 32, -1)
+        return m @ v, np.abs(m) @ v_err + (terms / 32 + 40) * E32 * (16 * size @ (np.abs(v) + v_err))
+
+    with np.errstate(invalid="ignore", over="ignore"):
+        for t in range(n):
+            for i in range(n_used):
+                e, r = int(ids[t, i]), w[t, i]
+                x_err = 2.0 ** -22 * np.abs(x[t]) + 2.0 ** -32
+                g, eg = product(gate[e], x[t], x_err, k)
+                u, eu = product(up[e], x[t], x_err, k)
+                s = g / (1 + np.exp(-g))
+                h = s * u
+                eh = 1.1 * eg * (np.abs(u) + eu) + np.abs(s) * eu
+                eh = (r * (eh + (8 + 12) * E32 * np.abs(h))) * (1 + 2.0 ** -20)
+                h = r * h
+                eh = eh + 2.0 ** -22 * np.abs(h) + 2.0 ** -32
+                d, ed = product(down[e], h, eh, ff * n_used * n)
+                y[t] += d
+                err[t] += ed
+    return y, err, ids, w
