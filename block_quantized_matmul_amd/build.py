@@ -21,7 +21,7 @@ LIB = os.path.join(PKG, "libqmm.so")
 
 SOURCES = ["qmm_api.hip", "dequant.hip", "gemv.hip", "gemv_stream.hip", "gemm.hip", "route.hip",
            "attn_api.hip", "lora.hip", "norm_rope.hip", "attn_prompt.hip", "attn_shared.hip",
-           "serve_api.hip", "kv4.hip", "attn_kv4.hip", "moe.hip"]
+           "serve_api.hip", "kv4.hip", "attn_kv4.hip", "moe.hip", "sample.hip"]
 
 # Packed fp32 VALU forms are disabled for every HIP translation unit; the
 # host pass does not know the feature and warns, which is harmless.

@@ -55,4 +55,17 @@ struct MoeLayer {
 int64_t moe_workspace_bytes(int64_t n_tokens, int64_t k, int64_t n_ff, int64_t n_experts, int64_t n_used);
 hipError_t launch_moe(const MoeLayer &m, void *workspace, hipStream_t stream);
 
+// qmm_sample.
+struct SampleCall {
+  const void *logits;
+  int type;
+  int64_t n_rows, vocab, row_stride;
+  const float *u, *temperature;  // all but u may be null
+  const int32_t *top_k;
+  const float *top_p, *min_p;
+  int32_t *tokens;
+  float *probs;  // may be null
+};
+hipError_t launch_sample(const SampleCall &c, hipStream_t stream);
+
 }  // namespace qmm

@@ -198,4 +198,24 @@ int qmm_moe(const void *X, int x_type, int64_t n_tokens, int64_t k, const float 
   return status_of(qmm::launch_moe(m, workspace, static_cast<hipStream_t>(stream)));
 }
 
+int qmm_sample(const void *logits, int type, int64_t n_rows, int64_t vocab, int64_t row_stride, const float *u,
+               const float *temperature, const int32_t *top_k, const float *top_p, const float *min_p,
+               int32_t *tokens, float *probs, void *stream) {
+  if (!is_type(type)) return QMM_ERR_TYPE;
+  if (n_rows < 0 || n_rows > kMaxRows || vocab <= 0 || vocab > QMM_SAMPLE_MAX_VOCAB) return QMM_ERR_SHAPE;
+  if (n_rows > 1 && row_stride < 0) return QMM_ERR_STRIDE;
+  if (n_rows > 1 && !product_within(n_rows, row_stride, kMaxStride)) return QMM_ERR_SHAPE;
+  if (n_rows == 0) return QMM_OK;
+  if (logits == nullptr || u == nullptr || tokens == nullptr) return QMM_ERR_NULL;
+  if (!aligned(logits, type == QMM_T_F32 ? 4 : 2)) return QMM_ERR_ALIGN;
+  for (const void *p : {static_cast<const void *>(u), static_cast<const void *>(temperature),
+                        static_cast<const void *>(top_k), static_cast<const void *>(top_p),
+                        static_cast<const void *>(min_p), static_cast<const void *>(tokens),
+                        static_cast<const void *>(probs)})
+    if (!aligned(p, 4)) return QMM_ERR_ALIGN;
+  const qmm::SampleCall c{logits, type, n_rows, vocab, n_rows > 1 ? row_stride : 0, u, temperature, top_k, top_p, min_p,
+                          tokens, probs};
+  return status_of(qmm::launch_sample(c, static_cast<hipStream_t>(stream)));
+}
+
 }  // extern "C"

@@ -1,7 +1,7 @@
 """The operators that complete a served decode step (C: include/qmm_serve.h).
 
-qmm_kv4_append, qmm_kv4_read and qmm_attn_kv4 (a 4-bit paged cache) and qmm_moe
-(a mixture-of-experts layer), in the same manner as attn.py: tensors supply pointers, strides and sizes, and the
+qmm_kv4_append, qmm_kv4_read and qmm_attn_kv4 (a 4-bit paged cache), qmm_moe
+(a mixture-of-experts layer) and qmm_sample, in the same manner as attn.py: tensors supply pointers, strides and sizes, and the
 library checks and runs. All tensors of a call are on one GPU, which need not
 be the current one; work is enqueued on `stream`, or on that GPU's current
 stream.
@@ -19,10 +19,11 @@ QMM_KV4_MAX_PAGE_TOKENS = 256
 QMM_MOE_MAX_TOKENS = 16
 QMM_MOE_MAX_EXPERTS = 512
 QMM_MOE_MAX_USED = 32
+QMM_SAMPLE_MAX_VOCAB = 524287
 
 __all__ = ["QMM_KV4_MAX_PAGE_TOKENS", "QMM_MOE_MAX_TOKENS", "QMM_MOE_MAX_EXPERTS", "QMM_MOE_MAX_USED",
-           "qmm_kv4_page_bytes", "qmm_kv4_append", "qmm_kv4_read", "qmm_attn_kv4", "qmm_attn_kv4_workspace_bytes",
-           "qmm_moe", "qmm_moe_workspace_bytes"]
+           "QMM_SAMPLE_MAX_VOCAB", "qmm_kv4_page_bytes", "qmm_kv4_append", "qmm_kv4_read", "qmm_attn_kv4",
+           "qmm_attn_kv4_workspace_bytes", "qmm_moe", "qmm_moe_workspace_bytes", "qmm_sample"]
 
 _vp, _i32, _i64, _f32, _f64 = ctypes.c_void_p, ctypes.c_int, ctypes.c_int64, ctypes.c_float, ctypes.c_double
 _ready = None
@@ -40,6 +41,7 @@ _SIGNATURES = {  # restype, then the arguments; host structs travel as bytes
     "qmm_moe": (_i32, [_vp, _i32, _i64, _i64, _vp, _i64, _i64, _i32, _vp, _vp, _i32, _i64, _i64, _i64, _vp, _i32, _i64,
                        _i64, _vp, _vp, _vp, _vp, _i64, _vp]),
     "qmm_moe_workspace_bytes": (_i64, [_i64] * 5),
+    "qmm_sample": (_i32, [_vp, _i32, _i64, _i64, _i64, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp]),
 }
 
 
@@ -256,3 +258,35 @@ def qmm_moe(X, router, gate, up, type_in, down, type_out, n_used, renormalise=Tr
               router.data_ptr(), experts, n_used, bool(renormalise), gate.data_ptr(), up.data_ptr(), type_in, ff, *strides,
               down.data_ptr(), type_out, *out_strides, Y.data_ptr(), _ptr(ids), _ptr(weights), ws, ws_bytes)
     return Y
+
+
+def qmm_sample(logits, u, temperature=None, top_k=None, top_p=None, min_p=None, tokens=None, probs=None, stream=None):
+    """The next token of every row of logits (C: qmm_sample).
+
+    logits [n_rows][vocab] fp32, fp16 or bf16, contiguous rows at any stride; u fp32
+    [n_rows], random numbers from [0, 1); temperature, top_p and min_p fp32 [n_rows],
+    top_k int32 [n_rows], each None for none. Of the tokens in the order of falling
+    logits, the first top_k, of those the shortest beginning that holds top_p of
+    their probability, and of those the ones above min_p of the largest are kept, and
+    the one where the sum of probabilities passes u is taken. tokens (int32
+    [n_rows]) is allocated if None; -1 where no logit is above -infinity. probs (fp32
+    [n_rows]), if given, receives the probabilities among what was kept. Returns
+    tokens."""
+    L = _lib()
+    place = _Place(stream, ("logits", "u", "temperature", "top_k", "top_p", "min_p", "tokens", "probs"),
+                   (logits, u, temperature, top_k, top_p, min_p, tokens, probs))
+    if logits.dim() != 2 or (logits.shape[1] > 1 and logits.stride(1) != 1):
+        raise ValueError("logits must be [n_rows][vocab] with contiguous rows")
+    n, vocab = logits.shape
+    for t, name in ((u, "u"), (temperature, "temperature"), (top_p, "top_p"), (min_p, "min_p"), (probs, "probs")):
+        if t is not None:
+            _floats(t, name, (n,))
+    if top_k is not None:
+        _ints(top_k, "top_k", n)
+    if tokens is None:
+        tokens = place.empty((n,), torch.int32)
+    else:
+        _ints(tokens, "tokens", n)
+    place.run(L.qmm_sample, "qmm_sample", logits.data_ptr(), _type(logits, "logits"), n, vocab, logits.stride(0),
+              u.data_ptr(), _ptr(temperature), _ptr(top_k), _ptr(top_p), _ptr(min_p), tokens.data_ptr(), _ptr(probs))
+    return tokens

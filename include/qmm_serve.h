@@ -8,7 +8,9 @@
  *   qmm_kv4_read    the values that places of such a cache hold;
  *   qmm_attn_kv4    attention of a decode batch over such a cache;
  *   qmm_moe         a whole mixture-of-experts layer for a few tokens, its
- *                   experts in the block types of the MUL_MATs.
+ *                   experts in the block types of the MUL_MATs;
+ *   qmm_sample      the next token of every row of logits: temperature, top-k,
+ *                   top-p, min-p and a given random number.
  *
  * Conventions are those of qmm_attn.h: every pointer is device memory owned by
  * the caller unless stated otherwise, nothing is retained or allocated, work
@@ -51,6 +53,7 @@ extern "C" {
 #define QMM_MOE_MAX_TOKENS 16
 #define QMM_MOE_MAX_EXPERTS 512
 #define QMM_MOE_MAX_USED 32
+#define QMM_SAMPLE_MAX_VOCAB 524287
 
 /* qmm_kv4_page_bytes - bytes of a page, or QMM_ERR_SHAPE. */
 int64_t qmm_kv4_page_bytes(int64_t page_tokens, int64_t n_kv_heads, int64_t head_dim);
@@ -182,6 +185,38 @@ int qmm_moe(const void *X, int x_type, int64_t n_tokens, int64_t k, const float 
 /* qmm_moe_workspace_bytes - the workspace qmm_moe needs for these sizes, or
  * QMM_ERR_SHAPE; grows with each of them. The same on every device. */
 int64_t qmm_moe_workspace_bytes(int64_t n_tokens, int64_t k, int64_t n_ff, int64_t n_experts, int64_t n_used);
+
+/*
+ * qmm_sample - for every row i of logits z, in the order of falling logits (of
+ * equal ones the lower index first), with p_j proportional to
+ * e^(z_j / temperature):
+ *   1. top_k > 0 keeps the first top_k tokens;
+ *   2. top_p < 1 keeps the shortest beginning of them whose share of their
+ *      probability reaches top_p, one token at least;
+ *   3. min_p > 0 keeps those with p_j >= min_p times the first one's;
+ *   4. tokens[i] is the first of what is left at which the sum of its
+ *      probabilities, as shares of what is left, exceeds u.
+ * A temperature that is not above 0 takes the first token.
+ *   logits       QMM_T_F32, QMM_T_F16 or QMM_T_BF16, [n_rows] rows of vocab
+ *                elements row_stride >= 0 apart, aligned to the type. A NaN counts
+ *                as -infinity, which has no probability; where the largest is
+ *                infinite, the infinite ones share it equally
+ *   vocab        1 .. QMM_SAMPLE_MAX_VOCAB
+ *   u            fp32 [n_rows], from [0, 1): below (and NaN) it counts as 0, above
+ *                as the largest number below 1
+ *   temperature, top_p, min_p  fp32 [n_rows], top_k int32 [n_rows]; each may be
+ *                NULL for 1, 1, 0 and 0: none. A NaN for top_p or min_p is none
+ *   tokens       int32 [n_rows]; -1 for a row without a probability (every logit
+ *                -infinity or NaN)
+ *   probs        fp32 [n_rows], the token's share of what step 4 chooses from
+ *                (NaN beside -1); may be NULL
+ * Numerics: weights in 64 bits, sums of them exact to 2^-44 of the largest; a
+ * token whose probability is below 2^-45 of the largest is not chosen.
+ * n_rows < 2^24; n_rows == 0 is a no-op.
+ */
+int qmm_sample(const void *logits, int type, int64_t n_rows, int64_t vocab, int64_t row_stride, const float *u,
+               const float *temperature, const int32_t *top_k, const float *top_p, const float *min_p,
+               int32_t *tokens, float *probs, void *stream);
 
 #ifdef __cplusplus
 }

@@ -214,3 +214,42 @@ def moe(x, router, gate, up, down, n_used, renormalise=True):
                 y[t] += d
                 err[t] += ed
     return y, err, ids, w
+
+
+# ------------------------------------------------------------- the choice of a token
+
+def sample(z, u, temperature=1.0, top_k=0, top_p=1.0, min_p=0.0):
+    """(token, probability, distance): one row, in 80 bits. The distance is how far, as a share of the kept mass, any
+    of the decisions on the way was from its border: a result of other arithmetic may differ where that is tiny."""
+    z = np.asarray(z, np.longdouble).copy()
+    z[np.isnan(z)] = -np.inf
+    if z.max() == -np.inf:
+        return -1, np.nan, 1.0
+    order = np.argsort(-z, kind="stable")
+    z = z[order]
+    if not temperature > 0:
+        return int(order[0]), 1.0, 1.0
+    with np.errstate(invalid="ignore", over="ignore", under="ignore"):
+        d = np.where(z == z[0], 0, z[0] - z)
+        w = np.where(np.isinf(d), 0, np.exp(-np.where(np.isinf(d), 0, d) / np.longdouble(temperature)))
+    near = 1.0
+    n = min(top_k, len(w)) if top_k > 0 else len(w)
+    if top_p < 1:  # (a NaN is none)
+        before = np.concatenate([[0], np.cumsum(w[:n])[:-1]])
+        goal = np.longdouble(max(top_p, 0)) * w[:n].sum()
+        m = max(1, int((before < goal).sum()))
+        near = min(near, float(np.abs(before[1:] - goal).min() / w[:n].sum()) if n > 1 else 1.0)
+    else:
+        m = n
+    if min_p > 0:
+        keep = w >= np.longdouble(min_p)
+        near = min(near, float(np.abs(w[1:] - min_p).min()) if len(w) > 1 and min_p < 1 else 1.0)
+        m = min(m, max(1, int(keep.sum())) if min_p < 1 else int((w == 1).sum()))
+    w = w[:m]
+    u = min(max(float(u), 0.0), 1 - 2.0 ** -24) if u == u else 0.0
+    after = np.cumsum(w)
+    goal = np.longdouble(u) * after[-1]
+    i = min(int((after <= goal).sum()), m - 1)
+    if m > 1 and u > 0:
+        near = min(near, float(np.abs(after[:-1] - goal).min() / after[-1]))
+    return int(order[i]), float(w[i] / after[-1]), near
