@@ -38,8 +38,8 @@ namespace qmm {
 
 namespace {
 
-constexpr int kThreads = 512;
-constexpr int kWaves = kThreads / 64;
+constexpr int kWaves = 4;  // wavefronts of a workgroup of the products
+constexpr int kThreads = 64 * kWaves;
 constexpr int kMaxTokens = QMM_MOE_MAX_TOKENS;
 constexpr int kRouteThreads = 1024;
 constexpr int kLogitThreads = 256;
@@ -65,10 +65,11 @@ __device__ __forceinline__ void split(float x, _Float16 &hi, _Float16 &lo) {
   const float rest = (x - static_cast<float>(hi)) * kLoScale;
   lo = static_cast<_Float16>(__builtin_fabsf(rest) < __builtin_inff() ? rest : 0.f);
 }
-// Operand halves: [block][column][g][j], columns 2 t and 2 t + 1 of token t.
+// Operand halves: [block][g][column][j], columns 2 t and 2 t + 1 of token t; 1 KiB per quad and token.
 __device__ __forceinline__ int64_t operand_at(int64_t block, int columns, int column, int g) {
-  return ((block * columns + column) * 4 + g) * 8;
+  return ((block * 4 + g) * columns + column) * 8;
 }
+constexpr int kQuadOps = 1024;  // bytes, of a token
 
 template <int QT> struct Quad {
   static constexpr int chunks = Block<QT>::bytes / 2;  // 16-byte pieces of a row's 8 blocks
@@ -149,33 +150,41 @@ template <int QT> constexpr bool has_min() { return QTraits<QT>::has_min || QTra
 
 // A wavefront's rows: G groups of 16, from which a lane copies piece lane + 64 j
 // of every quad. Rows past the last repeat it.
-template <int QT, int MT, int G> struct Rows {
+//
+// The blocks behind the last whole quad, the tail, are copied as the last 16-byte
+// pieces of the row, which begin before the tail where its length is no multiple
+// of 16, so that nothing behind the row is read. (Rows shorter than that go dword
+// by dword, take_short.)
+template <int QT, int G, int STAGES> struct Rows {
   static constexpr int kPieces = 16 * G * Quad<QT>::chunks;
   static constexpr int kCopies = (kPieces + 63) / 64;
-  static constexpr int kStage = kPieces * 16;                      // bytes of LDS
-  static constexpr int kStages = kStage > 6000 ? 2 : G == 1 ? 4 : 3;  // quads on their way, the one in use among them
-  static constexpr int kXLoads = 8 * MT;
+  static constexpr int kStage = kPieces * 16;   // bytes of LDS
+  static constexpr int kStages = STAGES;        // quads on their way, the one in use among them
   int64_t off[kCopies];  // from the expert's matrix (group 0's), of this lane's pieces in quad 0
   bool on_last;          // whether this lane has a piece in the last copy
-  int64_t nb1;
+  int tail_at, tail_pieces, tail_skip;  // of a row: its tail's first piece's byte, pieces, and bytes before the tail
 
   // With two groups they are the same rows of two matrices, `apart` bytes from each other.
-  __device__ __forceinline__ Rows(int64_t nb1_, int row0, int n_rows, int64_t apart, int lane) : nb1(nb1_) {
+  __device__ __forceinline__ Rows(int64_t nb1, int row0, int n_rows, int blocks, int64_t apart, int lane) {
 #pragma unroll
     for (int j = 0; j < kCopies; ++j) {
       const int c = min(64 * j + lane, kPieces - 1), r = c / Quad<QT>::chunks;
-      const int group = r / 16;
       const int64_t row = min(row0 + r % 16, n_rows - 1);
-      off[j] = row * nb1 + 16 * (c % Quad<QT>::chunks) + (group ? apart : 0);
+      off[j] = row * nb1 + 16 * (c % Quad<QT>::chunks) + (r / 16 ? apart : 0);
     }
     on_last = 64 * (kCopies - 1) + lane < kPieces;
+    const int bytes = (blocks % 8 * Block<QT>::bytes + 3) / 4 * 4;
+    tail_pieces = (bytes + 15) / 16;
+    tail_skip = 16 * tail_pieces - bytes;
+    tail_at = blocks / 8 * Quad<QT>::row - tail_skip;
   }
-  __device__ __forceinline__ void copy(const uint8_t *w, int q, uint32_t lds) const {
-    const uint8_t *p = w + static_cast<int64_t>(q) * Quad<QT>::row;
+  __device__ __forceinline__ void copy(const uint8_t *w, int q, bool tail, uint32_t lds, int lane) const {
+    const uint8_t *p = w + (tail ? tail_at : static_cast<int64_t>(q) * Quad<QT>::row);
 #pragma unroll
     for (int j = 0; j < kCopies; ++j) {
       if (j < kCopies - 1 || kPieces % 64 == 0 || on_last) {
         const uint8_t *from = p + off[j];
+        if (tail) from -= 16 * max((64 * j + lane) % Quad<QT>::chunks - (tail_pieces - 1), 0);
         asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, off" ::"v"(from), "s"(lds + 1024 * j)
                      : "memory", "m0");
       }
@@ -183,30 +192,15 @@ template <int QT, int MT, int G> struct Rows {
   }
 };
 
-template <int MT> struct Activations {
-  half8_t x[8][MT];
-};
-// The operands of quad q's blocks (those below `blocks`; zeros beyond, and in columns that no token has).
-template <int MT>
-__device__ __forceinline__ void load_activations(Activations<MT> &a, const _Float16 *ops, int q, int blocks, int columns,
-                                                 int lane) {
-#pragma unroll
-  for (int i = 0; i < 8; ++i)
-#pragma unroll
-    for (int t = 0; t < MT; ++t) {
-      const int column = 16 * t + (lane & 15);
-      a.x[i][t] = half8_t{};
-      if (column < columns && 8 * q + i < blocks)
-        a.x[i][t] = *reinterpret_cast<const half8_t *>(ops + operand_at(8 * q + i, columns, column, lane >> 4));
-    }
-}
-
-// A quad in LDS times its activations, into the rows' sums. `valid`: blocks that exist.
+// A quad in LDS times its activations (there too), into the rows' sums. `valid`: blocks that exist.
 template <int QT, int MT, int G>
-__device__ __forceinline__ void take_quad(const uint8_t *stage, const Activations<MT> &a, int valid, float4_t acc[G][MT],
-                                          int lane) {
+__device__ __forceinline__ void take_quad(const uint8_t *stage, const uint8_t *ops, int columns, int valid,
+                                          float4_t acc[G][MT], int lane) {
   const int g = lane >> 4;
   const uint8_t *rb = stage + (lane & 15) * Quad<QT>::row;
+  const uint8_t *xp[MT];  // columns that no token has repeat the last, for nothing
+#pragma unroll
+  for (int t = 0; t < MT; ++t) xp[t] = ops + 16 * (g * columns + min(16 * t + (lane & 15), columns - 1));
 #pragma unroll
   for (int u = 0; u < 4; ++u) {
     if (2 * u >= valid) break;
@@ -218,7 +212,7 @@ __device__ __forceinline__ void take_quad(const uint8_t *stage, const Activation
       if (2 * u + h >= valid) break;
 #pragma unroll
       for (int t = 0; t < MT; ++t) {
-        const half8_t x = a.x[2 * u + h][t];
+        const half8_t x = *reinterpret_cast<const half8_t *>(xp[t] + (2 * u + h) * 64 * columns);
         float4_t start{}, sums{};
         if constexpr (QT == QMM_TYPE_Q4_0) start = __builtin_amdgcn_mfma_f32_16x16x32_f16(x, sum_operand<QT>(), start, 0, 0, 0);
         if constexpr (has_min<QT>()) sums = __builtin_amdgcn_mfma_f32_16x16x32_f16(x, sum_operand<QT>(), sums, 0, 0, 0);
@@ -236,71 +230,96 @@ __device__ __forceinline__ void take_quad(const uint8_t *stage, const Activation
   }
 }
 
-// The blocks behind the last whole quad, copied dword by dword so that nothing
-// behind a row's last dword is read.
+// Rows of fewer than 8 blocks, copied dword by dword so that nothing behind a
+// row's last dword is read, and their activations. The wavefront has `ops` for itself.
 template <int QT, int MT, int G>
-__device__ __forceinline__ void take_tail(const uint8_t *w, int64_t nb1, int row0, int n_rows, int64_t apart, int blocks,
-                                          const _Float16 *ops, int columns, uint8_t *stage, float4_t acc[G][MT], int lane) {
-  const int q = blocks / 8, valid = blocks % 8;
-  const int dwords = (valid * Block<QT>::bytes + 3) / 4;
-  Activations<MT> a;
-  load_activations<MT>(a, ops, q, blocks, columns, lane);
+__device__ __forceinline__ void take_short(const uint8_t *w, int64_t nb1, int row0, int n_rows, int64_t apart, int blocks,
+                                           const _Float16 *x, int columns, uint8_t *stage, uint8_t *ops,
+                                           float4_t acc[G][MT], int lane) {
+  const int dwords = (blocks * Block<QT>::bytes + 3) / 4;
   wait_reads();  // of what lay in this place before
   for (int i = lane; i < 16 * G * dwords; i += 64) {
     const int r = i / dwords, at = i % dwords;
     const int64_t row = min(row0 + r % 16, n_rows - 1);
-    const uint8_t *from = w + row * nb1 + (r >= 16 ? apart : 0) + static_cast<int64_t>(q) * Quad<QT>::row + 4 * at;
+    const uint8_t *from = w + row * nb1 + (r >= 16 ? apart : 0) + 4 * at;
     *reinterpret_cast<uint32_t *>(stage + r * Quad<QT>::row + 4 * at) = *reinterpret_cast<const uint32_t *>(from);
   }
+  for (int i = lane; i < blocks * 4 * columns; i += 64)
+    *reinterpret_cast<half8_t *>(ops + 16 * i) = *reinterpret_cast<const half8_t *>(x + 8 * i);
   wait_reads();
-  take_quad<QT, MT, G>(stage, a, valid, acc, lane);
+  take_quad<QT, MT, G>(stage, ops, columns, blocks, acc, lane);
 }
 
-// Stages 0 .. n - 1 through LDS: at(i) gives stage i's matrix, quad and operands.
-template <int QT, int MT, int G, class At>
-__device__ __forceinline__ void stream(const Rows<QT, MT, G> &rows, const At &at, int n, int blocks, int columns,
-                                       uint8_t *ring, float4_t acc[G][MT], int lane) {
-  typedef Rows<QT, MT, G> R;
-  if (n <= 0) return;
-  const uint32_t lds = lds_addr(ring);
+// All wavefronts are here; what each has waited for itself is there for all.
+__device__ __forceinline__ void meet() {
+  asm volatile("" ::: "memory");
+  __builtin_amdgcn_s_barrier();
+  asm volatile("" ::: "memory");
+}
+
+// A workgroup's place in LDS: the wavefronts' rings of weights, then stage by stage
+// the activations of each part of the stages.
+template <class R> struct Lds {
+  uint8_t *base;
+  int parts, tokens;
+  static constexpr int kRings = kWaves * R::kStages * R::kStage + 128;  // (a pair of blocks is read whole, also where a tail ends with its first)
+  __device__ __forceinline__ uint8_t *weights(int wave, int slot) const { return base + (wave * R::kStages + slot) * R::kStage; }
+  __device__ __forceinline__ uint8_t *ops(int part, int slot) const {
+    return base + kRings + (slot * parts + part) * tokens * kQuadOps;
+  }
+};
+
+// Stages 0 .. n - 1 (at most `most`, the same for the workgroup) through LDS: at(i) gives
+// stage i's matrix, quad and operands. The wavefronts of a part, `peer` of `peers`,
+// have different rows of the same stages and copy its activations together, XC pieces
+// of 1 KiB each (where there are fewer, the last several times).
+template <int QT, int MT, int G, int XC, class R, class At>
+__device__ __forceinline__ void stream(const R &rows, const At &at, int n, int most, int blocks, const Lds<R> &lds, int part,
+                                       int peer, int peers, bool live, float4_t acc[G][MT], int wave, int lane) {
+  const int whole = blocks / 8, columns = 2 * lds.tokens;
   auto copy = [&](int i, int slot) {
     const auto s = at(i);
-    rows.copy(s.w, s.q, lds + slot * R::kStage);
+    rows.copy(s.w, s.q, s.q == whole, lds_addr(lds.weights(wave, slot)), lane);
+    const uint8_t *ops = reinterpret_cast<const uint8_t *>(s.ops) + static_cast<int64_t>(s.q) * lds.tokens * kQuadOps;
+    const int bytes = min(8, blocks - 8 * s.q) * 64 * columns;  // of a tail there are fewer
+#pragma unroll
+    for (int x = 0; x < XC; ++x) {
+      const int piece = min(peer + x * peers, (bytes - 1) / 1024);
+      const uint8_t *from = ops + min(piece * 1024 + 16 * lane, bytes - 16);
+      asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, off" ::"v"(from),
+                   "s"(lds_addr(lds.ops(part, slot)) + piece * 1024)
+                   : "memory", "m0");
+    }
   };
-  Activations<MT> a;
-  {
-    const auto s = at(0);
-    load_activations<MT>(a, s.ops, s.q, blocks, columns, lane);
-  }
 #pragma unroll
   for (int i = 0; i < R::kStages - 1; ++i)
     if (i < n) copy(i, i);
   int slot = 0, ahead = R::kStages - 1;
-  for (int i = 0; i < n; ++i) {
-    Activations<MT> next = a;
-    if (i + 1 < n) {
-      const auto s = at(i + 1);
-      load_activations<MT>(next, s.ops, s.q, blocks, columns, lane);
-    }
-    if (i + R::kStages - 1 < n) {
-      copy(i + R::kStages - 1, ahead);
-      // later than stage i's copies: those of the stages behind it and the loads just above
-      wait_loads<(R::kStages - 1) * R::kCopies + R::kXLoads>();
-    } else {
+  for (int i = 0; i < most; ++i) {
+    if (i + R::kStages - 1 <= n)  // the copies of the stages behind this one may be on their way
+      wait_loads<(R::kStages - 2) * (R::kCopies + XC)>();
+    else
       wait_loads<0>();
+    meet();
+    if (i + R::kStages - 1 < n) copy(i + R::kStages - 1, ahead);
+    if (i < n && live) {
+      const int q = at(i).q;
+      const uint8_t *ops = lds.ops(part, slot);
+      if (q < whole)
+        take_quad<QT, MT, G>(lds.weights(wave, slot), ops, columns, 8, acc, lane);
+      else
+        take_quad<QT, MT, G>(lds.weights(wave, slot) + rows.tail_skip, ops, columns, blocks % 8, acc, lane);
     }
-    take_quad<QT, MT, G>(ring + slot * R::kStage, a, 8, acc, lane);
     wait_reads();
-    a = next;
     slot = slot + 1 == R::kStages ? 0 : slot + 1;
     ahead = ahead + 1 == R::kStages ? 0 : ahead + 1;
   }
 }
 
-// Adds the partial sums of the `split` wavefronts that share rows, in order; the
-// first of them has the result. (The ring is free: every wavefront is done with it.)
-template <int MT, int G> __device__ __forceinline__ void add_parts(float4_t acc[G][MT], uint8_t *lds, int split, int wave, int lane) {
-  if (split == 1) return;
+// Adds the sums of the `parts` wavefronts that share rows, in order; the first of
+// them has the result. (Wavefront: part + parts * unit.)
+template <int MT, int G> __device__ __forceinline__ void add_parts(float4_t acc[G][MT], uint8_t *lds, int parts, int wave, int lane) {
+  if (parts == 1) return;
   __syncthreads();
   float4_t *at = reinterpret_cast<float4_t *>(lds) + lane;
 #pragma unroll
@@ -308,8 +327,8 @@ template <int MT, int G> __device__ __forceinline__ void add_parts(float4_t acc[
 #pragma unroll
     for (int t = 0; t < MT; ++t) at[((wave * G + k) * MT + t) * 64] = acc[k][t];
   __syncthreads();
-  if (wave % split != 0) return;
-  for (int s = 1; s < split; ++s)
+  if (wave % parts != 0) return;
+  for (int s = 1; s < parts; ++s)
 #pragma unroll
     for (int k = 0; k < G; ++k)
 #pragma unroll
@@ -340,7 +359,9 @@ struct MoeArgs {
   int64_t h_step;     // halves of one expert's h
   int n_tokens, k, n_ff, n_experts, n_used, renormalise, x_f16, type_in, type_out;
   int logit_groups;   // workgroups of the first launch that compute logits; the others prepare operands
-  int split_in, split_out;
+  int parts_in, parts_out;  // wavefronts of a workgroup that share rows
+  int groups_out;           // workgroups that share rows (their sums go to `partial`)
+  float *partial;           // [groups_out][n_tokens][k]
 };
 
 __device__ __forceinline__ float load_x(const MoeArgs &a, int64_t at) {
@@ -489,33 +510,37 @@ __device__ __forceinline__ float token_value(const float4_t &acc, int which) {
 }
 
 // gate, up and their product: blockIdx.y is the active expert, a unit 16 rows of both.
-template <int QT, int MT> __global__ __launch_bounds__(kThreads, 2) void moe_inner_kernel(MoeArgs a) {
-  typedef Rows<QT, MT, 2> R;
+template <int QT> using InnerRows = Rows<QT, 2, 2>;
+template <int QT, int MT, int XC> __global__ __launch_bounds__(kThreads, MT == 1 ? 4 : 3) void moe_inner_kernel(MoeArgs a) {
+  typedef InnerRows<QT> R;
   extern __shared__ __align__(1024) uint8_t smem[];
   if (static_cast<int>(blockIdx.y) >= a.table->n_active) return;
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int split = a.split_in, part = wave % split;
-  const int unit = blockIdx.x * (kWaves / split) + wave / split;
-  const int row0 = 16 * unit;
-  const bool live = row0 < a.n_ff;
-  const int blocks = a.k / 32, quads = blocks / 8, columns = 2 * a.n_tokens;
+  const int parts = a.parts_in, part = wave % parts, peer = wave / parts, peers = kWaves / parts;
+  const int row0 = 16 * (blockIdx.x * peers + peer);
+  const bool live = row0 < a.n_ff;  // (else it copies for the others)
+  const int blocks = a.k / 32;
   const uint8_t *w = a.gate + static_cast<int64_t>(__builtin_amdgcn_readfirstlane(a.active[blockIdx.y])) * a.nb2_in;
-  uint8_t *ring = smem + wave * (R::kStages * R::kStage);
+  const Lds<R> lds{smem, parts, a.n_tokens};
   float4_t acc[2][MT] = {};
-  if (live) {
-    const int lo = quads * part / split, hi = quads * (part + 1) / split;
-    const R rows(a.nb1_in, row0, a.n_ff, a.up_apart, lane);
-    stream<QT, MT, 2>(rows, [&](int i) { return Stage{w, lo + i, a.x_ops}; }, hi - lo, blocks, columns, ring, acc, lane);
-    if (blocks % 8 != 0 && part == split - 1)
-      take_tail<QT, MT, 2>(w, a.nb1_in, row0, a.n_ff, a.up_apart, blocks, a.x_ops, columns, ring, acc, lane);
+  if (blocks >= 8) {
+    const int stages = (blocks + 7) / 8;
+    const int lo = stages * part / parts, hi = stages * (part + 1) / parts;
+    const R rows(a.nb1_in, row0, a.n_ff, blocks, a.up_apart, lane);
+    stream<QT, MT, 2, XC>(rows, [&](int i) { return Stage{w, lo + i, a.x_ops}; }, hi - lo, (stages + parts - 1) / parts,
+                          blocks, lds, part, peer, peers, live, acc, wave, lane);
+  } else if (live && part == 0) {
+    take_short<QT, MT, 2>(w, a.nb1_in, row0, a.n_ff, a.up_apart, blocks, a.x_ops, 2 * a.n_tokens, lds.weights(wave, 0),
+                          smem + Lds<R>::kRings + wave * a.n_tokens * kQuadOps, acc, lane);
   }
-  add_parts<MT, 2>(acc, smem, split, wave, lane);
+  add_parts<MT, 2>(acc, smem, parts, wave, lane);
   if (part != 0 || !live) return;
   const int row = row0 + (lane & 15), g = lane >> 4;
   if (row >= a.n_ff) return;
   const Spot s = spot_of(a.type_out, row % 32);
   _Float16 *h = a.h_ops + blockIdx.y * a.h_step;
+  const int columns = 2 * a.n_tokens;
 #pragma unroll
   for (int t = 0; t < MT; ++t)
 #pragma unroll
@@ -532,68 +557,106 @@ template <int QT, int MT> __global__ __launch_bounds__(kThreads, 2) void moe_inn
     }
 }
 
-// down: 16 rows over all active experts' quads, split evenly between wavefronts.
-template <int QT, int MT> __global__ __launch_bounds__(kThreads, 2) void moe_outer_kernel(MoeArgs a) {
-  typedef Rows<QT, MT, 1> R;
+// down: 16 rows over all active experts' quads, split evenly between the parts of
+// the workgroups that share rows.
+template <int QT, int MT> using OuterRows = Rows<QT, 1, MT == 2 || QT == QMM_TYPE_Q8_0 ? 2 : 3>;
+template <int QT, int MT, int XC> __global__ __launch_bounds__(kThreads, 4) void moe_outer_kernel(MoeArgs a) {
+  typedef OuterRows<QT, MT> R;
   extern __shared__ __align__(1024) uint8_t smem[];
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int split = a.split_out, part = wave % split;
-  const int row0 = 16 * (blockIdx.x * (kWaves / split) + wave / split);
+  const int parts = a.parts_out, part = wave % parts, peer = wave / parts, peers = kWaves / parts;
+  const int group = blockIdx.x % a.groups_out;
+  const int row0 = 16 * (blockIdx.x / a.groups_out * peers + peer);
   const bool live = row0 < a.k;
   const int n_active = __builtin_amdgcn_readfirstlane(a.table->n_active);
-  const int blocks = a.n_ff / 32, quads = blocks / 8, columns = 2 * a.n_tokens;
-  uint8_t *ring = smem + wave * (R::kStages * R::kStage);
+  const int blocks = a.n_ff / 32;
+  const Lds<R> lds{smem, parts, a.n_tokens};
   float4_t acc[1][MT] = {};
-  if (live) {
-    const int64_t all = static_cast<int64_t>(n_active) * quads;
-    const int lo = static_cast<int>(all * part / split), hi = static_cast<int>(all * (part + 1) / split);
-    const R rows(a.nb1_out, row0, a.k, 0, lane);
-    auto expert = [&](int i) {
-      return a.down + static_cast<int64_t>(__builtin_amdgcn_readfirstlane(a.active[i])) * a.nb2_out;
-    };
+  auto expert = [&](int i) {
+    return a.down + static_cast<int64_t>(__builtin_amdgcn_readfirstlane(a.active[i])) * a.nb2_out;
+  };
+  const int all_parts = parts * a.groups_out, my_part = group * parts + part;
+  if (blocks >= 8) {
+    const int stages = (blocks + 7) / 8;
+    const int64_t all = static_cast<int64_t>(n_active) * stages;
+    const int lo = static_cast<int>(all * my_part / all_parts), hi = static_cast<int>(all * (my_part + 1) / all_parts);
+    const R rows(a.nb1_out, row0, a.k, blocks, 0, lane);
     auto at = [&](int i) {
-      const int e = (lo + i) / quads;
-      return Stage{expert(e), lo + i - e * quads, a.h_ops + e * a.h_step};
+      const int e = (lo + i) / stages;
+      return Stage{expert(e), lo + i - e * stages, a.h_ops + e * a.h_step};
     };
-    stream<QT, MT, 1>(rows, at, hi - lo, blocks, columns, ring, acc, lane);
-    if (blocks % 8 != 0)
-      for (int e = part; e < n_active; e += split)
-        take_tail<QT, MT, 1>(expert(e), a.nb1_out, row0, a.k, 0, blocks, a.h_ops + e * a.h_step, columns, ring, acc, lane);
+    stream<QT, MT, 1, XC>(rows, at, hi - lo, static_cast<int>((all + all_parts - 1) / all_parts), blocks, lds, part, peer,
+                          peers, live, acc, wave, lane);
+  } else if (live) {
+    for (int e = my_part; e < n_active; e += all_parts)
+      take_short<QT, MT, 1>(expert(e), a.nb1_out, row0, a.k, 0, blocks, a.h_ops + e * a.h_step, 2 * a.n_tokens,
+                            lds.weights(wave, 0), smem + Lds<R>::kRings + wave * a.n_tokens * kQuadOps, acc, lane);
   }
-  add_parts<MT, 1>(acc, smem, split, wave, lane);
+  add_parts<MT, 1>(acc, smem, parts, wave, lane);
   const int row = row0 + (lane & 15), g = lane >> 4;
   if (part != 0 || row >= a.k) return;
+  float *y = a.groups_out > 1 ? a.partial + static_cast<int64_t>(group) * a.n_tokens * a.k : a.y;
 #pragma unroll
   for (int t = 0; t < MT; ++t)
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
       const int token = 8 * t + 2 * g + k;
-      if (token < a.n_tokens) a.y[static_cast<int64_t>(token) * a.k + row] = token_value(acc[0][t], k);
+      if (token < a.n_tokens) y[static_cast<int64_t>(token) * a.k + row] = token_value(acc[0][t], k);
     }
+}
+
+// y: the sums of the workgroups that share rows, in order.
+__global__ __launch_bounds__(256) void moe_add_kernel(const float *partial, int groups, int64_t n, float *y) {
+  const int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
+  if (i >= n) return;
+  float sum = partial[i];
+  for (int g = 1; g < groups; ++g) sum += partial[g * n + i];
+  y[i] = sum;
 }
 
 int64_t round16(int64_t n) { return (n + 15) / 16 * 16; }
 int64_t most_active(int64_t n_tokens, int64_t n_experts, int64_t n_used) { return std::min(n_experts, n_tokens * n_used); }
 
-template <class R> constexpr size_t ring_bytes() { return static_cast<size_t>(kWaves) * R::kStages * R::kStage; }
+// How a product's rows and stages are divided. A quad's activations take 1 KiB a
+// token, as much as the weights of 7 rows, so wavefronts with different rows share
+// them and copy up to XC tokens' each. The other wavefronts of a workgroup take
+// other parts of the stages, and so do other workgroups, where rows are few.
+int pieces_for(int64_t n_tokens) { return n_tokens <= 4 ? 1 : n_tokens <= 8 ? 2 : 4; }
+struct Plan {
+  int peers, parts, groups;
+};
+Plan plan_for(int64_t n_tokens, int64_t units, int64_t copies, int64_t want, bool by_groups) {
+  Plan p{1, 1, 1};
+  while (p.peers * pieces_for(n_tokens) < n_tokens) p.peers *= 2;
+  // no more parts of a workgroup than make `want` workgroups
+  while (!by_groups && p.peers < kWaves && (units + 2 * p.peers - 1) / (2 * p.peers) * copies >= want) p.peers *= 2;
+  p.parts = kWaves / p.peers;
+  const int64_t groups = (units + p.peers - 1) / p.peers * copies;
+  while (by_groups && p.groups < 16 && groups * p.groups * 2 <= want) p.groups *= 2;
+  return p;
+}
+Plan inner_plan(int64_t n_tokens, int64_t n_ff, int64_t most) { return plan_for(n_tokens, (n_ff + 15) / 16, most, 768, false); }
+Plan outer_plan(int64_t n_tokens, int64_t k) { return plan_for(n_tokens, (k + 15) / 16, 1, 768, n_tokens > 1); }
 
-// Wavefronts that share a unit's rows: as few as give every CU about two workgroups.
-int split_for(int64_t units, int64_t want) {
-  int split = 1;
-  while (split < kWaves && units * split < want * kWaves) split *= 2;
-  return split;
+// The rings and the activations, or what take_short or the partial sums use instead.
+template <class R> size_t lds_bytes(const Plan &p, int64_t n_tokens, bool short_rows) {
+  return static_cast<size_t>(Lds<R>::kRings) + n_tokens * kQuadOps * (short_rows ? kWaves : R::kStages * p.parts);
 }
 
-template <int QT, int MT> hipError_t run_inner(const MoeArgs &a, int64_t most, hipStream_t stream) {
-  const int64_t units = (a.n_ff + 15) / 16, per = kWaves / a.split_in;
-  const dim3 grid(static_cast<unsigned>((units + per - 1) / per), static_cast<unsigned>(most));
-  return launch(moe_inner_kernel<QT, MT>, grid, dim3(kThreads), ring_bytes<Rows<QT, MT, 2>>(), stream, a);
+template <int QT, int MT, int XC> hipError_t run_inner(const MoeArgs &a, int64_t most, hipStream_t stream) {
+  const Plan p = inner_plan(a.n_tokens, a.n_ff, most);
+  const dim3 grid(static_cast<unsigned>(((a.n_ff + 15) / 16 + p.peers - 1) / p.peers), static_cast<unsigned>(most));
+  return launch(moe_inner_kernel<QT, MT, XC>, grid, dim3(kThreads), lds_bytes<InnerRows<QT>>(p, a.n_tokens, a.k < 256), stream, a);
 }
-template <int QT, int MT> hipError_t run_outer(const MoeArgs &a, hipStream_t stream) {
-  const int64_t units = (a.k + 15) / 16, per = kWaves / a.split_out;
-  const dim3 grid(static_cast<unsigned>((units + per - 1) / per));
-  return launch(moe_outer_kernel<QT, MT>, grid, dim3(kThreads), ring_bytes<Rows<QT, MT, 1>>(), stream, a);
+template <int QT, int MT, int XC> hipError_t run_outer(const MoeArgs &a, hipStream_t stream) {
+  const Plan p = outer_plan(a.n_tokens, a.k);
+  const dim3 grid(static_cast<unsigned>(((a.k + 15) / 16 + p.peers - 1) / p.peers * p.groups));
+  const hipError_t e = launch(moe_outer_kernel<QT, MT, XC>, grid, dim3(kThreads),
+                              lds_bytes<OuterRows<QT, MT>>(p, a.n_tokens, a.n_ff < 256), stream, a);
+  if (e != hipSuccess || p.groups == 1) return e;
+  const int64_t n = static_cast<int64_t>(a.n_tokens) * a.k;
+  return launch(moe_add_kernel, dim3(static_cast<unsigned>((n + 255) / 256)), dim3(256), 0, stream, a.partial, p.groups, n, a.y);
 }
 
 }  // namespace
@@ -601,7 +664,7 @@ template <int QT, int MT> hipError_t run_outer(const MoeArgs &a, hipStream_t str
 int64_t moe_workspace_bytes(int64_t n_tokens, int64_t k, int64_t n_ff, int64_t n_experts, int64_t n_used) {
   const int64_t most = most_active(n_tokens, n_experts, n_used);
   return round16(n_tokens * n_experts * 8) + 16 + round16(most * 4) + most * kMaxTokens * 4 + n_tokens * k * 4 +
-         most * n_tokens * n_ff * 4;
+         most * n_tokens * n_ff * 4 + outer_plan(n_tokens, k).groups * n_tokens * k * 4;
 }
 
 hipError_t launch_moe(const MoeLayer &m, void *workspace, hipStream_t stream) {
@@ -619,12 +682,14 @@ hipError_t launch_moe(const MoeLayer &m, void *workspace, hipStream_t stream) {
   a.share = reinterpret_cast<float *>(p), p += most * kMaxTokens * 4;
   a.x_ops = reinterpret_cast<_Float16 *>(p), p += m.n_tokens * m.k * 4;
   a.h_ops = reinterpret_cast<_Float16 *>(p);
-  a.h_step = m.n_tokens * m.n_ff * 2;
+  a.h_step = m.n_tokens * m.n_ff * 2, p += most * m.n_tokens * m.n_ff * 4;
+  a.partial = reinterpret_cast<float *>(p);
+  a.parts_in = inner_plan(m.n_tokens, m.n_ff, most).parts;
+  const Plan out = outer_plan(m.n_tokens, m.k);
+  a.parts_out = out.parts, a.groups_out = out.groups;
   a.n_tokens = static_cast<int>(m.n_tokens), a.k = static_cast<int>(m.k), a.n_ff = static_cast<int>(m.n_ff);
   a.n_experts = static_cast<int>(m.n_experts), a.n_used = static_cast<int>(m.n_used), a.renormalise = m.renormalise;
   a.type_in = m.type_in, a.type_out = m.type_out;
-  a.split_in = split_for(most * ((m.n_ff + 15) / 16), 384);
-  a.split_out = split_for((m.k + 15) / 16, 256);
   a.logit_groups = static_cast<int>(m.n_experts * ((m.n_tokens + kLogitTokens - 1) / kLogitTokens));
   const unsigned first = static_cast<unsigned>(a.logit_groups + (m.k * m.n_tokens + kLogitThreads - 1) / kLogitThreads);
   hipError_t e = launch(moe_prepare_kernel, dim3(first), dim3(kLogitThreads), 0, stream, a);
@@ -632,15 +697,17 @@ hipError_t launch_moe(const MoeLayer &m, void *workspace, hipStream_t stream) {
   const size_t lds = static_cast<size_t>(m.n_tokens * (m.n_experts + m.n_used) * 8 + (m.n_experts + 1) * 4);
   e = launch(moe_route_kernel, dim3(1), dim3(kRouteThreads), lds, stream, a);
   if (e != hipSuccess) return e;
-  const bool one = m.n_tokens <= 8;
+  const int xc = pieces_for(m.n_tokens);
   e = by_qtype_k(m.type_in, [&](auto q) {
     constexpr int QT = decltype(q)::value;
-    return one ? run_inner<QT, 1>(a, most, stream) : run_inner<QT, 2>(a, most, stream);
+    return xc == 1 ? run_inner<QT, 1, 1>(a, most, stream)
+                   : xc == 2 ? run_inner<QT, 1, 2>(a, most, stream) : run_inner<QT, 2, 4>(a, most, stream);
   });
   if (e != hipSuccess) return e;
   return by_qtype_k(m.type_out, [&](auto q) {
     constexpr int QT = decltype(q)::value;
-    return one ? run_outer<QT, 1>(a, stream) : run_outer<QT, 2>(a, stream);
+    return xc == 1 ? run_outer<QT, 1, 1>(a, stream)
+                   : xc == 2 ? run_outer<QT, 1, 2>(a, stream) : run_outer<QT, 2, 4>(a, stream);
   });
 }
 
