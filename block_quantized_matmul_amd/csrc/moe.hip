@@ -38,8 +38,7 @@ namespace qmm {
 
 namespace {
 
-constexpr int kWaves = 4;  // wavefronts of a workgroup of the products
-constexpr int kThreads = 64 * kWaves;
+constexpr int kInnerWaves = 4;  // wavefronts of a workgroup
 constexpr int kMaxTokens = QMM_MOE_MAX_TOKENS;
 constexpr int kRouteThreads = 1024;
 constexpr int kLogitThreads = 256;
@@ -258,11 +257,12 @@ __device__ __forceinline__ void meet() {
 }
 
 // A workgroup's place in LDS: the wavefronts' rings of weights, then stage by stage
-// the activations of each part of the stages.
-template <class R> struct Lds {
+// the activations of each part of the stages. (A pair of blocks is read whole, also
+// where a tail ends with its first, which may be a few bytes behind the last ring.)
+template <class R, int WAVES> struct Lds {
   uint8_t *base;
   int parts, tokens;
-  static constexpr int kRings = kWaves * R::kStages * R::kStage + 128;  // (a pair of blocks is read whole, also where a tail ends with its first)
+  static constexpr int kRings = WAVES * R::kStages * R::kStage;
   __device__ __forceinline__ uint8_t *weights(int wave, int slot) const { return base + (wave * R::kStages + slot) * R::kStage; }
   __device__ __forceinline__ uint8_t *ops(int part, int slot) const {
     return base + kRings + (slot * parts + part) * tokens * kQuadOps;
@@ -273,8 +273,8 @@ template <class R> struct Lds {
 // stage i's matrix, quad and operands. The wavefronts of a part, `peer` of `peers`,
 // have different rows of the same stages and copy its activations together, XC pieces
 // of 1 KiB each (where there are fewer, the last several times).
-template <int QT, int MT, int G, int XC, class R, class At>
-__device__ __forceinline__ void stream(const R &rows, const At &at, int n, int most, int blocks, const Lds<R> &lds, int part,
+template <int QT, int MT, int G, int XC, class R, class L, class At>
+__device__ __forceinline__ void stream(const R &rows, const At &at, int n, int most, int blocks, const L &lds, int part,
                                        int peer, int peers, bool live, float4_t acc[G][MT], int wave, int lane) {
   const int whole = blocks / 8, columns = 2 * lds.tokens;
   auto copy = [&](int i, int slot) {
@@ -376,6 +376,7 @@ __global__ __launch_bounds__(kLogitThreads) void moe_prepare_kernel(MoeArgs a) {
     const int e = blockIdx.x % a.n_experts, t0 = blockIdx.x / a.n_experts * kLogitTokens;
     const float *r = a.router + static_cast<int64_t>(e) * a.k;
     double s[kLogitTokens] = {};
+#pragma unroll 4
     for (int i = 4 * threadIdx.x; i < a.k; i += 4 * kLogitThreads) {
       const float4_a4 w = *reinterpret_cast<const float4_a4 *>(r + i);
 #pragma unroll
@@ -511,18 +512,19 @@ __device__ __forceinline__ float token_value(const float4_t &acc, int which) {
 
 // gate, up and their product: blockIdx.y is the active expert, a unit 16 rows of both.
 template <int QT> using InnerRows = Rows<QT, 2, 2>;
-template <int QT, int MT, int XC> __global__ __launch_bounds__(kThreads, MT == 1 ? 4 : 3) void moe_inner_kernel(MoeArgs a) {
+template <int QT, int MT, int XC> __global__ __launch_bounds__(64 * kInnerWaves, MT == 1 ? 4 : 3) void moe_inner_kernel(MoeArgs a) {
   typedef InnerRows<QT> R;
+  typedef Lds<R, kInnerWaves> L;
   extern __shared__ __align__(1024) uint8_t smem[];
   if (static_cast<int>(blockIdx.y) >= a.table->n_active) return;
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int parts = a.parts_in, part = wave % parts, peer = wave / parts, peers = kWaves / parts;
+  const int parts = a.parts_in, part = wave % parts, peer = wave / parts, peers = kInnerWaves / parts;
   const int row0 = 16 * (blockIdx.x * peers + peer);
   const bool live = row0 < a.n_ff;  // (else it copies for the others)
   const int blocks = a.k / 32;
   const uint8_t *w = a.gate + static_cast<int64_t>(__builtin_amdgcn_readfirstlane(a.active[blockIdx.y])) * a.nb2_in;
-  const Lds<R> lds{smem, parts, a.n_tokens};
+  const L lds{smem, parts, a.n_tokens};
   float4_t acc[2][MT] = {};
   if (blocks >= 8) {
     const int stages = (blocks + 7) / 8;
@@ -532,7 +534,7 @@ template <int QT, int MT, int XC> __global__ __launch_bounds__(kThreads, MT == 1
                           blocks, lds, part, peer, peers, live, acc, wave, lane);
   } else if (live && part == 0) {
     take_short<QT, MT, 2>(w, a.nb1_in, row0, a.n_ff, a.up_apart, blocks, a.x_ops, 2 * a.n_tokens, lds.weights(wave, 0),
-                          smem + Lds<R>::kRings + wave * a.n_tokens * kQuadOps, acc, lane);
+                          smem + L::kRings + wave * a.n_tokens * kQuadOps, acc, lane);
   }
   add_parts<MT, 2>(acc, smem, parts, wave, lane);
   if (part != 0 || !live) return;
@@ -559,19 +561,20 @@ template <int QT, int MT, int XC> __global__ __launch_bounds__(kThreads, MT == 1
 
 // down: 16 rows over all active experts' quads, split evenly between the parts of
 // the workgroups that share rows.
-template <int QT, int MT> using OuterRows = Rows<QT, 1, MT == 2 || QT == QMM_TYPE_Q8_0 ? 2 : 3>;
-template <int QT, int MT, int XC> __global__ __launch_bounds__(kThreads, 4) void moe_outer_kernel(MoeArgs a) {
-  typedef OuterRows<QT, MT> R;
+template <int QT> using OuterRows = Rows<QT, 1, 2>;
+template <int QT, int MT, int XC, int WAVES> __global__ __launch_bounds__(64 * WAVES, 4) void moe_outer_kernel(MoeArgs a) {
+  typedef OuterRows<QT> R;
+  typedef Lds<R, WAVES> L;
   extern __shared__ __align__(1024) uint8_t smem[];
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int parts = a.parts_out, part = wave % parts, peer = wave / parts, peers = kWaves / parts;
+  const int parts = a.parts_out, part = wave % parts, peer = wave / parts, peers = WAVES / parts;
   const int group = blockIdx.x % a.groups_out;
   const int row0 = 16 * (blockIdx.x / a.groups_out * peers + peer);
   const bool live = row0 < a.k;
   const int n_active = __builtin_amdgcn_readfirstlane(a.table->n_active);
   const int blocks = a.n_ff / 32;
-  const Lds<R> lds{smem, parts, a.n_tokens};
+  const L lds{smem, parts, a.n_tokens};
   float4_t acc[1][MT] = {};
   auto expert = [&](int i) {
     return a.down + static_cast<int64_t>(__builtin_amdgcn_readfirstlane(a.active[i])) * a.nb2_out;
@@ -591,7 +594,7 @@ template <int QT, int MT, int XC> __global__ __launch_bounds__(kThreads, 4) void
   } else if (live) {
     for (int e = my_part; e < n_active; e += all_parts)
       take_short<QT, MT, 1>(expert(e), a.nb1_out, row0, a.k, 0, blocks, a.h_ops + e * a.h_step, 2 * a.n_tokens,
-                            lds.weights(wave, 0), smem + Lds<R>::kRings + wave * a.n_tokens * kQuadOps, acc, lane);
+                            lds.weights(wave, 0), smem + L::kRings + wave * a.n_tokens * kQuadOps, acc, lane);
   }
   add_parts<MT, 1>(acc, smem, parts, wave, lane);
   const int row = row0 + (lane & 15), g = lane >> 4;
@@ -610,8 +613,13 @@ template <int QT, int MT, int XC> __global__ __launch_bounds__(kThreads, 4) void
 __global__ __launch_bounds__(256) void moe_add_kernel(const float *partial, int groups, int64_t n, float *y) {
   const int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
   if (i >= n) return;
-  float sum = partial[i];
-  for (int g = 1; g < groups; ++g) sum += partial[g * n + i];
+  float sum = 0.f;
+  for (int g = 0; g < groups; g += 4) {  // (a power of two, 4 at least)
+    float v[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) v[k] = partial[(g + k) * n + i];
+    sum += (v[0] + v[1]) + (v[2] + v[3]);
+  }
   y[i] = sum;
 }
 
@@ -624,36 +632,46 @@ int64_t most_active(int64_t n_tokens, int64_t n_experts, int64_t n_used) { retur
 // other parts of the stages, and so do other workgroups, where rows are few.
 int pieces_for(int64_t n_tokens) { return n_tokens <= 4 ? 1 : n_tokens <= 8 ? 2 : 4; }
 struct Plan {
-  int peers, parts, groups;
+  int waves, peers, parts, groups;
 };
-Plan plan_for(int64_t n_tokens, int64_t units, int64_t copies, int64_t want, bool by_groups) {
-  Plan p{1, 1, 1};
+// gate and up: `most` experts. Four workgroups a CU (40 KiB of LDS each), in one round if they fit.
+Plan inner_plan(int64_t n_tokens, int64_t n_ff, int64_t most) {
+  Plan p{kInnerWaves, 1, 1, 1};
+  const int64_t units = (n_ff + 15) / 16;
   while (p.peers * pieces_for(n_tokens) < n_tokens) p.peers *= 2;
-  // no more parts of a workgroup than make `want` workgroups
-  while (!by_groups && p.peers < kWaves && (units + 2 * p.peers - 1) / (2 * p.peers) * copies >= want) p.peers *= 2;
-  p.parts = kWaves / p.peers;
-  const int64_t groups = (units + p.peers - 1) / p.peers * copies;
-  while (by_groups && p.groups < 16 && groups * p.groups * 2 <= want) p.groups *= 2;
+  while (p.peers < p.waves && (units + p.peers - 1) / p.peers * most > 1024) p.peers *= 2;
+  p.parts = p.waves / p.peers;
   return p;
 }
-Plan inner_plan(int64_t n_tokens, int64_t n_ff, int64_t most) { return plan_for(n_tokens, (n_ff + 15) / 16, most, 768, false); }
-Plan outer_plan(int64_t n_tokens, int64_t k) { return plan_for(n_tokens, (k + 15) / 16, 1, 768, n_tokens > 1); }
+// down: one token's rows by 16 wavefronts each (8 for Q8_0, whose rings are larger);
+// of more tokens' by as many workgroups as make about 4 a CU, since only wavefronts
+// with different rows can share the tokens.
+Plan outer_plan(int64_t n_tokens, int64_t k, int qtype) {
+  Plan p{n_tokens > 1 ? 4 : qtype == QMM_TYPE_Q8_0 ? 8 : 16, 1, 1, 1};
+  const int64_t units = (k + 15) / 16;
+  while (p.peers * pieces_for(n_tokens) < n_tokens) p.peers *= 2;
+  p.parts = p.waves / p.peers;
+  if (n_tokens > 1) p.groups = 4;
+  while (n_tokens > 1 && p.groups < 16 && (units + p.peers - 1) / p.peers * p.groups * 2 <= 1024) p.groups *= 2;
+  return p;
+}
 
 // The rings and the activations, or what take_short or the partial sums use instead.
-template <class R> size_t lds_bytes(const Plan &p, int64_t n_tokens, bool short_rows) {
-  return static_cast<size_t>(Lds<R>::kRings) + n_tokens * kQuadOps * (short_rows ? kWaves : R::kStages * p.parts);
+template <class R, int WAVES> size_t lds_bytes(const Plan &p, int64_t n_tokens, bool short_rows) {
+  return static_cast<size_t>(Lds<R, WAVES>::kRings) + n_tokens * kQuadOps * (short_rows ? WAVES : R::kStages * p.parts);
 }
 
 template <int QT, int MT, int XC> hipError_t run_inner(const MoeArgs &a, int64_t most, hipStream_t stream) {
   const Plan p = inner_plan(a.n_tokens, a.n_ff, most);
   const dim3 grid(static_cast<unsigned>(((a.n_ff + 15) / 16 + p.peers - 1) / p.peers), static_cast<unsigned>(most));
-  return launch(moe_inner_kernel<QT, MT, XC>, grid, dim3(kThreads), lds_bytes<InnerRows<QT>>(p, a.n_tokens, a.k < 256), stream, a);
+  return launch(moe_inner_kernel<QT, MT, XC>, grid, dim3(64 * kInnerWaves),
+                lds_bytes<InnerRows<QT>, kInnerWaves>(p, a.n_tokens, a.k < 256), stream, a);
 }
-template <int QT, int MT, int XC> hipError_t run_outer(const MoeArgs &a, hipStream_t stream) {
-  const Plan p = outer_plan(a.n_tokens, a.k);
+template <int QT, int MT, int XC, int WAVES> hipError_t run_outer(const MoeArgs &a, hipStream_t stream) {
+  const Plan p = outer_plan(a.n_tokens, a.k, QT);
   const dim3 grid(static_cast<unsigned>(((a.k + 15) / 16 + p.peers - 1) / p.peers * p.groups));
-  const hipError_t e = launch(moe_outer_kernel<QT, MT, XC>, grid, dim3(kThreads),
-                              lds_bytes<OuterRows<QT, MT>>(p, a.n_tokens, a.n_ff < 256), stream, a);
+  const hipError_t e = launch(moe_outer_kernel<QT, MT, XC, WAVES>, grid, dim3(64 * WAVES),
+                              lds_bytes<OuterRows<QT>, WAVES>(p, a.n_tokens, a.n_ff < 256), stream, a);
   if (e != hipSuccess || p.groups == 1) return e;
   const int64_t n = static_cast<int64_t>(a.n_tokens) * a.k;
   return launch(moe_add_kernel, dim3(static_cast<unsigned>((n + 255) / 256)), dim3(256), 0, stream, a.partial, p.groups, n, a.y);
@@ -664,7 +682,7 @@ template <int QT, int MT, int XC> hipError_t run_outer(const MoeArgs &a, hipStre
 int64_t moe_workspace_bytes(int64_t n_tokens, int64_t k, int64_t n_ff, int64_t n_experts, int64_t n_used) {
   const int64_t most = most_active(n_tokens, n_experts, n_used);
   return round16(n_tokens * n_experts * 8) + 16 + round16(most * 4) + most * kMaxTokens * 4 + n_tokens * k * 4 +
-         most * n_tokens * n_ff * 4 + outer_plan(n_tokens, k).groups * n_tokens * k * 4;
+         most * n_tokens * n_ff * 4 + outer_plan(n_tokens, k, 0).groups * n_tokens * k * 4;
 }
 
 hipError_t launch_moe(const MoeLayer &m, void *workspace, hipStream_t stream) {
@@ -685,7 +703,7 @@ hipError_t launch_moe(const MoeLayer &m, void *workspace, hipStream_t stream) {
   a.h_step = m.n_tokens * m.n_ff * 2, p += most * m.n_tokens * m.n_ff * 4;
   a.partial = reinterpret_cast<float *>(p);
   a.parts_in = inner_plan(m.n_tokens, m.n_ff, most).parts;
-  const Plan out = outer_plan(m.n_tokens, m.k);
+  const Plan out = outer_plan(m.n_tokens, m.k, m.type_out);
   a.parts_out = out.parts, a.groups_out = out.groups;
   a.n_tokens = static_cast<int>(m.n_tokens), a.k = static_cast<int>(m.k), a.n_ff = static_cast<int>(m.n_ff);
   a.n_experts = static_cast<int>(m.n_experts), a.n_used = static_cast<int>(m.n_used), a.renormalise = m.renormalise;
@@ -706,8 +724,10 @@ hipError_t launch_moe(const MoeLayer &m, void *workspace, hipStream_t stream) {
   if (e != hipSuccess) return e;
   return by_qtype_k(m.type_out, [&](auto q) {
     constexpr int QT = decltype(q)::value;
-    return xc == 1 ? run_outer<QT, 1, 1>(a, stream)
-                   : xc == 2 ? run_outer<QT, 1, 2>(a, stream) : run_outer<QT, 2, 4>(a, stream);
+    return m.n_tokens == 1 ? run_outer<QT, 1, 1, QT == QMM_TYPE_Q8_0 ? 8 : 16>(a, stream)
+           : xc == 1       ? run_outer<QT, 1, 1, 4>(a, stream)
+           : xc == 2       ? run_outer<QT, 1, 2, 4>(a, stream)
+                           : run_outer<QT, 2, 4, 4>(a, stream);
   });
 }
 
