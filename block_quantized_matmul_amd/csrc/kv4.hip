@@ -151,54 +151,72 @@ template <int D> __device__ __forceinline__ uint8_t *tile_of(const Kv4Cache &c, 
          (static_cast<int64_t>(head) * (c.page_tokens / kKv4Tile) + place / kKv4Tile) * kv4_tile_bytes(D);
 }
 
-template <int D, bool WIDE> __global__ __launch_bounds__(kThreads) void append_kernel(AppendArgs a) {
+// Element e of a rotated, normalised head is (x[e] A[e] + x[partner] B[e]) times
+// the head's reciprocal norm, with A and B the same for every head of a token.
+__device__ __forceinline__ int partner_of(const AppendArgs &a, int e) {
+  if (e >= 2 * a.n_freqs) return e;
+  return a.neighbours ? e ^ 1 : e < a.n_freqs ? e + a.n_freqs : e - a.n_freqs;
+}
+// A and B of a token, by one wavefront: a lane has one sine and cosine, which
+// two elements share. Element e stands at (e % 8) (D / 8) + e / 8, since a lane
+// reads 8 in a row.
+template <int D> __device__ __forceinline__ void fill_turns(const AppendArgs &a, int position, double2 *turns, int lane) {
+  auto at = [&](int e) -> double2 & { return turns[e % 8 * (D / 8) + e / 8]; };
+  auto weight = [&](int e) { return a.norm && a.w ? static_cast<double>(a.w[e]) : 1.; };
+  if (lane < a.n_freqs) {
+    double sn, cs;
+    sincos_turn64(a.turn[lane] * static_cast<uint64_t>(static_cast<int64_t>(position)), sn, cs);
+    const int e = a.neighbours ? 2 * lane : lane, f = a.neighbours ? e + 1 : e + a.n_freqs;
+    const double we = weight(e), wf = weight(f);
+    at(e) = double2{cs * we, -sn * wf};
+    at(f) = double2{cs * wf, sn * we};
+  }
+#pragma unroll
+  for (int e = lane; e < D; e += 64)
+    if (e >= 2 * a.n_freqs) at(e) = double2{weight(e), 0.};
+  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+}
+
+template <int D, bool WIDE> __global__ __launch_bounds__(kThreads, 4) void append_kernel(AppendArgs a) {
   constexpr int kLanes = D / 8, kPer = 64 / kLanes;  // lanes per head, heads per pass of a wavefront
   constexpr int NB = D / 32;
+  __shared__ double2 all_turns[kWaves][D];
   const int lane = threadIdx.x & 63, sub = lane / kLanes, l = lane % kLanes;
-  const int64_t wave0 = static_cast<int64_t>(blockIdx.x) * kWaves + (threadIdx.x >> 6);
+  const int own = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  double2 *turns = all_turns[own];
   const int64_t n_waves = a.n_tokens * 2 * a.chunks, stride = static_cast<int64_t>(gridDim.x) * kWaves;
-  for (int64_t wave = wave0; wave < n_waves; wave += stride) {
+  for (int64_t wave = static_cast<int64_t>(blockIdx.x) * kWaves + own; wave < n_waves; wave += stride) {
     const int64_t token = wave / (2 * a.chunks);
-    const int at = static_cast<int>(wave % (2 * a.chunks));
-    const bool values = at >= a.chunks;
+    const int part = static_cast<int>(wave % (2 * a.chunks));
+    const bool values = part >= a.chunks;
+    const bool rotate = !values && a.n_freqs > 0, turned = rotate || (!values && a.norm);
     const int slot = a.slots[token];
+    const int position = rotate ? a.positions[token] : 0;
     if (slot < 0 || slot >= a.n_slots) continue;  // (the whole wavefront)
     const int t = slot & (kKv4Tile - 1);
-    const int head0 = (values ? at - a.chunks : at) * a.chunk * kPer, head1 = min(a.heads, head0 + a.chunk * kPer);
-
-    // this lane's rotation: element i turns with the one at partner[i]
-    const bool rotate = !values && a.n_freqs > 0;
-    double sn[8], cs[8];
-    int partner[8];
-    if (rotate) {
-      const uint64_t pos = static_cast<uint64_t>(static_cast<int64_t>(a.positions[token]));
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const int e = 8 * l + i;
-        const bool turns = e < 2 * a.n_freqs;
-        const bool first = a.neighbours ? !(e & 1) : e < a.n_freqs;
-        const int f = a.neighbours ? e / 2 : first ? e : e - a.n_freqs;
-        partner[i] = !turns ? e : a.neighbours ? e ^ 1 : first ? e + a.n_freqs : e - a.n_freqs;
-        sn[i] = 0., cs[i] = 1.;
-        if (turns) sincos_turn64(a.turn[f] * pos, sn[i], cs[i]);
-        if (first) sn[i] = -sn[i];
-      }
-    }
+    const int head0 = (values ? part - a.chunks : part) * a.chunk * kPer, head1 = min(a.heads, head0 + a.chunk * kPer);
+    const void *src = values ? a.v : a.k;
+    const int64_t token_at = token * (values ? a.vt : a.kt), apart = values ? a.vh : a.kh;
+    if (turned) fill_turns<D>(a, position, turns, lane);
     for (int h0 = head0; h0 < head1; h0 += kPer) {
       const bool live = h0 + sub < head1;
       const int head = live ? h0 + sub : head1 - 1;
-      const void *src = values ? a.v : a.k;
-      const int64_t x0 = values ? token * a.vt + head * a.vh : token * a.kt + head * a.kh;
+      const int64_t x0 = token_at + head * apart;
       float x[8];
       load_eight<WIDE>(src, x0 + 8 * l, a.type, x);
-      if (!values && (a.norm || rotate)) {
+      if (turned) {
         float p[8];
         if (rotate) {
           if (WIDE && !a.neighbours) {
-            load_eight<WIDE>(src, x0 + partner[0], a.type, p);
+            load_eight<WIDE>(src, x0 + partner_of(a, 8 * l), a.type, p);
+          } else if (a.neighbours && 2 * a.n_freqs == D) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) p[i] = x[i ^ 1];
           } else {
 #pragma unroll
-            for (int i = 0; i < 8; ++i) p[i] = load_one(src, x0 + partner[i], a.type);
+            for (int i = 0; i < 8; ++i) p[i] = load_one(src, x0 + partner_of(a, 8 * l + i), a.type);
           }
         }
         double scale = 1.;
@@ -212,14 +230,10 @@ template <int D, bool WIDE> __global__ __launch_bounds__(kThreads) void append_k
         }
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-          double y = static_cast<double>(x[i]) * scale;
-          if (a.norm && a.w) y *= static_cast<double>(a.w[8 * l + i]);
-          if (rotate) {
-            double z = static_cast<double>(p[i]) * scale;
-            if (a.norm && a.w) z *= static_cast<double>(a.w[partner[i]]);
-            y = __builtin_fma(y, cs[i], z * sn[i]);
-          }
-          x[i] = static_cast<float>(y);
+          const double2 turn = turns[i * kLanes + l];
+          double y = static_cast<double>(x[i]) * turn.x;
+          if (rotate) y = __builtin_fma(static_cast<double>(p[i]), turn.y, y);
+          x[i] = static_cast<float>(y * scale);
         }
       }
       uint32_t d_bits;
