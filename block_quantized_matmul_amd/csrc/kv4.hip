@@ -12,8 +12,8 @@
 // are therefore computed in 64 bits (at the rate of 32-bit arithmetic on this
 // chip, and few beside the loads), x is rounded to fp32 once, and from there on
 // the decisions are exact: d is m scaled by a power of two and rounded once, and
-// the code q that the reciprocal suggests is checked against its two borders,
-// d (q - 1/2) and d (q + 1/2), products of 11 and 5 bits.
+// the reciprocal only finds the border next to x, d (n - 1/2), a product of 11
+// and 5 bits, with which x is compared.
 #include "common.h"
 #include "launch.h"
 #include "rope.h"
@@ -112,13 +112,13 @@ __device__ __forceinline__ void sincos_turn64(uint64_t t, double &sin, double &c
 // Codes (as a dword, element i in nibble i) and scale of a block whose 32
 // elements lie 8 each in a quad of lanes.
 __device__ __forceinline__ uint32_t block_codes(const float x[8], uint32_t &d_bits) {
-  float most = x[0];
-  int bad = !(__builtin_fabsf(x[0]) < __builtin_inff());
+  float most = x[0], zero = x[0] * 0.f;  // a NaN if one is infinite or a NaN
 #pragma unroll
   for (int i = 1; i < 8; ++i) {
-    bad |= !(__builtin_fabsf(x[i]) < __builtin_inff());
+    zero = __builtin_fmaf(x[i], 0.f, zero);
     most = __builtin_fabsf(x[i]) > __builtin_fabsf(most) ? x[i] : most;
   }
+  int bad = zero != 0.f;
   const int lane = threadIdx.x & 63;
 #pragma unroll
   for (int d = 1; d <= 2; d *= 2) {  // the larger magnitude of the two, the lower lane's if they are equal
@@ -133,16 +133,16 @@ __device__ __forceinline__ uint32_t block_codes(const float x[8], uint32_t &d_bi
   d_bits = bad ? kHalfNan : d == 0.f ? 0 : __builtin_bit_cast(uint16_t, dh);  // (a zero of either sign is +0)
   if (bad || d == 0.f) return 0x88888888u;
   const float inv = 1.f / d, step = __builtin_fabsf(d);
-  uint32_t codes = 0;
+  float sum[2] = {0.f, 0.f};  // of 16^i times the codes, below 2^16
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    float q = __builtin_floorf(__builtin_fmaf(x[i], inv, 0.5f));  // off by one at most, next to a border
+  for (int i = 7; i >= 0; --i) {
+    // floor(x / d + 1/2) is n or n - 1 for the integer n next to it, however the reciprocal was rounded
+    const float n = __builtin_rintf(__builtin_fmaf(x[i], inv, 0.5f));
     const float y = d < 0.f ? -x[i] : x[i];
-    q = y < step * (q - 0.5f) ? q - 1.f : y >= step * (q + 0.5f) ? q + 1.f : q;  // borders of 16 bits: exact
-    q = __builtin_amdgcn_fmed3f(q, -8.f, 7.f);
-    codes |= static_cast<uint32_t>(static_cast<int>(q) + 8) << (4 * i);
+    const float q = y >= step * (n - 0.5f) ? n : n - 1.f;  // a border of 16 bits: exact
+    sum[i / 4] = __builtin_fmaf(sum[i / 4], 16.f, __builtin_amdgcn_fmed3f(q, -8.f, 7.f) + 8.f);
   }
-  return codes;
+  return static_cast<uint32_t>(sum[0]) | static_cast<uint32_t>(sum[1]) << 16;
 }
 
 template <int D> __device__ __forceinline__ uint8_t *tile_of(const Kv4Cache &c, int slot, int head) {
@@ -179,6 +179,13 @@ template <int D> __device__ __forceinline__ void fill_turns(const AppendArgs &a,
   __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
 }
 
+// Workgroups are dealt to the 8 XCDs in turn, each with an L2 of its own. Runs of
+// 8 go to the same one, so that the pieces of a line (neighbouring tokens') meet there.
+__device__ __forceinline__ uint32_t near_blocks(uint32_t block, uint32_t blocks) {
+  if (block >= blocks / 64 * 64) return block;
+  return block / 64 * 64 + block % 8 * 8 + block / 8 % 8;
+}
+
 template <int D, bool WIDE> __global__ __launch_bounds__(kThreads, 4) void append_kernel(AppendArgs a) {
   constexpr int kLanes = D / 8, kPer = 64 / kLanes;  // lanes per head, heads per pass of a wavefront
   constexpr int NB = D / 32;
@@ -187,7 +194,7 @@ template <int D, bool WIDE> __global__ __launch_bounds__(kThreads, 4) void appen
   const int own = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   double2 *turns = all_turns[own];
   const int64_t n_waves = a.n_tokens * 2 * a.chunks, stride = static_cast<int64_t>(gridDim.x) * kWaves;
-  for (int64_t wave = static_cast<int64_t>(blockIdx.x) * kWaves + own; wave < n_waves; wave += stride) {
+  for (int64_t wave = static_cast<int64_t>(near_blocks(blockIdx.x, gridDim.x)) * kWaves + own; wave < n_waves; wave += stride) {
     const int64_t token = wave / (2 * a.chunks);
     const int part = static_cast<int>(wave % (2 * a.chunks));
     const bool values = part >= a.chunks;
