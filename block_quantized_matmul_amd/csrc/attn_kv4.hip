@@ -33,8 +33,9 @@
 // binary16's range: p = 2^(c x - c m - E) d.
 //
 // Four wavefronts take chunks of 64 keys in turn, each with the next chunk on
-// its way while it computes; they join through LDS. Where rows are few, a row's
-// keys are split over workgroups and a second launch joins them.
+// its way while it computes; they join through LDS. Where rows are few, their
+// keys are split over workgroups, in ranges of one length for all rows, and a
+// second launch joins them.
 #include "attn_core.h"
 #include "launch.h"
 #include "serve.h"
@@ -49,8 +50,8 @@ constexpr int kThreads = 256;
 constexpr int kWaves = 4;
 constexpr int kChunk = 64;       // keys
 constexpr int kTiles = kChunk / kKv4Tile;
-constexpr int kWantGroups = 1024;  // workgroups: four per CU on 256 CUs
-constexpr int kMaxSplits = 128;
+constexpr int kFewGroups = 1024;  // fewer workgroups than this, four per CU on 256 CUs: rows are split
+constexpr int kWantGroups = 2048;  // into about this many
 constexpr float kWeightSlack = 4.f;  // weights up to 2^4,
 constexpr int kScaleTop = 7;         // scales in [2^7, 2^8) when the exponent is taken,
 constexpr float kScaleMost = 2048.f;  // and up to 2^11 before it follows: products below 2^15
@@ -62,17 +63,56 @@ struct Kv4Args {
   const uint8_t *cache;
   int64_t page_bytes, table_stride;
   const int32_t *tables, *lengths;
-  float *part_o;   // [splits][n_rows * n_heads][D]
+  float *part_o;   // [units][n_heads][D]
   float4_t *part;  // likewise: reference m, sum l, factor c
-  int n_rows, n_heads, group, n_kv, tiles, splits, cap;
+  int *first;      // [n_rows + 1]: a row's first unit
+  int n_rows, n_heads, group, n_kv, tiles, want, cap;  // want: units of equal length wanted, or 0: rows are not split
   int n_pages, page_shift;
   float c0;  // scale * log2(e)
 };
 
-// Splits of a row with n keys that are in use: at least a chunk for each wavefront.
-__device__ __forceinline__ int splits_of(int n, int splits) {
-  const int chunks = (n + kChunk - 1) / kChunk;
-  return max(1, min(splits, (chunks + kWaves - 1) / kWaves));
+// Chunks of row r's keys; a length that the table does not hold is none.
+__device__ __forceinline__ int chunks_of(const Kv4Args &a, int r) {
+  const int n = r < a.n_rows ? a.lengths[r] : 0;
+  return n < 0 || n > a.cap ? 0 : static_cast<int>((static_cast<int64_t>(n) + kChunk - 1) / kChunk);
+}
+// A unit of work is a range of a row's keys, all about the same length over all
+// rows, whatever their lengths: every workgroup sums the lengths to get it, and
+// counts the units of the rows before its own.
+struct Unit {
+  int row, split, used;  // unit `split` of the row's `used`; used = 0: none
+};
+__device__ __forceinline__ Unit find_unit(const Kv4Args &a, int unit, int lane) {
+  if (a.want == 0) return Unit{unit, 0, 1};
+  const int chunks0 = chunks_of(a, lane);
+  int64_t total = chunks0;
+  for (int r = 64; r < a.n_rows; r += 64) total += chunks_of(a, r + lane);
+#pragma unroll
+  for (int d = 1; d < 64; d *= 2) total += __shfl_xor(total, d);
+  const int each = static_cast<int>(max(static_cast<int64_t>(kWaves), (total + a.want - 1) / a.want));
+  int before = 0;
+  for (int r0 = 0; r0 < a.n_rows; r0 += 64) {
+    const int r = r0 + lane;
+    const int chunks = r0 == 0 ? chunks0 : chunks_of(a, r);
+    const int units = r >= a.n_rows ? 0 : max(1, chunks / each + (chunks % each != 0));
+    int upto = units;
+#pragma unroll
+    for (int d = 1; d < 64; d *= 2) {
+      const int other = __shfl_up(upto, d);
+      upto += lane >= d ? other : 0;
+    }
+    const int first = before + upto - units;
+    if (unit == 0 && r < a.n_rows) a.first[r] = first;
+    const uint64_t here = __ballot(unit >= first && unit < first + units);
+    before += __builtin_amdgcn_readlane(upto, 63);
+    if (here != 0 && unit != 0) {
+      const int l = __builtin_ctzll(here);
+      return Unit{r0 + l, unit - __builtin_amdgcn_readlane(first, l), __builtin_amdgcn_readlane(units, l)};
+    }
+  }
+  if (unit != 0) return Unit{0, 0, 0};
+  a.first[a.n_rows] = before;
+  return Unit{0, 0, max(1, __builtin_amdgcn_readfirstlane(chunks0) / each + (__builtin_amdgcn_readfirstlane(chunks0) % each != 0))};
 }
 
 // 8 codes as halves: element order 0, 4, 1, 5, 2, 6, 3, 7, in units of 2^-24
@@ -84,9 +124,10 @@ __device__ __forceinline__ half8_t unpack_codes(uint32_t v) {
 __device__ __forceinline__ int code_of(int j) { return (j & 1) * 4 + j / 2; }    // the element at place j
 __device__ __forceinline__ bool times16(int j) { return (j / 2) & 1; }           // whether it is 16 times as large
 
-// 16 bytes per lane from the lane's own address into LDS at lds + 16 lane.
-__device__ __forceinline__ void dma_lane_to_lds(const uint8_t *p, uint32_t lds) {
-  asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, off" ::"v"(p), "s"(lds) : "memory", "m0");
+// 16 bytes per lane from base + offset, the lane's own, into LDS at lds + 16 lane.
+__device__ __forceinline__ void dma_lane_to_lds(const uint8_t *base, uint32_t offset, uint32_t lds) {
+  asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, %1" ::"v"(offset), "s"(base), "s"(lds)
+               : "memory", "m0");
 }
 
 __device__ __forceinline__ float max_over_rows(float x) {  // over lanes l, l ^ 16, l ^ 32, l ^ 48
@@ -224,16 +265,16 @@ __global__ __launch_bounds__(kThreads, CT == 1 ? 3 : 2) void attn_kv4_kernel(Kv4
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int col = lane & 15, g = lane >> 4;
   // KV heads are the fastest index, so that workgroups on the same keys share an XCD's L2
-  const int kv = blockIdx.x % a.n_kv, unit = blockIdx.x / a.n_kv;
-  const int ct0 = unit % a.tiles * CT, split = unit / a.tiles % a.splits, row = unit / a.tiles / a.splits;
+  const int kv = blockIdx.x % a.n_kv, ct0 = blockIdx.x / a.n_kv % a.tiles * CT, unit = blockIdx.x / a.n_kv / a.tiles;
+  const Unit u = find_unit(a, unit, lane);
+  const int row = u.row, split = u.split, used = u.used;
+  if (used == 0) return;
   const int len = __builtin_amdgcn_readfirstlane(a.lengths[row]);
   const bool bad_len = len < 0 || len > a.cap;
   const int n = bad_len ? 0 : len;
-  const int used = splits_of(n, a.splits);
-  if (split >= used) return;
   const int chunks = (n + kChunk - 1) / kChunk;
-  const int lo = static_cast<int>(static_cast<int64_t>(split) * chunks / used);
-  const int hi = static_cast<int>(static_cast<int64_t>(split + 1) * chunks / used);
+  const int lo = __builtin_amdgcn_readfirstlane(static_cast<int>(static_cast<int64_t>(split) * chunks / used));
+  const int hi = __builtin_amdgcn_readfirstlane(static_cast<int>(static_cast<int64_t>(split + 1) * chunks / used));
   const int mine = max(0, (hi - lo - wave + kWaves - 1) / kWaves);  // chunks lo + wave, + kWaves, ..
 
   Column<D> s[CT];
@@ -295,13 +336,14 @@ __global__ __launch_bounds__(kThreads, CT == 1 ? 3 : 2) void attn_kv4_kernel(Kv4
       if constexpr (D == 128) {
 #pragma unroll
         for (int t = 0; t < kTiles; ++t)
-          dma_lane_to_lds(base[t] + 8 * D + (lane / 4) * kRow + 16 * ((lane & 3) ^ t), to + t * 1024);
+          dma_lane_to_lds(base[t], 8 * D + (lane / 4) * kRow + 16 * ((lane & 3) ^ t), to + t * 1024);
       } else {
 #pragma unroll
-        for (int t = 0; t < kTiles; t += 2)
-          dma_lane_to_lds((lane < 32 ? base[t] : base[t + 1]) + 8 * D + (lane % 32 / 2) * kRow +
-                              16 * ((lane & 1) ^ (lane >> 5)),
-                          to + t * 512);
+        for (int t = 0; t < kTiles; t += 2) {  // two tiles, each by half of the lanes
+          const uint32_t at = 8 * D + (lane % 32 / 2) * kRow + 16 * ((lane & 1) ^ (lane >> 5));
+          if (lane < 32) dma_lane_to_lds(base[t], at, to + t * 512);
+          if (lane >= 32) dma_lane_to_lds(base[t + 1], at, to + t * 512);
+        }
       }
     };
     auto load_scales = [&]() {
@@ -357,6 +399,7 @@ __global__ __launch_bounds__(kThreads, CT == 1 ? 3 : 2) void attn_kv4_kernel(Kv4
       if (more) {
         locate(i + 1);
         load_keys();
+        wait_reads();
         copy_values((i + 1) & 1);
       }
       half8_t p[CT][2];
@@ -439,7 +482,7 @@ __global__ __launch_bounds__(kThreads, CT == 1 ? 3 : 2) void attn_kv4_kernel(Kv4
       *reinterpret_cast<typename E::v4 *>(out + 16 * i) = y;
     }
   } else {
-    const int64_t item = (static_cast<int64_t>(split) * a.n_rows + row) * a.n_heads + head;
+    const int64_t item = static_cast<int64_t>(unit) * a.n_heads + head;
 #pragma unroll
     for (int i = 0; i < 2; ++i)
       *reinterpret_cast<float4_t *>(a.part_o + item * D + e0 + 16 * i) =
@@ -448,34 +491,45 @@ __global__ __launch_bounds__(kThreads, CT == 1 ? 3 : 2) void attn_kv4_kernel(Kv4
   }
 }
 
-// Joins the splits of a row's head: a thread has four outputs.
+// Joins the units of a row's head: a wavefront, D / 4 lanes per unit with four
+// outputs each, so that 2 (D = 64: 4) units are summed at a time.
 template <class E, int D> __global__ __launch_bounds__(kThreads) void attn_kv4_join_kernel(Kv4Args a) {
   typedef typename E::one one;
-  constexpr int kFours = D / 4;
-  const int64_t i = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x;
-  const int64_t item = i / kFours, items = static_cast<int64_t>(a.n_rows) * a.n_heads;
-  if (item >= items) return;
-  const int e = 4 * static_cast<int>(i % kFours);
-  const int row = static_cast<int>(item / a.n_heads), head = static_cast<int>(item % a.n_heads);
-  const int len = a.lengths[row];
-  const int used = len < 0 || len > a.cap ? 1 : splits_of(len, a.splits);
+  constexpr int kFours = D / 4, kAtOnce = 64 / kFours;
+  const int lane = threadIdx.x & 63;
+  const int item = __builtin_amdgcn_readfirstlane(static_cast<int>(blockIdx.x * kWaves + (threadIdx.x >> 6)));
+  if (item >= a.n_rows * a.n_heads) return;
+  const int row = item / a.n_heads, head = item % a.n_heads;
+  const int first = a.first[row], used = a.first[row + 1] - first;
   if (used == 1) return;  // written already
+  const float4_t *part = a.part + static_cast<int64_t>(first) * a.n_heads + head;
+  const float *part_o = a.part_o + (static_cast<int64_t>(first) * a.n_heads + head) * D + 4 * (lane % kFours);
   float m = -__builtin_inff();
-  for (int k = 0; k < used; ++k) m = fmaxf(m, a.part[k * items + item][0]);
+  for (int k = lane; k < used; k += 64) m = fmaxf(m, part[static_cast<int64_t>(k) * a.n_heads][0]);
+#pragma unroll
+  for (int d = 1; d < 64; d *= 2) m = fmaxf(m, __shfl_xor(m, d));
   float l = 0.f;
   float4_t v{};
-  for (int k = 0; k < used; ++k) {
-    const float4_t p = a.part[k * items + item];
+#pragma unroll 4
+  for (int k = lane / kFours; k < used; k += kAtOnce) {
+    const float4_t p = part[static_cast<int64_t>(k) * a.n_heads];
+    const float4_t o = *reinterpret_cast<const float4_t *>(part_o + static_cast<int64_t>(k) * a.n_heads * D);
     const float f = rescaling(p[0], m, p[2]);
     l = __builtin_fmaf(p[1], f, l);
-    const float4_t o = *reinterpret_cast<const float4_t *>(a.part_o + (k * items + item) * D + e);
 #pragma unroll
     for (int r = 0; r < 4; ++r) v[r] = __builtin_fmaf(o[r], f, v[r]);
   }
+#pragma unroll
+  for (int d = kFours; d < 64; d *= 2) {
+    l += __shfl_xor(l, d);
+#pragma unroll
+    for (int r = 0; r < 4; ++r) v[r] += __shfl_xor(v[r], d);
+  }
+  if (lane >= kFours) return;
   typename E::v4 y;
 #pragma unroll
   for (int r = 0; r < 4; ++r) y[r] = static_cast<one>(E::limit(v[r] * (1.f / l)));
-  *reinterpret_cast<typename E::v4 *>(static_cast<one *>(a.o) + row * a.ot + head * a.oh + e) = y;
+  *reinterpret_cast<typename E::v4 *>(static_cast<one *>(a.o) + row * a.ot + head * a.oh + 4 * lane) = y;
 }
 
 // Outputs: means of values up to 8 times binary16's largest scale. Where the
@@ -487,12 +541,11 @@ struct OutF16 : ElemF16 {
 };
 
 template <class E, int D> hipError_t run(const Kv4Args &a, const Kv4Plan &p, hipStream_t stream) {
-  const dim3 grid(static_cast<unsigned>(a.n_rows * p.splits * p.tiles * a.n_kv));
+  const dim3 grid(static_cast<unsigned>(p.units * p.tiles * a.n_kv));
   const hipError_t e = p.columns == 2 ? launch(attn_kv4_kernel<E, D, 2>, grid, dim3(kThreads), 0, stream, a)
                                       : launch(attn_kv4_kernel<E, D, 1>, grid, dim3(kThreads), 0, stream, a);
-  if (e != hipSuccess || p.splits == 1) return e;
-  const int64_t threads = static_cast<int64_t>(a.n_rows) * a.n_heads * (D / 4);
-  return launch(attn_kv4_join_kernel<E, D>, dim3(static_cast<unsigned>((threads + kThreads - 1) / kThreads)),
+  if (e != hipSuccess || p.want == 0) return e;
+  return launch(attn_kv4_join_kernel<E, D>, dim3(static_cast<unsigned>((a.n_rows * a.n_heads + kWaves - 1) / kWaves)),
                 dim3(kThreads), 0, stream, a);
 }
 
@@ -504,10 +557,19 @@ Kv4Plan kv4_plan(int64_t n_rows, int64_t n_q_heads, int64_t n_kv_heads, int64_t 
   const int64_t columns = (group + per - 1) / per;
   p.columns = columns > 1 ? 2 : 1;
   p.tiles = (columns + p.columns - 1) / p.columns;
-  const int64_t groups = n_rows * n_kv_heads * p.tiles;
-  const int64_t most = std::max<int64_t>(1, std::min<int64_t>(kMaxSplits, cap / (kWaves * kChunk)));
-  p.splits = groups == 0 ? 1 : std::max<int64_t>(1, std::min((kWantGroups + groups - 1) / groups, most));
+  const int64_t per_unit = n_kv_heads * p.tiles, most = cap / (kWaves * kChunk);
+  p.units = n_rows;
+  if (n_rows > 0 && n_rows * per_unit < kFewGroups && most > 1) {
+    p.want = (kWantGroups + per_unit - 1) / per_unit;
+    // sum_r max(1, ceil(chunks_r / each)), each at least total / want and kWaves
+    p.units = std::min(p.want + n_rows, n_rows * (most + 1));
+  }
   return p;
+}
+
+int64_t kv4_workspace_bytes(const Kv4Plan &p, int64_t n_rows, int64_t n_q_heads, int64_t head_dim) {
+  // a unit's head: its outputs, reference, sum, factor and a spare
+  return p.want == 0 ? 0 : p.units * n_q_heads * (head_dim + 4) * 4 + (n_rows + 1 + 3) / 4 * 16;
 }
 
 hipError_t launch_attn_kv4(int type, const qmm_heads &Q, const qmm_heads &O, int64_t n_rows, int64_t n_q_heads,
@@ -521,10 +583,11 @@ hipError_t launch_attn_kv4(int type, const qmm_heads &Q, const qmm_heads &O, int
   a.cache = cache.data, a.page_bytes = cache.page_bytes, a.tables = tables, a.table_stride = table_stride;
   a.lengths = lengths;
   a.part_o = static_cast<float *>(workspace);
-  a.part = reinterpret_cast<float4_t *>(a.part_o + p.splits * n_rows * n_q_heads * head_dim);
+  a.part = reinterpret_cast<float4_t *>(a.part_o + p.units * n_q_heads * head_dim);
+  a.first = reinterpret_cast<int *>(a.part + p.units * n_q_heads);
   a.n_rows = static_cast<int>(n_rows), a.n_heads = static_cast<int>(n_q_heads);
   a.group = static_cast<int>(n_q_heads / n_kv_heads), a.n_kv = static_cast<int>(n_kv_heads);
-  a.tiles = static_cast<int>(p.tiles), a.splits = static_cast<int>(p.splits), a.cap = static_cast<int>(cap);
+  a.tiles = static_cast<int>(p.tiles), a.want = static_cast<int>(p.want), a.cap = static_cast<int>(cap);
   a.n_pages = static_cast<int>(cache.n_pages), a.page_shift = cache.page_shift;
   a.c0 = scale * 1.4426950408889634f;
   auto by_dim = [&](auto elem) {

@@ -25,14 +25,15 @@ hipError_t launch_kv4_append(int type, const qmm_heads &K, const qmm_heads &V, i
 hipError_t launch_kv4_read(int type, const qmm_heads &K, const qmm_heads &V, int64_t n_rows, int64_t n_kv_heads,
                            int64_t head_dim, const int32_t *slots, const Kv4Cache &cache, hipStream_t stream);
 
-// qmm_attn_kv4's split: every row and KV head in `splits` ranges of keys (fewer
-// where a sequence is short), `tiles` workgroups for the heads of a group.
+// qmm_attn_kv4's split into units, which are rows, or ranges of their keys.
 struct Kv4Plan {
-  int64_t tiles;
+  int64_t tiles;    // workgroups for the heads of a group
   int64_t columns;  // column tiles of a workgroup, 1 or 2
-  int64_t splits;
+  int64_t units;    // at most
+  int64_t want;     // ranges of equal length that are wanted; 0: units are rows
 };
 Kv4Plan kv4_plan(int64_t n_rows, int64_t n_q_heads, int64_t n_kv_heads, int64_t head_dim, int64_t cap);
+int64_t kv4_workspace_bytes(const Kv4Plan &p, int64_t n_rows, int64_t n_q_heads, int64_t head_dim);
 hipError_t launch_attn_kv4(int type, const qmm_heads &Q, const qmm_heads &O, int64_t n_rows, int64_t n_q_heads,
                            int64_t n_kv_heads, int64_t head_dim, const Kv4Cache &cache, const int32_t *tables,
                            int64_t table_stride, int64_t table_width, const int32_t *lengths, float scale,

@@ -131,8 +131,7 @@ int64_t qmm_attn_kv4_workspace_bytes(int64_t n_rows, int64_t n_q_heads, int64_t 
   if (table_width < 0 || table_width > kMaxDim / page_tokens) return QMM_ERR_SHAPE;
   if (n_rows == 0) return 0;
   const qmm::Kv4Plan p = qmm::kv4_plan(n_rows, n_q_heads, n_kv_heads, head_dim, table_width * page_tokens);
-  // a split's row is head_dim outputs, reference, sum, factor and a spare
-  return p.splits == 1 ? 0 : p.splits * n_rows * n_q_heads * (head_dim + 4) * 4;
+  return qmm::kv4_workspace_bytes(p, n_rows, n_q_heads, head_dim);
 }
 
 int qmm_attn_kv4(int type, const qmm_heads *Q, const qmm_heads *O, int64_t n_rows, int64_t n_q_heads,
