@@ -51,7 +51,10 @@ constexpr int kWaves = 4;
 constexpr int kChunk = 64;       // keys
 constexpr int kTiles = kChunk / kKv4Tile;
 constexpr int kFewGroups = 1024;  // fewer workgroups than this, four per CU on 256 CUs: rows are split
-constexpr int kWantGroups = 2048;  // into about this many
+// Workgroups of a CU that its registers hold: as many as run at once are wanted.
+// 48 rows of up to 8000 keys in 768, 1024, 1536, 2048, 4096 workgroups: 68, 75,
+// 75, 75, 90 us; 3 rows of 60000: 26, 31, 29, 34, 40 us.
+constexpr int resident(int64_t head_dim, int64_t columns) { return columns == 2 ? 2 : head_dim == 128 ? 3 : 4; }
 constexpr float kWeightSlack = 4.f;  // weights up to 2^4,
 constexpr int kScaleTop = 7;         // scales in [2^7, 2^8) when the exponent is taken,
 constexpr float kScaleMost = 2048.f;  // and up to 2^11 before it follows: products below 2^15
@@ -143,6 +146,12 @@ __device__ __forceinline__ float sum_over_rows(float x) {
   const float2_t two = both_halves(__builtin_bit_cast(float, static_cast<uint32_t>(r[0])) +
                                    __builtin_bit_cast(float, static_cast<uint32_t>(r[1])));
   return two.x + two.y;
+}
+// The same value, but one that the compiler does not compute ahead of the loop
+// and then keep in scratch memory, whose loads would wait for all others.
+__device__ __forceinline__ uint32_t here(uint32_t x) {
+  asm volatile("" : "+v"(x));
+  return x;
 }
 template <int CTRL> __device__ __forceinline__ float dpp(float x) {
   return __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, x), CTRL, 0xF, 0xF, true));
@@ -254,7 +263,7 @@ __device__ __forceinline__ void weigh(Column<D> &s, float x[kTiles][4], const u3
 }
 
 template <class E, int D, int CT>
-__global__ __launch_bounds__(kThreads, CT == 1 ? 3 : 2) void attn_kv4_kernel(Kv4Args a) {
+__global__ __launch_bounds__(kThreads, resident(D, CT)) void attn_kv4_kernel(Kv4Args a) {
   typedef typename E::one one;
   constexpr int NB = D / 32, H = 16 / NB;
   constexpr int kBuffer = kChunk * D / 2;  // bytes of a chunk's value codes
@@ -332,15 +341,15 @@ __global__ __launch_bounds__(kThreads, CT == 1 ? 3 : 2) void attn_kv4_kernel(Kv4
     // Rows of the values' codes, the 16-byte chunk c of a row of tile t at c ^ t, so that
     // the 16 rows of a read (four of each tile) lie on different banks
     auto copy_values = [&](int buffer) {
-      const uint32_t to = buf0 + buffer * kBuffer;
+      const uint32_t to = buf0 + buffer * kBuffer, l = here(lane);
       if constexpr (D == 128) {
+        const uint32_t at = 8 * D + 16 * l;  // row l / 4, chunk l % 4
 #pragma unroll
-        for (int t = 0; t < kTiles; ++t)
-          dma_lane_to_lds(base[t], 8 * D + (lane / 4) * kRow + 16 * ((lane & 3) ^ t), to + t * 1024);
+        for (int t = 0; t < kTiles; ++t) dma_lane_to_lds(base[t], at ^ (16 * t), to + t * 1024);
       } else {
 #pragma unroll
         for (int t = 0; t < kTiles; t += 2) {  // two tiles, each by half of the lanes
-          const uint32_t at = 8 * D + (lane % 32 / 2) * kRow + 16 * ((lane & 1) ^ (lane >> 5));
+          const uint32_t at = 8 * D + ((16 * l % 512) ^ (16 * (l / 32)));
           if (lane < 32) dma_lane_to_lds(base[t], at, to + t * 512);
           if (lane >= 32) dma_lane_to_lds(base[t + 1], at, to + t * 512);
         }
@@ -384,7 +393,7 @@ __global__ __launch_bounds__(kThreads, CT == 1 ? 3 : 2) void attn_kv4_kernel(Kv4
       if (left < kChunk) {  // places past the length: no weight, and no scale, which may be a NaN
 #pragma unroll
         for (int t = 0; t < kTiles; ++t) {
-          const int keep = left - 16 * t - 4 * g;
+          const int keep = left - 16 * t - 4 * static_cast<int>(here(g));
 #pragma unroll
           for (int r = 0; r < 4; ++r)
             if (r >= keep) {
@@ -406,7 +415,7 @@ __global__ __launch_bounds__(kThreads, CT == 1 ? 3 : 2) void attn_kv4_kernel(Kv4
 #pragma unroll
       for (int k = 0; k < CT; ++k) weigh<D>(s[k], x[k], dv, p[k]);
       if (more) load_scales();
-      const uint32_t va = buf0 + (i & 1) * kBuffer + v_at;
+      const uint32_t va = here(buf0 + (i & 1) * kBuffer + v_at);
 #pragma unroll
       for (int dt = 0; dt < D / 16; ++dt) {
         typedef int int2_t __attribute__((ext_vector_type(2)));
@@ -560,7 +569,8 @@ Kv4Plan kv4_plan(int64_t n_rows, int64_t n_q_heads, int64_t n_kv_heads, int64_t 
   const int64_t per_unit = n_kv_heads * p.tiles, most = cap / (kWaves * kChunk);
   p.units = n_rows;
   if (n_rows > 0 && n_rows * per_unit < kFewGroups && most > 1) {
-    p.want = (kWantGroups + per_unit - 1) / per_unit;
+    // half a range per row more, since a row's last is short on average
+    p.want = std::max(n_rows, 256 * resident(head_dim, p.columns) / per_unit - n_rows / 2);
     // sum_r max(1, ceil(chunks_r / each)), each at least total / want and kWaves
     p.units = std::min(p.want + n_rows, n_rows * (most + 1));
   }
