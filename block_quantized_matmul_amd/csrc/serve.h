@@ -67,6 +67,7 @@ struct SampleCall {
   int32_t *tokens;
   float *probs;  // may be null
 };
-hipError_t launch_sample(const SampleCall &c, hipStream_t stream);
+int64_t sample_workspace_bytes(int64_t n_rows, int64_t vocab);
+hipError_t launch_sample(const SampleCall &c, void *workspace, hipStream_t stream);
 
 }  // namespace qmm

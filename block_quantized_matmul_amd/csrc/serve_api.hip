@@ -12,6 +12,7 @@ constexpr int64_t kMaxDim = (int64_t{1} << 31) - 1;
 constexpr int64_t kMaxElems = int64_t{1} << 60;
 constexpr int64_t kMaxStride = kMaxElems / 4;
 constexpr int64_t kMaxRows = (int64_t{1} << 24) - 1;  // of a launch's workgroups
+constexpr int64_t kMaxSampleRows = (int64_t{1} << 22) - 1;  // likewise, of 1024 threads
 constexpr double kMaxFreq = 64.;  // radians per position, as in qmm_norm_rope
 
 bool product_within(int64_t a, int64_t b, int64_t limit) { return b == 0 || a <= limit / b; }
@@ -197,11 +198,17 @@ int qmm_moe(const void *X, int x_type, int64_t n_tokens, int64_t k, const float 
   return status_of(qmm::launch_moe(m, workspace, static_cast<hipStream_t>(stream)));
 }
 
+int64_t qmm_sample_workspace_bytes(int64_t n_rows, int64_t vocab) {
+  if (n_rows < 0 || n_rows > kMaxSampleRows || vocab <= 0 || vocab > QMM_SAMPLE_MAX_VOCAB) return QMM_ERR_SHAPE;
+  return qmm::sample_workspace_bytes(n_rows, vocab);
+}
+
 int qmm_sample(const void *logits, int type, int64_t n_rows, int64_t vocab, int64_t row_stride, const float *u,
                const float *temperature, const int32_t *top_k, const float *top_p, const float *min_p,
-               int32_t *tokens, float *probs, void *stream) {
+               int32_t *tokens, float *probs, void *workspace, int64_t workspace_bytes, void *stream) {
   if (!is_type(type)) return QMM_ERR_TYPE;
-  if (n_rows < 0 || n_rows > kMaxRows || vocab <= 0 || vocab > QMM_SAMPLE_MAX_VOCAB) return QMM_ERR_SHAPE;
+  const int64_t need = qmm_sample_workspace_bytes(n_rows, vocab);
+  if (need < 0) return static_cast<int>(need);
   if (n_rows > 1 && row_stride < 0) return QMM_ERR_STRIDE;
   if (n_rows > 1 && !product_within(n_rows, row_stride, kMaxStride)) return QMM_ERR_SHAPE;
   if (n_rows == 0) return QMM_OK;
@@ -212,9 +219,11 @@ int qmm_sample(const void *logits, int type, int64_t n_rows, int64_t vocab, int6
                         static_cast<const void *>(min_p), static_cast<const void *>(tokens),
                         static_cast<const void *>(probs)})
     if (!aligned(p, 4)) return QMM_ERR_ALIGN;
+  if (workspace == nullptr || workspace_bytes < need) return QMM_ERR_WORKSPACE;
+  if (!aligned(workspace, 16)) return QMM_ERR_ALIGN;
   const qmm::SampleCall c{logits, type, n_rows, vocab, n_rows > 1 ? row_stride : 0, u, temperature, top_k, top_p, min_p,
                           tokens, probs};
-  return status_of(qmm::launch_sample(c, static_cast<hipStream_t>(stream)));
+  return status_of(qmm::launch_sample(c, workspace, static_cast<hipStream_t>(stream)));
 }
 
 }  // extern "C"

@@ -23,7 +23,8 @@ QMM_SAMPLE_MAX_VOCAB = 524287
 
 __all__ = ["QMM_KV4_MAX_PAGE_TOKENS", "QMM_MOE_MAX_TOKENS", "QMM_MOE_MAX_EXPERTS", "QMM_MOE_MAX_USED",
            "QMM_SAMPLE_MAX_VOCAB", "qmm_kv4_page_bytes", "qmm_kv4_append", "qmm_kv4_read", "qmm_attn_kv4",
-           "qmm_attn_kv4_workspace_bytes", "qmm_moe", "qmm_moe_workspace_bytes", "qmm_sample"]
+           "qmm_attn_kv4_workspace_bytes", "qmm_moe", "qmm_moe_workspace_bytes", "qmm_sample",
+           "qmm_sample_workspace_bytes"]
 
 _vp, _i32, _i64, _f32, _f64 = ctypes.c_void_p, ctypes.c_int, ctypes.c_int64, ctypes.c_float, ctypes.c_double
 _ready = None
@@ -41,7 +42,8 @@ _SIGNATURES = {  # restype, then the arguments; host structs travel as bytes
     "qmm_moe": (_i32, [_vp, _i32, _i64, _i64, _vp, _i64, _i64, _i32, _vp, _vp, _i32, _i64, _i64, _i64, _vp, _i32, _i64,
                        _i64, _vp, _vp, _vp, _vp, _i64, _vp]),
     "qmm_moe_workspace_bytes": (_i64, [_i64] * 5),
-    "qmm_sample": (_i32, [_vp, _i32, _i64, _i64, _i64, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp]),
+    "qmm_sample": (_i32, [_vp, _i32, _i64, _i64, _i64, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _i64, _vp]),
+    "qmm_sample_workspace_bytes": (_i64, [_i64] * 2),
 }
 
 
@@ -260,7 +262,12 @@ def qmm_moe(X, router, gate, up, type_in, down, type_out, n_used, renormalise=Tr
     return Y
 
 
-def qmm_sample(logits, u, temperature=None, top_k=None, top_p=None, min_p=None, tokens=None, probs=None, stream=None):
+def qmm_sample_workspace_bytes(n_rows: int, vocab: int) -> int:
+    return int(_lib().qmm_sample_workspace_bytes(int(n_rows), int(vocab)))
+
+
+def qmm_sample(logits, u, temperature=None, top_k=None, top_p=None, min_p=None, tokens=None, probs=None, workspace=None,
+               stream=None):
     """The next token of every row of logits (C: qmm_sample).
 
     logits [n_rows][vocab] fp32, fp16 or bf16, contiguous rows at any stride; u fp32
@@ -270,11 +277,11 @@ def qmm_sample(logits, u, temperature=None, top_k=None, top_p=None, min_p=None, 
     their probability, and of those the ones above min_p of the largest are kept, and
     the one where the sum of probabilities passes u is taken. tokens (int32
     [n_rows]) is allocated if None; -1 where no logit is above -infinity. probs (fp32
-    [n_rows]), if given, receives the probabilities among what was kept. Returns
-    tokens."""
+    [n_rows]), if given, receives the probabilities among what was kept. Without a
+    workspace, one of qmm_sample_workspace_bytes bytes is allocated. Returns tokens."""
     L = _lib()
-    place = _Place(stream, ("logits", "u", "temperature", "top_k", "top_p", "min_p", "tokens", "probs"),
-                   (logits, u, temperature, top_k, top_p, min_p, tokens, probs))
+    place = _Place(stream, ("logits", "u", "temperature", "top_k", "top_p", "min_p", "tokens", "probs", "workspace"),
+                   (logits, u, temperature, top_k, top_p, min_p, tokens, probs, workspace))
     if logits.dim() != 2 or (logits.shape[1] > 1 and logits.stride(1) != 1):
         raise ValueError("logits must be [n_rows][vocab] with contiguous rows")
     n, vocab = logits.shape
@@ -287,6 +294,8 @@ def qmm_sample(logits, u, temperature=None, top_k=None, top_p=None, min_p=None, 
         tokens = place.empty((n,), torch.int32)
     else:
         _ints(tokens, "tokens", n)
+    _keep, ws, ws_bytes = place.workspace(workspace, L.qmm_sample_workspace_bytes(n, vocab), "qmm_sample_workspace_bytes")
     place.run(L.qmm_sample, "qmm_sample", logits.data_ptr(), _type(logits, "logits"), n, vocab, logits.stride(0),
-              u.data_ptr(), _ptr(temperature), _ptr(top_k), _ptr(top_p), _ptr(min_p), tokens.data_ptr(), _ptr(probs))
+              u.data_ptr(), _ptr(temperature), _ptr(top_k), _ptr(top_p), _ptr(min_p), tokens.data_ptr(), _ptr(probs),
+              ws, ws_bytes)
     return tokens

@@ -212,11 +212,17 @@ int64_t qmm_moe_workspace_bytes(int64_t n_tokens, int64_t k, int64_t n_ff, int64
  *                (NaN beside -1); may be NULL
  * Numerics: weights in 64 bits, sums of them exact to 2^-44 of the largest; a
  * token whose probability is below 2^-45 of the largest is not chosen.
- * n_rows < 2^24; n_rows == 0 is a no-op.
+ *   workspace    at least qmm_sample_workspace_bytes(n_rows, vocab) bytes, 16-byte
+ *                aligned
+ * n_rows < 2^22; n_rows == 0 is a no-op.
  */
 int qmm_sample(const void *logits, int type, int64_t n_rows, int64_t vocab, int64_t row_stride, const float *u,
                const float *temperature, const int32_t *top_k, const float *top_p, const float *min_p,
-               int32_t *tokens, float *probs, void *stream);
+               int32_t *tokens, float *probs, void *workspace, int64_t workspace_bytes, void *stream);
+
+/* qmm_sample_workspace_bytes - the workspace qmm_sample needs, or QMM_ERR_SHAPE;
+ * grows with both. The same on every device. */
+int64_t qmm_sample_workspace_bytes(int64_t n_rows, int64_t vocab);
 
 #ifdef __cplusplus
 }
