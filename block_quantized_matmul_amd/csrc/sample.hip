@@ -4,7 +4,7 @@
 // and then rising index, so the whole is three selections along it: the first
 // top_k, the first whose mass reaches top_p of theirs, and the element where the
 // mass passes u times that of what is left. No sort is needed: one histogram of
-// counts and masses over 1024 equal ranges of the logits below the largest finds
+// counts and masses over 2048 equal ranges of the logits below the largest finds
 // the range that holds a selection's place, and the few elements of that range are
 // ranked by comparing each with each, after dividing the range again, or equal
 // elements by index, where they are more than kFew. Rows that this does not fit (with
@@ -36,7 +36,8 @@ namespace {
 constexpr int kThreads = 1024;
 constexpr int kWaves = kThreads / 64;
 constexpr int kBits = 11;      // of a key, at a time
-constexpr int kBins = kThreads;  // ranges of logits, one per thread
+constexpr int kBins = 2048;     // ranges of logits
+constexpr int kOwn = kBins / kThreads;
 constexpr int kChunk = 8 * kThreads;
 constexpr int kList = 16384;   // elements of a row that are looked at in the end
 constexpr int kAtOnce = 8;
@@ -163,13 +164,18 @@ struct Found {
 
 struct Shared {
   uint32_t n[1 << kBits];
-  uint64_t m[1 << kBits];
+  uint64_t m[(1 << kBits) + 1];
   double table[kFractions];
   uint32_t wave_n[kWaves];
   uint64_t wave_m[kWaves];
   float few_z[kFew + kAtOnce];
   int few_i[kFew + kAtOnce];
   uint64_t few_w[kFew + kAtOnce];
+  struct alignas(16) {
+    float z;
+    int i;
+    uint64_t w;
+  } quick[kQuick];
   int bin, few;
   int bins[3];
   uint32_t before, listed, at;
@@ -411,21 +417,25 @@ __device__ __forceinline__ Goal goal_of(const Row &r, int kind, uint64_t total) 
   return Goal{kind, static_cast<uint32_t>(r.top_k), kind == BELOW ? fmax(mass, 0.5) : mass};
 }
 
-struct Range {  // a thread's: the counts and masses in front of it and behind it
+// Counts and masses in front of a range and behind it. Starts rise, so there is one
+// range whose start is the last that a goal reaches.
+struct Range {
   uint32_t n0, n1;
   uint64_t m0, m1;
+  __device__ __forceinline__ bool is_last(const Goal &goal, int bin) const {
+    return goal.reaches(n0, m0) && (bin == kBins - 1 || !goal.reaches(n1, m1));
+  }
 };
 // The mass up to and with the last element whose start a goal reaches, and that
 // element's index (-1: not by ranges), of the elements in the row's list.
 __device__ __forceinline__ uint64_t resolve(Shared &s, const Element *list, int listed, const Element &own_element,
-                                            const Range &own_range, const Row &r, const Weights &w, int per,
+                                            const Range own_range[kOwn], const Row &r, const Weights &w, int per,
                                             const Goal &goal, int &index) {
   index = -1;
   const int t = threadIdx.x;
-  // (starts rise from thread to thread, so one thread has the last that is reached)
-  if (goal.reaches(own_range.n0, own_range.m0) &&
-      (t == kThreads - 1 || !goal.reaches(own_range.n1, own_range.m1)))
-    s.bin = t, s.before = own_range.n0, s.mass = own_range.m0;
+#pragma unroll
+  for (int b = 0; b < kOwn; ++b)
+    if (own_range[b].is_last(goal, kOwn * t + b)) s.bin = kOwn * t + b, s.before = own_range[b].n0, s.mass = own_range[b].m0;
   if (t == 0) s.few = 0;
   __syncthreads();
   const int bin = s.bin;
@@ -564,21 +574,22 @@ __device__ __forceinline__ void pick_few(Shared &s, const SampleArgs &a, int row
   uint32_t n = st.n[bin];
   uint64_t m = st.m[bin], total = st.m[kBins];
   const uint64_t left = st.left;
-  s.few_z[t] = e.z, s.few_i[t] = e.i, s.few_w[t] = own;
+  s.quick[t] = {e.z, e.i, own};
   if (t < 3) s.bins[t] = -1;
   __syncthreads();
-  int pos = 0;  // in the order, among the listed
+  uint32_t with = 0;  // in front of it in its range
   for (int k0 = 0; k0 < listed; k0 += kAtOnce) {
 #pragma unroll
     for (int k = k0; k < k0 + kAtOnce; ++k) {
-      const float z = s.few_z[k];
-      const bool first = z > e.z || (z == e.z && s.few_i[k] < e.i);
-      const bool with = first && static_cast<int>(place_of(r.most, z, r.scale)) == bin;
-      pos += first;
-      n += with;
-      m += with ? s.few_w[k] : 0;
+      const auto o = s.quick[k];
+      // (what is in front of it is not in a later range)
+      const bool first = (o.z > e.z || (o.z == e.z && o.i < e.i)) && place_of(r.most, o.z, r.scale) >= static_cast<float>(bin);
+      with += first;
+      m += first ? o.w : 0;
     }
   }
+  n += with;
+  const int pos = bin * kQuick + static_cast<int>(with);  // rises along the order
 #pragma unroll 1
   for (int kind = COUNT; kind <= UPTO; ++kind) {
     if (kind == COUNT && !r.counted) continue;
@@ -636,7 +647,8 @@ template <int TYPE> __global__ __launch_bounds__(kThreads) void sample_mass_kern
   load_eight<TYPE>(a.z, row * a.stride, a.vocab, chunk, x);
   const Row r = row_of(s, a, row);
   if (r.most == -__builtin_inff()) return;  // nothing to choose from
-  s.n[t] = 0, s.m[t] = 0;
+#pragma unroll
+  for (int k = 0; k < kOwn; ++k) s.n[k * kThreads + t] = 0, s.m[k * kThreads + t] = 0;
   __syncthreads();
   const Weights w{static_cast<double>(r.most), r.c, s.table};
   uint64_t left = 0;
@@ -655,26 +667,38 @@ template <int TYPE> __global__ __launch_bounds__(kThreads) void sample_mass_kern
   __syncthreads();
   Part *parts = a.parts + static_cast<int64_t>(row) * a.chunks;
   RowState &st = a.rows[row];
-  put(&parts[chunk].n[t], s.n[t]), put(&parts[chunk].m[t], s.m[t]);
+#pragma unroll
+  for (int k = 0; k < kOwn; ++k) {
+    const int at = k * kThreads + t;
+    put(&parts[chunk].n[at], s.n[at]), put(&parts[chunk].m[at], s.m[at]);
+  }
   if (r.limit > 0) left = sum_of(s, left);
   if (t == 0) put(&parts[chunk].left, left);
   if (!last_here(s, &st.arrived[0], a.chunks, 0)) return;
 
-  uint32_t n = 0, all_n;
-  uint64_t m = 0, all_m;
+  uint32_t own_n[kOwn] = {}, n = 0, all_n;  // ranges kOwn t, ..
+  uint64_t own_m[kOwn] = {}, m = 0, all_m;
 #pragma unroll 4
-  for (int k = 0; k < a.chunks; ++k) n += get(&parts[k].n[t]), m += get(&parts[k].m[t]);
+  for (int k = 0; k < a.chunks; ++k)
+#pragma unroll
+    for (int b = 0; b < kOwn; ++b) own_n[b] += get(&parts[k].n[kOwn * t + b]), own_m[b] += get(&parts[k].m[kOwn * t + b]);
   left = 0;
   if (r.limit > 0 && t < a.chunks) left = get(&parts[t].left);  // (a row has at most 64)
   if (r.limit > 0) left = sum_of(s, left);
-  const uint32_t own_n = n;
-  const uint64_t own_m = m;
+#pragma unroll
+  for (int b = 0; b < kOwn; ++b) n += own_n[b], m += own_m[b];
   scan(s, n, m, all_n, all_m);
   if (r.limit == 0) left = all_m;
-  st.n[t] = n, st.m[t] = m;
-  s.n[t] = n, s.m[t] = m;
+  Range range[kOwn];
+#pragma unroll
+  for (int b = 0; b < kOwn; ++b) {
+    range[b] = {n, n + own_n[b], m, m + own_m[b]};
+    st.n[kOwn * t + b] = n, st.m[kOwn * t + b] = m;
+    s.m[kOwn * t + b] = m;
+    n += own_n[b], m += own_m[b];
+  }
   if (t == 0) {
-    st.n[kBins] = s.n[kBins] = all_n, st.m[kBins] = s.m[kBins] = all_m;
+    st.n[kBins] = all_n, st.m[kBins] = s.m[kBins] = all_m;
     st.left = left;
   }
   // The last range whose start each selection reaches, for the least and the most that
@@ -691,7 +715,9 @@ template <int TYPE> __global__ __launch_bounds__(kThreads) void sample_mass_kern
       for (int k = 0; k < 2; ++k)
       {
         const Goal goal = goal_of(r, kind, k ? hi_total : lo_total);
-        if (goal.reaches(n, m) && (t == kThreads - 1 || !goal.reaches(n + own_n, m + own_m))) s.bins[k] = t;
+#pragma unroll
+        for (int b = 0; b < kOwn; ++b)
+          if (range[b].is_last(goal, kOwn * t + b)) s.bins[k] = kOwn * t + b;
       }
       __syncthreads();
       lo = s.bins[0], hi = s.bins[1];
@@ -754,7 +780,12 @@ template <int TYPE> __global__ __launch_bounds__(kThreads) void sample_pick_kern
     return;
   }
   const int per = (a.vocab + kThreads - 1) / kThreads;  // indexes of a part, at most kFew
-  const Range own_range{st.n[t], st.n[t + 1], st.m[t], st.m[t + 1]};
+  Range own_range[kOwn];
+#pragma unroll
+  for (int b = 0; b < kOwn; ++b) {
+    const int at = kOwn * t + b;
+    own_range[b] = {st.n[at], st.n[at + 1], st.m[at], st.m[at + 1]};
+  }
   const Element own_element = t < static_cast<int>(min(listed, static_cast<uint32_t>(kList))) ? get(list + t) : Element{0.f, 0};
   const uint64_t left = st.left;
   uint64_t total = st.m[kBins];
