@@ -656,6 +656,13 @@ Plan outer_plan(int64_t n_tokens, int64_t k, int qtype) {
   return p;
 }
 
+// At most, in elements, and growing with both sizes: a plan of more than 4 groups has at most 1024 workgroups.
+int64_t most_partial(int64_t n_tokens, int64_t k) {
+  if (n_tokens == 1) return 0;
+  const int64_t peers = outer_plan(n_tokens, k, 0).peers;
+  return n_tokens * std::max(4 * k, std::min(16 * k, 1024 * 16 * peers));
+}
+
 // The rings and the activations, or what take_short or the partial sums use instead.
 template <class R, int WAVES> size_t lds_bytes(const Plan &p, int64_t n_tokens, bool short_rows) {
   return static_cast<size_t>(Lds<R, WAVES>::kRings) + n_tokens * kQuadOps * (short_rows ? WAVES : R::kStages * p.parts);
@@ -682,7 +689,7 @@ template <int QT, int MT, int XC, int WAVES> hipError_t run_outer(const MoeArgs 
 int64_t moe_workspace_bytes(int64_t n_tokens, int64_t k, int64_t n_ff, int64_t n_experts, int64_t n_used) {
   const int64_t most = most_active(n_tokens, n_experts, n_used);
   return round16(n_tokens * n_experts * 8) + 16 + round16(most * 4) + most * kMaxTokens * 4 + n_tokens * k * 4 +
-         most * n_tokens * n_ff * 4 + outer_plan(n_tokens, k, 0).groups * n_tokens * k * 4;
+         most * n_tokens * n_ff * 4 + most_partial(n_tokens, k) * 4;
 }
 
 hipError_t launch_moe(const MoeLayer &m, void *workspace, hipStream_t stream) {

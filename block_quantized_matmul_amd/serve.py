@@ -23,7 +23,7 @@ QMM_SAMPLE_MAX_VOCAB = 524287
 
 __all__ = ["QMM_KV4_MAX_PAGE_TOKENS", "QMM_MOE_MAX_TOKENS", "QMM_MOE_MAX_EXPERTS", "QMM_MOE_MAX_USED",
            "QMM_SAMPLE_MAX_VOCAB", "qmm_kv4_page_bytes", "qmm_kv4_append", "qmm_kv4_read", "qmm_attn_kv4",
-           "qmm_attn_kv4_workspace_bytes", "qmm_moe", "qmm_moe_workspace_bytes", "qmm_sample",
+           "qmm_attn_kv4_workspace_bytes", "qmm_attn_kv4_workspace_max_bytes", "qmm_moe", "qmm_moe_workspace_bytes", "qmm_sample",
            "qmm_sample_workspace_bytes"]
 
 _vp, _i32, _i64, _f32, _f64 = ctypes.c_void_p, ctypes.c_int, ctypes.c_int64, ctypes.c_float, ctypes.c_double
@@ -153,6 +153,13 @@ def qmm_attn_kv4_workspace_bytes(n_rows: int, n_q_heads: int, n_kv_heads: int, h
                                  page_tokens: int) -> int:
     return int(_lib().qmm_attn_kv4_workspace_bytes(int(n_rows), int(n_q_heads), int(n_kv_heads), int(head_dim),
                                                    int(table_width), int(page_tokens)))
+
+
+def qmm_attn_kv4_workspace_max_bytes(head_dim: int) -> int:
+    """What no qmm_attn_kv4 call with heads of head_dim (64 or 128) needs more than."""
+    if head_dim not in (64, 128):
+        raise ValueError("head_dim must be 64 or 128")
+    return 2048 * (1024 // head_dim) * (head_dim + 4) * 4 + 16 * 1024
 
 
 def qmm_attn_kv4(Q, cache, page_tokens, n_kv_heads, tables, lengths, scale=None, O=None, workspace=None, stream=None):

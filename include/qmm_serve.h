@@ -139,9 +139,18 @@ int qmm_attn_kv4(int type, const qmm_heads *Q, const qmm_heads *O, int64_t n_row
                  void *workspace, int64_t workspace_bytes, void *stream);
 
 /* qmm_attn_kv4_workspace_bytes - the workspace qmm_attn_kv4 needs for these
- * sizes, or QMM_ERR_SHAPE. The same on every device. */
+ * sizes, or QMM_ERR_SHAPE. The same on every device. More rows may need less
+ * (they are split less): a workspace for calls of several sizes is as large as
+ * qmm_attn_kv4_workspace_max_bytes says. */
 int64_t qmm_attn_kv4_workspace_bytes(int64_t n_rows, int64_t n_q_heads, int64_t n_kv_heads, int64_t head_dim,
                                      int64_t table_width, int64_t page_tokens);
+
+/* qmm_attn_kv4_workspace_max_bytes - what no call with heads of head_dim needs
+ * more than, 9 MB: rows are split where they take fewer than 1024 workgroups, into
+ * at most 2048, which have at most 1024 / head_dim heads of head_dim + 4 numbers. */
+static inline int64_t qmm_attn_kv4_workspace_max_bytes(int64_t head_dim) {
+  return 2048 * (1024 / head_dim) * (head_dim + 4) * 4 + 16 * 1024;
+}
 
 /*
  * qmm_moe - a mixture-of-experts layer of up to QMM_MOE_MAX_TOKENS tokens:
@@ -213,7 +222,7 @@ int64_t qmm_moe_workspace_bytes(int64_t n_tokens, int64_t k, int64_t n_ff, int64
  * Numerics: weights in 64 bits, sums of them exact to 2^-44 of the largest; a
  * token whose probability is below 2^-45 of the largest is not chosen.
  *   workspace    at least qmm_sample_workspace_bytes(n_rows, vocab) bytes, 16-byte
- *                aligned
+ *                aligned; overwritten; two calls in flight must not share one
  * n_rows < 2^22; n_rows == 0 is a no-op.
  */
 int qmm_sample(const void *logits, int type, int64_t n_rows, int64_t vocab, int64_t row_stride, const float *u,
