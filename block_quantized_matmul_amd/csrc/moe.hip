@@ -154,11 +154,11 @@ template <int QT> constexpr bool has_min() { return QTraits<QT>::has_min || QTra
 // pieces of the row, which begin before the tail where its length is no multiple
 // of 16, so that nothing behind the row is read. (Rows shorter than that go dword
 // by dword, take_short.)
-template <int QT, int G, int STAGES> struct Rows {
+template <int QT, int G> struct Rows {
   static constexpr int kPieces = 16 * G * Quad<QT>::chunks;
   static constexpr int kCopies = (kPieces + 63) / 64;
   static constexpr int kStage = kPieces * 16;   // bytes of LDS
-  static constexpr int kStages = STAGES;        // quads on their way, the one in use among them
+  static constexpr int kStages = 2;             // quads in use or on their way
   int64_t off[kCopies];  // from the expert's matrix (group 0's), of this lane's pieces in quad 0
   bool on_last;          // whether this lane has a piece in the last copy
   int tail_at, tail_pieces, tail_skip;  // of a row: its tail's first piece's byte, pieces, and bytes before the tail
@@ -191,10 +191,30 @@ template <int QT, int G, int STAGES> struct Rows {
   }
 };
 
+// The operands of some of the tokens: pieces of 16 bytes, of every lane group of
+// every block two of each token, in memory among those of all tokens (`stride`
+// columns), or by themselves.
+struct Ops {
+  const _Float16 *p;
+  uint32_t columns, stride;
+  uint64_t tokens;   // in order, 4 bits each
+  uint32_t inverse;  // 2^16 / columns, rounded up: exact quotients of pieces of a quad, of which there are at most 1024
+  __device__ __forceinline__ Ops(const _Float16 *ops, int count, uint64_t which, int of_tokens)
+      : p(ops), columns(2 * count), stride(2 * of_tokens), tokens(which), inverse((65536 + 2 * count - 1) / (2 * count)) {}
+  __device__ __forceinline__ Ops(const _Float16 *ops, int count) : p(ops), columns(2 * count), stride(2 * count), tokens(0), inverse(0) {}
+  // Where piece i of quad q is.
+  __device__ __forceinline__ const uint8_t *piece(int q, uint32_t i) const {
+    const uint8_t *quad = reinterpret_cast<const uint8_t *>(p) + static_cast<int64_t>(q) * (32 * 16) * stride;
+    if (stride == columns) return quad + 16 * i;
+    const uint32_t group = i * inverse >> 16, column = i - group * columns;
+    return quad + 16 * (group * stride + 2 * (static_cast<uint32_t>(tokens >> (2 * (column & ~1u))) & 15u) + (column & 1u));
+  }
+};
+
 // A quad in LDS times its activations (there too), into the rows' sums. `valid`: blocks that exist.
-template <int QT, int MT, int G>
+template <int QT, int MT, int G, int MTS>
 __device__ __forceinline__ void take_quad(const uint8_t *stage, const uint8_t *ops, int columns, int valid,
-                                          float4_t acc[G][MT], int lane) {
+                                          float4_t acc[G][MTS], int lane) {
   const int g = lane >> 4;
   const uint8_t *rb = stage + (lane & 15) * Quad<QT>::row;
   const uint8_t *xp[MT];  // columns that no token has repeat the last, for nothing
@@ -229,12 +249,21 @@ __device__ __forceinline__ void take_quad(const uint8_t *stage, const uint8_t *o
   }
 }
 
+// With one column tile where one is enough.
+template <int QT, int MT, int G>
+__device__ __forceinline__ void take_some(const uint8_t *stage, const uint8_t *ops, int columns, int valid,
+                                          float4_t acc[G][MT], int lane) {
+  if (MT == 1 || columns <= 16)
+    take_quad<QT, 1, G>(stage, ops, columns, valid, acc, lane);
+  else
+    take_quad<QT, MT, G>(stage, ops, columns, valid, acc, lane);
+}
+
 // Rows of fewer than 8 blocks, copied dword by dword so that nothing behind a
 // row's last dword is read, and their activations. The wavefront has `ops` for itself.
 template <int QT, int MT, int G>
 __device__ __forceinline__ void take_short(const uint8_t *w, int64_t nb1, int row0, int n_rows, int64_t apart, int blocks,
-                                           const _Float16 *x, int columns, uint8_t *stage, uint8_t *ops,
-                                           float4_t acc[G][MT], int lane) {
+                                           const Ops &x, uint8_t *stage, uint8_t *ops, float4_t acc[G][MT], int lane) {
   const int dwords = (blocks * Block<QT>::bytes + 3) / 4;
   wait_reads();  // of what lay in this place before
   for (int i = lane; i < 16 * G * dwords; i += 64) {
@@ -243,11 +272,17 @@ __device__ __forceinline__ void take_short(const uint8_t *w, int64_t nb1, int ro
     const uint8_t *from = w + row * nb1 + (r >= 16 ? apart : 0) + 4 * at;
     *reinterpret_cast<uint32_t *>(stage + r * Quad<QT>::row + 4 * at) = *reinterpret_cast<const uint32_t *>(from);
   }
-  for (int i = lane; i < blocks * 4 * columns; i += 64)
-    *reinterpret_cast<half8_t *>(ops + 16 * i) = *reinterpret_cast<const half8_t *>(x + 8 * i);
+  for (int i = lane; i < blocks * 4 * static_cast<int>(x.columns); i += 64)
+    *reinterpret_cast<half8_t *>(ops + 16 * i) = *reinterpret_cast<const half8_t *>(x.piece(0, i));
   wait_reads();
-  take_quad<QT, MT, G>(stage, ops, columns, blocks, acc, lane);
+  take_some<QT, MT, G>(stage, ops, x.columns, blocks, acc, lane);
 }
+
+struct Stage {
+  const uint8_t *w;
+  int q, index;  // quad, and index of the expert
+  Ops ops;
+};
 
 // All wavefronts are here; what each has waited for itself is there for all.
 __device__ __forceinline__ void meet() {
@@ -269,50 +304,42 @@ template <class R, int WAVES> struct Lds {
   }
 };
 
-// Stages 0 .. n - 1 (at most `most`, the same for the workgroup) through LDS: at(i) gives
-// stage i's matrix, quad and operands. The wavefronts of a part, `peer` of `peers`,
-// have different rows of the same stages and copy its activations together, XC pieces
-// of 1 KiB each (where there are fewer, the last several times).
-template <int QT, int MT, int G, int XC, class R, class L, class At>
-__device__ __forceinline__ void stream(const R &rows, const At &at, int n, int most, int blocks, const L &lds, int part,
-                                       int peer, int peers, bool live, float4_t acc[G][MT], int wave, int lane) {
-  const int whole = blocks / 8, columns = 2 * lds.tokens;
-  auto copy = [&](int i, int slot) {
-    const auto s = at(i);
+// n stages (at most `most`, the same for the workgroup) through LDS, from `first`
+// on: a stage is a quad of an expert's matrix, and advance(s) goes to the next. The wavefronts of a part, `peer` of
+// `peers`, have different rows of the same stages and copy its activations together.
+// Behind an expert's last stage comes flush(its index).
+template <int QT, int MT, int G, class R, class L, class Advance, class Flush>
+__device__ __forceinline__ void stream(const R &rows, const Stage &first, const Advance &advance, const Flush &flush, int n,
+                                       int most, int blocks, const L &lds, int part, int peer, int peers, bool live,
+                                       float4_t acc[G][MT], int wave, int lane) {
+  const int whole = blocks / 8;
+  auto copy = [&](const Stage &s, int slot) {
     rows.copy(s.w, s.q, s.q == whole, lds_addr(lds.weights(wave, slot)), lane);
-    const uint8_t *ops = reinterpret_cast<const uint8_t *>(s.ops) + static_cast<int64_t>(s.q) * lds.tokens * kQuadOps;
-    const int bytes = min(8, blocks - 8 * s.q) * 64 * columns;  // of a tail there are fewer
-#pragma unroll
-    for (int x = 0; x < XC; ++x) {
-      const int piece = min(peer + x * peers, (bytes - 1) / 1024);
-      const uint8_t *from = ops + min(piece * 1024 + 16 * lane, bytes - 16);
-      asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, off" ::"v"(from),
-                   "s"(lds_addr(lds.ops(part, slot)) + piece * 1024)
+    const int pieces = min(8, blocks - 8 * s.q) * 4 * s.ops.columns;  // (of a tail there are fewer)
+    for (int k = 64 * peer; k < pieces; k += 64 * peers)
+      asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, off" ::"v"(
+                       s.ops.piece(s.q, min(k + lane, pieces - 1))),
+                   "s"(lds_addr(lds.ops(part, slot)) + 16 * k)
                    : "memory", "m0");
-    }
   };
-#pragma unroll
-  for (int i = 0; i < R::kStages - 1; ++i)
-    if (i < n) copy(i, i);
-  int slot = 0, ahead = R::kStages - 1;
+  Stage next = first;
+  if (n > 0) copy(next, 0);
   for (int i = 0; i < most; ++i) {
-    if (i + R::kStages - 1 <= n)  // the copies of the stages behind this one may be on their way
-      wait_loads<(R::kStages - 2) * (R::kCopies + XC)>();
-    else
-      wait_loads<0>();
+    wait_loads<0>();
     meet();
-    if (i + R::kStages - 1 < n) copy(i + R::kStages - 1, ahead);
+    const Stage s = next;
+    if (i + 1 < n) {
+      advance(next);
+      copy(next, (i + 1) & 1);
+    }
     if (i < n && live) {
-      const int q = at(i).q;
-      const uint8_t *ops = lds.ops(part, slot);
-      if (q < whole)
-        take_quad<QT, MT, G>(lds.weights(wave, slot), ops, columns, 8, acc, lane);
-      else
-        take_quad<QT, MT, G>(lds.weights(wave, slot) + rows.tail_skip, ops, columns, blocks % 8, acc, lane);
+      const uint8_t *ops = lds.ops(part, i & 1);
+      const bool tail = s.q == whole;
+      take_some<QT, MT, G>(lds.weights(wave, i & 1) + (tail ? rows.tail_skip : 0), ops, s.ops.columns, tail ? blocks % 8 : 8,
+                           acc, lane);
+      if (i + 1 == n || s.q == (blocks + 7) / 8 - 1) flush(s.index);
     }
     wait_reads();
-    slot = slot + 1 == R::kStages ? 0 : slot + 1;
-    ahead = ahead + 1 == R::kStages ? 0 : ahead + 1;
   }
 }
 
@@ -341,6 +368,10 @@ struct Table {  // what the choice leaves for the products
   int n_active;
   int pad[3];
 };
+struct Active {  // an expert that was chosen
+  int expert, count;  // by so many tokens,
+  uint64_t tokens;    // these, in order, 4 bits each
+};
 struct MoeArgs {
   const void *x;
   const float *router;
@@ -353,13 +384,14 @@ struct MoeArgs {
   // workspace
   double *logits;     // [n_tokens][n_experts]
   Table *table;
-  int32_t *active;    // [most active] experts, in order
-  float *share;       // [most active][kMaxTokens] routing weights
-  _Float16 *x_ops, *h_ops;  // operands of x, and of h expert by expert
+  Active *active;     // [most active], in order
+  float *share;       // [most active][kMaxTokens] routing weights of its tokens
+  _Float16 *x_ops, *h_ops;  // operands of x, and of h expert by expert, of its tokens alone
   int64_t h_step;     // halves of one expert's h
   int n_tokens, k, n_ff, n_experts, n_used, renormalise, x_f16, type_in, type_out;
   int logit_groups;   // workgroups of the first launch that compute logits; the others prepare operands
   int parts_in, parts_out;  // wavefronts of a workgroup that share rows
+  int sums_out;             // where the tokens' sums lie in LDS
   int groups_out;           // workgroups that share rows (their sums go to `partial`)
   float *partial;           // [groups_out][n_tokens][k]
 };
@@ -432,12 +464,13 @@ __global__ __launch_bounds__(kRouteThreads) void moe_route_kernel(MoeArgs a) {
   double *l = reinterpret_cast<double *>(smem);                    // [n][experts], NaN as -infinity
   float *w = reinterpret_cast<float *>(l + items);                 // [n][n_used]
   int *id = reinterpret_cast<int *>(w + n * a.n_used);             // [n][n_used]
-  int *place = id + n * a.n_used;                                  // [experts]
+  int *place = id + n * a.n_used;                                  // [experts + 1]
+  uint32_t *by = reinterpret_cast<uint32_t *>(place + experts + 1);  // [experts] a bit for each token
   for (int i = threadIdx.x; i < items; i += kRouteThreads) {
     const double v = a.logits[i];
     l[i] = v != v ? -__builtin_inf() : v;
   }
-  for (int i = threadIdx.x; i < experts; i += kRouteThreads) place[i] = 0;
+  for (int i = threadIdx.x; i < experts; i += kRouteThreads) by[i] = 0;
   __syncthreads();
   for (int i = threadIdx.x; i < items; i += kRouteThreads) {
     const int t = i / experts, e = i % experts;
@@ -446,7 +479,7 @@ __global__ __launch_bounds__(kRouteThreads) void moe_route_kernel(MoeArgs a) {
     for (int k = 0; k < experts; ++k) rank += row[k] > mine || (row[k] == mine && k < e);
     if (rank < a.n_used) {
       id[t * a.n_used + rank] = e;
-      place[e] = 1;  // (any of several writes the same)
+      atomicOr(&by[e], 1u << t);
     }
   }
   __syncthreads();
@@ -477,33 +510,29 @@ __global__ __launch_bounds__(kRouteThreads) void moe_route_kernel(MoeArgs a) {
     int before = 0;
     for (int e0 = 0; e0 < experts; e0 += 64) {
       const int e = e0 + lane;
-      const bool on = e < experts && place[e];
+      const uint32_t tokens = e < experts ? by[e] : 0;
+      const bool on = tokens != 0;
       const uint64_t mask = __ballot(on);
       if (on) {
         const int at = before + __popcll(mask & ((uint64_t{1} << lane) - 1));
         place[e] = at;
-        a.active[at] = e;
+        uint64_t list = 0;
+        int count = 0;
+        for (int t = 0; t < n; ++t)
+          if (tokens >> t & 1) list |= static_cast<uint64_t>(t) << (4 * count++);
+        a.active[at] = Active{e, count, list};
       }
       before += __popcll(mask);
     }
     if (lane == 0) a.table->n_active = before;
-    id[n * a.n_used + experts] = before;  // (behind place)
   }
   __syncthreads();
-  const int n_active = id[n * a.n_used + experts];
-  for (int i = threadIdx.x; i < n_active * kMaxTokens; i += kRouteThreads) a.share[i] = 0.f;
-  __syncthreads();
   for (int i = threadIdx.x; i < n * a.n_used; i += kRouteThreads) {
-    // a zero share stands for "not chosen"; a chosen weight that underflowed to it is as good as that
-    a.share[place[id[i]] * kMaxTokens + i / a.n_used] = w[i];
+    const int t = i / a.n_used, e = id[i];
+    a.share[place[e] * kMaxTokens + __popc(by[e] & ((1u << t) - 1))] = w[i];
   }
 }
 
-struct Stage {
-  const uint8_t *w;
-  int q;
-  const _Float16 *ops;
-};
 
 // Columns 4 g + e of a tile: hi and lo of tokens 8 t + 2 g and 8 t + 2 g + 1.
 __device__ __forceinline__ float token_value(const float4_t &acc, int which) {
@@ -511,8 +540,8 @@ __device__ __forceinline__ float token_value(const float4_t &acc, int which) {
 }
 
 // gate, up and their product: blockIdx.y is the active expert, a unit 16 rows of both.
-template <int QT> using InnerRows = Rows<QT, 2, 2>;
-template <int QT, int MT, int XC> __global__ __launch_bounds__(64 * kInnerWaves, MT == 1 ? 4 : 3) void moe_inner_kernel(MoeArgs a) {
+template <int QT> using InnerRows = Rows<QT, 2>;
+template <int QT, int MT> __global__ __launch_bounds__(64 * kInnerWaves, MT == 1 ? 4 : 3) void moe_inner_kernel(MoeArgs a) {
   typedef InnerRows<QT> R;
   typedef Lds<R, kInnerWaves> L;
   extern __shared__ __align__(1024) uint8_t smem[];
@@ -523,17 +552,19 @@ template <int QT, int MT, int XC> __global__ __launch_bounds__(64 * kInnerWaves,
   const int row0 = 16 * (blockIdx.x * peers + peer);
   const bool live = row0 < a.n_ff;  // (else it copies for the others)
   const int blocks = a.k / 32;
-  const uint8_t *w = a.gate + static_cast<int64_t>(__builtin_amdgcn_readfirstlane(a.active[blockIdx.y])) * a.nb2_in;
+  const Active mine = a.active[blockIdx.y];
+  const uint8_t *w = a.gate + static_cast<int64_t>(mine.expert) * a.nb2_in;
+  const Ops x(a.x_ops, mine.count, mine.tokens, a.n_tokens);
   const L lds{smem, parts, a.n_tokens};
   float4_t acc[2][MT] = {};
   if (blocks >= 8) {
     const int stages = (blocks + 7) / 8;
     const int lo = stages * part / parts, hi = stages * (part + 1) / parts;
     const R rows(a.nb1_in, row0, a.n_ff, blocks, a.up_apart, lane);
-    stream<QT, MT, 2, XC>(rows, [&](int i) { return Stage{w, lo + i, a.x_ops}; }, hi - lo, (stages + parts - 1) / parts,
-                          blocks, lds, part, peer, peers, live, acc, wave, lane);
+    stream<QT, MT, 2>(rows, Stage{w, lo, 0, x}, [](Stage &s) { ++s.q; }, [](int) {}, hi - lo,
+                      (stages + parts - 1) / parts, blocks, lds, part, peer, peers, live, acc, wave, lane);
   } else if (live && part == 0) {
-    take_short<QT, MT, 2>(w, a.nb1_in, row0, a.n_ff, a.up_apart, blocks, a.x_ops, 2 * a.n_tokens, lds.weights(wave, 0),
+    take_short<QT, MT, 2>(w, a.nb1_in, row0, a.n_ff, a.up_apart, blocks, x, lds.weights(wave, 0),
                           smem + L::kRings + wave * a.n_tokens * kQuadOps, acc, lane);
   }
   add_parts<MT, 2>(acc, smem, parts, wave, lane);
@@ -542,13 +573,13 @@ template <int QT, int MT, int XC> __global__ __launch_bounds__(64 * kInnerWaves,
   if (row >= a.n_ff) return;
   const Spot s = spot_of(a.type_out, row % 32);
   _Float16 *h = a.h_ops + blockIdx.y * a.h_step;
-  const int columns = 2 * a.n_tokens;
+  const int columns = 2 * mine.count;
 #pragma unroll
   for (int t = 0; t < MT; ++t)
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
-      const int token = 8 * t + 2 * g + k;
-      if (token >= a.n_tokens) continue;
+      const int token = 8 * t + 2 * g + k;  // among the expert's
+      if (token >= mine.count) continue;
       const float share = a.share[blockIdx.y * kMaxTokens + token];
       const float gate = token_value(acc[0][t], k), up = token_value(acc[1][t], k);
       const float v = share == 0.f ? 0.f : gate / (1.f + expf(-gate)) * up * share;
@@ -560,13 +591,14 @@ template <int QT, int MT, int XC> __global__ __launch_bounds__(64 * kInnerWaves,
 }
 
 // down: 16 rows over all active experts' quads, split evenly between the parts of
-// the workgroups that share rows.
-template <int QT> using OuterRows = Rows<QT, 1, 2>;
-template <int QT, int MT, int XC, int WAVES> __global__ __launch_bounds__(64 * WAVES, 4) void moe_outer_kernel(MoeArgs a) {
+// the workgroups that share rows. Columns are an expert's tokens, so its sums are
+// added to the tokens' own (in LDS, each wavefront's) behind its last quad.
+template <int QT> using OuterRows = Rows<QT, 1>;
+template <int QT, int MT, int WAVES> __global__ __launch_bounds__(64 * WAVES, 4) void moe_outer_kernel(MoeArgs a) {
   typedef OuterRows<QT> R;
   typedef Lds<R, WAVES> L;
   extern __shared__ __align__(1024) uint8_t smem[];
-  const int lane = threadIdx.x & 63;
+  const int lane = threadIdx.x & 63, g = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int parts = a.parts_out, part = wave % parts, peer = wave / parts, peers = WAVES / parts;
   const int group = blockIdx.x % a.groups_out;
@@ -575,38 +607,55 @@ template <int QT, int MT, int XC, int WAVES> __global__ __launch_bounds__(64 * W
   const int n_active = __builtin_amdgcn_readfirstlane(a.table->n_active);
   const int blocks = a.n_ff / 32;
   const L lds{smem, parts, a.n_tokens};
+  float *sums = reinterpret_cast<float *>(smem + a.sums_out) + wave * a.n_tokens * 16;  // [n_tokens][16 rows]
+  for (int i = lane; i < 16 * a.n_tokens; i += 64) sums[i] = 0.f;
   float4_t acc[1][MT] = {};
-  auto expert = [&](int i) {
-    return a.down + static_cast<int64_t>(__builtin_amdgcn_readfirstlane(a.active[i])) * a.nb2_out;
+  auto flush = [&](int index) {
+    const Active &e = a.active[index];
+#pragma unroll
+    for (int t = 0; t < MT; ++t) {
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        const int i = 8 * t + 2 * g + k;
+        if (i < e.count) sums[static_cast<int>(e.tokens >> (4 * i) & 15) * 16 + (lane & 15)] += token_value(acc[0][t], k);
+      }
+      acc[0][t] = float4_t{};
+    }
   };
+  auto matrix = [&](int index) { return a.down + static_cast<int64_t>(a.active[index].expert) * a.nb2_out; };
+  auto operands = [&](int index) { return Ops(a.h_ops + index * a.h_step, a.active[index].count); };
   const int all_parts = parts * a.groups_out, my_part = group * parts + part;
   if (blocks >= 8) {
     const int stages = (blocks + 7) / 8;
     const int64_t all = static_cast<int64_t>(n_active) * stages;
-    const int lo = static_cast<int>(all * my_part / all_parts), hi = static_cast<int>(all * (my_part + 1) / all_parts);
+    const int lo = __builtin_amdgcn_readfirstlane(static_cast<int>(all * my_part / all_parts));
+    const int hi = __builtin_amdgcn_readfirstlane(static_cast<int>(all * (my_part + 1) / all_parts));
     const R rows(a.nb1_out, row0, a.k, blocks, 0, lane);
-    auto at = [&](int i) {
-      const int e = (lo + i) / stages;
-      return Stage{expert(e), lo + i - e * stages, a.h_ops + e * a.h_step};
+    const int e0 = min(__builtin_amdgcn_readfirstlane(lo / stages), n_active - 1);
+    auto advance = [&](Stage &s) {
+      if (++s.q < stages) return;
+      s.q = 0, ++s.index;
+      s.w = matrix(s.index), s.ops = operands(s.index);
     };
-    stream<QT, MT, 1, XC>(rows, at, hi - lo, static_cast<int>((all + all_parts - 1) / all_parts), blocks, lds, part, peer,
-                          peers, live, acc, wave, lane);
+    stream<QT, MT, 1>(rows, Stage{matrix(e0), lo - e0 * stages, e0, operands(e0)}, advance, flush, hi - lo, static_cast<int>((all + all_parts - 1) / all_parts), blocks, lds, part, peer,
+                      peers, live, acc, wave, lane);
   } else if (live) {
-    for (int e = my_part; e < n_active; e += all_parts)
-      take_short<QT, MT, 1>(expert(e), a.nb1_out, row0, a.k, 0, blocks, a.h_ops + e * a.h_step, 2 * a.n_tokens,
-                            lds.weights(wave, 0), smem + L::kRings + wave * a.n_tokens * kQuadOps, acc, lane);
-  }
-  add_parts<MT, 1>(acc, smem, parts, wave, lane);
-  const int row = row0 + (lane & 15), g = lane >> 4;
-  if (part != 0 || row >= a.k) return;
-  float *y = a.groups_out > 1 ? a.partial + static_cast<int64_t>(group) * a.n_tokens * a.k : a.y;
-#pragma unroll
-  for (int t = 0; t < MT; ++t)
-#pragma unroll
-    for (int k = 0; k < 2; ++k) {
-      const int token = 8 * t + 2 * g + k;
-      if (token < a.n_tokens) y[static_cast<int64_t>(token) * a.k + row] = token_value(acc[0][t], k);
+    for (int e = my_part; e < n_active; e += all_parts) {
+      take_short<QT, MT, 1>(matrix(e), a.nb1_out, row0, a.k, 0, blocks, operands(e), lds.weights(wave, 0),
+                            smem + L::kRings + wave * a.n_tokens * kQuadOps, acc, lane);
+      flush(e);
     }
+  }
+  __syncthreads();
+  if (part != 0) return;
+  float *y = a.groups_out > 1 ? a.partial + static_cast<int64_t>(group) * a.n_tokens * a.k : a.y;
+  for (int i = lane; i < 16 * a.n_tokens; i += 64) {
+    const int row = row0 + i % 16;
+    if (row >= a.k) continue;
+    float sum = sums[i];
+    for (int s = 1; s < parts; ++s) sum += sums[s * a.n_tokens * 16 + i];
+    y[static_cast<int64_t>(i / 16) * a.k + row] = sum;
+  }
 }
 
 // y: the sums of the workgroups that share rows, in order.
@@ -664,21 +713,22 @@ int64_t most_partial(int64_t n_tokens, int64_t k) {
 }
 
 // The rings and the activations, or what take_short or the partial sums use instead.
-template <class R, int WAVES> size_t lds_bytes(const Plan &p, int64_t n_tokens, bool short_rows) {
-  return static_cast<size_t>(Lds<R, WAVES>::kRings) + n_tokens * kQuadOps * (short_rows ? WAVES : R::kStages * p.parts);
+template <class R, int WAVES> int lds_bytes(const Plan &p, int64_t n_tokens, bool short_rows) {
+  return Lds<R, WAVES>::kRings + static_cast<int>(n_tokens) * kQuadOps * (short_rows ? WAVES : R::kStages * p.parts);
 }
 
-template <int QT, int MT, int XC> hipError_t run_inner(const MoeArgs &a, int64_t most, hipStream_t stream) {
+template <int QT, int MT> hipError_t run_inner(const MoeArgs &a, int64_t most, hipStream_t stream) {
   const Plan p = inner_plan(a.n_tokens, a.n_ff, most);
   const dim3 grid(static_cast<unsigned>(((a.n_ff + 15) / 16 + p.peers - 1) / p.peers), static_cast<unsigned>(most));
-  return launch(moe_inner_kernel<QT, MT, XC>, grid, dim3(64 * kInnerWaves),
+  return launch(moe_inner_kernel<QT, MT>, grid, dim3(64 * kInnerWaves),
                 lds_bytes<InnerRows<QT>, kInnerWaves>(p, a.n_tokens, a.k < 256), stream, a);
 }
-template <int QT, int MT, int XC, int WAVES> hipError_t run_outer(const MoeArgs &a, hipStream_t stream) {
+template <int QT, int MT, int WAVES> hipError_t run_outer(MoeArgs a, hipStream_t stream) {
   const Plan p = outer_plan(a.n_tokens, a.k, QT);
   const dim3 grid(static_cast<unsigned>(((a.k + 15) / 16 + p.peers - 1) / p.peers * p.groups));
-  const hipError_t e = launch(moe_outer_kernel<QT, MT, XC, WAVES>, grid, dim3(64 * WAVES),
-                              lds_bytes<OuterRows<QT>, WAVES>(p, a.n_tokens, a.n_ff < 256), stream, a);
+  a.sums_out = lds_bytes<OuterRows<QT>, WAVES>(p, a.n_tokens, a.n_ff < 256);
+  const hipError_t e = launch(moe_outer_kernel<QT, MT, WAVES>, grid, dim3(64 * WAVES),
+                              static_cast<size_t>(a.sums_out + WAVES * a.n_tokens * 64), stream, a);
   if (e != hipSuccess || p.groups == 1) return e;
   const int64_t n = static_cast<int64_t>(a.n_tokens) * a.k;
   return launch(moe_add_kernel, dim3(static_cast<unsigned>((n + 255) / 256)), dim3(256), 0, stream, a.partial, p.groups, n, a.y);
@@ -688,7 +738,7 @@ template <int QT, int MT, int XC, int WAVES> hipError_t run_outer(const MoeArgs 
 
 int64_t moe_workspace_bytes(int64_t n_tokens, int64_t k, int64_t n_ff, int64_t n_experts, int64_t n_used) {
   const int64_t most = most_active(n_tokens, n_experts, n_used);
-  return round16(n_tokens * n_experts * 8) + 16 + round16(most * 4) + most * kMaxTokens * 4 + n_tokens * k * 4 +
+  return round16(n_tokens * n_experts * 8) + 16 + most * static_cast<int64_t>(sizeof(Active)) + most * kMaxTokens * 4 + n_tokens * k * 4 +
          most * n_tokens * n_ff * 4 + most_partial(n_tokens, k) * 4;
 }
 
@@ -703,7 +753,7 @@ hipError_t launch_moe(const MoeLayer &m, void *workspace, hipStream_t stream) {
   uint8_t *p = static_cast<uint8_t *>(workspace);
   a.logits = reinterpret_cast<double *>(p), p += round16(m.n_tokens * m.n_experts * 8);
   a.table = reinterpret_cast<Table *>(p), p += 16;
-  a.active = reinterpret_cast<int32_t *>(p), p += round16(most * 4);
+  a.active = reinterpret_cast<Active *>(p), p += most * sizeof(Active);
   a.share = reinterpret_cast<float *>(p), p += most * kMaxTokens * 4;
   a.x_ops = reinterpret_cast<_Float16 *>(p), p += m.n_tokens * m.k * 4;
   a.h_ops = reinterpret_cast<_Float16 *>(p);
@@ -719,22 +769,19 @@ hipError_t launch_moe(const MoeLayer &m, void *workspace, hipStream_t stream) {
   const unsigned first = static_cast<unsigned>(a.logit_groups + (m.k * m.n_tokens + kLogitThreads - 1) / kLogitThreads);
   hipError_t e = launch(moe_prepare_kernel, dim3(first), dim3(kLogitThreads), 0, stream, a);
   if (e != hipSuccess) return e;
-  const size_t lds = static_cast<size_t>(m.n_tokens * (m.n_experts + m.n_used) * 8 + (m.n_experts + 1) * 4);
+  const size_t lds = static_cast<size_t>(m.n_tokens * (m.n_experts + m.n_used) * 8 + (2 * m.n_experts + 1) * 4);
   e = launch(moe_route_kernel, dim3(1), dim3(kRouteThreads), lds, stream, a);
   if (e != hipSuccess) return e;
-  const int xc = pieces_for(m.n_tokens);
   e = by_qtype_k(m.type_in, [&](auto q) {
     constexpr int QT = decltype(q)::value;
-    return xc == 1 ? run_inner<QT, 1, 1>(a, most, stream)
-                   : xc == 2 ? run_inner<QT, 1, 2>(a, most, stream) : run_inner<QT, 2, 4>(a, most, stream);
+    return m.n_tokens <= 8 ? run_inner<QT, 1>(a, most, stream) : run_inner<QT, 2>(a, most, stream);
   });
   if (e != hipSuccess) return e;
   return by_qtype_k(m.type_out, [&](auto q) {
     constexpr int QT = decltype(q)::value;
-    return m.n_tokens == 1 ? run_outer<QT, 1, 1, QT == QMM_TYPE_Q8_0 ? 8 : 16>(a, stream)
-           : xc == 1       ? run_outer<QT, 1, 1, 4>(a, stream)
-           : xc == 2       ? run_outer<QT, 1, 2, 4>(a, stream)
-                           : run_outer<QT, 2, 4, 4>(a, stream);
+    return m.n_tokens == 1  ? run_outer<QT, 1, QT == QMM_TYPE_Q8_0 ? 8 : 16>(a, stream)
+           : m.n_tokens <= 8 ? run_outer<QT, 1, 4>(a, stream)
+                             : run_outer<QT, 2, 4>(a, stream);
   });
 }
 
