@@ -39,7 +39,7 @@ namespace qmm {
 namespace {
 
 constexpr int kInnerWaves = 4;  // wavefronts of a workgroup
-constexpr int kMaxTokens = QMM_MOE_MAX_TOKENS;
+constexpr int kSetTokens = 8;  // of a set: its columns are a tile of the matrix cores
 constexpr int kRouteThreads = 1024;
 constexpr int kLogitThreads = 256;
 constexpr int kLogitTokens = 4;  // tokens of a logit workgroup
@@ -212,14 +212,12 @@ struct Ops {
 };
 
 // A quad in LDS times its activations (there too), into the rows' sums. `valid`: blocks that exist.
-template <int QT, int MT, int G, int MTS>
+template <int QT, int G>
 __device__ __forceinline__ void take_quad(const uint8_t *stage, const uint8_t *ops, int columns, int valid,
-                                          float4_t acc[G][MTS], int lane) {
+                                          float4_t acc[G], int lane) {
   const int g = lane >> 4;
   const uint8_t *rb = stage + (lane & 15) * Quad<QT>::row;
-  const uint8_t *xp[MT];  // columns that no token has repeat the last, for nothing
-#pragma unroll
-  for (int t = 0; t < MT; ++t) xp[t] = ops + 16 * (g * columns + min(16 * t + (lane & 15), columns - 1));
+  const uint8_t *xp = ops + 16 * (g * columns + min(lane & 15, columns - 1));  // the others repeat the last, for nothing
 #pragma unroll
   for (int u = 0; u < 4; ++u) {
     if (2 * u >= valid) break;
@@ -229,41 +227,28 @@ __device__ __forceinline__ void take_quad(const uint8_t *stage, const uint8_t *o
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       if (2 * u + h >= valid) break;
+      const half8_t x = *reinterpret_cast<const half8_t *>(xp + (2 * u + h) * 64 * columns);
+      float4_t start{}, sums{};
+      if constexpr (QT == QMM_TYPE_Q4_0) start = __builtin_amdgcn_mfma_f32_16x16x32_f16(x, sum_operand<QT>(), start, 0, 0, 0);
+      if constexpr (has_min<QT>()) sums = __builtin_amdgcn_mfma_f32_16x16x32_f16(x, sum_operand<QT>(), sums, 0, 0, 0);
 #pragma unroll
-      for (int t = 0; t < MT; ++t) {
-        const half8_t x = *reinterpret_cast<const half8_t *>(xp[t] + (2 * u + h) * 64 * columns);
-        float4_t start{}, sums{};
-        if constexpr (QT == QMM_TYPE_Q4_0) start = __builtin_amdgcn_mfma_f32_16x16x32_f16(x, sum_operand<QT>(), start, 0, 0, 0);
-        if constexpr (has_min<QT>()) sums = __builtin_amdgcn_mfma_f32_16x16x32_f16(x, sum_operand<QT>(), sums, 0, 0, 0);
+      for (int k = 0; k < G; ++k) {
+        const float4_t part = __builtin_amdgcn_mfma_f32_16x16x32_f16(x, op[k][h].codes, start, 0, 0, 0);
 #pragma unroll
-        for (int k = 0; k < G; ++k) {
-          const float4_t part = __builtin_amdgcn_mfma_f32_16x16x32_f16(x, op[k][h].codes, start, 0, 0, 0);
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            acc[k][t][e] = __builtin_fmaf(op[k][h].d, part[e], acc[k][t][e]);
-            if constexpr (has_min<QT>()) acc[k][t][e] = __builtin_fmaf(op[k][h].m, sums[e], acc[k][t][e]);
-          }
+        for (int e = 0; e < 4; ++e) {
+          acc[k][e] = __builtin_fmaf(op[k][h].d, part[e], acc[k][e]);
+          if constexpr (has_min<QT>()) acc[k][e] = __builtin_fmaf(op[k][h].m, sums[e], acc[k][e]);
         }
       }
     }
   }
 }
 
-// With one column tile where one is enough.
-template <int QT, int MT, int G>
-__device__ __forceinline__ void take_some(const uint8_t *stage, const uint8_t *ops, int columns, int valid,
-                                          float4_t acc[G][MT], int lane) {
-  if (MT == 1 || columns <= 16)
-    take_quad<QT, 1, G>(stage, ops, columns, valid, acc, lane);
-  else
-    take_quad<QT, MT, G>(stage, ops, columns, valid, acc, lane);
-}
-
 // Rows of fewer than 8 blocks, copied dword by dword so that nothing behind a
 // row's last dword is read, and their activations. The wavefront has `ops` for itself.
-template <int QT, int MT, int G>
+template <int QT, int G>
 __device__ __forceinline__ void take_short(const uint8_t *w, int64_t nb1, int row0, int n_rows, int64_t apart, int blocks,
-                                           const Ops &x, uint8_t *stage, uint8_t *ops, float4_t acc[G][MT], int lane) {
+                                           const Ops &x, uint8_t *stage, uint8_t *ops, float4_t acc[G], int lane) {
   const int dwords = (blocks * Block<QT>::bytes + 3) / 4;
   wait_reads();  // of what lay in this place before
   for (int i = lane; i < 16 * G * dwords; i += 64) {
@@ -275,7 +260,7 @@ __device__ __forceinline__ void take_short(const uint8_t *w, int64_t nb1, int ro
   for (int i = lane; i < blocks * 4 * static_cast<int>(x.columns); i += 64)
     *reinterpret_cast<half8_t *>(ops + 16 * i) = *reinterpret_cast<const half8_t *>(x.piece(0, i));
   wait_reads();
-  take_some<QT, MT, G>(stage, ops, x.columns, blocks, acc, lane);
+  take_quad<QT, G>(stage, ops, x.columns, blocks, acc, lane);
 }
 
 struct Stage {
@@ -308,10 +293,10 @@ template <class R, int WAVES> struct Lds {
 // on: a stage is a quad of an expert's matrix, and advance(s) goes to the next. The wavefronts of a part, `peer` of
 // `peers`, have different rows of the same stages and copy its activations together.
 // Behind an expert's last stage comes flush(its index).
-template <int QT, int MT, int G, class R, class L, class Advance, class Flush>
+template <int QT, int G, class R, class L, class Advance, class Flush>
 __device__ __forceinline__ void stream(const R &rows, const Stage &first, const Advance &advance, const Flush &flush, int n,
                                        int most, int blocks, const L &lds, int part, int peer, int peers, bool live,
-                                       float4_t acc[G][MT], int wave, int lane) {
+                                       float4_t acc[G], int wave, int lane) {
   const int whole = blocks / 8;
   auto copy = [&](const Stage &s, int slot) {
     rows.copy(s.w, s.q, s.q == whole, lds_addr(lds.weights(wave, slot)), lane);
@@ -335,7 +320,7 @@ __device__ __forceinline__ void stream(const R &rows, const Stage &first, const 
     if (i < n && live) {
       const uint8_t *ops = lds.ops(part, i & 1);
       const bool tail = s.q == whole;
-      take_some<QT, MT, G>(lds.weights(wave, i & 1) + (tail ? rows.tail_skip : 0), ops, s.ops.columns, tail ? blocks % 8 : 8,
+      take_quad<QT, G>(lds.weights(wave, i & 1) + (tail ? rows.tail_skip : 0), ops, s.ops.columns, tail ? blocks % 8 : 8,
                            acc, lane);
       if (i + 1 == n || s.q == (blocks + 7) / 8 - 1) flush(s.index);
     }
@@ -345,21 +330,17 @@ __device__ __forceinline__ void stream(const R &rows, const Stage &first, const 
 
 // Adds the sums of the `parts` wavefronts that share rows, in order; the first of
 // them has the result. (Wavefront: part + parts * unit.)
-template <int MT, int G> __device__ __forceinline__ void add_parts(float4_t acc[G][MT], uint8_t *lds, int parts, int wave, int lane) {
+template <int G> __device__ __forceinline__ void add_parts(float4_t acc[G], uint8_t *lds, int parts, int wave, int lane) {
   if (parts == 1) return;
   __syncthreads();
   float4_t *at = reinterpret_cast<float4_t *>(lds) + lane;
 #pragma unroll
-  for (int k = 0; k < G; ++k)
-#pragma unroll
-    for (int t = 0; t < MT; ++t) at[((wave * G + k) * MT + t) * 64] = acc[k][t];
+  for (int k = 0; k < G; ++k) at[(wave * G + k) * 64] = acc[k];
   __syncthreads();
   if (wave % parts != 0) return;
   for (int s = 1; s < parts; ++s)
 #pragma unroll
-    for (int k = 0; k < G; ++k)
-#pragma unroll
-      for (int t = 0; t < MT; ++t) acc[k][t] += at[(((wave + s) * G + k) * MT + t) * 64];
+    for (int k = 0; k < G; ++k) acc[k] += at[((wave + s) * G + k) * 64];
 }
 
 // ----------------------------------------------------------------- kernels
@@ -368,8 +349,8 @@ struct Table {  // what the choice leaves for the products
   int n_active;
   int pad[3];
 };
-struct Active {  // an expert that was chosen
-  int expert, count;  // by so many tokens,
+struct Active {  // a set: an expert that was chosen,
+  int expert, count;  // by so many tokens (of more than 8, some: it has two sets),
   uint64_t tokens;    // these, in order, 4 bits each
 };
 struct MoeArgs {
@@ -385,10 +366,10 @@ struct MoeArgs {
   double *logits;     // [n_tokens][n_experts]
   Table *table;
   Active *active;     // [most active], in order
-  float *share;       // [most active][kMaxTokens] routing weights of its tokens
-  _Float16 *x_ops, *h_ops;  // operands of x, and of h expert by expert, of its tokens alone
-  int64_t h_step;     // halves of one expert's h
-  int n_tokens, k, n_ff, n_experts, n_used, renormalise, x_f16, type_in, type_out;
+  float *share;       // [most active][kSetTokens] routing weights of its tokens
+  _Float16 *x_ops, *h_ops;  // operands of x, and of h set by set, of its tokens alone
+  int64_t h_step;     // halves of one set's h
+  int n_tokens, set_tokens, k, n_ff, n_experts, n_used, renormalise, x_f16, type_in, type_out;
   int logit_groups;   // workgroups of the first launch that compute logits; the others prepare operands
   int parts_in, parts_out;  // wavefronts of a workgroup that share rows
   int sums_out;             // where the tokens' sums lie in LDS
@@ -510,38 +491,37 @@ __global__ __launch_bounds__(kRouteThreads) void moe_route_kernel(MoeArgs a) {
     int before = 0;
     for (int e0 = 0; e0 < experts; e0 += 64) {
       const int e = e0 + lane;
-      const uint32_t tokens = e < experts ? by[e] : 0;
-      const bool on = tokens != 0;
-      const uint64_t mask = __ballot(on);
-      if (on) {
-        const int at = before + __popcll(mask & ((uint64_t{1} << lane) - 1));
-        place[e] = at;
-        uint64_t list = 0;
-        int count = 0;
-        for (int t = 0; t < n; ++t)
-          if (tokens >> t & 1) list |= static_cast<uint64_t>(t) << (4 * count++);
-        a.active[at] = Active{e, count, list};
+      uint32_t tokens = e < experts ? by[e] : 0;
+      const int count = __popc(tokens);
+      const uint64_t some = __ballot(count > 0), many = __ballot(count > kSetTokens), in_front = (uint64_t{1} << lane) - 1;
+      int at = before + __popcll(some & in_front) + __popcll(many & in_front);
+      if (count > 0) place[e] = at;
+      while (tokens) {
+        Active set{e, 0, 0};
+        for (; tokens && set.count < kSetTokens; tokens &= tokens - 1)
+          set.tokens |= static_cast<uint64_t>(__builtin_ctz(tokens)) << (4 * set.count++);
+        a.active[at++] = set;
       }
-      before += __popcll(mask);
+      before += __popcll(some) + __popcll(many);
     }
     if (lane == 0) a.table->n_active = before;
   }
   __syncthreads();
   for (int i = threadIdx.x; i < n * a.n_used; i += kRouteThreads) {
     const int t = i / a.n_used, e = id[i];
-    a.share[place[e] * kMaxTokens + __popc(by[e] & ((1u << t) - 1))] = w[i];
+    a.share[place[e] * kSetTokens + __popc(by[e] & ((1u << t) - 1))] = w[i];  // (its second set comes right behind)
   }
 }
 
 
-// Columns 4 g + e of a tile: hi and lo of tokens 8 t + 2 g and 8 t + 2 g + 1.
+// Columns 4 g + e: hi and lo of tokens 2 g and 2 g + 1.
 __device__ __forceinline__ float token_value(const float4_t &acc, int which) {
   return __builtin_fmaf(acc[2 * which + 1], 1.f / kLoScale, acc[2 * which]);
 }
 
 // gate, up and their product: blockIdx.y is the active expert, a unit 16 rows of both.
 template <int QT> using InnerRows = Rows<QT, 2>;
-template <int QT, int MT> __global__ __launch_bounds__(64 * kInnerWaves, MT == 1 ? 4 : 3) void moe_inner_kernel(MoeArgs a) {
+template <int QT> __global__ __launch_bounds__(64 * kInnerWaves, 4) void moe_inner_kernel(MoeArgs a) {
   typedef InnerRows<QT> R;
   typedef Lds<R, kInnerWaves> L;
   extern __shared__ __align__(1024) uint8_t smem[];
@@ -555,19 +535,19 @@ template <int QT, int MT> __global__ __launch_bounds__(64 * kInnerWaves, MT == 1
   const Active mine = a.active[blockIdx.y];
   const uint8_t *w = a.gate + static_cast<int64_t>(mine.expert) * a.nb2_in;
   const Ops x(a.x_ops, mine.count, mine.tokens, a.n_tokens);
-  const L lds{smem, parts, a.n_tokens};
-  float4_t acc[2][MT] = {};
+  const L lds{smem, parts, a.set_tokens};
+  float4_t acc[2] = {};
   if (blocks >= 8) {
     const int stages = (blocks + 7) / 8;
     const int lo = stages * part / parts, hi = stages * (part + 1) / parts;
     const R rows(a.nb1_in, row0, a.n_ff, blocks, a.up_apart, lane);
-    stream<QT, MT, 2>(rows, Stage{w, lo, 0, x}, [](Stage &s) { ++s.q; }, [](int) {}, hi - lo,
+    stream<QT, 2>(rows, Stage{w, lo, 0, x}, [](Stage &s) { ++s.q; }, [](int) {}, hi - lo,
                       (stages + parts - 1) / parts, blocks, lds, part, peer, peers, live, acc, wave, lane);
   } else if (live && part == 0) {
-    take_short<QT, MT, 2>(w, a.nb1_in, row0, a.n_ff, a.up_apart, blocks, x, lds.weights(wave, 0),
-                          smem + L::kRings + wave * a.n_tokens * kQuadOps, acc, lane);
+    take_short<QT, 2>(w, a.nb1_in, row0, a.n_ff, a.up_apart, blocks, x, lds.weights(wave, 0),
+                          smem + L::kRings + wave * a.set_tokens * kQuadOps, acc, lane);
   }
-  add_parts<MT, 2>(acc, smem, parts, wave, lane);
+  add_parts<2>(acc, smem, parts, wave, lane);
   if (part != 0 || !live) return;
   const int row = row0 + (lane & 15), g = lane >> 4;
   if (row >= a.n_ff) return;
@@ -575,26 +555,24 @@ template <int QT, int MT> __global__ __launch_bounds__(64 * kInnerWaves, MT == 1
   _Float16 *h = a.h_ops + blockIdx.y * a.h_step;
   const int columns = 2 * mine.count;
 #pragma unroll
-  for (int t = 0; t < MT; ++t)
-#pragma unroll
-    for (int k = 0; k < 2; ++k) {
-      const int token = 8 * t + 2 * g + k;  // among the expert's
-      if (token >= mine.count) continue;
-      const float share = a.share[blockIdx.y * kMaxTokens + token];
-      const float gate = token_value(acc[0][t], k), up = token_value(acc[1][t], k);
-      const float v = share == 0.f ? 0.f : gate / (1.f + expf(-gate)) * up * share;
-      _Float16 hi, lo;
-      qmm::split(v, hi, lo);
-      h[operand_at(row / 32, columns, 2 * token, s.g) + s.j] = hi;
-      h[operand_at(row / 32, columns, 2 * token + 1, s.g) + s.j] = lo;
-    }
+  for (int k = 0; k < 2; ++k) {
+    const int token = 2 * g + k;  // among the set's
+    if (token >= mine.count) continue;
+    const float share = a.share[blockIdx.y * kSetTokens + token];
+    const float gate = token_value(acc[0], k), up = token_value(acc[1], k);
+    const float v = share == 0.f ? 0.f : gate / (1.f + expf(-gate)) * up * share;
+    _Float16 hi, lo;
+    qmm::split(v, hi, lo);
+    h[operand_at(row / 32, columns, 2 * token, s.g) + s.j] = hi;
+    h[operand_at(row / 32, columns, 2 * token + 1, s.g) + s.j] = lo;
+  }
 }
 
 // down: 16 rows over all active experts' quads, split evenly between the parts of
 // the workgroups that share rows. Columns are an expert's tokens, so its sums are
 // added to the tokens' own (in LDS, each wavefront's) behind its last quad.
 template <int QT> using OuterRows = Rows<QT, 1>;
-template <int QT, int MT, int WAVES> __global__ __launch_bounds__(64 * WAVES, 4) void moe_outer_kernel(MoeArgs a) {
+template <int QT, int WAVES> __global__ __launch_bounds__(64 * WAVES, 4) void moe_outer_kernel(MoeArgs a) {
   typedef OuterRows<QT> R;
   typedef Lds<R, WAVES> L;
   extern __shared__ __align__(1024) uint8_t smem[];
@@ -606,21 +584,18 @@ template <int QT, int MT, int WAVES> __global__ __launch_bounds__(64 * WAVES, 4)
   const bool live = row0 < a.k;
   const int n_active = __builtin_amdgcn_readfirstlane(a.table->n_active);
   const int blocks = a.n_ff / 32;
-  const L lds{smem, parts, a.n_tokens};
+  const L lds{smem, parts, a.set_tokens};
   float *sums = reinterpret_cast<float *>(smem + a.sums_out) + wave * a.n_tokens * 16;  // [n_tokens][16 rows]
   for (int i = lane; i < 16 * a.n_tokens; i += 64) sums[i] = 0.f;
-  float4_t acc[1][MT] = {};
+  float4_t acc[1] = {};
   auto flush = [&](int index) {
     const Active &e = a.active[index];
 #pragma unroll
-    for (int t = 0; t < MT; ++t) {
-#pragma unroll
-      for (int k = 0; k < 2; ++k) {
-        const int i = 8 * t + 2 * g + k;
-        if (i < e.count) sums[static_cast<int>(e.tokens >> (4 * i) & 15) * 16 + (lane & 15)] += token_value(acc[0][t], k);
-      }
-      acc[0][t] = float4_t{};
+    for (int k = 0; k < 2; ++k) {
+      const int i = 2 * g + k;
+      if (i < e.count) sums[static_cast<int>(e.tokens >> (4 * i) & 15) * 16 + (lane & 15)] += token_value(acc[0], k);
     }
+    acc[0] = float4_t{};
   };
   auto matrix = [&](int index) { return a.down + static_cast<int64_t>(a.active[index].expert) * a.nb2_out; };
   auto operands = [&](int index) { return Ops(a.h_ops + index * a.h_step, a.active[index].count); };
@@ -637,12 +612,12 @@ template <int QT, int MT, int WAVES> __global__ __launch_bounds__(64 * WAVES, 4)
       s.q = 0, ++s.index;
       s.w = matrix(s.index), s.ops = operands(s.index);
     };
-    stream<QT, MT, 1>(rows, Stage{matrix(e0), lo - e0 * stages, e0, operands(e0)}, advance, flush, hi - lo, static_cast<int>((all + all_parts - 1) / all_parts), blocks, lds, part, peer,
+    stream<QT, 1>(rows, Stage{matrix(e0), lo - e0 * stages, e0, operands(e0)}, advance, flush, hi - lo, static_cast<int>((all + all_parts - 1) / all_parts), blocks, lds, part, peer,
                       peers, live, acc, wave, lane);
   } else if (live) {
     for (int e = my_part; e < n_active; e += all_parts) {
-      take_short<QT, MT, 1>(matrix(e), a.nb1_out, row0, a.k, 0, blocks, operands(e), lds.weights(wave, 0),
-                            smem + L::kRings + wave * a.n_tokens * kQuadOps, acc, lane);
+      take_short<QT, 1>(matrix(e), a.nb1_out, row0, a.k, 0, blocks, operands(e), lds.weights(wave, 0),
+                            smem + L::kRings + wave * a.set_tokens * kQuadOps, acc, lane);
       flush(e);
     }
   }
@@ -673,13 +648,17 @@ __global__ __launch_bounds__(256) void moe_add_kernel(const float *partial, int 
 }
 
 int64_t round16(int64_t n) { return (n + 15) / 16 * 16; }
-int64_t most_active(int64_t n_tokens, int64_t n_experts, int64_t n_used) { return std::min(n_experts, n_tokens * n_used); }
+// Sets, at most.
+int64_t most_active(int64_t n_tokens, int64_t n_experts, int64_t n_used) {
+  return std::min(n_experts, n_tokens * n_used) + std::min(n_experts, n_tokens * n_used / (kSetTokens + 1));
+}
+int64_t set_tokens(int64_t n_tokens) { return std::min<int64_t>(n_tokens, kSetTokens); }
 
 // How a product's rows and stages are divided. A quad's activations take 1 KiB a
 // token, as much as the weights of 7 rows, so wavefronts with different rows share
 // them and copy up to XC tokens' each. The other wavefronts of a workgroup take
 // other parts of the stages, and so do other workgroups, where rows are few.
-int pieces_for(int64_t n_tokens) { return n_tokens <= 4 ? 1 : n_tokens <= 8 ? 2 : 4; }
+int pieces_for(int64_t n_tokens) { return n_tokens <= 4 ? 1 : 2; }
 struct Plan {
   int waves, peers, parts, groups;
 };
@@ -687,7 +666,7 @@ struct Plan {
 Plan inner_plan(int64_t n_tokens, int64_t n_ff, int64_t most) {
   Plan p{kInnerWaves, 1, 1, 1};
   const int64_t units = (n_ff + 15) / 16;
-  while (p.peers * pieces_for(n_tokens) < n_tokens) p.peers *= 2;
+  while (p.peers * pieces_for(n_tokens) < set_tokens(n_tokens)) p.peers *= 2;
   while (p.peers < p.waves && (units + p.peers - 1) / p.peers * most > 1024) p.peers *= 2;
   p.parts = p.waves / p.peers;
   return p;
@@ -698,7 +677,7 @@ Plan inner_plan(int64_t n_tokens, int64_t n_ff, int64_t most) {
 Plan outer_plan(int64_t n_tokens, int64_t k, int qtype) {
   Plan p{n_tokens > 1 ? 4 : qtype == QMM_TYPE_Q8_0 ? 8 : 16, 1, 1, 1};
   const int64_t units = (k + 15) / 16;
-  while (p.peers * pieces_for(n_tokens) < n_tokens) p.peers *= 2;
+  while (p.peers * pieces_for(n_tokens) < set_tokens(n_tokens)) p.peers *= 2;
   p.parts = p.waves / p.peers;
   if (n_tokens > 1) p.groups = 4;
   while (n_tokens > 1 && p.groups < 16 && (units + p.peers - 1) / p.peers * p.groups * 2 <= 1024) p.groups *= 2;
@@ -714,20 +693,20 @@ int64_t most_partial(int64_t n_tokens, int64_t k) {
 
 // The rings and the activations, or what take_short or the partial sums use instead.
 template <class R, int WAVES> int lds_bytes(const Plan &p, int64_t n_tokens, bool short_rows) {
-  return Lds<R, WAVES>::kRings + static_cast<int>(n_tokens) * kQuadOps * (short_rows ? WAVES : R::kStages * p.parts);
+  return Lds<R, WAVES>::kRings + static_cast<int>(set_tokens(n_tokens)) * kQuadOps * (short_rows ? WAVES : R::kStages * p.parts);
 }
 
-template <int QT, int MT> hipError_t run_inner(const MoeArgs &a, int64_t most, hipStream_t stream) {
+template <int QT> hipError_t run_inner(const MoeArgs &a, int64_t most, hipStream_t stream) {
   const Plan p = inner_plan(a.n_tokens, a.n_ff, most);
   const dim3 grid(static_cast<unsigned>(((a.n_ff + 15) / 16 + p.peers - 1) / p.peers), static_cast<unsigned>(most));
-  return launch(moe_inner_kernel<QT, MT>, grid, dim3(64 * kInnerWaves),
+  return launch(moe_inner_kernel<QT>, grid, dim3(64 * kInnerWaves),
                 lds_bytes<InnerRows<QT>, kInnerWaves>(p, a.n_tokens, a.k < 256), stream, a);
 }
-template <int QT, int MT, int WAVES> hipError_t run_outer(MoeArgs a, hipStream_t stream) {
+template <int QT, int WAVES> hipError_t run_outer(MoeArgs a, hipStream_t stream) {
   const Plan p = outer_plan(a.n_tokens, a.k, QT);
   const dim3 grid(static_cast<unsigned>(((a.k + 15) / 16 + p.peers - 1) / p.peers * p.groups));
   a.sums_out = lds_bytes<OuterRows<QT>, WAVES>(p, a.n_tokens, a.n_ff < 256);
-  const hipError_t e = launch(moe_outer_kernel<QT, MT, WAVES>, grid, dim3(64 * WAVES),
+  const hipError_t e = launch(moe_outer_kernel<QT, WAVES>, grid, dim3(64 * WAVES),
                               static_cast<size_t>(a.sums_out + WAVES * a.n_tokens * 64), stream, a);
   if (e != hipSuccess || p.groups == 1) return e;
   const int64_t n = static_cast<int64_t>(a.n_tokens) * a.k;
@@ -738,8 +717,8 @@ template <int QT, int MT, int WAVES> hipError_t run_outer(MoeArgs a, hipStream_t
 
 int64_t moe_workspace_bytes(int64_t n_tokens, int64_t k, int64_t n_ff, int64_t n_experts, int64_t n_used) {
   const int64_t most = most_active(n_tokens, n_experts, n_used);
-  return round16(n_tokens * n_experts * 8) + 16 + most * static_cast<int64_t>(sizeof(Active)) + most * kMaxTokens * 4 + n_tokens * k * 4 +
-         most * n_tokens * n_ff * 4 + most_partial(n_tokens, k) * 4;
+  return round16(n_tokens * n_experts * 8) + 16 + most * static_cast<int64_t>(sizeof(Active)) + most * kSetTokens * 4 + n_tokens * k * 4 +
+         most * set_tokens(n_tokens) * n_ff * 4 + most_partial(n_tokens, k) * 4;
 }
 
 hipError_t launch_moe(const MoeLayer &m, void *workspace, hipStream_t stream) {
@@ -754,10 +733,11 @@ hipError_t launch_moe(const MoeLayer &m, void *workspace, hipStream_t stream) {
   a.logits = reinterpret_cast<double *>(p), p += round16(m.n_tokens * m.n_experts * 8);
   a.table = reinterpret_cast<Table *>(p), p += 16;
   a.active = reinterpret_cast<Active *>(p), p += most * sizeof(Active);
-  a.share = reinterpret_cast<float *>(p), p += most * kMaxTokens * 4;
+  a.share = reinterpret_cast<float *>(p), p += most * kSetTokens * 4;
   a.x_ops = reinterpret_cast<_Float16 *>(p), p += m.n_tokens * m.k * 4;
   a.h_ops = reinterpret_cast<_Float16 *>(p);
-  a.h_step = m.n_tokens * m.n_ff * 2, p += most * m.n_tokens * m.n_ff * 4;
+  a.h_step = set_tokens(m.n_tokens) * m.n_ff * 2, p += most * a.h_step * 2;
+  a.set_tokens = static_cast<int>(set_tokens(m.n_tokens));
   a.partial = reinterpret_cast<float *>(p);
   a.parts_in = inner_plan(m.n_tokens, m.n_ff, most).parts;
   const Plan out = outer_plan(m.n_tokens, m.k, m.type_out);
@@ -774,14 +754,12 @@ hipError_t launch_moe(const MoeLayer &m, void *workspace, hipStream_t stream) {
   if (e != hipSuccess) return e;
   e = by_qtype_k(m.type_in, [&](auto q) {
     constexpr int QT = decltype(q)::value;
-    return m.n_tokens <= 8 ? run_inner<QT, 1>(a, most, stream) : run_inner<QT, 2>(a, most, stream);
+    return run_inner<QT>(a, most, stream);
   });
   if (e != hipSuccess) return e;
   return by_qtype_k(m.type_out, [&](auto q) {
     constexpr int QT = decltype(q)::value;
-    return m.n_tokens == 1  ? run_outer<QT, 1, QT == QMM_TYPE_Q8_0 ? 8 : 16>(a, stream)
-           : m.n_tokens <= 8 ? run_outer<QT, 1, 4>(a, stream)
-                             : run_outer<QT, 2, 4>(a, stream);
+    return m.n_tokens == 1 ? run_outer<QT, QT == QMM_TYPE_Q8_0 ? 8 : 16>(a, stream) : run_outer<QT, 4>(a, stream);
   });
 }
 
