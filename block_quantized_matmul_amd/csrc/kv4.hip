@@ -47,8 +47,8 @@ struct ReadArgs {
   int64_t kt, kh, vt, vh;
   const int32_t *slots;
   Kv4Cache cache;
-  int64_t n_rows, n_slots;
-  int heads, type;
+  int64_t n_rows, n_slots, chunks;
+  int heads, type, rows_shift;
 };
 
 __device__ __forceinline__ float load_one(const void *p, int64_t at, int type) {
@@ -180,10 +180,10 @@ template <int D> __device__ __forceinline__ void fill_turns(const AppendArgs &a,
 }
 
 // Workgroups are dealt to the 8 XCDs in turn, each with an L2 of its own. Runs of
-// 8 go to the same one, so that the pieces of a line (neighbouring tokens') meet there.
-__device__ __forceinline__ uint32_t near_blocks(uint32_t block, uint32_t blocks) {
-  if (block >= blocks / 64 * 64) return block;
-  return block / 64 * 64 + block % 8 * 8 + block / 8 % 8;
+// RUN go to the same one, so that the pieces of a line (neighbouring tokens') meet there.
+template <int RUN> __device__ __forceinline__ uint32_t near_blocks(uint32_t block, uint32_t blocks) {
+  if (block >= blocks / (8 * RUN) * (8 * RUN)) return block;
+  return block / (8 * RUN) * (8 * RUN) + block % 8 * RUN + block / 8 % RUN;
 }
 
 template <int D, bool WIDE> __global__ __launch_bounds__(kThreads, 4) void append_kernel(AppendArgs a) {
@@ -194,7 +194,7 @@ template <int D, bool WIDE> __global__ __launch_bounds__(kThreads, 4) void appen
   const int own = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   double2 *turns = all_turns[own];
   const int64_t n_waves = a.n_tokens * 2 * a.chunks, stride = static_cast<int64_t>(gridDim.x) * kWaves;
-  for (int64_t wave = static_cast<int64_t>(near_blocks(blockIdx.x, gridDim.x)) * kWaves + own; wave < n_waves; wave += stride) {
+  for (int64_t wave = static_cast<int64_t>(near_blocks<8>(blockIdx.x, gridDim.x)) * kWaves + own; wave < n_waves; wave += stride) {
     const int64_t token = wave / (2 * a.chunks);
     const int part = static_cast<int>(wave % (2 * a.chunks));
     const bool values = part >= a.chunks;
@@ -287,15 +287,23 @@ template <bool WIDE> __device__ __forceinline__ void store_eight(void *p, int64_
   }
 }
 
-// A lane writes 8 elements: row, head, keys or values, dword from the index.
+// A lane writes 8 elements. A row's lanes are those of its keys, then its values,
+// head by head, in a.chunks wavefronts; where they are few, a wavefront has 2^a.rows_shift rows.
 template <int D, bool WIDE> __global__ __launch_bounds__(kThreads) void read_kernel(ReadArgs a) {
   constexpr int kLanes = D / 8, NB = D / 32;
-  const int both = a.k && a.v ? 2 : 1;
-  const int64_t n = a.n_rows * both * a.heads * kLanes, step = static_cast<int64_t>(gridDim.x) * kThreads;
-  for (int64_t i = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x; i < n; i += step) {
-    const int l = static_cast<int>(i % kLanes), head = static_cast<int>(i / kLanes % a.heads);
-    const int64_t rest = i / kLanes / a.heads, row = rest / both;
-    const bool values = a.k == nullptr || rest % both == 1;
+  const int lane = threadIdx.x & 63, lanes = a.heads * kLanes;  // of the keys or the values
+  const int shift = 6 - a.rows_shift, sub = lane >> shift, mine = lane & ((1 << shift) - 1);
+  const int64_t n = ((a.n_rows + (1 << a.rows_shift) - 1) >> a.rows_shift) * a.chunks;
+  const int64_t stride = static_cast<int64_t>(gridDim.x) * kWaves;
+  int64_t wave = static_cast<int64_t>(near_blocks<16>(blockIdx.x, gridDim.x)) * kWaves + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  for (; wave < n; wave += stride) {
+    const int64_t first = a.chunks == 1 ? wave : wave / a.chunks;
+    const int64_t row = (first << a.rows_shift) + sub;
+    const int64_t item = (wave - first * a.chunks) * 64 + mine;
+    const bool values = a.k == nullptr || item >= lanes;
+    const int64_t at = values && a.k != nullptr ? item - lanes : item;
+    if (row >= a.n_rows || at >= lanes || (values && a.v == nullptr)) continue;
+    const int l = static_cast<int>(at % kLanes), head = static_cast<int>(at / kLanes);
     const int slot = a.slots[row];
     const int b = l / 4, g = l % 4;
     uint32_t codes = 0;
@@ -358,8 +366,12 @@ hipError_t launch_kv4_read(int type, const qmm_heads &K, const qmm_heads &V, int
   a.k = K.data, a.v = V.data, a.kt = K.token_stride, a.kh = K.head_stride, a.vt = V.token_stride, a.vh = V.head_stride;
   a.slots = slots, a.cache = cache, a.n_rows = n_rows, a.n_slots = cache.n_pages * cache.page_tokens;
   a.heads = static_cast<int>(n_kv_heads), a.type = type;
-  const int64_t lanes = n_rows * (K.data && V.data ? 2 : 1) * n_kv_heads * (head_dim / 8);
-  const unsigned grid = grid_for((lanes + kThreads - 1) / kThreads);
+  const int64_t lanes = (K.data && V.data ? 2 : 1) * n_kv_heads * (head_dim / 8);
+  while ((lanes << (a.rows_shift + 1)) <= 64) ++a.rows_shift;
+  if ((lanes << a.rows_shift) != 64) a.rows_shift = 0;  // (three heads of 64)
+  a.chunks = (lanes + 63) / 64;
+  const int64_t waves = ((n_rows + (1 << a.rows_shift) - 1) >> a.rows_shift) * a.chunks;
+  const unsigned grid = grid_for((waves + kWaves - 1) / kWaves);
   const bool w = (K.data == nullptr || wide(K, n_rows, n_kv_heads)) && (V.data == nullptr || wide(V, n_rows, n_kv_heads));
   auto go = [&](auto kernel) { return launch(kernel, dim3(grid), dim3(kThreads), 0, stream, a); };
   if (head_dim == 128) return w ? go(read_kernel<128, true>) : go(read_kernel<128, false>);
