@@ -3,10 +3,11 @@
 //   r = softmax(R x), the `used` largest;  y = sum_e r_e D_e h_e,
 //   h_e = silu(G_e x) * (U_e x)
 //
-// Bound by memory for few tokens: the chosen experts' blocks are read once. Four
-// launches: the router's logits and the activations' operands; the choice; gate and
-// up with the activation; down with the sum over experts; and for more than one token
-// a fifth, the sum over workgroups that share rows of down.
+// Bound by memory for few tokens: the chosen experts' blocks are read once. Three to
+// five launches: the router's logits and the activations' operands; the choice, where
+// gate's and up's workgroups are too many to make it themselves; gate and up with the
+// activation; down with the sum over experts; and for more than one token the sum over
+// workgroups that share rows of down.
 //
 // The columns of an expert's products are the tokens that chose it, at most 8 (an
 // expert of more has two sets, and its blocks are read twice, the second time mostly
@@ -31,8 +32,8 @@
 // the weights of 7 rows, so the wavefronts of a workgroup that have different rows of
 // the same stages copy them together; those that share rows add their sums at the end.
 //
-// Measured (one MI355X): 1 token, 2 of 8 experts of 14336 x 4096 Q4_0: 4.9 + 4.9 + 35 +
-// 23 us, 198 MB at 3.8 TB/s in the products (copies alone, in pieces of 144 bytes a row,
+// Measured (one MI355X): 1 token, 2 of 8 experts of 14336 x 4096 Q4_0: 4.9 + 37 + 23
+// us, 198 MB at 3.8 TB/s in the products (copies alone, in pieces of 144 bytes a row,
 // take 31 + 20; of 288 bytes 28 + 17, but leave room for half as many wavefronts). 5
 // tokens, 6 of 64 experts of 1408 x 2048, Q4_0 and Q8_0: 4.2 + 5.2 + 28 + 21 + 4.6 us.
 // 16 tokens, 2 of 8 experts of 14336 x 4096 Q4_K: 9 + 5 + 160 + 95 + 5 us, 793 MB at 3.1
@@ -380,7 +381,7 @@ struct MoeArgs {
   float *share;       // [most active][kSetTokens] routing weights of its tokens
   _Float16 *x_ops, *h_ops;  // operands of x, and of h set by set, of its tokens alone
   int64_t h_step;     // halves of one set's h
-  int n_tokens, set_tokens, k, n_ff, n_experts, n_used, renormalise, x_f16, type_in, type_out;
+  int n_tokens, set_tokens, most, route_here, k, n_ff, n_experts, n_used, renormalise, x_f16, type_in, type_out;
   int logit_groups;   // workgroups of the first launch that compute logits; the others prepare operands
   int parts_in, parts_out;  // wavefronts of a workgroup that share rows
   int sums_out;             // where the tokens' sums lie in LDS
@@ -447,24 +448,34 @@ __global__ __launch_bounds__(kLogitThreads) void moe_prepare_kernel(MoeArgs a) {
   a.x_ops[operand_at(e / 32, 2 * a.n_tokens, 2 * t + 1, s.g) + s.j] = lo;
 }
 
-// The choice, by one workgroup: an expert's rank among a token's is the number of
+// The choice, by a workgroup: an expert's rank among a token's is the number of
 // larger logits, of equal ones before it (a NaN is below all others), and those
-// of rank below n_used are chosen.
-__global__ __launch_bounds__(kRouteThreads) void moe_route_kernel(MoeArgs a) {
-  extern __shared__ __align__(16) uint8_t smem[];
+// of rank below n_used are chosen. The sets and their tokens' weights are left in LDS,
+// and where `write`, in the workspace and the outputs.
+struct Routed {
+  const Active *sets;
+  const float *share;  // [sets][kSetTokens]
+  int n;
+};
+constexpr int64_t route_lds(int64_t n, int64_t experts, int64_t used, int64_t most) {
+  return n * experts * 8 + most * (static_cast<int64_t>(sizeof(Active)) + kSetTokens * 4) + n * used * 8 + (2 * experts + 1) * 4;
+}
+template <int THREADS> __device__ __forceinline__ Routed route(const MoeArgs &a, uint8_t *smem, bool write) {
   const int n = a.n_tokens, experts = a.n_experts, items = n * experts;
-  double *l = reinterpret_cast<double *>(smem);                    // [n][experts], NaN as -infinity
-  float *w = reinterpret_cast<float *>(l + items);                 // [n][n_used]
-  int *id = reinterpret_cast<int *>(w + n * a.n_used);             // [n][n_used]
-  int *place = id + n * a.n_used;                                  // [experts + 1]
+  double *l = reinterpret_cast<double *>(smem);                      // [n][experts], NaN as -infinity
+  Active *sets = reinterpret_cast<Active *>(l + items);              // [most]
+  float *share = reinterpret_cast<float *>(sets + a.most);           // [most][kSetTokens]
+  float *w = share + a.most * kSetTokens;                            // [n][n_used]
+  int *id = reinterpret_cast<int *>(w + n * a.n_used);               // [n][n_used]
+  int *place = id + n * a.n_used;                                    // [experts + 1], the last: sets in all
   uint32_t *by = reinterpret_cast<uint32_t *>(place + experts + 1);  // [experts] a bit for each token
-  for (int i = threadIdx.x; i < items; i += kRouteThreads) {
+  for (int i = threadIdx.x; i < items; i += THREADS) {
     const double v = a.logits[i];
     l[i] = v != v ? -__builtin_inf() : v;
   }
-  for (int i = threadIdx.x; i < experts; i += kRouteThreads) by[i] = 0;
+  for (int i = threadIdx.x; i < experts; i += THREADS) by[i] = 0;
   __syncthreads();
-  for (int i = threadIdx.x; i < items; i += kRouteThreads) {
+  for (int i = threadIdx.x; i < items; i += THREADS) {
     const int t = i / experts, e = i % experts;
     const double mine = l[i], *row = l + t * experts;
     int rank = 0;
@@ -477,7 +488,7 @@ __global__ __launch_bounds__(kRouteThreads) void moe_route_kernel(MoeArgs a) {
   __syncthreads();
   // weights: a wavefront per token
   const int lane = threadIdx.x & 63;
-  for (int t = threadIdx.x >> 6; t < n; t += kRouteThreads / 64) {
+  for (int t = threadIdx.x >> 6; t < n; t += THREADS / 64) {
     const double *row = a.logits + static_cast<int64_t>(t) * experts;
     const double top = l[t * experts + id[t * a.n_used]];
     float sum = 0.f;
@@ -492,12 +503,11 @@ __global__ __launch_bounds__(kRouteThreads) void moe_route_kernel(MoeArgs a) {
       const int e = id[t * a.n_used + k];
       const float v = expf(static_cast<float>(row[e] - top)) / sum;
       w[t * a.n_used + k] = v;
-      if (a.ids) a.ids[t * a.n_used + k] = e;
-      if (a.weights) a.weights[t * a.n_used + k] = v;
+      if (write && a.ids) a.ids[t * a.n_used + k] = e;
+      if (write && a.weights) a.weights[t * a.n_used + k] = v;
     }
   }
-  __syncthreads();
-  // the active experts in order, by the first wavefront
+  // the sets in order, by the first wavefront
   if (threadIdx.x < 64) {
     int before = 0;
     for (int e0 = 0; e0 < experts; e0 += 64) {
@@ -511,19 +521,30 @@ __global__ __launch_bounds__(kRouteThreads) void moe_route_kernel(MoeArgs a) {
         Active set{e, 0, 0};
         for (; tokens && set.count < kSetTokens; tokens &= tokens - 1)
           set.tokens |= static_cast<uint64_t>(__builtin_ctz(tokens)) << (4 * set.count++);
-        a.active[at++] = set;
+        if (write) a.active[at] = set;
+        sets[at++] = set;
       }
       before += __popcll(some) + __popcll(many);
     }
-    if (lane == 0) a.table->n_active = before;
+    if (lane == 0) {
+      place[experts] = before;
+      if (write) a.table->n_active = before;
+    }
   }
   __syncthreads();
-  for (int i = threadIdx.x; i < n * a.n_used; i += kRouteThreads) {
+  for (int i = threadIdx.x; i < n * a.n_used; i += THREADS) {
     const int t = i / a.n_used, e = id[i];
-    a.share[place[e] * kSetTokens + __popc(by[e] & ((1u << t) - 1))] = w[i];  // (its second set comes right behind)
+    const int at = place[e] * kSetTokens + __popc(by[e] & ((1u << t) - 1));  // (its second set comes right behind)
+    share[at] = w[i];
+    if (write) a.share[at] = w[i];
   }
+  __syncthreads();
+  return {sets, share, place[experts]};
 }
-
+__global__ __launch_bounds__(kRouteThreads) void moe_route_kernel(MoeArgs a) {
+  extern __shared__ __align__(16) uint8_t smem[];
+  route<kRouteThreads>(a, smem, true);
+}
 
 // Columns 4 g + e: hi and lo of tokens 2 g and 2 g + 1.
 __device__ __forceinline__ float token_value(const float4_t &acc, int which) {
@@ -536,14 +557,33 @@ template <int QT> __global__ __launch_bounds__(64 * kInnerWaves, 4) void moe_inn
   typedef InnerRows<QT> R;
   typedef Lds<R, kInnerWaves> L;
   extern __shared__ __align__(1024) uint8_t smem[];
-  if (static_cast<int>(blockIdx.y) >= a.table->n_active) return;
+  Active mine;
+  float shares[2];  // of the set's tokens 2 g and 2 g + 1
+  {
+    const int at = blockIdx.y * kSetTokens + 2 * ((threadIdx.x & 63) >> 4);
+    if (a.route_here) {
+      const Routed routed = route<64 * kInnerWaves>(a, smem, blockIdx.x == 0 && blockIdx.y == 0);
+      if (static_cast<int>(blockIdx.y) >= routed.n) return;
+      const Active &set = routed.sets[blockIdx.y];
+      mine.expert = __builtin_amdgcn_readfirstlane(set.expert), mine.count = __builtin_amdgcn_readfirstlane(set.count);
+      mine.tokens = static_cast<uint64_t>(__builtin_amdgcn_readfirstlane(static_cast<uint32_t>(set.tokens >> 32))) << 32 |
+                    static_cast<uint32_t>(__builtin_amdgcn_readfirstlane(static_cast<uint32_t>(set.tokens)));
+#pragma unroll
+      for (int k = 0; k < 2; ++k) shares[k] = routed.share[at + k];
+      __syncthreads();  // the rings take its place
+    } else {
+      if (static_cast<int>(blockIdx.y) >= a.table->n_active) return;
+      mine = a.active[blockIdx.y];
+#pragma unroll
+      for (int k = 0; k < 2; ++k) shares[k] = a.share[at + k];
+    }
+  }
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int parts = a.parts_in, part = wave % parts, peer = wave / parts, peers = kInnerWaves / parts;
   const int row0 = 16 * (blockIdx.x * peers + peer);
   const bool live = row0 < a.n_ff;  // (else it copies for the others)
   const int blocks = a.k / 32;
-  const Active mine = a.active[blockIdx.y];
   const uint8_t *w = a.gate + static_cast<int64_t>(mine.expert) * a.nb2_in;
   const Ops x(a.x_ops, mine.count, mine.tokens, a.n_tokens);
   const L lds{smem, parts, a.set_tokens};
@@ -569,7 +609,7 @@ template <int QT> __global__ __launch_bounds__(64 * kInnerWaves, 4) void moe_inn
   for (int k = 0; k < 2; ++k) {
     const int token = 2 * g + k;  // among the set's
     if (token >= mine.count) continue;
-    const float share = a.share[blockIdx.y * kSetTokens + token];
+    const float share = shares[k];
     const float gate = token_value(acc[0], k), up = token_value(acc[1], k);
     const float v = share == 0.f ? 0.f : gate / (1.f + expf(-gate)) * up * share;
     _Float16 hi, lo;
@@ -675,11 +715,12 @@ struct Plan {
   int waves, peers, parts, groups;
 };
 // gate and up: `most` sets. Four workgroups a CU (40 KiB of LDS each), in one round if they fit.
+constexpr int64_t kOneRound = 1024;
 Plan inner_plan(int64_t n_tokens, int64_t n_ff, int64_t most) {
   Plan p{kInnerWaves, 1, 1, 1};
   const int64_t units = (n_ff + 15) / 16;
   while (p.peers * pieces_for(n_tokens) < set_tokens(n_tokens)) p.peers *= 2;
-  while (p.peers < p.waves && (units + p.peers - 1) / p.peers * most > 1024) p.peers *= 2;
+  while (p.peers < p.waves && (units + p.peers - 1) / p.peers * most > kOneRound) p.peers *= 2;
   p.parts = p.waves / p.peers;
   return p;
 }
@@ -712,7 +753,9 @@ template <int QT> hipError_t run_inner(const MoeArgs &a, int64_t most, hipStream
   const Plan p = inner_plan(a.n_tokens, a.n_ff, most);
   const dim3 grid(static_cast<unsigned>(((a.n_ff + 15) / 16 + p.peers - 1) / p.peers), static_cast<unsigned>(most));
   return launch(moe_inner_kernel<QT>, grid, dim3(64 * kInnerWaves),
-                lds_bytes<InnerRows<QT>, kInnerWaves>(p, a.n_tokens, a.k < 256), stream, a);
+                std::max<size_t>(lds_bytes<InnerRows<QT>, kInnerWaves>(p, a.n_tokens, a.k < 256),
+                                 a.route_here ? route_lds(a.n_tokens, a.n_experts, a.n_used, a.most) : 0),
+                stream, a);
 }
 template <int QT, int WAVES> hipError_t run_outer(MoeArgs a, hipStream_t stream) {
   const Plan p = outer_plan(a.n_tokens, a.k, QT);
@@ -751,7 +794,6 @@ hipError_t launch_moe(const MoeLayer &m, void *workspace, hipStream_t stream) {
   a.h_step = set_tokens(m.n_tokens) * m.n_ff * 2, p += most * a.h_step * 2;
   a.set_tokens = static_cast<int>(set_tokens(m.n_tokens));
   a.partial = reinterpret_cast<float *>(p);
-  a.parts_in = inner_plan(m.n_tokens, m.n_ff, most).parts;
   const Plan out = outer_plan(m.n_tokens, m.k, m.type_out);
   a.parts_out = out.parts, a.groups_out = out.groups;
   a.n_tokens = static_cast<int>(m.n_tokens), a.k = static_cast<int>(m.k), a.n_ff = static_cast<int>(m.n_ff);
@@ -761,9 +803,19 @@ hipError_t launch_moe(const MoeLayer &m, void *workspace, hipStream_t stream) {
   const unsigned first = static_cast<unsigned>(a.logit_groups + (m.k * m.n_tokens + kLogitThreads - 1) / kLogitThreads);
   hipError_t e = launch(moe_prepare_kernel, dim3(first), dim3(kLogitThreads), 0, stream, a);
   if (e != hipSuccess) return e;
-  const size_t lds = static_cast<size_t>(m.n_tokens * (m.n_experts + m.n_used) * 8 + (2 * m.n_experts + 1) * 4);
-  e = launch(moe_route_kernel, dim3(1), dim3(kRouteThreads), lds, stream, a);
-  if (e != hipSuccess) return e;
+  // Where a thread has a logit at most, and the next launch's workgroups run all at
+  // once, each makes the choice for itself (1 token of 8 experts: 37 us instead of 35 + 5
+  // and a launch; 16 tokens, in many rounds: 180 instead of 160 + 5).
+  a.most = static_cast<int>(most);
+  const Plan in = inner_plan(m.n_tokens, m.n_ff, most);
+  a.parts_in = in.parts;
+  a.route_here = m.n_tokens * m.n_experts <= 64 * kInnerWaves &&
+                 ((m.n_ff + 15) / 16 + in.peers - 1) / in.peers * most <= kOneRound;
+  if (!a.route_here) {
+    e = launch(moe_route_kernel, dim3(1), dim3(kRouteThreads),
+               static_cast<size_t>(route_lds(m.n_tokens, m.n_experts, m.n_used, most)), stream, a);
+    if (e != hipSuccess) return e;
+  }
   e = by_qtype_k(m.type_in, [&](auto q) {
     constexpr int QT = decltype(q)::value;
     return run_inner<QT>(a, most, stream);
