@@ -81,7 +81,7 @@ struct RowState {
   uint32_t n[kBins + 1];
   uint32_t arrived[2];    // workgroups, of the second and third launch
   uint32_t listed;
-  int lo[3], hi[3];       // ranges that may hold a selection's place
+  int lo[3], hi[3];       // ranges that may hold a selection's place; none where it is known
   uint64_t left;
 };
 
@@ -597,7 +597,7 @@ __device__ __forceinline__ void pick_few(Shared &s, const SampleArgs &a, int row
   const int pos = bin * kQuick + static_cast<int>(with);  // rises along the order
 #pragma unroll 1
   for (int kind = COUNT; kind <= UPTO; ++kind) {
-    if (kind == COUNT && !r.counted) continue;
+    if (kind == COUNT && (!r.counted || st.hi[COUNT] < 0)) continue;
     if (kind == BELOW && !(r.top_p < 1.f)) continue;
     if (kind == UPTO) total = min(total, left);
     int last = mine && goal_of(r, kind, total).reaches(n, m) ? pos : -1;
@@ -717,8 +717,7 @@ template <int TYPE> __global__ __launch_bounds__(kThreads) void sample_mass_kern
       if (t < 2) s.bins[t] = 0;
       __syncthreads();
 #pragma unroll
-      for (int k = 0; k < 2; ++k)
-      {
+      for (int k = 0; k < 2; ++k) {
         const Goal goal = goal_of(r, kind, k ? hi_total : lo_total);
 #pragma unroll
         for (int b = 0; b < kOwn; ++b)
@@ -727,6 +726,9 @@ template <int TYPE> __global__ __launch_bounds__(kThreads) void sample_mass_kern
       __syncthreads();
       lo = s.bins[0], hi = s.bins[1];
       lo_total = min(lo_total, s.m[lo]), hi_total = min(hi_total, s.m[hi + 1]);
+      // where top_k ends among elements without a weight, it leaves all the mass (peaked
+      // rows, whose last range has most of the elements)
+      if (kind == COUNT && s.m[lo] == s.m[hi + 1]) hi = -1;
       __syncthreads();
     }
     if (t == 0) st.lo[kind] = lo, st.hi[kind] = hi;
@@ -796,7 +798,7 @@ template <int TYPE> __global__ __launch_bounds__(kThreads) void sample_pick_kern
   uint64_t total = st.m[kBins];
 #pragma unroll 1
   for (int kind = COUNT; kind <= UPTO; ++kind) {
-    if (kind == COUNT && !r.counted) continue;
+    if (kind == COUNT && (!r.counted || (ranges && st.hi[COUNT] < 0))) continue;
     if (kind == BELOW && !(r.top_p < 1.f)) continue;
     if (kind == UPTO) total = min(total, left);
     const Goal goal = goal_of(r, kind, total);

@@ -44,6 +44,22 @@ def test_many_equal(kind, distinct, vocab):
     check(z, g.random(n), "many equal", **kw)
 
 
+@pytest.mark.parametrize("kind", ["f32", "bf16"])
+@pytest.mark.parametrize("vocab", [3873, 50000])
+def test_top_k_ends_among_elements_without_a_weight(kind, vocab):
+    """Peaked rows: a few likely tokens, all others below 2^-45 of the largest; and some of others on either side."""
+    g = rng(85, vocab)
+    n = 8
+    say(f"sample peaked {kind} {vocab}")
+    z = 2 * g.standard_normal((n, vocab))
+    for i in range(n):
+        z[i, g.permutation(vocab)[:5 + 9 * i]] += 60 + 3 * g.standard_normal(5 + 9 * i)
+    kw = dict(top_k=np.array([200, 150, 23, 33, 40, 3000, 0, 60]), top_p=np.array([1.0, 0.9, 1.0, 0.99, 0.7, 1.0, 0.95, 1.0]),
+              temperature=np.array([0.5, 0.7, 1.0, 1.0, 0.3, 1.0, 1.0, 1.9]),
+              min_p=np.array([0.0, 0.0, 0.0, 0.01, 0.0, 0.05, 0.0, 0.0]))
+    check(rounded(z, kind), g.random(n), "peaked", **kw)
+
+
 def test_few_and_many_in_one_call():
     """Rows that go different ways, among them rows without a probability."""
     g = rng(83)
