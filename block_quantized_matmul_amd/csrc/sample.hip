@@ -4,7 +4,7 @@
 // and then rising index, so the whole is three selections along it: the first
 // top_k, the first whose mass reaches top_p of theirs, and the element where the
 // mass passes u times that of what is left. No sort is needed: one histogram of
-// counts and masses over 2048 equal ranges of the logits below the largest finds
+// counts and masses over 1024 equal ranges of the logits below the largest finds
 // the range that holds a selection's place, and the few elements of that range are
 // ranked by comparing each with each, after dividing the range again, or equal
 // elements by index, where they are more than kFew. Rows that this does not fit (with
@@ -24,10 +24,11 @@
 // selection's place is not known before the one in front of it, its bounds are, and
 // the ranges between them are few.
 //
-// Measured (fp32): one row of 32000 2.7 + 13 + 8 us (a workgroup of 16 wavefronts for
-// the row, which reads it five times: 33); 64 rows 4 + 18 + 17 (41); 37 rows of 130001,
-// flat, so that ranges have hundreds of elements: 6 + 30 + 48 (116). With 1024 ranges
-// these are 23, 47 and 70 us, with a list of up to 512 ranked together 23, 46 and 107.
+// Measured (fp32): one row of 32000 2.7 + 11 + 8 us (a workgroup of 16 wavefronts for
+// the row, which reads it five times: 33); 64 rows 4 + 16 + 19 (41); 37 rows of 130001,
+// flat, so that ranges have hundreds of elements: 6 + 24 + 30 (116). With 2048 ranges
+// these are 25, 44 and 67 us in all instead of 22, 39 and 60; with up to 256 elements
+// ranked all together, and then 2048 ranges, 24, 39 and 84.
 #include "common.h"
 #include "launch.h"
 #include "serve.h"
@@ -41,12 +42,12 @@ namespace {
 constexpr int kThreads = 1024;
 constexpr int kWaves = kThreads / 64;
 constexpr int kBits = 11;      // of a key, at a time
-constexpr int kBins = 2048;     // ranges of logits
+constexpr int kBins = 1024;     // ranges of logits
 constexpr int kOwn = kBins / kThreads;
 constexpr int kChunk = 8 * kThreads;
 constexpr int kList = 16384;   // elements of a row that are looked at in the end
 constexpr int kAtOnce = 8;
-constexpr int kQuick = 256;     // of those: elements that are ranked all together
+constexpr int kQuick = 64;      // of those: elements that are ranked all together, by one wavefront
 constexpr int kFew = 512;      // elements that are ranked one by one
 constexpr int kPoint = 44;     // binary places of a weight
 constexpr int kFractions = 64;  // of an octave, in the table of powers (k >> 6 below)
@@ -467,8 +468,8 @@ __device__ __forceinline__ uint64_t resolve(Shared &s, const Element *list, int 
     }
     __syncthreads();
     members = s.few;
-    // (ranking takes 0.02 us per element, dividing again 4 us)
-    if (members <= (sub < 0 ? kFew / 4 : kFew)) break;
+    // (ranking takes 0.08 us per element, dividing again 4 us)
+    if (members <= (sub < 0 ? kFew / 16 : kFew)) break;
     const bool by_index = sub >= 0;
     if (part >= 0) return 0;
     if (by_index) {  // equal ones only
@@ -565,9 +566,9 @@ __device__ __forceinline__ int nth(Shared &s, const void *z, int64_t at, int voc
   return s.few;
 }
 
-// The three selections among few elements in question, as nearly always: by as many
-// threads, which find each one's place and its start at once. (The other wavefronts
-// of the workgroup end: 16 take turns at every instruction.)
+// The three selections among few elements in question, as nearly always, by one
+// wavefront, which finds each one's place and its start at once. (The others of
+// the workgroup end: 16 take turns at every instruction.)
 __device__ __forceinline__ void pick_few(Shared &s, const SampleArgs &a, int row, const Element *list, int listed,
                                          const RowState &st, const Row &r, const Weights &w) {
   const int t = threadIdx.x;
