@@ -56,6 +56,9 @@ constexpr int kThreads = 256;
 constexpr int kWaves = 4;
 constexpr int kChunk = 64;       // keys
 constexpr int kTiles = kChunk / kKv4Tile;
+// Tables of fewer than 5 x 256 keys are not worth a second launch: one row of 700 in a
+// table of 704 keys 9.2 us undivided, 12.8 divided; of 1000 11.0 and 12.8.
+constexpr int kFewestUnits = 5;
 constexpr int kFewGroups = 1024;  // fewer workgroups than this, four per CU on 256 CUs: rows are split
 // Workgroups of a CU that its registers hold: as many as run at once are wanted.
 // 48 rows of up to 8000 keys in 768, 1024, 1536, 2048, 4096 workgroups: 68, 75,
@@ -574,7 +577,7 @@ Kv4Plan kv4_plan(int64_t n_rows, int64_t n_q_heads, int64_t n_kv_heads, int64_t 
   p.tiles = (columns + p.columns - 1) / p.columns;
   const int64_t per_unit = n_kv_heads * p.tiles, most = cap / (kWaves * kChunk);
   p.units = n_rows;
-  if (n_rows > 0 && n_rows * per_unit < kFewGroups && most > 1) {
+  if (n_rows > 0 && n_rows * per_unit < kFewGroups && most >= kFewestUnits) {
     // half a range per row more, since a row's last is short on average
     p.want = std::max(n_rows, 256 * resident(head_dim, p.columns) / per_unit - n_rows / 2);
     // sum_r max(1, ceil(chunks_r / each)), each at least total / want and kWaves

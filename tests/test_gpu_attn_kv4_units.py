@@ -12,17 +12,19 @@ from test_gpu_attn_kv4 import check, run, setup
 pytestmark = pytest.mark.gpu
 
 
+@pytest.mark.parametrize("wide", [False, True])
 @pytest.mark.parametrize("rows,hq,heads,dim,longest", [(63, 4, 4, 64, 900), (64, 2, 1, 128, 700), (65, 1, 1, 64, 600),
                                                        (200, 2, 2, 64, 400),
                                                        (200, 2, 2, 64, 800), (130, 20, 1, 128, 500)])
-def test_many_ragged_rows(rows, hq, heads, dim, longest):
+def test_many_ragged_rows(rows, hq, heads, dim, longest, wide):
+    """In tables as wide as the longest row, and in wide ones, whose rows are divided."""
     g = rng(90, rows, dim)
-    say(f"attn_kv4 units {rows} {hq} {heads} {dim}")
+    say(f"attn_kv4 units {rows} {hq} {heads} {dim} {wide}")
     lens = [int(x) for x in np.where(g.random(rows) < 0.2, g.integers(0, longest, rows), g.integers(0, 40, rows))]
     lens[0], lens[-1], lens[rows // 2] = 0, longest, longest
-    q, cache, tables = setup(g, lens, 32, hq, heads, dim, "f16")
+    q, cache, tables = setup(g, lens, 32, hq, heads, dim, "f16", width=100 if wide else None)
     need = qmm.qmm_attn_kv4_workspace_bytes(rows, hq, heads, dim, tables.shape[1], 32)
-    assert (need > 0) == (tables.shape[1] * 32 >= 512)  # tables of fewer keys are not divided
+    assert (need > 0) == wide
     check(q, cache, 32, heads, tables, lens, "f16", "ragged")
 
 

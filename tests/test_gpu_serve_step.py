@@ -23,7 +23,7 @@ pytestmark = pytest.mark.gpu
 
 Q4, Q8 = qmm.QMM_TYPE_Q4_0, qmm.QMM_TYPE_Q8_0
 B, WIDTH, HQ, HKV, DIM, FF, EXPERTS, USED, VOCAB = 5, 256, 8, 2, 64, 192, 6, 2, 700
-PAGE, PAGES, TABLE = 16, 24, 40  # (a table of 640 tokens, so that rows are split)
+PAGE, PAGES, TABLE = 16, 24, 100  # (a table of 1600 tokens, so that rows are split)
 FREQS = [10000.0 ** (-i / 32) for i in range(32)]
 
 
