@@ -201,7 +201,8 @@ template <int D, bool WIDE> __global__ __launch_bounds__(kThreads, 4) void appen
   const int own = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   double2 *turns = all_turns[own];
   const int64_t n_waves = a.n_tokens * 2 * a.chunks, stride = static_cast<int64_t>(gridDim.x) * kWaves;
-  for (int64_t wave = static_cast<int64_t>(near_blocks<8>(blockIdx.x, gridDim.x)) * kWaves + own; wave < n_waves; wave += stride) {
+  const int64_t first = static_cast<int64_t>(near_blocks<8>(blockIdx.x, gridDim.x)) * kWaves + own;
+  for (int64_t wave = first; wave < n_waves; wave += stride) {
     const int64_t token = wave / (2 * a.chunks);
     const int part = static_cast<int>(wave % (2 * a.chunks));
     const bool values = part >= a.chunks;
@@ -302,7 +303,8 @@ template <int D, bool WIDE> __global__ __launch_bounds__(kThreads) void read_ker
   const int shift = 6 - a.rows_shift, sub = lane >> shift, mine = lane & ((1 << shift) - 1);
   const int64_t n = ((a.n_rows + (1 << a.rows_shift) - 1) >> a.rows_shift) * a.chunks;
   const int64_t stride = static_cast<int64_t>(gridDim.x) * kWaves;
-  int64_t wave = static_cast<int64_t>(near_blocks<16>(blockIdx.x, gridDim.x)) * kWaves + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  int64_t wave = static_cast<int64_t>(near_blocks<16>(blockIdx.x, gridDim.x)) * kWaves +
+                 __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   for (; wave < n; wave += stride) {
     const int64_t first = a.chunks == 1 ? wave : wave / a.chunks;
     const int64_t row = (first << a.rows_shift) + sub;

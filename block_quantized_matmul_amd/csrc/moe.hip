@@ -9,12 +9,12 @@
 // activation; down with the sum over experts; and for more than one token the sum over
 // workgroups that share rows of down.
 //
-// The columns of an expert's products are the tokens that chose it, at most 8 (an
-// expert of more has two sets, and its blocks are read twice, the second time mostly
-// from caches; all tokens as columns of every expert: 16 tokens
-// on 8 experts 357 us instead of 254). The routing weight is multiplied into h, so down's sums
-// over experts are additions to the tokens' rows, in order, by each wavefront for its
-// part of the (expert, n_ff) axis; there is no output per expert.
+// The columns of an expert's products are the tokens that chose it, at most 8: an
+// expert of more has two sets, and its blocks are read twice. (With all tokens as
+// columns of every expert, 16 tokens on 8 experts took 357 us instead of 254.) The
+// routing weight is multiplied into h, so down's sums over experts are additions to
+// the tokens' rows, in order, by each wavefront for its part of the (expert, n_ff)
+// axis; there is no output per expert.
 //
 // Operands. v_mfma_f32_16x16x32_f16 sums a block of 32 weights of 16 rows with 16
 // columns. An activation x takes two columns, hi = fp16(x) and lo = fp16(2^11 (x -
@@ -213,7 +213,8 @@ struct Ops {
   uint32_t inverse;  // 2^16 / columns, rounded up: exact quotients of pieces of a quad, of which there are at most 1024
   __device__ __forceinline__ Ops(const _Float16 *ops, int count, uint64_t which, int of_tokens)
       : p(ops), columns(2 * count), stride(2 * of_tokens), tokens(which), inverse((65536 + 2 * count - 1) / (2 * count)) {}
-  __device__ __forceinline__ Ops(const _Float16 *ops, int count) : p(ops), columns(2 * count), stride(2 * count), tokens(0), inverse(0) {}
+  __device__ __forceinline__ Ops(const _Float16 *ops, int count)
+      : p(ops), columns(2 * count), stride(2 * count), tokens(0), inverse(0) {}
   // Where piece i of quad q is.
   __device__ __forceinline__ const uint8_t *piece(int q, uint32_t i) const {
     const uint8_t *quad = reinterpret_cast<const uint8_t *>(p) + static_cast<int64_t>(q) * (32 * 16) * stride;
@@ -663,8 +664,8 @@ template <int QT, int WAVES> __global__ __launch_bounds__(64 * WAVES, 4) void mo
       s.q = 0, ++s.index;
       s.w = matrix(s.index), s.ops = operands(s.index);
     };
-    stream<QT, 1>(rows, Stage{matrix(e0), lo - e0 * stages, e0, operands(e0)}, advance, flush, hi - lo, static_cast<int>((all + all_parts - 1) / all_parts), blocks, lds, part, peer,
-                      peers, live, acc, wave, lane);
+    stream<QT, 1>(rows, Stage{matrix(e0), lo - e0 * stages, e0, operands(e0)}, advance, flush, hi - lo,
+                  static_cast<int>((all + all_parts - 1) / all_parts), blocks, lds, part, peer, peers, live, acc, wave, lane);
   } else if (live) {
     for (int e = my_part; e < n_active; e += all_parts) {
       take_short<QT, 1>(matrix(e), a.nb1_out, row0, a.k, 0, blocks, operands(e), lds.weights(wave, 0),

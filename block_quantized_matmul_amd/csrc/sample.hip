@@ -773,7 +773,8 @@ template <int TYPE> __global__ __launch_bounds__(kThreads) void sample_pick_kern
 #pragma unroll
     for (int k = 0; k < 8; ++k)
       if (take >> k & 1) {
-        if (place < kList) put(reinterpret_cast<uint64_t *>(list + place), __builtin_bit_cast(uint64_t, Element{x[k], index_of(chunk, k)}));
+        if (place < kList)
+          put(reinterpret_cast<uint64_t *>(list + place), __builtin_bit_cast(uint64_t, Element{x[k], index_of(chunk, k)}));
         ++place;
       }
   }

@@ -1,10 +1,10 @@
 """The operators that complete a served decode step (C: include/qmm_serve.h).
 
 qmm_kv4_append, qmm_kv4_read and qmm_attn_kv4 (a 4-bit paged cache), qmm_moe
-(a mixture-of-experts layer) and qmm_sample, in the same manner as attn.py: tensors supply pointers, strides and sizes, and the
-library checks and runs. All tensors of a call are on one GPU, which need not
-be the current one; work is enqueued on `stream`, or on that GPU's current
-stream.
+(a mixture-of-experts layer) and qmm_sample, in the same manner as attn.py:
+tensors supply pointers, strides and sizes, and the library checks and runs. All
+tensors of a call are on one GPU, which need not be the current one; work is
+enqueued on `stream`, or on that GPU's current stream.
 """
 from __future__ import annotations
 
@@ -23,8 +23,8 @@ QMM_SAMPLE_MAX_VOCAB = 524287
 
 __all__ = ["QMM_KV4_MAX_PAGE_TOKENS", "QMM_MOE_MAX_TOKENS", "QMM_MOE_MAX_EXPERTS", "QMM_MOE_MAX_USED",
            "QMM_SAMPLE_MAX_VOCAB", "qmm_kv4_page_bytes", "qmm_kv4_append", "qmm_kv4_read", "qmm_attn_kv4",
-           "qmm_attn_kv4_workspace_bytes", "qmm_attn_kv4_workspace_max_bytes", "qmm_moe", "qmm_moe_workspace_bytes", "qmm_sample",
-           "qmm_sample_workspace_bytes"]
+           "qmm_attn_kv4_workspace_bytes", "qmm_attn_kv4_workspace_max_bytes", "qmm_moe", "qmm_moe_workspace_bytes",
+           "qmm_sample", "qmm_sample_workspace_bytes"]
 
 _vp, _i32, _i64, _f32, _f64 = ctypes.c_void_p, ctypes.c_int, ctypes.c_int64, ctypes.c_float, ctypes.c_double
 _ready = None
