@@ -219,8 +219,8 @@ int64_t qmm_moe_workspace_bytes(int64_t n_tokens, int64_t k, int64_t n_ff, int64
  *                -infinity or NaN)
  *   probs        fp32 [n_rows], the token's share of what step 4 chooses from
  *                (NaN beside -1); may be NULL
- * Numerics: weights in 64 bits, sums of them exact to 2^-44 of the largest; a
- * token whose probability is below 2^-45 of the largest is not chosen.
+ * Numerics: a weight is exact to 2^-44 of the row's largest, and sums of weights
+ * are exact; a token whose probability is below 2^-45 of the largest is not chosen.
  *   workspace    at least qmm_sample_workspace_bytes(n_rows, vocab) bytes, 16-byte
  *                aligned; overwritten; two calls in flight must not share one
  * n_rows < 2^22; n_rows == 0 is a no-op.
