@@ -83,10 +83,11 @@ struct Kv4Args {
   float c0;  // scale * log2(e)
 };
 
+__device__ __forceinline__ int chunks_in(int n) { return n / kChunk + (n % kChunk != 0); }  // (n up to 2^31 - 1)
 // Chunks of row r's keys; a length that the table does not hold is none.
 __device__ __forceinline__ int chunks_of(const Kv4Args &a, int r) {
   const int n = r < a.n_rows ? a.lengths[r] : 0;
-  return n < 0 || n > a.cap ? 0 : static_cast<int>((static_cast<int64_t>(n) + kChunk - 1) / kChunk);
+  return n < 0 || n > a.cap ? 0 : chunks_in(n);
 }
 // A unit of work is a range of a row's keys, all about the same length over all
 // rows, whatever their lengths: every workgroup sums the lengths to get it, and
@@ -290,7 +291,7 @@ __global__ __launch_bounds__(kThreads, resident(D, CT)) void attn_kv4_kernel(Kv4
   const int len = __builtin_amdgcn_readfirstlane(a.lengths[row]);
   const bool bad_len = len < 0 || len > a.cap;
   const int n = bad_len ? 0 : len;
-  const int chunks = (n + kChunk - 1) / kChunk;
+  const int chunks = chunks_in(n);
   const int lo = __builtin_amdgcn_readfirstlane(static_cast<int>(static_cast<int64_t>(split) * chunks / used));
   const int hi = __builtin_amdgcn_readfirstlane(static_cast<int>(static_cast<int64_t>(split + 1) * chunks / used));
   const int mine = max(0, (hi - lo - wave + kWaves - 1) / kWaves);  // chunks lo + wave, + kWaves, ..
