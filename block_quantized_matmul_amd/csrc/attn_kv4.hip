@@ -29,8 +29,9 @@
 //
 // Weights are binary16 in the second product, relative to two references: the
 // row's maximum m (as in attn_core.h) and for each column an exponent E that
-// follows the values' scales, so that neither large nor small scales leave
-// binary16's range: p = 2^(c x - c m - E) d.
+// follows the largest weight times scale, p = 2^(c x - c m - E) d, so that no product
+// leaves binary16's range above, and those that do below are too small to count
+// (whatever the scales alone: a key without a weight may have any).
 //
 // Four wavefronts take chunks of 64 keys in turn, each with the next chunk on
 // its way while it computes; they join through LDS. Where rows are few, their
@@ -64,9 +65,10 @@ constexpr int kFewGroups = 1024;  // fewer workgroups than this, four per CU on 
 // 48 rows of up to 8000 keys in 768, 1024, 1536, 2048, 4096 workgroups: 68, 75,
 // 75, 75, 90 us; 3 rows of 60000: 26, 31, 29, 34, 40 us.
 constexpr int resident(int64_t head_dim, int64_t columns) { return columns == 2 ? 2 : head_dim == 128 ? 3 : 4; }
-constexpr float kWeightSlack = 4.f;  // weights up to 2^4,
-constexpr int kScaleTop = 7;         // scales in [2^7, 2^8) when the exponent is taken,
-constexpr float kScaleMost = 2048.f;  // and up to 2^11 before it follows: products below 2^15
+constexpr float kWeightSlack = 4.f;  // weights up to 2^4
+constexpr int kProductTop = 7;       // the largest product is in [2^7, 2^8) when the exponent is taken,
+constexpr float kProductMost = 32768.f;  // and up to 2^15 before it follows
+constexpr int kLeastExponent = -100;  // where it starts: weights up to 2^4 times scales below 2^16 stay within fp32
 
 struct Kv4Args {
   const void *q;
@@ -182,7 +184,7 @@ template <int D> struct Column {
   half8_t q[NB];      // the first product's operand for block b: zeros but in columns (h, b)
   float start;        // -8 sum q, where the scores' sum starts
   float c;            // weights are 2^(c x - c m) for raw scores x
-  float m, mu_e, l;   // reference, its Reference::mu plus E, this lane's part of the sum (relative to 2^E too)
+  float m, mu_e, l;   // reference, its Reference::mu plus E, this lane's part of the sum
   int e;              // E
   float4_t o[D / 16];  // outputs 16 dt + 4 g + r of column lane % 16, in units of 2^(E - 24), but for
   float4_t zero;      // -8 sum p, to be added to each
@@ -219,7 +221,7 @@ template <class E, int D> __device__ __forceinline__ void start_column(Column<D>
   s.c = fminf(fmaxf(__builtin_ldexpf(a.c0, 12 + ex), 0x1p-126f), 0x1p126f);
   s.m = -__builtin_inff();
   s.mu_e = s.l = 0.f;
-  s.e = 0;
+  s.e = kLeastExponent;
 #pragma unroll
   for (int i = 0; i < D / 16; ++i) s.o[i] = float4_t{};
   s.zero = float4_t{};
@@ -233,33 +235,20 @@ __device__ __forceinline__ void weigh(Column<D> &s, float x[kTiles][4], const u3
 #pragma unroll
   for (int i = 2; i < 4 * kTiles; ++i) mx = fmaxf(mx, x[i / 4][i % 4]);
   mx = max_over_rows(mx);
-  // the largest of the lane's scales, as bits (a NaN is above all others and makes its products NaN whatever E)
-  typedef uint16_t u16x2 __attribute__((ext_vector_type(2)));
-  u16x2 top = {0, 0};
-#pragma unroll
-  for (int t = 0; t < kTiles; ++t) {
-    top = __builtin_elementwise_max(top, __builtin_bit_cast(u16x2, dv[t].x & 0x7FFF7FFFu));
-    top = __builtin_elementwise_max(top, __builtin_bit_cast(u16x2, dv[t].y & 0x7FFF7FFFu));
-  }
-  const float dmax = half_bits_to_float(min(max(top.x, top.y), static_cast<uint16_t>(0x7BFF)));
-  if (__any((mx - s.m) * s.c > kWeightSlack || __builtin_ldexpf(dmax, -s.e) > kScaleMost)) {
+  float f = 1.f;  // from sums relative to the old m to those relative to the new one
+  const bool moved = __any((mx - s.m) * s.c > kWeightSlack);
+  if (moved) {
     const float m = fmaxf(s.m, mx);
-    const float d = max_over_rows(dmax);
-    const int e = d > 0.f ? (__builtin_amdgcn_frexp_expf(d) - 1) - kScaleTop : s.e;
-    const float f = __builtin_ldexpf(rescaling(s.m, m, s.c), s.e - e);
-    s.m = m, s.e = e;
-    s.mu_e = Reference(m, s.c).mu + static_cast<float>(e);
-    s.l *= f;
-    s.zero *= f;
-#pragma unroll
-    for (int i = 0; i < D / 16; ++i) s.o[i] *= f;
+    f = rescaling(s.m, m, s.c);
+    s.m = m, s.l *= f;
+    s.mu_e = Reference(m, s.c).mu + static_cast<float>(s.e);
   }
   const float sub = Reference(s.m, s.c).sub;
   if (__any(sub != 0.f)) {
 #pragma unroll
     for (int i = 0; i < 4 * kTiles; ++i) x[i / 4][i % 4] -= sub;
   }
-  float sum[2] = {0.f, 0.f};
+  float sum[2] = {0.f, 0.f}, most = 0.f;  // (a NaN is not above others: its column is NaNs whatever E)
 #pragma unroll
   for (int t = 0; t < kTiles; ++t)
 #pragma unroll
@@ -267,9 +256,29 @@ __device__ __forceinline__ void weigh(Column<D> &s, float x[kTiles][4], const u3
       const int j = 4 * (t & 1) + r;  // the key's place in its step: one whose codes count 16 times has a 16th of the weight
       const float w = __builtin_amdgcn_exp2f(__builtin_fmaf(x[t][r], s.c, -s.mu_e - (times16(j) ? 4.f : 0.f)));
       sum[times16(j)] += w;
-      p[t >> 1][j] = static_cast<_Float16>(__builtin_fmaf(w, half_at(dv[t], r), 0.f));
+      x[t][r] = __builtin_fmaf(w, half_at(dv[t], r), 0.f);
+      most = fmaxf(most, __builtin_fabsf(x[t][r]));
     }
-  s.l += __builtin_fmaf(sum[1], 16.f, sum[0]);
+  s.l += __builtin_ldexpf(__builtin_fmaf(sum[1], 16.f, sum[0]), s.e);
+  if (moved || __any(most > kProductMost)) {
+    // The largest product so far: the chunk's, or one before, which was 2^7 at least when E was taken. Without
+    // any, E starts again.
+    most = fmaxf(__builtin_ldexpf(f, kProductTop), max_over_rows(most));
+    const int least = kLeastExponent - s.e;
+    const int up = most > 0.f ? max(__builtin_amdgcn_frexp_expf(most) - 1 - kProductTop, least) : least;
+    s.e += up, s.mu_e += static_cast<float>(up);
+    const float down = __builtin_ldexpf(1.f, -up);
+#pragma unroll
+    for (int i = 0; i < 4 * kTiles; ++i) x[i / 4][i % 4] *= down;
+    f *= down;
+    s.zero *= f;
+#pragma unroll
+    for (int i = 0; i < D / 16; ++i) s.o[i] *= f;
+  }
+#pragma unroll
+  for (int t = 0; t < kTiles; ++t)
+#pragma unroll
+    for (int r = 0; r < 4; ++r) p[t >> 1][4 * (t & 1) + r] = static_cast<_Float16>(x[t][r]);
 }
 
 template <class E, int D, int CT>
@@ -464,7 +473,7 @@ __global__ __launch_bounds__(kThreads, resident(D, CT)) void attn_kv4_kernel(Kv4
         for (int q = 1; q < NB; ++q) v = b == q ? s[k].o[2 * q + i][r] : v;
         at[(4 * i + r) * 64] = (v + s[k].zero[r]) * unit_v;
       }
-    const float l = __builtin_ldexpf(sum_over_rows(s[k].l), s[k].e);
+    const float l = sum_over_rows(s[k].l);
     at[8 * 64] = s[k].m;
     at[9 * 64] = poison ? __builtin_bit_cast(float, 0x7FC00000u) : l;
   }
