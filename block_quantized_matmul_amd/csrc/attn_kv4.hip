@@ -31,7 +31,10 @@
 // row's maximum m (as in attn_core.h) and for each column an exponent E that
 // follows the largest weight times scale, p = 2^(c x - c m - E) d, so that no product
 // leaves binary16's range above, and those that do below are too small to count
-// (whatever the scales alone: a key without a weight may have any).
+// (whatever the scales alone: a key without a weight may have any). Each p is two
+// numbers, the nearest and what is left (with the first alone, outputs of 700 keys were
+// off by rms 2.8e-4 in fp16, of which their own rounding is 2.0e-4). That costs 2 us of
+// 49 and of 25 (below).
 //
 // Four wavefronts take chunks of 64 keys in turn, each with the next chunk on
 // its way while it computes; they join through LDS. Where rows are few, their
@@ -39,10 +42,9 @@
 // second launch joins them.
 //
 // Measured: 48 rows of up to 8000 keys (192000 in all), 8 KV heads of 128, groups of 4,
-// bf16: 58 us + 5 for the join, 221 MB at 3.8 TB/s; 3 rows of up to 60000, 16 heads of
-// 64, fp16: 26 + 5 us, 103 MB at 4.0 TB/s. Vector instructions fill half of the cycles
-// (codes to operands a third of them), and registers hold two to four wavefronts a
-// SIMD, so waits are not always covered; a second chunk on its way is not built.
+// bf16: 51 us + 5 for the join, 221 MB at 4.3 TB/s; 3 rows of up to 60000, 16 heads of
+// 64, fp16: 27 + 5 us, 103 MB at 3.8 TB/s. Registers hold two to four wavefronts a SIMD,
+// so waits are not always covered; a second chunk on its way is not built.
 #include "attn_core.h"
 #include "launch.h"
 #include "serve.h"
@@ -62,8 +64,9 @@ constexpr int kTiles = kChunk / kKv4Tile;
 constexpr int kFewestUnits = 5;
 constexpr int kFewGroups = 1024;  // fewer workgroups than this, four per CU on 256 CUs: rows are split
 // Workgroups of a CU that its registers hold: as many as run at once are wanted.
-// 48 rows of up to 8000 keys in 768, 1024, 1536, 2048, 4096 workgroups: 68, 75,
-// 75, 75, 90 us; 3 rows of 60000: 26, 31, 29, 34, 40 us.
+// Kernel and join of 48 rows of up to 8000 keys, of which 768 run at once, in 512, 768,
+// 1024, 1536, 2048, 4096 workgroups: 66, 55, 61, 57, 61, 68 us; of 3 rows of 60000, of
+// which 1024 do: 38, 32, 32, 36, 38, 49.
 constexpr int resident(int64_t head_dim, int64_t columns) { return columns == 2 ? 2 : head_dim == 128 ? 3 : 4; }
 constexpr float kWeightSlack = 4.f;  // weights up to 2^4
 constexpr int kProductTop = 7;       // the largest product is in [2^7, 2^8) when the exponent is taken,
@@ -228,9 +231,10 @@ template <class E, int D> __device__ __forceinline__ void start_column(Column<D>
 }
 
 // Weights of a chunk's raw scores x (a lane's keys 16 t + 4 g + r), times the
-// values' scales, as the second product's operands of its two steps.
+// values' scales, as the second product's operands of its two steps, and what
+// their rounding leaves.
 template <int D>
-__device__ __forceinline__ void weigh(Column<D> &s, float x[kTiles][4], const u32x2_t dv[kTiles], half8_t p[2]) {
+__device__ __forceinline__ void weigh(Column<D> &s, float x[kTiles][4], const u32x2_t dv[kTiles], half8_t p[2][2]) {
   float mx = fmaxf(x[0][0], x[0][1]);
 #pragma unroll
   for (int i = 2; i < 4 * kTiles; ++i) mx = fmaxf(mx, x[i / 4][i % 4]);
@@ -278,7 +282,17 @@ __device__ __forceinline__ void weigh(Column<D> &s, float x[kTiles][4], const u3
 #pragma unroll
   for (int t = 0; t < kTiles; ++t)
 #pragma unroll
-    for (int r = 0; r < 4; ++r) p[t >> 1][4 * (t & 1) + r] = static_cast<_Float16>(x[t][r]);
+    for (int r = 0; r < 4; ++r) p[0][t >> 1][4 * (t & 1) + r] = static_cast<_Float16>(x[t][r]);
+  float minus = -1.f;
+  asm("" : "+s"(minus));  // (or the subtraction's operand is converted by an instruction of its own)
+#pragma unroll
+  for (int t = 0; t < kTiles; ++t) {
+    const u32x4_t u = __builtin_bit_cast(u32x4_t, p[0][t >> 1]);
+    const u32x2_t four = t & 1 ? u32x2_t{u.z, u.w} : u32x2_t{u.x, u.y};
+#pragma unroll
+    for (int r = 0; r < 4; ++r)
+      p[1][t >> 1][4 * (t & 1) + r] = static_cast<_Float16>(__builtin_fmaf(half_at(four, r), minus, x[t][r]));
+  }
 }
 
 template <class E, int D, int CT>
@@ -430,7 +444,7 @@ __global__ __launch_bounds__(kThreads, resident(D, CT)) void attn_kv4_kernel(Kv4
         wait_reads();
         copy_values((i + 1) & 1);
       }
-      half8_t p[CT][2];
+      half8_t p[CT][2][2];
 #pragma unroll
       for (int k = 0; k < CT; ++k) weigh<D>(s[k], x[k], dv, p[k]);
       if (more) load_scales();
@@ -445,14 +459,18 @@ __global__ __launch_bounds__(kThreads, resident(D, CT)) void attn_kv4_kernel(Kv4
           const half8_t values = unpack_codes(static_cast<uint32_t>(v[step]));
 #pragma unroll
           for (int k = 0; k < CT; ++k)
-            s[k].o[dt] = __builtin_amdgcn_mfma_f32_16x16x32_f16(values, p[k][step], s[k].o[dt], 0, 0, 0);
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+              s[k].o[dt] = __builtin_amdgcn_mfma_f32_16x16x32_f16(values, p[k][h][step], s[k].o[dt], 0, 0, 0);
         }
       }
 #pragma unroll
       for (int step = 0; step < 2; ++step)
 #pragma unroll
         for (int k = 0; k < CT; ++k)
-          s[k].zero = __builtin_amdgcn_mfma_f32_16x16x32_f16(minus8, p[k][step], s[k].zero, 0, 0, 0);
+#pragma unroll
+          for (int h = 0; h < 2; ++h)
+            s[k].zero = __builtin_amdgcn_mfma_f32_16x16x32_f16(minus8, p[k][h][step], s[k].zero, 0, 0, 0);
     }
   }
 

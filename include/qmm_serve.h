@@ -127,9 +127,9 @@ int qmm_kv4_read(int type, const qmm_heads *K, const qmm_heads *V, int64_t n_row
  * O may be Q itself, with equal strides; otherwise it overlaps nothing.
  * Numerics: codes and Q are multiplied exactly (a Q's element below 2^-25 of the
  * row's largest counts as less than its rounding); scores, maximum and sums in
- * fp32; each weight times its value's scale is rounded to binary16 relative to the
- * largest such product of the row (one below 2^-21 of it to 2^-32 of it), and the
- * output once at the end. A Q with an infinity or a NaN gives NaNs.
+ * fp32; each weight times its value's scale is taken as two binary16 numbers (error
+ * at most 2^-22 of it, or 2^-28 of the row's largest such product), and the output is
+ * rounded once. A Q with an infinity or a NaN gives NaNs.
  * n_rows < 2^24, n_rows * n_q_heads < 2^24, table_width * page_tokens < 2^31,
  * n_pages >= 1 (QMM_ERR_SHAPE).
  */
