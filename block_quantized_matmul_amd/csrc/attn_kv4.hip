@@ -10,7 +10,10 @@
 //    is the subnormal n 2^-24, one in bits 4..7 is 16 n 2^-24, and the matrix
 //    cores take subnormals exactly. The 16 is taken out of the other operand,
 //    the 2^-24 out of the result, and the zero point 8 is a constant per column:
-//    -8 sum q starts the scores' sum, -8 sum p is a column of its own.
+//    -8 sum q starts the scores' sum, 8 sum p is a column of its own, taken off in
+//    the end. (Sums of subnormals are cut off downwards by some 2^-21 of their terms;
+//    the difference of two such sums is not. With -8 sum p added, 60000 keys' outputs
+//    were 7e-7 of the values too low, a third of their fp16 rounding.)
 //  * A block's scale belongs to a key and 32 elements. The matrix cores' 16
 //    columns hold H = 16 / NB query heads of the group times the NB = D / 32
 //    blocks: column (h, b) of the first operand has q_h's elements of block b
@@ -32,9 +35,9 @@
 // follows the largest weight times scale, p = 2^(c x - c m - E) d, so that no product
 // leaves binary16's range above, and those that do below are too small to count
 // (whatever the scales alone: a key without a weight may have any). Each p is two
-// numbers, the nearest and what is left (with the first alone, outputs of 700 keys were
-// off by rms 2.8e-4 in fp16, of which their own rounding is 2.0e-4). That costs 2 us of
-// 49 and of 25 (below).
+// numbers, the nearest and what is left, so that outputs are off by their own rounding
+// alone (rms 2.0e-4 in fp16, 1.65e-3 in bf16; with the first number alone fp16 outputs
+// of 700 and of 60000 keys by 2.8e-4). That costs 2 us of 49 and of 25 (below).
 //
 // Four wavefronts take chunks of 64 keys in turn, each with the next chunk on
 // its way while it computes; they join through LDS. Where rows are few, their
@@ -190,7 +193,7 @@ template <int D> struct Column {
   float m, mu_e, l;   // reference, its Reference::mu plus E, this lane's part of the sum
   int e;              // E
   float4_t o[D / 16];  // outputs 16 dt + 4 g + r of column lane % 16, in units of 2^(E - 24), but for
-  float4_t zero;      // -8 sum p, to be added to each
+  float4_t zero;      // 8 sum p, to be taken from each
 };
 
 template <class E, int D> __device__ __forceinline__ void start_column(Column<D> &s, const Kv4Args &a, int row, int head0,
@@ -396,7 +399,7 @@ __global__ __launch_bounds__(kThreads, resident(D, CT)) void attn_kv4_kernel(Kv4
     const int ri = lane & 15, rj = (ri & 3) * 2 + ((ri >> 2) & 1);
     const int r_tile = 2 * (ri >> 3) + (rj >> 2), r_row = 16 * r_tile + 4 * g + (rj & 3);
     const uint32_t v_at = r_row * kRow + 16 * (r_tile & (D / 32 - 1));
-    const half8_t minus8 = __builtin_bit_cast(half8_t, u32x4_t{0x80088008u, 0x80808080u, 0x80088008u, 0x80808080u});
+    const half8_t eights = __builtin_bit_cast(half8_t, u32x4_t{0x00080008u, 0x00800080u, 0x00080008u, 0x00800080u});
 
     locate(0);
     load_keys();
@@ -470,7 +473,7 @@ __global__ __launch_bounds__(kThreads, resident(D, CT)) void attn_kv4_kernel(Kv4
         for (int k = 0; k < CT; ++k)
 #pragma unroll
           for (int h = 0; h < 2; ++h)
-            s[k].zero = __builtin_amdgcn_mfma_f32_16x16x32_f16(minus8, p[k][h][step], s[k].zero, 0, 0, 0);
+            s[k].zero = __builtin_amdgcn_mfma_f32_16x16x32_f16(eights, p[k][h][step], s[k].zero, 0, 0, 0);
     }
   }
 
@@ -489,7 +492,7 @@ __global__ __launch_bounds__(kThreads, resident(D, CT)) void attn_kv4_kernel(Kv4
         float v = s[k].o[i][r];
 #pragma unroll
         for (int q = 1; q < NB; ++q) v = b == q ? s[k].o[2 * q + i][r] : v;
-        at[(4 * i + r) * 64] = (v + s[k].zero[r]) * unit_v;
+        at[(4 * i + r) * 64] = (v - s[k].zero[r]) * unit_v;
       }
     const float l = sum_over_rows(s[k].l);
     at[8 * 64] = s[k].m;
