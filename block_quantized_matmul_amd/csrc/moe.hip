@@ -461,24 +461,26 @@ struct Routed {
 constexpr int64_t route_lds(int64_t n, int64_t experts, int64_t used, int64_t most) {
   return n * experts * 8 + most * (static_cast<int64_t>(sizeof(Active)) + kSetTokens * 4) + n * used * 8 + (2 * experts + 1) * 4;
 }
+// An integer of a logit's order; a NaN's is below all others.
+__device__ __forceinline__ int64_t order_of(double x) {
+  const int64_t bits = __builtin_bit_cast(int64_t, x + 0.);  // (-0 is 0)
+  return x != x ? INT64_MIN : bits < 0 ? bits ^ INT64_MAX : bits;
+}
 template <int THREADS> __device__ __forceinline__ Routed route(const MoeArgs &a, uint8_t *smem, bool write) {
   const int n = a.n_tokens, experts = a.n_experts, items = n * experts;
-  double *l = reinterpret_cast<double *>(smem);                      // [n][experts], NaN as -infinity
+  int64_t *l = reinterpret_cast<int64_t *>(smem);                    // [n][experts] order_of
   Active *sets = reinterpret_cast<Active *>(l + items);              // [most]
   float *share = reinterpret_cast<float *>(sets + a.most);           // [most][kSetTokens]
   float *w = share + a.most * kSetTokens;                            // [n][n_used]
   int *id = reinterpret_cast<int *>(w + n * a.n_used);               // [n][n_used]
   int *place = id + n * a.n_used;                                    // [experts + 1], the last: sets in all
   uint32_t *by = reinterpret_cast<uint32_t *>(place + experts + 1);  // [experts] a bit for each token
-  for (int i = threadIdx.x; i < items; i += THREADS) {
-    const double v = a.logits[i];
-    l[i] = v != v ? -__builtin_inf() : v;
-  }
+  for (int i = threadIdx.x; i < items; i += THREADS) l[i] = order_of(a.logits[i]);
   for (int i = threadIdx.x; i < experts; i += THREADS) by[i] = 0;
   __syncthreads();
   for (int i = threadIdx.x; i < items; i += THREADS) {
     const int t = i / experts, e = i % experts;
-    const double mine = l[i], *row = l + t * experts;
+    const int64_t mine = l[i], *row = l + t * experts;
     int rank = 0;
     for (int k = 0; k < experts; ++k) rank += row[k] > mine || (row[k] == mine && k < e);
     if (rank < a.n_used) {
@@ -491,7 +493,7 @@ template <int THREADS> __device__ __forceinline__ Routed route(const MoeArgs &a,
   const int lane = threadIdx.x & 63;
   for (int t = threadIdx.x >> 6; t < n; t += THREADS / 64) {
     const double *row = a.logits + static_cast<int64_t>(t) * experts;
-    const double top = l[t * experts + id[t * a.n_used]];
+    const double top = row[id[t * a.n_used]];
     float sum = 0.f;
     if (a.renormalise) {
       for (int k = lane; k < a.n_used; k += 64) sum += expf(static_cast<float>(row[id[t * a.n_used + k]] - top));

@@ -172,7 +172,7 @@ def choice(x, router, n_used, renormalise=True):
     logits = np.asarray(x, np.longdouble) @ np.asarray(router, np.longdouble).T
     with np.errstate(invalid="ignore", over="ignore"):
         key = np.where(np.isnan(logits), -np.inf, logits)
-        ids = np.argsort(-key, axis=-1, kind="stable")[:, :n_used]
+        ids = np.lexsort((np.isnan(logits), -key), axis=-1)[:, :n_used]  # (a NaN behind -infinity)
         top = np.take_along_axis(key, ids[:, :1], -1)
         w = np.exp(np.take_along_axis(logits, ids, -1) - top)
         total = w.sum(-1, keepdims=True) if renormalise else np.exp(logits - top).sum(-1, keepdims=True)
