@@ -56,6 +56,7 @@ constexpr int kRouteThreads = 1024;
 constexpr int kLogitThreads = 256;
 constexpr int kLogitTokens = 4;  // tokens of a logit workgroup
 constexpr float kLoScale = 2048.f;
+constexpr int kLdsBytes = 160 * 1024;  // of a CU
 
 // ------------------------------------------------------------- operands
 
@@ -717,16 +718,6 @@ int pieces_for(int64_t n_tokens) { return n_tokens <= 4 ? 1 : 2; }
 struct Plan {
   int waves, peers, parts, groups;
 };
-// gate and up: `most` sets. Four workgroups a CU (40 KiB of LDS each), in one round if they fit.
-constexpr int64_t kOneRound = 1024;
-Plan inner_plan(int64_t n_tokens, int64_t n_ff, int64_t most) {
-  Plan p{kInnerWaves, 1, 1, 1};
-  const int64_t units = (n_ff + 15) / 16;
-  while (p.peers * pieces_for(n_tokens) < set_tokens(n_tokens)) p.peers *= 2;
-  while (p.peers < p.waves && (units + p.peers - 1) / p.peers * most > kOneRound) p.peers *= 2;
-  p.parts = p.waves / p.peers;
-  return p;
-}
 // down: one token's rows by 16 wavefronts each (8 for Q8_0, whose rings are larger);
 // of more tokens' by as many workgroups as make about 4 a CU, since only wavefronts
 // with different rows can share the tokens.
@@ -752,13 +743,40 @@ template <class R, int WAVES> int lds_bytes(const Plan &p, int64_t n_tokens, boo
   return Lds<R, WAVES>::kRings + static_cast<int>(set_tokens(n_tokens)) * kQuadOps * (short_rows ? WAVES : R::kStages * p.parts);
 }
 
-template <int QT> hipError_t run_inner(const MoeArgs &a, int64_t most, hipStream_t stream) {
-  const Plan p = inner_plan(a.n_tokens, a.n_ff, most);
-  const dim3 grid(static_cast<unsigned>(((a.n_ff + 15) / 16 + p.peers - 1) / p.peers), static_cast<unsigned>(most));
+// gate and up, of `most` sets: workgroups of few rows, but in one round if that is
+// possible, of as many as a CU's registers (four) and LDS hold: two of Q8_0, whose rings
+// are larger. (1 token, 8 of 256 experts of 2048 x 4096 Q4_0: 51 us in one round, 63 in
+// a third more workgroups than run at once; 2 of 8 of 14336 x 4096 Q8_0 90 and 95.)
+template <int QT> struct InnerPlan : Plan {
+  int64_t blocks;  // workgroups of a set
+  bool one_round;
+  InnerPlan(const MoeArgs &a, int64_t most) : Plan{kInnerWaves, 1, 1, 1} {
+    const int64_t units = (a.n_ff + 15) / 16;
+    while (peers * pieces_for(a.n_tokens) < set_tokens(a.n_tokens)) peers *= 2;
+    for (;; peers *= 2) {
+      parts = waves / peers, blocks = (units + peers - 1) / peers;
+      one_round = blocks * most <= 256 * std::min(4, kLdsBytes / lds(a));
+      if (one_round || peers == waves) return;
+    }
+  }
+  int lds(const MoeArgs &a) const { return lds_bytes<InnerRows<QT>, kInnerWaves>(*this, a.n_tokens, a.k < 256); }
+};
+
+// Where a thread has a logit at most, and the workgroups run all at once, each makes
+// the choice for itself (1 token of 8 experts: 37 us instead of 35 + 5 and a launch; 16
+// tokens, in many rounds: 180 instead of 160 + 5).
+template <int QT> hipError_t run_inner(MoeArgs &a, hipStream_t stream) {
+  const InnerPlan<QT> p(a, a.most);
+  const int64_t route = route_lds(a.n_tokens, a.n_experts, a.n_used, a.most);
+  a.parts_in = p.parts;
+  a.route_here = a.n_tokens * a.n_experts <= 64 * kInnerWaves && p.one_round;
+  if (!a.route_here) {
+    const hipError_t e = launch(moe_route_kernel, dim3(1), dim3(kRouteThreads), static_cast<size_t>(route), stream, a);
+    if (e != hipSuccess) return e;
+  }
+  const dim3 grid(static_cast<unsigned>(p.blocks), static_cast<unsigned>(a.most));
   return launch(moe_inner_kernel<QT>, grid, dim3(64 * kInnerWaves),
-                std::max<size_t>(lds_bytes<InnerRows<QT>, kInnerWaves>(p, a.n_tokens, a.k < 256),
-                                 a.route_here ? route_lds(a.n_tokens, a.n_experts, a.n_used, a.most) : 0),
-                stream, a);
+                static_cast<size_t>(std::max<int64_t>(p.lds(a), a.route_here ? route : 0)), stream, a);
 }
 template <int QT, int WAVES> hipError_t run_outer(MoeArgs a, hipStream_t stream) {
   const Plan p = outer_plan(a.n_tokens, a.k, QT);
@@ -806,22 +824,10 @@ hipError_t launch_moe(const MoeLayer &m, void *workspace, hipStream_t stream) {
   const unsigned first = static_cast<unsigned>(a.logit_groups + (m.k * m.n_tokens + kLogitThreads - 1) / kLogitThreads);
   hipError_t e = launch(moe_prepare_kernel, dim3(first), dim3(kLogitThreads), 0, stream, a);
   if (e != hipSuccess) return e;
-  // Where a thread has a logit at most, and the next launch's workgroups run all at
-  // once, each makes the choice for itself (1 token of 8 experts: 37 us instead of 35 + 5
-  // and a launch; 16 tokens, in many rounds: 180 instead of 160 + 5).
   a.most = static_cast<int>(most);
-  const Plan in = inner_plan(m.n_tokens, m.n_ff, most);
-  a.parts_in = in.parts;
-  a.route_here = m.n_tokens * m.n_experts <= 64 * kInnerWaves &&
-                 ((m.n_ff + 15) / 16 + in.peers - 1) / in.peers * most <= kOneRound;
-  if (!a.route_here) {
-    e = launch(moe_route_kernel, dim3(1), dim3(kRouteThreads),
-               static_cast<size_t>(route_lds(m.n_tokens, m.n_experts, m.n_used, most)), stream, a);
-    if (e != hipSuccess) return e;
-  }
   e = by_qtype_k(m.type_in, [&](auto q) {
     constexpr int QT = decltype(q)::value;
-    return run_inner<QT>(a, most, stream);
+    return run_inner<QT>(a, stream);
   });
   if (e != hipSuccess) return e;
   return by_qtype_k(m.type_out, [&](auto q) {
