@@ -33,6 +33,7 @@
 #include "launch.h"
 #include "serve.h"
 
+#include <algorithm>
 #include <type_traits>
 
 namespace qmm {
@@ -59,10 +60,10 @@ struct SampleArgs {
   const int32_t *top_k;
   int32_t *tokens;
   float *probs;
-  int vocab, chunks;
+  int vocab, chunks, room;
   // workspace
   struct RowState *rows;  // [n_rows]
-  struct Element *list;   // [n_rows][kList]
+  struct Element *list;   // [n_rows][room]
   struct Part *parts;     // [n_rows][chunks]
 };
 struct alignas(8) Element {
@@ -760,7 +761,7 @@ template <int TYPE> __global__ __launch_bounds__(kThreads) void sample_pick_kern
     return;
   }
   RowState &st = a.rows[row];
-  Element *list = a.list + static_cast<int64_t>(row) * kList;
+  Element *list = a.list + static_cast<int64_t>(row) * a.room;
   const int lo[3] = {st.lo[0], st.lo[1], st.lo[2]}, hi[3] = {st.hi[0], st.hi[1], st.hi[2]};
   __syncthreads();
   if (r.by_range) {
@@ -835,19 +836,21 @@ template <int TYPE> __global__ __launch_bounds__(kThreads) void sample_pick_kern
 }
 
 int64_t chunks_of(int64_t vocab) { return (vocab + kChunk - 1) / kChunk; }
+// Of a row's list: all that it can have, in whole lines.
+int64_t room_of(int64_t vocab) { return std::min<int64_t>(kList, (vocab + 15) / 16 * 16); }
 
 }  // namespace
 
 int64_t sample_workspace_bytes(int64_t n_rows, int64_t vocab) {
-  return n_rows * static_cast<int64_t>(sizeof(RowState) + kList * sizeof(Element) + chunks_of(vocab) * sizeof(Part));
+  return n_rows * static_cast<int64_t>(sizeof(RowState) + room_of(vocab) * sizeof(Element) + chunks_of(vocab) * sizeof(Part));
 }
 
 hipError_t launch_sample(const SampleCall &c, void *workspace, hipStream_t stream) {
   SampleArgs a{c.logits, c.row_stride, c.u, c.temperature, c.top_p, c.min_p, c.top_k, c.tokens, c.probs, static_cast<int>(c.vocab)};
-  a.chunks = static_cast<int>(chunks_of(c.vocab));
+  a.chunks = static_cast<int>(chunks_of(c.vocab)), a.room = static_cast<int>(room_of(c.vocab));
   a.rows = static_cast<RowState *>(workspace);
   a.list = reinterpret_cast<Element *>(a.rows + c.n_rows);
-  a.parts = reinterpret_cast<Part *>(a.list + c.n_rows * kList);
+  a.parts = reinterpret_cast<Part *>(a.list + c.n_rows * a.room);
   const dim3 grid(static_cast<unsigned>(c.n_rows), static_cast<unsigned>(a.chunks));
   auto go = [&](auto type) {
     constexpr int T = decltype(type)::value;
