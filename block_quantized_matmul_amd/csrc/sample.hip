@@ -65,27 +65,40 @@ struct SampleArgs {
   struct RowState *rows;  // [n_rows]
   struct Element *list;   // [n_rows][room]
   struct Part *parts;     // [n_rows][chunks]
+  struct Top *tops;       // [n_rows][chunks]
 };
 struct alignas(8) Element {
   float z;
   int i;
 };
+// What workgroups of one launch write and others of it read (`put` and `get`: the
+// parts, the lists and the counters) shares no line with what they read in the ordinary
+// way, whatever the workspace's alignment. A line that an L2 has taken in for the one
+// is then never asked for the other.
+constexpr int kLine = 128;
 struct Part {  // a chunk's
   uint64_t m[kBins];
   uint32_t n[kBins];
-  uint64_t left;    // mass that min_p leaves
-  uint32_t pad[32];  // (what is written here and read in one launch is in no line with the rest)
-  float most, least;  // its largest logit, and its smallest finite one
+  uint64_t left;  // mass that min_p leaves
+  uint8_t apart[kLine];
+};
+struct Top {  // a chunk's largest logit, and its smallest finite one
+  float most, least;
 };
 enum { COUNT, BELOW, UPTO };
 struct RowState {
+  uint32_t arrived[2];  // workgroups, of the second and third launch
+  uint32_t listed;
+  uint8_t apart[kLine + 4];
   uint64_t m[kBins + 1];  // mass and count in front of every range
   uint32_t n[kBins + 1];
-  uint32_t arrived[2];    // workgroups, of the second and third launch
-  uint32_t listed;
   int lo[3], hi[3];       // ranges that may hold a selection's place; none where it is known
   uint64_t left;
+  uint8_t behind[kLine];
 };
+static_assert(offsetof(RowState, m) - offsetof(RowState, listed) >= kLine + sizeof(uint32_t) &&
+              sizeof(RowState) - offsetof(RowState, left) >= kLine + sizeof(uint64_t) &&
+              sizeof(Part) - offsetof(Part, left) >= kLine + sizeof(uint64_t) && sizeof(RowState) % 8 == 0);
 
 template <int TYPE> __device__ __forceinline__ float load_logit(const void *z, int64_t at) {
   float x;
@@ -340,8 +353,8 @@ __device__ __forceinline__ Row row_of(Shared &s, const SampleArgs &a, int row) {
   Row r;
   float most = -__builtin_inff(), least = __builtin_inff();
   for (int k = lane; k < a.chunks; k += 64) {
-    const Part &p = a.parts[static_cast<int64_t>(row) * a.chunks + k];
-    most = fmaxf(most, p.most), least = fminf(least, p.least);
+    const Top top = a.tops[static_cast<int64_t>(row) * a.chunks + k];
+    most = fmaxf(most, top.most), least = fminf(least, top.least);
   }
 #pragma unroll
   for (int d = 32; d > 0; d /= 2) most = fmaxf(most, __shfl_xor(most, d)), least = fminf(least, __shfl_xor(least, d));
@@ -644,8 +657,7 @@ template <int TYPE> __global__ __launch_bounds__(kThreads) void sample_top_kerne
   __syncthreads();
   if (threadIdx.x != 0) return;
   for (int k = 1; k < kWaves; ++k) most = fmaxf(most, high[k]), least = fminf(least, low[k]);
-  Part &p = a.parts[static_cast<int64_t>(row) * a.chunks + chunk];
-  p.most = most, p.least = least;
+  a.tops[static_cast<int64_t>(row) * a.chunks + chunk] = {most, least};
   if (chunk == 0) {
     RowState &st = a.rows[row];
     st.arrived[0] = st.arrived[1] = st.listed = 0;
@@ -842,7 +854,8 @@ int64_t room_of(int64_t vocab) { return std::min<int64_t>(kList, (vocab + 15) / 
 }  // namespace
 
 int64_t sample_workspace_bytes(int64_t n_rows, int64_t vocab) {
-  return n_rows * static_cast<int64_t>(sizeof(RowState) + room_of(vocab) * sizeof(Element) + chunks_of(vocab) * sizeof(Part));
+  return n_rows * static_cast<int64_t>(sizeof(RowState) + room_of(vocab) * sizeof(Element) +
+                                       chunks_of(vocab) * (sizeof(Part) + sizeof(Top)));
 }
 
 hipError_t launch_sample(const SampleCall &c, void *workspace, hipStream_t stream) {
@@ -851,6 +864,7 @@ hipError_t launch_sample(const SampleCall &c, void *workspace, hipStream_t strea
   a.rows = static_cast<RowState *>(workspace);
   a.list = reinterpret_cast<Element *>(a.rows + c.n_rows);
   a.parts = reinterpret_cast<Part *>(a.list + c.n_rows * a.room);
+  a.tops = reinterpret_cast<Top *>(a.parts + c.n_rows * a.chunks);
   const dim3 grid(static_cast<unsigned>(c.n_rows), static_cast<unsigned>(a.chunks));
   auto go = [&](auto type) {
     constexpr int T = decltype(type)::value;
