@@ -43,14 +43,12 @@ namespace {
 constexpr int kThreads = 1024;
 constexpr int kWaves = kThreads / 64;
 constexpr int kBits = 11;      // of a key, at a time
-constexpr int kBins = 1024;     // ranges of logits
-constexpr int kOwn = kBins / kThreads;
+constexpr int kBins = kThreads;  // ranges of logits, one a thread
 constexpr int kChunk = 8 * kThreads;
 constexpr int kList = 16384;   // elements of a row that are looked at in the end
 constexpr int kAtOnce = 8;
 constexpr int kQuick = 64;      // of those: elements that are ranked all together, by one wavefront
 constexpr int kFew = 512;      // elements that are ranked one by one
-constexpr int kPoint = 44;     // binary places of a weight
 constexpr int kFractions = 64;  // of an octave, in the table of powers (k >> 6 below)
 
 struct SampleArgs {
@@ -455,13 +453,11 @@ struct Range {
 // The mass up to and with the last element whose start a goal reaches, and that
 // element's index (-1: not by ranges), of the elements in the row's list.
 __device__ __forceinline__ uint64_t resolve(Shared &s, const Element *list, int listed, const Element &own_element,
-                                            const Range own_range[kOwn], const Row &r, const Weights &w, int per,
+                                            const Range &own_range, const Row &r, const Weights &w, int per,
                                             const Goal &goal, int &index) {
   index = -1;
   const int t = threadIdx.x;
-#pragma unroll
-  for (int b = 0; b < kOwn; ++b)
-    if (own_range[b].is_last(goal, kOwn * t + b)) s.bin = kOwn * t + b, s.before = own_range[b].n0, s.mass = own_range[b].m0;
+  if (own_range.is_last(goal, t)) s.bin = t, s.before = own_range.n0, s.mass = own_range.m0;
   if (t == 0) s.few = 0;
   __syncthreads();
   const int bin = s.bin;
@@ -672,8 +668,7 @@ template <int TYPE> __global__ __launch_bounds__(kThreads) void sample_mass_kern
   load_eight<TYPE>(a.z, row * a.stride, a.vocab, chunk, x);
   const Row r = row_of(s, a, row);
   if (r.most == -__builtin_inff()) return;  // nothing to choose from
-#pragma unroll
-  for (int k = 0; k < kOwn; ++k) s.n[k * kThreads + t] = 0, s.m[k * kThreads + t] = 0;
+  s.n[t] = 0, s.m[t] = 0;
   __syncthreads();
   const Weights w{static_cast<double>(r.most), r.c, s.table};
   uint64_t left = 0;
@@ -692,36 +687,25 @@ template <int TYPE> __global__ __launch_bounds__(kThreads) void sample_mass_kern
   __syncthreads();
   Part *parts = a.parts + static_cast<int64_t>(row) * a.chunks;
   RowState &st = a.rows[row];
-#pragma unroll
-  for (int k = 0; k < kOwn; ++k) {
-    const int at = k * kThreads + t;
-    put(&parts[chunk].n[at], s.n[at]), put(&parts[chunk].m[at], s.m[at]);
-  }
+  put(&parts[chunk].n[t], s.n[t]), put(&parts[chunk].m[t], s.m[t]);
   if (r.limit > 0) left = sum_of(s, left);
   if (t == 0) put(&parts[chunk].left, left);
   if (!last_here(s, &st.arrived[0], a.chunks, 0)) return;
 
-  uint32_t own_n[kOwn] = {}, n = 0, all_n;  // ranges kOwn t, ..
-  uint64_t own_m[kOwn] = {}, m = 0, all_m;
+  uint32_t own_n = 0, all_n;  // of range t
+  uint64_t own_m = 0, all_m;
 #pragma unroll 4
-  for (int k = 0; k < a.chunks; ++k)
-#pragma unroll
-    for (int b = 0; b < kOwn; ++b) own_n[b] += get(&parts[k].n[kOwn * t + b]), own_m[b] += get(&parts[k].m[kOwn * t + b]);
+  for (int k = 0; k < a.chunks; ++k) own_n += get(&parts[k].n[t]), own_m += get(&parts[k].m[t]);
   left = 0;
   if (r.limit > 0 && t < a.chunks) left = get(&parts[t].left);  // (a row has at most 64)
   if (r.limit > 0) left = sum_of(s, left);
-#pragma unroll
-  for (int b = 0; b < kOwn; ++b) n += own_n[b], m += own_m[b];
+  uint32_t n = own_n;
+  uint64_t m = own_m;
   scan(s, n, m, all_n, all_m);
   if (r.limit == 0) left = all_m;
-  Range range[kOwn];
-#pragma unroll
-  for (int b = 0; b < kOwn; ++b) {
-    range[b] = {n, n + own_n[b], m, m + own_m[b]};
-    st.n[kOwn * t + b] = n, st.m[kOwn * t + b] = m;
-    s.m[kOwn * t + b] = m;
-    n += own_n[b], m += own_m[b];
-  }
+  const Range range{n, n + own_n, m, m + own_m};
+  st.n[t] = n, st.m[t] = m;
+  s.m[t] = m;
   if (t == 0) {
     st.n[kBins] = all_n, st.m[kBins] = s.m[kBins] = all_m;
     st.left = left;
@@ -739,9 +723,7 @@ template <int TYPE> __global__ __launch_bounds__(kThreads) void sample_mass_kern
 #pragma unroll
       for (int k = 0; k < 2; ++k) {
         const Goal goal = goal_of(r, kind, k ? hi_total : lo_total);
-#pragma unroll
-        for (int b = 0; b < kOwn; ++b)
-          if (range[b].is_last(goal, kOwn * t + b)) s.bins[k] = kOwn * t + b;
+        if (range.is_last(goal, t)) s.bins[k] = t;
       }
       __syncthreads();
       lo = s.bins[0], hi = s.bins[1];
@@ -808,12 +790,7 @@ template <int TYPE> __global__ __launch_bounds__(kThreads) void sample_pick_kern
     return;
   }
   const int per = (a.vocab + kThreads - 1) / kThreads;  // indexes of a part, at most kFew
-  Range own_range[kOwn];
-#pragma unroll
-  for (int b = 0; b < kOwn; ++b) {
-    const int at = kOwn * t + b;
-    own_range[b] = {st.n[at], st.n[at + 1], st.m[at], st.m[at + 1]};
-  }
+  const Range own_range{st.n[t], st.n[t + 1], st.m[t], st.m[t + 1]};
   const Element own_element = t < static_cast<int>(min(listed, static_cast<uint32_t>(kList))) ? get(list + t) : Element{0.f, 0};
   const uint64_t left = st.left;
   uint64_t total = st.m[kBins];
