@@ -214,7 +214,8 @@ int64_t qmm_moe_workspace_bytes(int64_t n_tokens, int64_t k, int64_t n_ff, int64
  *   u            fp32 [n_rows], from [0, 1): below (and NaN) it counts as 0, above
  *                as the largest number below 1
  *   temperature, top_p, min_p  fp32 [n_rows], top_k int32 [n_rows]; each may be
- *                NULL for 1, 1, 0 and 0: none. A NaN for top_p or min_p is none
+ *                NULL for 1, 1, 0 and 0: none. A NaN for top_p or min_p is none, a
+ *                min_p above 1 counts as 1
  *   tokens       int32 [n_rows]; -1 for a row without a probability (every logit
  *                -infinity or NaN)
  *   probs        fp32 [n_rows], the token's share of what step 4 chooses from
