@@ -119,10 +119,10 @@ def attend(q, k, v, dk, dv, scale, kind):
     most (15 + 8) |d| |q|, summed in fp32, and q below 2^-33 of its largest element
     is lost. That error, the exponent's own (a few steps of the scores' size) and
     the exponential's 2^-22 change the output by at most 2 d max |v|. A weight times
-    a scale is rounded to binary16, 2^-11, or where it is below 2^-14 relative to
-    2^7 of the largest scale and a weight of 2^-4 at least, absolutely: codes of
-    16 times the size, so 2^-25 2^4 2^4 2^-7 of the largest scale and 8 codes. The
-    outputs' sums have terms of 23 w |d|."""
+    a scale is two binary16 numbers, 2^-22, or absolutely half a step of binary16's
+    smallest, where the largest product is 2^7 at least: with codes of 16 times the
+    size, and 8 of them, 2^-25 2^4 2^3 2^-7 of it. The outputs' sums have terms of
+    23 w |d|."""
     n, dim = k.shape
     if n == 0:
         return np.zeros(dim), np.zeros(dim)
@@ -131,14 +131,13 @@ def attend(q, k, v, dk, dv, scale, kind):
     s_abs = 23 * (blocks @ np.abs(q)) * scale
     lost = 2.0 ** -33 * np.abs(q).max() * 23 * blocks.sum(-1).max() * scale
     w = np.exp(s - s.max())
-    total = w.sum()
-    w = w / total
+    w = w / w.sum()
     o = w @ v
     size = w @ np.repeat(np.abs(dv), 32, -1)
-    most = np.repeat(np.abs(dv).max(0), 32, -1)
+    most = np.repeat((w[:, None] * np.abs(dv)).max(0), 32, -1)
     u = HALF_STEP[kind]
     d = (dim + 16) * E32 * s_abs.max() + lost + 16 * E32 * (np.abs(s).max() + 16) + 2.0 ** -22
-    err = 2.0 ** -11 * (w @ np.abs(v)) + (n + 64) * E32 * 23 * size + n / total * 2.0 ** -21 * most \
+    err = 2.0 ** -22 * (w @ np.abs(v)) + (n + 64) * E32 * 23 * size + n * 2.0 ** -25 * most \
         + 2 * d * np.abs(v).max(0)
     return o, err + u * (np.abs(o) + err) + SUBNORMAL[kind]
 
