@@ -45,9 +45,10 @@
 // second launch joins them.
 //
 // Measured: 48 rows of up to 8000 keys (192000 in all), 8 KV heads of 128, groups of 4,
-// bf16: 51 us + 5 for the join, 221 MB at 4.3 TB/s; 3 rows of up to 60000, 16 heads of
-// 64, fp16: 27 + 5 us, 103 MB at 3.8 TB/s. Registers hold two to four wavefronts a SIMD,
-// so waits are not always covered; a second chunk on its way is not built.
+// bf16: 51 us + 5 for the join, 221 MB at 4.4 TB/s; 3 rows of up to 60000, 16 heads of
+// 64, fp16: 27 + 5 us, 103 MB at 3.8 TB/s. Matrix cores are busy in 83 and 74 % of the
+// cycles, vector instructions fill 52 and 67 %, and registers hold two to four wavefronts
+// a SIMD, so waits are not always covered; a second chunk on its way is not built.
 #include "attn_core.h"
 #include "launch.h"
 #include "serve.h"
@@ -62,8 +63,10 @@ constexpr int kThreads = 256;
 constexpr int kWaves = 4;
 constexpr int kChunk = 64;       // keys
 constexpr int kTiles = kChunk / kKv4Tile;
-// Tables of fewer than 5 x 256 keys are not worth a second launch: one row of 700 in a
-// table of 704 keys 9.2 us undivided, 12.8 divided; of 1000 11.0 and 12.8.
+// Tables of fewer than 5 x 256 keys are not worth a second launch: one row of 700 keys
+// whole 9.5 us, divided 11.8; of 1000 10.0 and 12.0; of 1200 11.3 and 12.2 (in a graph,
+// without the host's part, 8.2 and 9.1; 9.6 and 9.0; 11.1 and 9.1). The host does not
+// know the lengths, so a short row in a wide table is divided.
 constexpr int kFewestUnits = 5;
 constexpr int kFewGroups = 1024;  // fewer workgroups than this, four per CU on 256 CUs: rows are split
 // Workgroups of a CU that its registers hold: as many as run at once are wanted.
